@@ -460,6 +460,97 @@ mok_status_t mok_backward(const mok_config_t* cfg, const uint16_t* dy,
                           float* d_router_w, const mok_weight_grads_t* grads,
                           void* ws, size_t ws_bytes, void* stream);
 
+/* ======================================================================
+ * Operators around the layer: what a block and a training or serving step
+ * need next to it.  The conventions above hold; tensors whose type an
+ * argument selects are passed as void*.
+ * ====================================================================== */
+#define MOK_DTYPE_BF16 0
+#define MOK_DTYPE_F32  1
+
+/* The bf16 values of MXFP8 codes and scales: codes E4M3 [rows][K], scales E8M0
+ * [rows][ceil(K/32)] -> out bf16 [rows][K].  K % 32 == 0, or one row of any
+ * length.  Exact unless a value leaves bf16's range.  `scales` needs no
+ * alignment. */
+mok_status_t mok_mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
+                                  uint16_t* out, void* stream);
+
+/* ---- root-mean-square norm with the residual's addition -----------------
+ * Per row of H:  h = x + residual,  rstd = (mean(h^2) + eps)^-1/2,
+ * y_j = weight_j * h_j * rstd, all in fp32 from the unrounded h.
+ *   x [rows][H] bf16 or fp32; residual the same shape, bf16 or fp32, or NULL
+ *   (then h = x and nothing is written to h); weight [H] bf16 or fp32.
+ *   h: x + residual rounded to the residual's type (may be `residual`, or x
+ *   where the types agree); rstd fp32 [rows], kept for the backward.
+ *   y bf16 [rows][H] and / or codes, scales: the MXFP8 form of the fp32 y
+ *   (E4M3 [rows][H], E8M0 [rows][H/32], rounded once, by mok_mxfp8_quantize's
+ *   block rule); at least one of the two, the other NULL.
+ * Any H up to MOK_NORM_MAX_H (the MXFP8 output: H % 32 == 0); any number of
+ * rows, none included.  Non-finite inputs give non-finite outputs in their
+ * row; in a block that holds one, the MXFP8 scale is unspecified. */
+#define MOK_NORM_MAX_H 32768
+mok_status_t mok_rms_norm(const void* x, int x_dtype, const void* residual, int residual_dtype, const void* weight,
+                          int weight_dtype, int64_t rows, int H, float eps, void* h, uint16_t* y, uint8_t* codes,
+                          uint8_t* scales, float* rstd, void* stream);
+
+/* Its backward.  With g = weight * dy and xhat = h * rstd:
+ *   dx = rstd (g - xhat mean(g xhat)) + dh,   d_weight = sum over rows of dy xhat.
+ * dy bf16 [rows][H]; h as the forward stored it (or its x) in h_dtype; dh the
+ * gradient that reaches h from its other uses, in h's type, or NULL.  dx, in
+ * h's type, is the gradient of x and of the residual (it may be dh); dx_bf16
+ * (NULL, or with an fp32 h) gets it in bf16 as well.  d_weight fp32 [H],
+ * summed in a fixed order.  An MXFP8 output is differentiated as if it were
+ * not rounded. */
+size_t mok_rms_norm_bwd_workspace_bytes(int64_t rows, int H);
+mok_status_t mok_rms_norm_bwd(const uint16_t* dy, const void* h, int h_dtype, const void* weight, int weight_dtype,
+                              const float* rstd, const void* dh, int64_t rows, int H, void* dx, uint16_t* dx_bf16,
+                              float* d_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- AdamW over many tensors --------------------------------------------
+ * For every element, t = cfg->step (from 1), g' = *grad_scale * g:
+ *   m = b1 m + (1 - b1) g',   v = b2 v + (1 - b2) g'^2,
+ *   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps).
+ * Parameters bf16 or fp32; bf16 ones with an fp32 master copy each (all
+ * tensors of a call or none), which then holds the exact p and p its rounding.
+ * State kinds:
+ *   MOK_ADAMW_STATE_F32    m and v fp32 [n].
+ *   MOK_ADAMW_STATE_MXFP8  m holds E4M3 codes [n] of m, v those of sqrt(v),
+ *     m_scale and v_scale E8M0 scales [ceil(n/32)] (no alignment needed).
+ *     The update uses the new m and v unrounded; what is kept is rounded
+ *     stochastically: with s the block's scale exponent (mok_mxfp8_quantize's
+ *     rule), |value| 2^-s goes to the upper or lower neighbour on the E4M3
+ *     grid by 16 random bits, and a positive sqrt(v) never to zero.  The bits
+ *     are the high (m) and low (sqrt v) half of mix(i + key), i the element's
+ *     flat index, key = seed 0x9E3779B1 + step 0xB504F333 + index 0xBB67AE85
+ *     and mix(z): h = z 0x9E3779B1; h ^= h >> 15; h *= 0xB504F333;
+ *     h ^= h >> 16, all modulo 2^32.  The same call gives the same bits.
+ * `tensors` is a HOST array; all pointers in it are device pointers, 16-byte
+ * aligned but for the scales.  grad_scale: a device scalar (gradient clipping,
+ * loss scaling) or NULL for 1. */
+#define MOK_ADAMW_STATE_F32   0
+#define MOK_ADAMW_STATE_MXFP8 1
+typedef struct {
+  int param_dtype;   /* MOK_DTYPE_* */
+  int grad_dtype;    /* MOK_DTYPE_* */
+  int state;         /* MOK_ADAMW_STATE_* */
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  uint64_t seed;     /* of the MXFP8 states' rounding */
+} mok_adamw_config_t;
+typedef struct {
+  void* p;           /* [n] */
+  float* master;     /* [n] or NULL */
+  const void* g;     /* [n] */
+  void* m;           /* [n] fp32, or E4M3 codes */
+  void* v;           /* [n] fp32, or E4M3 codes of sqrt(v) */
+  uint8_t* m_scale;  /* [ceil(n/32)] or NULL */
+  uint8_t* v_scale;  /* [ceil(n/32)] or NULL */
+  int64_t n;         /* elements; 0: skipped */
+  int32_t index;     /* the tensor's place in the model, for its rounding bits */
+} mok_adamw_tensor_t;
+mok_status_t mok_adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
+                            const float* grad_scale, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

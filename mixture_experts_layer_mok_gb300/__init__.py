@@ -18,7 +18,8 @@ from . import _lib
 from ._lib import MokError  # noqa: F401
 
 __all__ = ["schedule", "schedule_noalloc", "mxfp8_quantize", "mxfp8_quantize_t", "mxfp8_quantize_dual", "forward",
-           "backward", "Schedule", "Weights", "Context", "MokError", "quantize_weights", "macrobatch_plan", "MODES"]
+           "backward", "Schedule", "Weights", "Context", "MokError", "quantize_weights", "macrobatch_plan", "MODES",
+           "mxfp8_dequantize", "rms_norm", "rms_norm_backward", "NormOutput", "AdamW"]
 
 # forward/backward precision: "bf16"; "mxfp8" (MXFP8 forward GEMMs, bf16
 # backward); "mxfp8_full" (MXFP8 forward and backward GEMMs)
@@ -379,3 +380,8 @@ def backward(dy, x, router_w, sched: Schedule, ctx: Context, weights: Weights, m
                                 C.byref(ctx.c), C.byref(wsd), _ptr(grads["dx"]), _ptr(grads["d_router_w"]),
                                 C.byref(g), _ptr(ws_buf), ws_buf.numel(), _stream(stream)), "mok_backward")
     return grads
+
+
+# the operators around the layer
+from .ops import NormOutput, mxfp8_dequantize, rms_norm, rms_norm_backward  # noqa: E402,F401
+from .optim import AdamW  # noqa: E402,F401

@@ -79,6 +79,24 @@ class MokWeightGrads(C.Structure):
                 ("d_ws_down", P)]
 
 
+MOK_DTYPE_BF16 = 0
+MOK_DTYPE_F32 = 1
+MOK_NORM_MAX_H = 32768
+MOK_ADAMW_STATE_F32 = 0
+MOK_ADAMW_STATE_MXFP8 = 1
+
+
+class MokAdamwConfig(C.Structure):
+    _fields_ = [("param_dtype", C.c_int), ("grad_dtype", C.c_int), ("state", C.c_int), ("lr", C.c_double),
+                ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double), ("weight_decay", C.c_double),
+                ("step", C.c_int64), ("seed", C.c_uint64)]
+
+
+class MokAdamwTensor(C.Structure):
+    _fields_ = [("p", P), ("master", P), ("g", P), ("m", P), ("v", P), ("m_scale", P), ("v_scale", P),
+                ("n", C.c_int64), ("index", C.c_int32)]
+
+
 # name -> (restype, argtypes); every symbol include/mok.h declares
 SIGNATURES = {
     "mok_version": (C.c_int, []),
@@ -102,6 +120,11 @@ SIGNATURES = {
     "mok_macrobatch_plan": (C.c_int, [I32P, C.c_int, C.c_int64, I32P, C.POINTER(C.c_int)]),
     "mok_backward": (C.c_int, [C.POINTER(MokConfig), P, P, P, C.POINTER(MokSchedule), C.POINTER(MokCtx),
                                C.POINTER(MokWeights), P, P, C.POINTER(MokWeightGrads), P, C.c_size_t, P]),
+    "mok_mxfp8_dequantize": (C.c_int, [P, P, C.c_int64, C.c_int64, P, P]),
+    "mok_rms_norm": (C.c_int, [P, C.c_int, P, C.c_int, P, C.c_int, C.c_int64, C.c_int, C.c_float, P, P, P, P, P, P]),
+    "mok_rms_norm_bwd_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int]),
+    "mok_rms_norm_bwd": (C.c_int, [P, P, C.c_int, P, C.c_int, P, P, C.c_int64, C.c_int, P, P, P, P, C.c_size_t, P]),
+    "mok_adamw_step": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int, P, P]),
 }
 
 _lib = None

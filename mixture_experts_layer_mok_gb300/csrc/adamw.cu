@@ -1,0 +1,265 @@
+// The AdamW step over many tensors in one launch, with 32-bit or MXFP8 states.
+//
+//   g' = grad_scale g
+//   m  = b1 m + (1 - b1) g',   v = b2 v + (1 - b2) g'^2
+//   p  = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// MXFP8 states keep m and r = sqrt(v) as E4M3 codes with one E8M0 scale per
+// 32 consecutive elements: 2 + 1/16 bytes per element instead of 8.  r rather
+// than v, because E4M3 spans 2^17.8 between its largest and smallest value,
+// which is 2^35.6 in v.  Both are rounded stochastically (up with probability
+// equal to the distance from the lower neighbour): b2 = 0.999 changes r by
+// 0.05% a step, far less than half of E4M3's 6 to 12% spacing, so rounding to
+// nearest would never move it.  A positive r is never rounded to zero: m's
+// step is bounded by about 3.2 r, so with the smallest code kept |m| / r stays
+// bounded whatever both were rounded to.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "gemm.cuh"
+#include "internal.h"
+#include "ops.h"
+
+namespace mok {
+namespace {
+
+template <int CAP>
+struct AdamwList {
+  AdamwTensor t[CAP];
+  int n;
+};
+
+__device__ __forceinline__ uint32_t mix_bits(uint32_t i, uint32_t key) {
+  uint32_t h = (i + key) * 0x9E3779B1u;   // multipliers from the fractions of phi and sqrt 2
+  h ^= h >> 15;
+  h *= 0xB504F333u;
+  return h ^ (h >> 16);
+}
+
+template <class T>
+__device__ __forceinline__ void load8(const T* p, bool whole, int left, float* f) {
+  if (whole) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 r = __ldcs(reinterpret_cast<const float4*>(p) + i);
+        f[4 * i] = r.x, f[4 * i + 1] = r.y, f[4 * i + 2] = r.z, f[4 * i + 3] = r.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[i] = 0.f;
+      if (i < left) {
+        if constexpr (sizeof(T) == 2)
+          f[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+        else
+          f[i] = p[i];
+      }
+    }
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T* p, bool whole, int left, const float* f) {
+  if (whole) {
+    if constexpr (sizeof(T) == 2) {
+      __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                     pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+    } else {
+      __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+      __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) {
+        if constexpr (sizeof(T) == 2)
+          p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+        else
+          p[i] = f[i];
+      }
+  }
+}
+
+__device__ __forceinline__ void load_codes8(const uint8_t* p, float scale, bool whole, int left, float* f) {
+  uint32_t w[2] = {0u, 0u};
+  if (whole) {
+    const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
+    w[0] = q.x, w[1] = q.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+  }
+  e4m3x4_values(w[0], f);
+  e4m3x4_values(w[1], f + 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] *= scale;
+}
+
+// |y| <= 448 onto the E4M3 grid, rounded up or down by 16 random bits: the
+// bits are added below the last kept place of the fp32 form and the rest is
+// cut off.  Below 2^-6 the grid is uniform (2^-9), as it is in [2^-6, 2^-5):
+// such a value is moved there and back.
+__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t rand16) {
+  const float a = fabsf(y);
+  const float off = a < 0.015625f ? 0.015625f : 0.f;
+  const float t = a + off;
+  const float q = __uint_as_float((__float_as_uint(t) + (rand16 << 4)) & 0xFFF00000u) - off;
+  return q;   // sign dropped
+}
+
+// Writes 8 values as codes with the scale of their block of 32 (four
+// neighbouring lanes); `v` are values before rounding, `rand` their bits
+// (m: the high half, r: the low one).
+template <bool R>
+__device__ __forceinline__ void store_codes8(uint8_t* codes, uint8_t* scales, long long block, bool whole, int left,
+                                             const float* v, const uint32_t* rand) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const int s = mx_scale_exponent(amax);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = v[i] * inv;
+    q[i] = e4m3_stochastic(y, R ? rand[i] & 0xFFFFu : rand[i] >> 16);
+    if (R) {
+      if (q[i] == 0.f && y > 0.f) q[i] = 0.001953125f;   // 2^-9, the smallest code
+    } else {
+      q[i] = copysignf(q[i], y);
+    }
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * k], q[4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * k + 2], q[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
+    w[k] = lo | (hi << 16);
+  }
+  if (whole) {
+    __stcs(reinterpret_cast<uint2*>(codes), make_uint2(w[0], w[1]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) codes[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+  }
+  if ((threadIdx.x & 3) == 0 && left > 0) scales[block] = static_cast<uint8_t>(s + 127);
+}
+
+// One block of 256 threads per kAdamwBlock elements of one tensor, 8 per
+// thread.
+template <class PT, class GT, bool MASTER, bool MX, int CAP>
+__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ AdamwList<CAP> list, const AdamwScalars s) {
+  griddep_wait();
+  griddep_launch_dependents();
+  // the tensor this block works on: the last one that begins at or before it
+  int lo = 0, hi = list.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (list.t[mid].first <= static_cast<int>(blockIdx.x))
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const AdamwTensor& t = list.t[lo];
+  const long long i0 = static_cast<long long>(blockIdx.x - t.first) * kAdamwBlock + threadIdx.x * 8;
+  const long long rest = t.n - i0;
+  const int left = rest >= 8 ? 8 : rest > 0 ? static_cast<int>(rest) : 0;
+  const bool whole = left == 8;
+  if (!MX && left == 0) return;
+  float g[8], p[8], m[8], v[8];
+  load8(static_cast<const GT*>(t.g) + i0, whole, left, g);
+  if (MASTER)
+    load8(t.master + i0, whole, left, p);
+  else
+    load8(static_cast<const PT*>(t.p) + i0, whole, left, p);
+  const long long block = i0 >> 5;
+  if (MX) {
+    float ms = 0.f, rs = 0.f;
+    if (left > 0) {
+      ms = e8m0_value(t.m_scale[block]);
+      rs = e8m0_value(t.r_scale[block]);
+    }
+    load_codes8(static_cast<const uint8_t*>(t.m) + i0, ms, whole, left, m);
+    load_codes8(static_cast<const uint8_t*>(t.v) + i0, rs, whole, left, v);
+  } else {
+    load8(static_cast<const float*>(t.m) + i0, whole, left, m);
+    load8(static_cast<const float*>(t.v) + i0, whole, left, v);
+  }
+  const float gs = s.grad_scale ? __ldg(s.grad_scale) : 1.f;
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float gi = g[i] * gs;
+    m[i] = fmaf(s.beta1, m[i], s.one_minus_beta1 * gi);
+    const float v0 = MX ? v[i] * v[i] : v[i];
+    v[i] = fmaf(s.beta2, v0, s.one_minus_beta2 * gi * gi);
+    r[i] = sqrtf(v[i]);
+    p[i] = fmaf(-s.step_size, __fdividef(m[i], fmaf(r[i], s.inv_sqrt_bc2, s.eps)), p[i] * s.decay);
+  }
+  if (MASTER) store8(t.master + i0, whole, left, p);
+  store8(static_cast<PT*>(t.p) + i0, whole, left, p);
+  if (MX) {
+    uint32_t rand[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rand[i] = mix_bits(static_cast<uint32_t>(i0) + i, t.key);
+    store_codes8<false>(static_cast<uint8_t*>(t.m) + i0, t.m_scale, block, whole, left, m, rand);
+    store_codes8<true>(static_cast<uint8_t*>(t.v) + i0, t.r_scale, block, whole, left, r, rand);
+  } else {
+    store8(static_cast<float*>(t.m) + i0, whole, left, m);
+    store8(static_cast<float*>(t.v) + i0, whole, left, v);
+  }
+}
+
+template <class PT, class GT, bool MASTER, bool MX, int CAP>
+cudaError_t launch_cap(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, cudaStream_t st) {
+  AdamwList<CAP> list;
+  memcpy(list.t, t, sizeof(AdamwTensor) * n);
+  list.n = n;
+  return launch_dependent(adamw_kernel<PT, GT, MASTER, MX, CAP>, dim3(blocks), dim3(256), 0, st, list, s);
+}
+
+template <class PT, class GT, bool MASTER, bool MX>
+cudaError_t launch_typed(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, cudaStream_t st) {
+  return n <= 16 ? launch_cap<PT, GT, MASTER, MX, 16>(t, n, blocks, s, st)
+                 : launch_cap<PT, GT, MASTER, MX, kAdamwMaxTensors>(t, n, blocks, s, st);
+}
+
+template <class PT, class GT, bool MASTER>
+cudaError_t launch_state(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, int mx, cudaStream_t st) {
+  return mx ? launch_typed<PT, GT, MASTER, true>(t, n, blocks, s, st)
+            : launch_typed<PT, GT, MASTER, false>(t, n, blocks, s, st);
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, int p_f32, int g_f32,
+                         int master, int mx, cudaStream_t st) {
+  if (p_f32)
+    return g_f32 ? launch_state<float, float, false>(t, n, blocks, s, mx, st)
+                 : launch_state<float, uint16_t, false>(t, n, blocks, s, mx, st);
+  if (master)
+    return g_f32 ? launch_state<uint16_t, float, true>(t, n, blocks, s, mx, st)
+                 : launch_state<uint16_t, uint16_t, true>(t, n, blocks, s, mx, st);
+  return g_f32 ? launch_state<uint16_t, float, false>(t, n, blocks, s, mx, st)
+               : launch_state<uint16_t, uint16_t, false>(t, n, blocks, s, mx, st);
+}
+
+}  // namespace mok

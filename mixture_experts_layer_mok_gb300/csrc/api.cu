@@ -16,13 +16,16 @@
 #include "../../include/mok.h"
 #include "gemm.cuh"
 #include "gemm_mx.cuh"
+#include "api_util.h"
 #include "internal.h"
 
 using namespace mok;
 
 namespace {
-
 thread_local char g_err[512] = "";
+}  // namespace
+
+namespace mok {
 
 mok_status_t fail(mok_status_t code, const char* fmt, ...) {
   va_list ap;
@@ -32,13 +35,9 @@ mok_status_t fail(mok_status_t code, const char* fmt, ...) {
   return code;
 }
 
-#define MOK_CUDA(call)                                                                     \
-  do {                                                                                     \
-    cudaError_t e_ = (call);                                                               \
-    if (e_ != cudaSuccess)                                                                 \
-      return fail(MOK_ERR_CUDA, "%s failed: %s (%s:%d)", #call, cudaGetErrorString(e_),    \
-                  __FILE__, __LINE__);                                                     \
-  } while (0)
+}  // namespace mok
+
+namespace {
 
 // ---------------------------------------------------------------- device info
 struct DevInfo {
@@ -48,6 +47,10 @@ struct DevInfo {
 };
 DevInfo g_dev[64];
 std::mutex g_dev_mu;
+
+}  // namespace
+
+namespace mok {
 
 mok_status_t device_info(int* num_sms) {
   int dev = 0;
@@ -69,11 +72,14 @@ mok_status_t device_info(int* num_sms) {
   return MOK_OK;
 }
 
+}  // namespace mok
+
+namespace {
+
 // ---------------------------------------------------------------- TMA descriptors
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
+
+namespace mok {
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
@@ -88,6 +94,10 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
+
+}  // namespace mok
+
+namespace {
 
 // 2-D bf16 tensor [outer][inner] with a box of box_outer rows x bk elements
 // (bk = the kernel's K-block: 64 -> 128-byte swizzle, 32 -> 64-byte swizzle);
@@ -220,8 +230,6 @@ struct Carver {
     return p;
   }
 };
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 long long max_tiles_of(int T, int k, int E) {
   return (static_cast<long long>(T) * k + static_cast<long long>(kTileRows - 1) * E) / kTileRows;

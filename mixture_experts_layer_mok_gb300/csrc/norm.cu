@@ -1,0 +1,451 @@
+// Root-mean-square norm with the residual's addition, an output in bf16 and /
+// or MXFP8, and its backward; and the reader of MXFP8 tensors.
+//
+// Forward, per row:  h = x + residual,  r = (mean(h^2) + eps)^-1/2,
+//                    y_j = w_j h_j r.
+// Backward, with g_j = w_j dy_j and xhat_j = h_j r:
+//                    dx_j = r (g_j - xhat_j mean(g xhat)) + dh_j,
+//                    dw_j = sum over rows of dy_j xhat_j.
+// Both are bound by memory: a row is read once and stays in registers between
+// the sum over it and the values that need the sum.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gemm.cuh"
+#include "internal.h"
+#include "ops.h"
+
+namespace mok {
+namespace {
+
+struct NoType {};
+
+// V consecutive values (8, or 1 where a row's length is not a multiple of 8)
+// as they lie in memory.
+template <class T, int V>
+struct Raw {
+  T v[V];
+};
+template <>
+struct Raw<uint16_t, 8> {
+  uint4 v;
+};
+template <>
+struct Raw<float, 8> {
+  float4 v[2];
+};
+template <int V>
+struct Raw<NoType, V> {};
+
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
+  Raw<T, V> r;
+  if constexpr (V == 8 && sizeof(T) == 2) {
+    r.v = __ldcs(reinterpret_cast<const uint4*>(p));
+  } else if constexpr (V == 8) {
+    r.v[0] = __ldcs(reinterpret_cast<const float4*>(p));
+    r.v[1] = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = p[i];
+  }
+  return r;
+}
+
+__device__ __forceinline__ void unpack(const Raw<uint16_t, 8>& r, float* f) {
+  const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const Raw<float, 8>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[4 * i] = r.v[i].x;
+    f[4 * i + 1] = r.v[i].y;
+    f[4 * i + 2] = r.v[i].z;
+    f[4 * i + 3] = r.v[i].w;
+  }
+}
+__device__ __forceinline__ void unpack(const Raw<uint16_t, 1>& r, float* f) {
+  f[0] = __uint_as_float(static_cast<uint32_t>(r.v[0]) << 16);
+}
+__device__ __forceinline__ void unpack(const Raw<float, 1>& r, float* f) { f[0] = r.v[0]; }
+
+template <int V>
+__device__ __forceinline__ void store_vals(uint16_t* p, const float* f) {
+  if constexpr (V == 8) {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                                                   pack_bf16(f[6], f[7])));
+  } else {
+    p[0] = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_vals(float* p, const float* f) {
+  if constexpr (V == 8) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+  } else {
+    p[0] = f[0];
+  }
+}
+
+// V weights at element j (bf16 or fp32), through the read-only cache: every
+// row reads the same ones.
+template <int V>
+__device__ __forceinline__ void load_weight(const void* w, bool f32, int j, float* f) {
+  if (f32) {
+    const float* p = static_cast<const float*>(w) + j;
+    if constexpr (V == 8) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+      f[0] = __ldg(p);
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(w) + j;
+    if constexpr (V == 8) {
+      Raw<uint16_t, 8> r;
+      r.v = __ldg(reinterpret_cast<const uint4*>(p));
+      unpack(r, f);
+    } else {
+      f[0] = __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// Sum over the threads of a row: the warp, or the block (`red`: one slot per
+// warp; the caller alternates two of them, so that one barrier per row is
+// enough).  Fixed order.
+template <bool WARP_ROW>
+__device__ __forceinline__ float row_sum(float s, float* red) {
+  s = warp_sum(s);
+  if constexpr (!WARP_ROW) {
+    const int nw = (blockDim.x + 31) >> 5;
+    if (nw > 1) {
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+      __syncthreads();
+      s = 0.f;
+      for (int i = 0; i < nw; ++i) s += red[i];
+    }
+  }
+  return s;
+}
+
+constexpr int kWarpRows = 4;   // rows of a block in the one-warp-per-row kernels
+
+// XT: x's type; RT: the residual's (NoType: none).  V values per load, ITEMS
+// loads per thread; WARP_ROW: one warp per row, else one block.
+template <class XT, class RT, int V, int ITEMS, bool WARP_ROW, int MAXT>
+__global__ void __launch_bounds__(MAXT) rms_norm_kernel(const NormArgs a) {
+  constexpr bool kRes = !std::is_same_v<RT, NoType>;
+  __shared__ float red[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int T = WARP_ROW ? 32 : blockDim.x;
+  const int tid = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
+  const long long row = WARP_ROW ? static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP_ROW && row >= a.rows) return;   // whole warps; no block barrier in this form
+  const int nv = a.H / V;
+  const long long base = row * a.H;
+  Raw<XT, V> rx[ITEMS];
+  Raw<RT, V> rr[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = tid + i * T;
+    if (c < nv) {
+      rx[i] = load_raw<XT, V>(static_cast<const XT*>(a.x) + base + c * V);
+      if constexpr (kRes) rr[i] = load_raw<RT, V>(static_cast<const RT*>(a.residual) + base + c * V);
+    }
+  }
+  float v[ITEMS][V];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = tid + i * T;
+    if (c < nv) {
+      unpack(rx[i], v[i]);
+      if constexpr (kRes) {
+        float r[V];
+        unpack(rr[i], r);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] += r[j];
+        store_vals<V>(static_cast<RT*>(a.h) + base + c * V, v[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[i][j] = 0.f;
+    }
+  }
+  ss = row_sum<WARP_ROW>(ss, red);
+  const float rstd = rsqrtf(ss / static_cast<float>(a.H) + a.eps);
+  if (tid == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = tid + i * T;
+    if (c < nv) {
+      float w[V];
+      load_weight<V>(a.weight, a.weight_f32, c * V, w);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[i][j] *= rstd * w[j];
+      if (a.y) store_vals<V>(a.y + base + c * V, v[i]);
+    }
+    if constexpr (V == 8) {
+      if (a.codes) {
+        // four neighbouring lanes hold a block of 32 (H is a multiple of 32,
+        // so the four are all inside the row or all outside); lanes outside
+        // hold zeros and only take part in the shuffles
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int s = mx_scale_exponent(amax);
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+        uint32_t q[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[i][4 * k] * inv, v[i][4 * k + 1] * inv),
+                                                       __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[i][4 * k + 2] * inv, v[i][4 * k + 3] * inv),
+                                                       __NV_SATFINITE, __NV_E4M3);
+          q[k] = lo | (hi << 16);
+        }
+        if (c < nv) {
+          __stcs(reinterpret_cast<uint2*>(a.codes + base + c * 8), make_uint2(q[0], q[1]));
+          if ((c & 3) == 0) a.scales[row * (a.H / 32) + (c >> 2)] = static_cast<uint8_t>(s + 127);
+        }
+      }
+    }
+  }
+}
+
+// The backward: a grid of fixed size, each block (or warp) walking rows and
+// keeping its columns' share of dw in registers; `part` gets one row of sums
+// per walker, which norm_dw_kernel adds in order.
+template <class HT, int V, int ITEMS, bool WARP_ROW, int MAXT>
+__global__ void __launch_bounds__(MAXT) rms_norm_bwd_kernel(const NormBwdArgs a) {
+  __shared__ float red[2][32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int T = WARP_ROW ? 32 : blockDim.x;
+  const int tid = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
+  const long long walkers = WARP_ROW ? static_cast<long long>(gridDim.x) * kWarpRows : gridDim.x;
+  const long long walker = WARP_ROW ? static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  const int nv = a.H / V;
+  float acc[ITEMS][V], w[ITEMS][V];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = tid + i * T;
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[i][j] = w[i][j] = 0.f;
+    if (c < nv) load_weight<V>(a.weight, a.weight_f32, c * V, w[i]);
+  }
+  const float inv_h = 1.f / static_cast<float>(a.H);
+  int odd = 0;
+  for (long long row = walker; row < a.rows; row += walkers, odd ^= 1) {
+    const long long base = row * a.H;
+    const float rstd = __ldg(a.rstd + row);
+    Raw<uint16_t, V> rdy[ITEMS];
+    Raw<HT, V> rh[ITEMS], rdh[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = tid + i * T;
+      if (c < nv) {
+        rdy[i] = load_raw<uint16_t, V>(a.dy + base + c * V);
+        rh[i] = load_raw<HT, V>(static_cast<const HT*>(a.h) + base + c * V);
+        if (a.dh) rdh[i] = load_raw<HT, V>(static_cast<const HT*>(a.dh) + base + c * V);
+      }
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (tid + i * T < nv) {
+        float dy[V], h[V];
+        unpack(rdy[i], dy);
+        unpack(rh[i], h);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float t = dy[j] * (h[j] * rstd);
+          acc[i][j] += t;
+          dot = fmaf(t, w[i][j], dot);
+        }
+      }
+    }
+    dot = row_sum<WARP_ROW>(dot, red[odd]) * inv_h;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = tid + i * T;
+      if (c < nv) {
+        float dy[V], h[V], d[V];
+        unpack(rdy[i], dy);
+        unpack(rh[i], h);
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[j] = rstd * fmaf(-h[j] * rstd, dot, dy[j] * w[i][j]);
+        if (a.dh) {
+          float r[V];
+          unpack(rdh[i], r);
+#pragma unroll
+          for (int j = 0; j < V; ++j) d[j] += r[j];
+        }
+        store_vals<V>(static_cast<HT*>(a.dx) + base + c * V, d);
+        if (sizeof(HT) == 4 && a.dx16) store_vals<V>(a.dx16 + base + c * V, d);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = tid + i * T;
+    if (c < nv) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) a.part[walker * a.H + c * V + j] = acc[i][j];
+    }
+  }
+}
+
+// Column sums of [n][H] fp32 partial rows, in a fixed order: 32 columns per
+// block, 32 rows in step, then the 32 running sums.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part, int n, int H,
+                                                          float* __restrict__ out) {
+  __shared__ float s[32][33];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int col = blockIdx.x * 32 + threadIdx.x;
+  float v = 0.f;
+  if (col < H)
+    for (int r = threadIdx.y; r < n; r += 32) v += part[static_cast<long long>(r) * H + col];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0 && col < H) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += s[i][threadIdx.x];
+    out[col] = v;
+  }
+}
+
+// E4M3 codes and E8M0 scales -> bf16: 8 codes per thread.
+__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales, long long n,
+                                                            uint16_t* __restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long c = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; c * 8 < n; c += step) {
+    const float s = e8m0_value(scales[c >> 2]);
+    if (c * 8 + 8 <= n) {
+      const uint2 q = __ldcs(reinterpret_cast<const uint2*>(codes) + c);
+      float f[8];
+      e4m3x4_values(q.x, f);
+      e4m3x4_values(q.y, f + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= s;
+      store_vals<8>(out + c * 8, f);
+    } else {
+      for (long long i = c * 8; i < n; ++i) {
+        float f[4];
+        e4m3x4_values(codes[i], f);
+        f[0] *= s;
+        store_vals<1>(out + i, f);
+      }
+    }
+  }
+}
+
+int ceil32(int n) { return (n + 31) / 32 * 32; }
+
+template <class XT, class RT>
+cudaError_t norm_launch(const NormArgs& a, cudaStream_t st) {
+  const unsigned rows = static_cast<unsigned>(a.rows);
+  const unsigned wgrid = static_cast<unsigned>((a.rows + kWarpRows - 1) / kWarpRows);
+  if (a.H % 8) {
+    if (a.H <= 4096)
+      return launch_dependent(rms_norm_kernel<XT, RT, 1, 4, false, 1024>, dim3(rows), dim3(ceil32((a.H + 3) / 4)), 0, st, a);
+    return launch_dependent(rms_norm_kernel<XT, RT, 1, 32, false, 1024>, dim3(rows), dim3(ceil32((a.H + 31) / 32)), 0, st, a);
+  }
+  const int nv = a.H / 8;
+  if (nv <= 32) return launch_dependent(rms_norm_kernel<XT, RT, 8, 1, true, 128>, dim3(wgrid), dim3(128), 0, st, a);
+  if (nv <= 64) return launch_dependent(rms_norm_kernel<XT, RT, 8, 2, true, 128>, dim3(wgrid), dim3(128), 0, st, a);
+  if (nv <= 128) return launch_dependent(rms_norm_kernel<XT, RT, 8, 4, true, 128>, dim3(wgrid), dim3(128), 0, st, a);
+  if (nv <= 256)
+    return launch_dependent(rms_norm_kernel<XT, RT, 8, 1, false, 256>, dim3(rows), dim3(ceil32(nv)), 0, st, a);
+  if (nv <= 512)
+    return launch_dependent(rms_norm_kernel<XT, RT, 8, 2, false, 256>, dim3(rows), dim3(ceil32((nv + 1) / 2)), 0, st, a);
+  if (nv <= 1024)
+    return launch_dependent(rms_norm_kernel<XT, RT, 8, 4, false, 256>, dim3(rows), dim3(ceil32((nv + 3) / 4)), 0, st, a);
+  return launch_dependent(rms_norm_kernel<XT, RT, 8, 4, false, 1024>, dim3(rows), dim3(ceil32((nv + 3) / 4)), 0, st, a);
+}
+
+template <class HT>
+cudaError_t norm_bwd_launch(const NormBwdArgs& a, int walkers, cudaStream_t st) {
+  const unsigned blocks = static_cast<unsigned>(walkers), wblocks = blocks / kWarpRows;
+  if (a.H % 8) {
+    if (a.H <= 4096)
+      return launch_dependent(rms_norm_bwd_kernel<HT, 1, 4, false, 1024>, dim3(blocks), dim3(ceil32((a.H + 3) / 4)), 0, st, a);
+    return launch_dependent(rms_norm_bwd_kernel<HT, 1, 32, false, 1024>, dim3(blocks), dim3(ceil32((a.H + 31) / 32)), 0, st, a);
+  }
+  const int nv = a.H / 8;
+  if (nv <= 32) return launch_dependent(rms_norm_bwd_kernel<HT, 8, 1, true, 128>, dim3(wblocks), dim3(128), 0, st, a);
+  if (nv <= 64) return launch_dependent(rms_norm_bwd_kernel<HT, 8, 2, true, 128>, dim3(wblocks), dim3(128), 0, st, a);
+  if (nv <= 512)
+    return launch_dependent(rms_norm_bwd_kernel<HT, 8, 1, false, 512>, dim3(blocks), dim3(ceil32(nv)), 0, st, a);
+  if (nv <= 1024)
+    return launch_dependent(rms_norm_bwd_kernel<HT, 8, 2, false, 512>, dim3(blocks), dim3(ceil32((nv + 1) / 2)), 0, st, a);
+  return launch_dependent(rms_norm_bwd_kernel<HT, 8, 4, false, 1024>, dim3(blocks), dim3(ceil32((nv + 3) / 4)), 0, st, a);
+}
+
+}  // namespace
+
+int norm_bwd_walkers(long long rows, int H) {
+  const bool warp_row = H % 8 == 0 && H <= 512;
+  const long long most = warp_row ? 608 * kWarpRows : 608;   // 4 blocks on each of 152 SMs
+  long long n = rows < most ? rows : most;
+  if (warp_row) n = (n + kWarpRows - 1) / kWarpRows * kWarpRows;
+  return static_cast<int>(n);
+}
+
+cudaError_t launch_rms_norm(const NormArgs& a, int x_f32, int residual, cudaStream_t st) {
+  if (a.rows == 0) return cudaSuccess;
+  if (x_f32) {
+    if (residual == 0) return norm_launch<float, NoType>(a, st);
+    return residual == 1 ? norm_launch<float, uint16_t>(a, st) : norm_launch<float, float>(a, st);
+  }
+  if (residual == 0) return norm_launch<uint16_t, NoType>(a, st);
+  return residual == 1 ? norm_launch<uint16_t, uint16_t>(a, st) : norm_launch<uint16_t, float>(a, st);
+}
+
+cudaError_t launch_column_sum(const float* part, int n, int H, float* out, cudaStream_t st) {
+  return launch_dependent(column_sum_kernel, dim3((H + 31) / 32), dim3(32, 32), 0, st, part, n, H, out);
+}
+
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight, cudaStream_t st) {
+  const int walkers = norm_bwd_walkers(a.rows, a.H);
+  if (walkers > 0) {
+    const cudaError_t err = h_f32 ? norm_bwd_launch<float>(a, walkers, st) : norm_bwd_launch<uint16_t>(a, walkers, st);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_column_sum(a.part, walkers, a.H, d_weight, st);
+}
+
+cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out, int num_sms,
+                                 cudaStream_t st) {
+  long long grid = (n / 8 + 256) / 256;
+  if (grid > 16ll * num_sms) grid = 16ll * num_sms;
+  return launch_dependent(mx_dequantize_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, codes, scales, n, out);
+}
+
+}  // namespace mok

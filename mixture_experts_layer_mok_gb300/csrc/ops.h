@@ -1,0 +1,94 @@
+// Internal launch interface of the operators around the layer: the norm, the
+// dense projection and the optimiser step.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mok {
+
+// The value 2^(s - 127) of an E8M0 scale (255: NaN).
+__device__ __forceinline__ float e8m0_value(uint32_t s) {
+  return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
+}
+
+// The values of the four E4M3 codes in a word, lowest byte first.
+__device__ __forceinline__ void e4m3x4_values(uint32_t w, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3);
+    const float2 v = __half22float2(__half2(h));
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
+// ---------------------------------------------------------------- norm
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* h;          // x + residual in the residual's type (with a residual)
+  uint16_t* y;      // bf16 output or NULL
+  uint8_t* codes;   // MXFP8 output or NULL
+  uint8_t* scales;
+  float* rstd;
+  long long rows;
+  int H;
+  int weight_f32;
+  float eps;
+};
+struct NormBwdArgs {
+  const uint16_t* dy;
+  const void* h;
+  const void* weight;
+  const float* rstd;
+  const void* dh;     // gradient of h from its other uses, or NULL
+  void* dx;           // in h's type
+  uint16_t* dx16;     // fp32 h: also in bf16, or NULL
+  float* part;        // [norm_bwd_walkers][H]
+  long long rows;
+  int H;
+  int weight_f32;
+};
+// Partial rows of the weight gradient (part of the workspace's size).
+int norm_bwd_walkers(long long rows, int H);
+// residual: 0 none, 1 bf16, 2 fp32.
+cudaError_t launch_rms_norm(const NormArgs& a, int x_f32, int residual, cudaStream_t st);
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight, cudaStream_t st);
+// out[j] = sum over n rows of part[.][j], in a fixed order (n = 0: zeros).
+cudaError_t launch_column_sum(const float* part, int n, int H, float* out, cudaStream_t st);
+cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out, int num_sms,
+                                 cudaStream_t st);
+
+// ---------------------------------------------------------------- AdamW
+struct AdamwTensor {
+  void* p;
+  float* master;
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* r_scale;
+  long long n;
+  uint32_t key;     // seeds the tensor's rounding bits
+  int first;        // its first block of the launch
+};
+struct AdamwScalars {
+  float beta1, one_minus_beta1, beta2, one_minus_beta2;
+  float decay;         // 1 - lr weight_decay
+  float step_size;     // lr / (1 - beta1^t)
+  float inv_sqrt_bc2;  // (1 - beta2^t)^-1/2
+  float eps;
+  const float* grad_scale;  // device scalar or NULL
+};
+constexpr int kAdamwBlock = 2048;   // elements per thread block
+// Tensors one launch takes at most, and the launch itself; t[i].first is set.
+constexpr int kAdamwMaxTensors = 400;
+cudaError_t launch_adamw(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, int p_f32, int g_f32,
+                         int master, int mx, cudaStream_t st);
+
+}  // namespace mok

@@ -1,0 +1,155 @@
+"""AdamW over a model's tensors, with 32-bit or MXFP8 states (argument
+marshalling only: the step is libmok's ``mok_adamw_step``)."""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from .ops import _DTYPE, _check, _handle, _on
+
+_STATE = {"fp32": _lib.MOK_ADAMW_STATE_F32, "mxfp8": _lib.MOK_ADAMW_STATE_MXFP8}
+_KEPT = {"fp32": ("m", "v"), "mxfp8": ("m", "m_scale", "r", "r_scale")}
+_FIELD = {"masters": "master", "m": "m", "v": "v", "r": "v", "m_scale": "m_scale", "r_scale": "v_scale"}
+
+
+class AdamW:
+    """Decoupled-weight-decay Adam over ``params`` (contiguous CUDA tensors,
+    bf16 or fp32, updated in place), all of them in one launch per kind.
+
+    ``state``: "fp32" keeps m and v in 32 bits; "mxfp8" keeps m and
+    r = sqrt(v) as E4M3 codes with one E8M0 scale per 32 elements, rounded
+    stochastically with bits that ``seed``, the step, the tensor's place in
+    ``params`` and the element's index determine.  ``master``: bf16 parameters
+    also get an fp32 copy that takes the update; the parameter is its rounding.
+
+    ``buffers`` hands in state tensors instead of fresh zeros: a dict of lists
+    (one entry per parameter, None for a master of an fp32 parameter) with the
+    keys of ``state_dict()["buffers"]``; ``step`` is the count they stand at."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 state: str = "fp32", master: bool = False, seed: int = 0, step: int = 0, buffers: dict | None = None):
+        self.params = list(params)
+        if state not in _STATE:
+            raise ValueError(f"state must be one of {sorted(_STATE)}")
+        for i, p in enumerate(self.params):
+            _check(p, f"params[{i}]", None, (torch.bfloat16, torch.float32))
+        self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
+        self.state, self.seed, self.step_count = state, int(seed), int(step)
+        if buffers is None:
+            buffers = self._fresh(master)
+        self._take(buffers)
+
+    def _fresh(self, master):
+        def zeros(p, n, dtype):
+            return torch.zeros(n, dtype=dtype, device=p.device)
+
+        out = {}
+        for name in _KEPT[self.state]:
+            if name.endswith("_scale"):   # the scale of a block of zeros is 2^0
+                out[name] = [torch.full(((p.numel() + 31) // 32,), 127, dtype=torch.uint8, device=p.device)
+                             for p in self.params]
+            else:
+                dtype = torch.float32 if self.state == "fp32" else torch.uint8
+                out[name] = [zeros(p, p.numel(), dtype) for p in self.params]
+        if master:
+            out["masters"] = [p.detach().reshape(-1).float() if p.dtype == torch.bfloat16 else None
+                              for p in self.params]
+        return out
+
+    def _take(self, buffers):
+        want = set(_KEPT[self.state])
+        if not want <= set(buffers) or set(buffers) - want - {"masters"}:
+            raise ValueError(f"buffers: expected {sorted(want)} and optionally masters, got {sorted(buffers)}")
+        for name, ts in buffers.items():
+            if len(ts) != len(self.params):
+                raise ValueError(f"buffers[{name!r}]: expected {len(self.params)} tensors, got {len(ts)}")
+            for i, (p, t) in enumerate(zip(self.params, ts)):
+                if name == "masters" and p.dtype == torch.float32 and t is None:
+                    continue
+                n = (p.numel() + 31) // 32 if name.endswith("_scale") else p.numel()
+                dtype = torch.float32 if name == "masters" or self.state == "fp32" else torch.uint8
+                _check(t, f"buffers[{name!r}][{i}]", None, (dtype,))
+                if t.numel() != n or (name == "masters" and p.dtype == torch.float32):
+                    raise ValueError(f"buffers[{name!r}][{i}]: expected {n} elements for a "
+                                     f"{p.dtype} parameter of {p.numel()}, got {t.numel()}")
+        self.buffers = {k: list(v) for k, v in buffers.items()}
+        # one launch list per parameter type (master copies belong to the bf16 ones)
+        self._groups = []
+        for dtype in (torch.bfloat16, torch.float32):
+            idx = [i for i, p in enumerate(self.params) if p.dtype == dtype]
+            if not idx:
+                continue
+            arr = (_lib.MokAdamwTensor * len(idx))()
+            for a, i in zip(arr, idx):
+                a.p, a.n, a.index = self.params[i].data_ptr(), self.params[i].numel(), i
+                for name, ts in self.buffers.items():
+                    if ts[i] is not None:
+                        setattr(a, _FIELD[name], ts[i].data_ptr())
+            self._groups.append((dtype, idx, arr))
+
+    def state_dict(self) -> dict:
+        """The step count, the state kind and the state tensors themselves."""
+        return {"step": self.step_count, "state": self.state, "seed": self.seed, "buffers": self.buffers}
+
+    def load_state_dict(self, sd: dict) -> None:
+        """Copies another optimiser's state (of the same kind and shapes) into this one's."""
+        if sd["state"] != self.state or set(sd["buffers"]) != set(self.buffers):
+            raise ValueError("the state is of another kind")
+        pairs = []
+        for name, ts in self.buffers.items():
+            if len(sd["buffers"][name]) != len(ts):
+                raise ValueError(f"{name}: another number of tensors")
+            for i, (mine, other) in enumerate(zip(ts, sd["buffers"][name])):
+                if (mine is None) != (other is None) or (mine is not None and
+                                                         (mine.dtype != other.dtype or mine.numel() != other.numel())):
+                    raise ValueError(f"{name}[{i}]: another type or length")
+                if mine is not None:
+                    pairs.append((mine, other))
+        for mine, other in pairs:
+            mine.copy_(other.reshape(mine.shape))
+        self.step_count, self.seed = int(sd["step"]), int(sd["seed"])
+
+    def step(self, grads=None, grad_scale=None, lr: float | None = None, stream=None) -> None:
+        """One step.  ``grads``: one gradient per parameter, of its shape, bf16
+        or fp32 (default: each ``param.grad``); None entries are skipped.
+        ``grad_scale``: a one-element fp32 CUDA tensor that multiplies every
+        gradient (clipping, loss scaling).  ``lr`` replaces the learning rate
+        for this step."""
+        if grads is None:
+            grads = [p.grad for p in self.params]
+        if len(grads) != len(self.params):
+            raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
+        if grad_scale is not None:
+            _check(grad_scale, "grad_scale", None, (torch.float32,))
+            if grad_scale.numel() != 1:
+                raise ValueError("grad_scale: expected one element")
+        runs = []
+        for dtype, idx, arr in self._groups:
+            kinds = set()
+            for a, i in zip(arr, idx):
+                g, p = grads[i], self.params[i]
+                if g is None:
+                    a.n = 0
+                    continue
+                if g.shape != p.shape or g.dtype not in _DTYPE or not g.is_cuda or not g.is_contiguous():
+                    _check(g, f"grads[{i}]", p.shape, tuple(_DTYPE))
+                if (a.p or 0) != p.data_ptr():
+                    raise ValueError(f"params[{i}] moved to other memory: build the optimiser again")
+                a.n, a.g = g.numel(), g.data_ptr()
+                kinds.add(g.dtype)
+            for kind in kinds:
+                part = arr
+                if len(kinds) > 1:   # gradients of two types: a list for each
+                    sub = [a for a, i in zip(arr, idx) if grads[i] is not None and grads[i].dtype == kind]
+                    part = (_lib.MokAdamwTensor * len(sub))(*sub)
+                runs.append((dtype, kind, part))
+        lib = _lib.load()
+        cfg = _lib.MokAdamwConfig(state=_STATE[self.state], lr=self.lr if lr is None else lr, beta1=self.betas[0],
+                                  beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
+                                  step=self.step_count + 1, seed=self.seed & (2 ** 64 - 1))
+        scale = None if grad_scale is None else grad_scale.data_ptr()
+        with _on(stream):
+            for dtype, kind, part in runs:
+                cfg.param_dtype, cfg.grad_dtype = _DTYPE[dtype], _DTYPE[kind]
+                _lib.check(lib.mok_adamw_step(cfg, part, len(part), scale, _handle()), "mok_adamw_step")
+        self.step_count += 1
