@@ -506,6 +506,39 @@ mok_status_t mok_rms_norm_bwd(const uint16_t* dy, const void* h, int h_dtype, co
                               const float* rstd, const void* dh, int64_t rows, int H, void* dx, uint16_t* dx_bf16,
                               float* d_weight, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- dense projection with bias, activation and residual ----------------
+ *   z = x W^T + bias,   y = act(z) + residual.
+ * x bf16 [M][K], w bf16 [N][K]; bias [N] or NULL, residual [M][N] or NULL, each
+ * bf16 or fp32; y [M][N] bf16 or fp32 (it may be the residual, where the types
+ * agree); z, when not NULL, receives the pre-activations in bf16 for the
+ * backward.  The sum, the activation and the additions are fp32, y is rounded
+ * once.  GELU is 0.5 z (1 + erf(z / sqrt 2)); GELU_TANH the form with
+ * tanh(sqrt(2/pi) (z + 0.044715 z^3)).  N and K are multiples of 8; any M,
+ * none included (one token: the same call). */
+#define MOK_ACT_NONE      0
+#define MOK_ACT_RELU      1
+#define MOK_ACT_SILU      2
+#define MOK_ACT_GELU      3
+#define MOK_ACT_GELU_TANH 4
+mok_status_t mok_linear(const uint16_t* x, const uint16_t* w, const void* bias, int bias_dtype, const void* residual,
+                        int residual_dtype, int activation, int64_t M, int N, int K, void* y, int y_dtype, uint16_t* z,
+                        void* stream);
+
+/* Its backward, from dy [M][N] (bf16 or fp32) and the saved z (bf16; needed
+ * with an activation):  dz = dy act'(z),  dx = dz W,  d_weight = dz^T x,
+ * d_bias = sum over rows of dz.  dx bf16 [M][K], d_weight bf16 [N][K], d_bias
+ * fp32 [N]; a NULL one is not computed (then x or w may be NULL too).  The
+ * products take dz rounded to bf16, the tensor core's operand type; d_bias
+ * sums the unrounded values in a fixed order.  The residual's gradient is dy. */
+size_t mok_linear_bwd_workspace_bytes(int64_t M, int N, int activation, int dy_dtype, int with_bias);
+mok_status_t mok_linear_bwd(const void* dy, int dy_dtype, const uint16_t* x, const uint16_t* w, const uint16_t* z,
+                            int activation, int64_t M, int N, int K, uint16_t* dx, uint16_t* d_weight, float* d_bias,
+                            void* ws, size_t ws_bytes, void* stream);
+/* Synchronises the current device and reads (and clears) the status word of
+ * its projections: MOK_OK, or MOK_ERR_TIMEOUT once a bounded device-side wait
+ * gave up since the last read (that call's outputs are then undefined). */
+mok_status_t mok_linear_status(int* status);
+
 /* ---- AdamW over many tensors --------------------------------------------
  * For every element, t = cfg->step (from 1), g' = *grad_scale * g:
  *   m = b1 m + (1 - b1) g',   v = b2 v + (1 - b2) g'^2,

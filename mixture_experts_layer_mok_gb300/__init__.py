@@ -19,7 +19,8 @@ from ._lib import MokError  # noqa: F401
 
 __all__ = ["schedule", "schedule_noalloc", "mxfp8_quantize", "mxfp8_quantize_t", "mxfp8_quantize_dual", "forward",
            "backward", "Schedule", "Weights", "Context", "MokError", "quantize_weights", "macrobatch_plan", "MODES",
-           "mxfp8_dequantize", "rms_norm", "rms_norm_backward", "NormOutput", "AdamW"]
+           "mxfp8_dequantize", "rms_norm", "rms_norm_backward", "NormOutput", "linear", "linear_backward",
+           "linear_status", "AdamW"]
 
 # forward/backward precision: "bf16"; "mxfp8" (MXFP8 forward GEMMs, bf16
 # backward); "mxfp8_full" (MXFP8 forward and backward GEMMs)
@@ -383,5 +384,6 @@ def backward(dy, x, router_w, sched: Schedule, ctx: Context, weights: Weights, m
 
 
 # the operators around the layer
-from .ops import NormOutput, mxfp8_dequantize, rms_norm, rms_norm_backward  # noqa: E402,F401
+from .ops import (NormOutput, linear, linear_backward, linear_status, mxfp8_dequantize, rms_norm,  # noqa: E402,F401
+                  rms_norm_backward)
 from .optim import AdamW  # noqa: E402,F401

@@ -82,6 +82,7 @@ class MokWeightGrads(C.Structure):
 MOK_DTYPE_BF16 = 0
 MOK_DTYPE_F32 = 1
 MOK_NORM_MAX_H = 32768
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 MOK_ADAMW_STATE_F32 = 0
 MOK_ADAMW_STATE_MXFP8 = 1
 
@@ -124,6 +125,11 @@ SIGNATURES = {
     "mok_rms_norm": (C.c_int, [P, C.c_int, P, C.c_int, P, C.c_int, C.c_int64, C.c_int, C.c_float, P, P, P, P, P, P]),
     "mok_rms_norm_bwd_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int]),
     "mok_rms_norm_bwd": (C.c_int, [P, P, C.c_int, P, C.c_int, P, P, C.c_int64, C.c_int, P, P, P, P, C.c_size_t, P]),
+    "mok_linear": (C.c_int, [P, P, P, C.c_int, P, C.c_int, C.c_int, C.c_int64, C.c_int, C.c_int, P, C.c_int, P, P]),
+    "mok_linear_bwd_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int]),
+    "mok_linear_bwd": (C.c_int, [P, C.c_int, P, P, P, C.c_int, C.c_int64, C.c_int, C.c_int, P, P, P, P, C.c_size_t,
+                                 P]),
+    "mok_linear_status": (C.c_int, [I32P]),
     "mok_adamw_step": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int, P, P]),
 }
 

@@ -23,6 +23,21 @@ struct NvtxRange {
 bool is_dtype(int d) { return d == MOK_DTYPE_BF16 || d == MOK_DTYPE_F32; }
 
 
+// Tile coordinates are 32-bit; a tile may begin up to 256 rows past the end.
+constexpr int64_t kMaxM = 0x7fffffffll - 512;
+
+mok_status_t check_linear(int64_t M, int N, int K, int activation) {
+  if (M < 0 || M > kMaxM || N < 8 || K < 8 || N % 8 || K % 8 || N > 0x7fffffff - 512 || K > 0x7fffffff - 512)
+    return fail(MOK_ERR_INVALID_ARG, "need 0 <= M < 2^31 - 512 and N, K positive multiples of 8");
+  if (activation < MOK_ACT_NONE || activation > MOK_ACT_GELU_TANH) return fail(MOK_ERR_INVALID_ARG, "unknown activation");
+  return MOK_OK;
+}
+
+// The workspace's dz part, padded so that what follows is aligned.
+size_t dz_bytes(bool dz, int64_t M, int N) {
+  return dz ? (static_cast<size_t>(M) * N * sizeof(uint16_t) + 255) / 256 * 256 : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -119,6 +134,103 @@ mok_status_t mok_rms_norm_bwd(const uint16_t* dy, const void* h, int h_dtype, co
   a.H = H;
   a.weight_f32 = weight_dtype == MOK_DTYPE_F32;
   MOK_CUDA(launch_rms_norm_bwd(a, h_dtype == MOK_DTYPE_F32, d_weight, static_cast<cudaStream_t>(stream)));
+  return MOK_OK;
+}
+
+// ---------------------------------------------------------------- dense projection
+mok_status_t mok_linear(const uint16_t* x, const uint16_t* w, const void* bias, int bias_dtype, const void* residual,
+                        int residual_dtype, int activation, int64_t M, int N, int K, void* y, int y_dtype, uint16_t* z,
+                        void* stream) {
+  NvtxRange nvtx("mok_linear");
+  mok_status_t st = check_linear(M, N, K, activation);
+  if (st) return st;
+  if (!is_dtype(y_dtype) || (bias && !is_dtype(bias_dtype)) || (residual && !is_dtype(residual_dtype)))
+    return fail(MOK_ERR_INVALID_ARG, "unknown dtype");
+  if (M == 0) return MOK_OK;
+  if (!x || !w || !y) return fail(MOK_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(y) || !aligned16(z))
+    return fail(MOK_ERR_INVALID_ARG, "misaligned pointer");
+  int sms = 0;
+  st = device_info(&sms);
+  if (st) return st;
+  LinearParams p = {};
+  MOK_CUDA(linear_status_word(&p.status));
+  p.L = N;
+  p.C = static_cast<int>(M);
+  p.act = activation;
+  p.out = y;
+  p.out_f32 = y_dtype == MOK_DTYPE_F32;
+  p.bias = bias;
+  p.bias_f32 = bias_dtype == MOK_DTYPE_F32;
+  p.residual = residual;
+  p.residual_f32 = residual_dtype == MOK_DTYPE_F32;
+  p.z = z;
+  return run_linear(LIN_FWD, {w, x, K}, p, sms, static_cast<cudaStream_t>(stream));
+}
+
+size_t mok_linear_bwd_workspace_bytes(int64_t M, int N, int activation, int dy_dtype, int with_bias) {
+  if (M < 0 || M > kMaxM || N < 8 || N % 8 || activation < 0 || activation > MOK_ACT_GELU_TANH || !is_dtype(dy_dtype))
+    return 0;
+  const bool dz = activation != MOK_ACT_NONE || dy_dtype == MOK_DTYPE_F32;
+  return dz_bytes(dz, M, N) + (with_bias ? static_cast<size_t>(dz_partials(M, N)) * N * sizeof(float) : 0) + 256;
+}
+
+mok_status_t mok_linear_bwd(const void* dy, int dy_dtype, const uint16_t* x, const uint16_t* w, const uint16_t* z,
+                            int activation, int64_t M, int N, int K, uint16_t* dx, uint16_t* d_weight, float* d_bias,
+                            void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("mok_linear_bwd");
+  mok_status_t st = check_linear(M, N, K, activation);
+  if (st) return st;
+  if (!is_dtype(dy_dtype)) return fail(MOK_ERR_INVALID_ARG, "unknown dtype");
+  const bool act = activation != MOK_ACT_NONE, make_dz = act || dy_dtype == MOK_DTYPE_F32;
+  if (M > 0 && (!dy || (act && !z) || (d_weight && !x) || (dx && !w))) return fail(MOK_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(w) || !aligned16(z) || !aligned16(dx) || !aligned16(d_weight) ||
+      !aligned16(d_bias) || !aligned16(ws))
+    return fail(MOK_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t need = mok_linear_bwd_workspace_bytes(M, N, activation, dy_dtype, d_bias != nullptr);
+  if (!ws || ws_bytes < need) return fail(MOK_ERR_INVALID_ARG, "workspace too small: %zu < %zu", ws ? ws_bytes : 0, need);
+  int sms = 0;
+  st = device_info(&sms);
+  if (st) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {   // sums over no rows
+    if (d_weight) MOK_CUDA(cudaMemsetAsync(d_weight, 0, static_cast<size_t>(N) * K * sizeof(uint16_t), s));
+    if (d_bias) MOK_CUDA(cudaMemsetAsync(d_bias, 0, static_cast<size_t>(N) * sizeof(float), s));
+    return MOK_OK;
+  }
+  uint16_t* dz = make_dz ? static_cast<uint16_t*>(ws) : nullptr;
+  float* part = d_bias ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dz_bytes(make_dz, M, N)) : nullptr;
+  if (dz || part)
+    MOK_CUDA(launch_linear_dz(dy, dy_dtype == MOK_DTYPE_F32, z, activation, M, N, dz, part, s));
+  if (d_bias) MOK_CUDA(launch_column_sum(part, dz_partials(M, N), N, d_bias, s));
+  const uint16_t* g = make_dz ? dz : static_cast<const uint16_t*>(dy);
+  LinearParams p = {};
+  MOK_CUDA(linear_status_word(&p.status));
+  p.L = K;
+  if (d_weight) {
+    p.C = N;
+    p.out = d_weight;
+    st = run_linear(LIN_DW, {x, g, M}, p, sms, s);
+    if (st) return st;
+  }
+  if (dx) {
+    p.C = static_cast<int>(M);
+    p.out = dx;
+    st = run_linear(LIN_DX, {w, g, N}, p, sms, s);
+  }
+  return st;
+}
+
+mok_status_t mok_linear_status(int* status) {
+  if (!status) return fail(MOK_ERR_INVALID_ARG, "NULL argument");
+  int sms = 0;
+  mok_status_t st = device_info(&sms);
+  if (st) return st;
+  int* word = nullptr;
+  MOK_CUDA(linear_status_word(&word));
+  MOK_CUDA(cudaDeviceSynchronize());
+  MOK_CUDA(cudaMemcpy(status, word, sizeof(int), cudaMemcpyDeviceToHost));
+  if (*status) MOK_CUDA(cudaMemset(word, 0, sizeof(int)));
   return MOK_OK;
 }
 

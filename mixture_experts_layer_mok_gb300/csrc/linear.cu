@@ -1,0 +1,228 @@
+// Launches of the dense products (linear.cuh): operand maps, the choice of
+// kernel and tile, and the elementwise pass of the backward.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "api_util.h"
+#include "internal.h"
+#include "linear.cuh"
+
+namespace mok {
+namespace {
+
+// bf16 [outer][inner] with a box of box_outer rows x 64 elements, 128-byte
+// swizzle; zeros outside.
+mok_status_t operand_map(CUtensorMap* m, const void* base, long long inner, long long outer, int box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(MOK_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(MOK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for [%lld x %lld]", static_cast<int>(r), outer, inner);
+  return MOK_OK;
+}
+
+template <bool AMN, bool BMN, int BN, bool FWD>
+cudaError_t launch_split(const LinearMaps& maps, const LinearParams& p, cudaStream_t st) {
+  using C = SplitCfg<AMN, BMN, BN>;
+  auto kern = linear_split_kernel<AMN, BMN, BN, FWD>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.L + 127) / 128 * p.split), static_cast<unsigned>((p.C + BN - 1) / BN));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+__device__ int g_linear_status;   // first error since the last read
+
+// CTA pairs of the kernel that are resident at once, looked up once per device.
+template <bool AMN, bool BMN, bool FWD>
+cudaError_t launch_pair(const LinearMaps& maps, const LinearParams& p, int num_sms, cudaStream_t st) {
+  using C = PairCfg<AMN, BMN>;
+  auto kern = linear_pair_kernel<AMN, BMN, FWD>;
+  static int resident[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;   // the occupancy query takes the cluster shape only
+  if (resident[dev] == 0) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (err != cudaSuccess) return err;
+    cfg.gridDim = dim3(2 * (num_sms / 2));
+    int n = 0;
+    err = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (err != cudaSuccess) return err;
+    if (n <= 0) return cudaErrorInvalidConfiguration;
+    resident[dev] = n;
+  }
+  const int items = p.l_tiles * p.c_tiles, pairs = items < resident[dev] ? items : resident[dev];
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+template <bool AMN, bool BMN, bool FWD>
+mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sms, cudaStream_t st) {
+  LinearParams p = q;
+  p.nk = static_cast<int>((o.K + kLinBK - 1) / kLinBK);
+  LinearMaps maps;
+  const long long lt = (p.L + 255) / 256, ct = (static_cast<long long>(p.C) + 255) / 256;
+  const bool pair = lt * ct >= num_sms / 2;
+  int bn = 128;
+  if (!pair) {
+    if (!BMN && p.C <= 16) bn = 16;
+    else if (!BMN && p.C <= 32) bn = 32;
+    else if (p.C <= 64) bn = 64;
+  }
+  mok_status_t s = AMN ? operand_map(&maps.a, o.a, p.L, o.K, 64) : operand_map(&maps.a, o.a, o.K, p.L, 128);
+  if (s) return s;
+  s = BMN ? operand_map(&maps.b, o.b, p.C, o.K, 64) : operand_map(&maps.b, o.b, o.K, p.C, pair ? 128 : bn);
+  if (s) return s;
+  if (pair) {
+    if (lt * ct > 0x7fffffffll) return fail(MOK_ERR_INVALID_ARG, "product too large");
+    p.l_tiles = static_cast<int>(lt);
+    p.c_tiles = static_cast<int>(ct);
+    p.group = 8;
+    MOK_CUDA((launch_pair<AMN, BMN, FWD>(maps, p, num_sms, st)));
+    return MOK_OK;
+  }
+  const long long tiles = (p.L + 127) / 128 * ((p.C + bn - 1) / bn);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * num_sms && p.nk / (split * 2) >= 4) split *= 2;
+  p.split = split;
+  cudaError_t err = cudaSuccess;
+  if (bn == 128) {
+    err = launch_split<AMN, BMN, 128, FWD>(maps, p, st);
+  } else if (bn == 64) {
+    err = launch_split<AMN, BMN, 64, FWD>(maps, p, st);
+  } else if constexpr (!BMN) {
+    err = bn == 32 ? launch_split<AMN, BMN, 32, FWD>(maps, p, st) : launch_split<AMN, BMN, 16, FWD>(maps, p, st);
+  }
+  MOK_CUDA(err);
+  return MOK_OK;
+}
+
+// ---------------------------------------------------------------- dz
+constexpr int kDzRows = 8;   // rows in step in a block; 32 threads x 8 columns wide
+
+template <class DY, int ACT>
+__global__ void __launch_bounds__(256) linear_dz_kernel(const DY* __restrict__ dy, const uint16_t* __restrict__ z,
+                                                        long long M, int N, uint16_t* __restrict__ dz,
+                                                        float* __restrict__ part) {
+  __shared__ float s[kDzRows][32][9];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int col = (blockIdx.x * 32 + threadIdx.x) * 8;
+  float sum[8] = {};
+  if (col < N) {
+    for (long long r = static_cast<long long>(blockIdx.y) * kDzRows + threadIdx.y; r < M;
+         r += static_cast<long long>(gridDim.y) * kDzRows) {
+      const long long at = r * N + col;
+      float d[8];
+      if constexpr (sizeof(DY) == 4) {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(dy + at));
+        const float4 b = __ldcs(reinterpret_cast<const float4*>(dy + at) + 1);
+        d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+      } else {
+        const uint4 a = __ldcs(reinterpret_cast<const uint4*>(dy + at));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = bf16_at(&a, i);
+      }
+      if constexpr (ACT != LIN_NONE) {
+        const uint4 a = __ldcs(reinterpret_cast<const uint4*>(z + at));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] *= act_slope<ACT>(bf16_at(&a, i));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += d[i];
+      if (dz)   // read again at once by the products: kept in L2
+        *reinterpret_cast<uint4*>(dz + at) =
+            make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[threadIdx.y][threadIdx.x][i] = sum[i];
+  __syncthreads();
+  const int t = threadIdx.y * 32 + threadIdx.x, c = t >> 3, i = t & 7;   // one column per thread
+  float v = 0.f;
+#pragma unroll
+  for (int r = 0; r < kDzRows; ++r) v += s[r][c][i];
+  const int out = (blockIdx.x * 32 + c) * 8 + i;
+  if (out < N) part[static_cast<long long>(blockIdx.y) * N + out] = v;
+}
+
+template <class DY>
+cudaError_t launch_dz(const DY* dy, const uint16_t* z, int act, long long M, int N, uint16_t* dz, float* part, cudaStream_t st) {
+  const dim3 grid((N + 255) / 256, dz_partials(M, N)), block(32, kDzRows);
+  switch (act) {
+    case LIN_RELU: return launch_dependent(linear_dz_kernel<DY, LIN_RELU>, grid, block, 0, st, dy, z, M, N, dz, part);
+    case LIN_SILU: return launch_dependent(linear_dz_kernel<DY, LIN_SILU>, grid, block, 0, st, dy, z, M, N, dz, part);
+    case LIN_GELU: return launch_dependent(linear_dz_kernel<DY, LIN_GELU>, grid, block, 0, st, dy, z, M, N, dz, part);
+    case LIN_GELU_TANH:
+      return launch_dependent(linear_dz_kernel<DY, LIN_GELU_TANH>, grid, block, 0, st, dy, z, M, N, dz, part);
+    default: return launch_dependent(linear_dz_kernel<DY, LIN_NONE>, grid, block, 0, st, dy, z, M, N, dz, part);
+  }
+}
+
+}  // namespace
+
+cudaError_t linear_status_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_linear_status);
+}
+
+mok_status_t run_linear(LinKind kind, const LinearOperands& o, const LinearParams& p, int num_sms, cudaStream_t st) {
+  switch (kind) {
+    case LIN_FWD: return run_kind<false, false, true>(o, p, num_sms, st);
+    case LIN_DX: return run_kind<true, false, false>(o, p, num_sms, st);
+    default: return run_kind<true, true, false>(o, p, num_sms, st);
+  }
+}
+
+int dz_partials(long long M, int N) {
+  // about 8 blocks for each of 152 SMs, a block no shorter than 4 steps
+  const long long want = (1216 + (N + 255) / 256 - 1) / ((N + 255) / 256);
+  const long long most = (M + 4 * kDzRows - 1) / (4 * kDzRows);
+  const long long n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+
+cudaError_t launch_linear_dz(const void* dy, int dy_f32, const uint16_t* z, int act, long long M, int N, uint16_t* dz,
+                             float* part, cudaStream_t st) {
+  if (M == 0) return cudaSuccess;
+  return dy_f32 ? launch_dz(static_cast<const float*>(dy), z, act, M, N, dz, part, st)
+                : launch_dz(static_cast<const uint16_t*>(dy), z, act, M, N, dz, part, st);
+}
+
+}  // namespace mok

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/mok.h"
+
 namespace mok {
 
 // The value 2^(s - 127) of an E8M0 scale (255: NaN).
@@ -63,6 +65,45 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight
 cudaError_t launch_column_sum(const float* part, int n, int H, float* out, cudaStream_t st);
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out, int num_sms,
                                  cudaStream_t st);
+
+// ---------------------------------------------------------------- dense projection
+enum LinAct : int { LIN_NONE = 0, LIN_RELU = 1, LIN_SILU = 2, LIN_GELU = 3, LIN_GELU_TANH = 4 };
+
+struct LinearParams {
+  long long L;      // the output's contiguous length
+  int C;            // the output's rows
+  int nk;           // K-blocks of 64
+  int split;        // split kernel: CTAs of a cluster along K
+  int l_tiles;      // pair kernel: 256-wide tiles, and the order's group
+  int c_tiles;
+  int group;
+  int act;          // forward epilogue
+  int out_f32;
+  int bias_f32;
+  int residual_f32;
+  const void* bias;      // [L] or NULL
+  const void* residual;  // [C][L] or NULL
+  void* out;             // [C][L]
+  uint16_t* z;           // [C][L] bf16 pre-activations, or NULL
+  int* status;           // device word: MOK_ERR_TIMEOUT once a bounded wait gave up
+};
+// One of the products described in linear.cuh.  a: [L][K], or [K][L] with
+// a_mn; b: [C][K], or [K][C] with b_mn; bf16, contiguous.
+struct LinearOperands {
+  const uint16_t* a;
+  const uint16_t* b;
+  long long K;
+};
+// The device word that a bounded wait which gave up sets (current device).
+cudaError_t linear_status_word(int** word);
+enum LinKind : int { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2 };
+mok_status_t run_linear(LinKind kind, const LinearOperands& o, const LinearParams& p, int num_sms, cudaStream_t st);
+
+// dz = dy act'(z) in bf16 (dz may be NULL) and the partial column sums of its
+// fp32 values ([dz_partials][N], part may be NULL).
+int dz_partials(long long M, int N);
+cudaError_t launch_linear_dz(const void* dy, int dy_f32, const uint16_t* z, int act, long long M, int N, uint16_t* dz,
+                             float* part, cudaStream_t st);
 
 // ---------------------------------------------------------------- AdamW
 struct AdamwTensor {

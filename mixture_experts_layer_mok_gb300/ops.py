@@ -1,5 +1,6 @@
 """The operators around the layer: the norm with the residual's addition and
-an MXFP8 output, the MXFP8 reader, and their gradients (argument marshalling
+an MXFP8 output, the MXFP8 reader, the dense projection with its epilogue, and
+their gradients (argument marshalling
 only; the arithmetic is in libmok's kernels, ``include/mok.h``).
 
 Every call takes ``stream``: the work, and the memory of what the call
@@ -137,3 +138,90 @@ def rms_norm_backward(dy, h, weight, rstd, d_h=None, bf16_dx: bool = False, stre
                                         out["dx"].data_ptr(), _opt(out.get("dx_bf16")), out["d_weight"].data_ptr(),
                                         ws.data_ptr(), ws.numel(), _handle()), "mok_rms_norm_bwd")
     return out
+
+
+def _activation(name):
+    if name not in _lib.ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_lib.ACTIVATIONS)}")
+    return _lib.ACTIVATIONS[name]
+
+
+def _linear_dims(x, weight):
+    _check(weight, "weight")
+    if weight.dim() != 2 or weight.shape[0] % 8 or weight.shape[1] % 8 or 0 in weight.shape:
+        raise ValueError(f"weight: expected [N, K] with N and K positive multiples of 8, got {tuple(weight.shape)}")
+    _check(x, "x")
+    if x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"x: expected a last axis of {weight.shape[1]}, got {tuple(x.shape)}")
+    N, K = weight.shape
+    return x.numel() // K, N, K
+
+
+def linear(x, weight, bias=None, activation: str = "none", residual=None, out_dtype=torch.bfloat16,
+           save_z: bool = False, stream=None):
+    """y = act(x weight^T + bias) + residual; returns (y, z).  x bf16 [..., K],
+    weight bf16 [N, K] (N and K multiples of 8); bias [N] and residual
+    [..., N], bf16 or fp32; ``activation`` "none", "relu", "silu", "gelu" (by
+    erf) or "gelu_tanh".  y has ``out_dtype`` (bf16 or fp32), rounded once from
+    fp32.  ``save_z`` keeps the pre-activations in bf16 for ``linear_backward``
+    (else z is None)."""
+    M, N, K = _linear_dims(x, weight)
+    act = _activation(activation)
+    if out_dtype not in _DTYPE:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    shape = x.shape[:-1] + (N,)
+    if bias is not None:
+        _check(bias, "bias", (N,), _BF16_F32)
+    if residual is not None:
+        _check(residual, "residual", shape, _BF16_F32)
+    lib = _lib.load()
+    with _on(stream):
+        y = torch.empty(shape, dtype=out_dtype, device=x.device)
+        z = torch.empty(shape, dtype=torch.bfloat16, device=x.device) if save_z else None
+        _lib.check(lib.mok_linear(x.data_ptr(), weight.data_ptr(), _opt(bias),
+                                  0 if bias is None else _DTYPE[bias.dtype], _opt(residual),
+                                  0 if residual is None else _DTYPE[residual.dtype], act, M, N, K, y.data_ptr(),
+                                  _DTYPE[out_dtype], _opt(z), _handle()), "mok_linear")
+    return y, z
+
+
+def linear_backward(dy, x, weight, z=None, activation: str = "none", bias: bool = False,
+                    need=("dx", "d_weight"), stream=None) -> dict:
+    """Gradients of ``linear``: dy bf16 or fp32 [..., N], z from its
+    ``save_z`` (with an activation).  Returns those of dx bf16 [..., K] and
+    d_weight bf16 [N, K] that ``need`` names, and with ``bias`` d_bias fp32
+    [N].  The residual's gradient is dy itself."""
+    M, N, K = _linear_dims(x, weight)
+    act = _activation(activation)
+    shape = x.shape[:-1] + (N,)
+    _check(dy, "dy", shape, _BF16_F32)
+    if act:
+        _check(z, "z", shape)
+    if not set(need) <= {"dx", "d_weight"}:
+        raise ValueError("need names dx and d_weight")
+    lib = _lib.load()
+    nbytes = lib.mok_linear_bwd_workspace_bytes(M, N, act, _DTYPE[dy.dtype], int(bias))
+    if nbytes == 0:
+        raise ValueError("shape outside the kernels' contract")
+    with _on(stream):
+        out = {}
+        if "dx" in need:
+            out["dx"] = torch.empty_like(x)
+        if "d_weight" in need:
+            out["d_weight"] = torch.empty_like(weight)
+        if bias:
+            out["d_bias"] = torch.empty(N, dtype=torch.float32, device=x.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        _lib.check(lib.mok_linear_bwd(dy.data_ptr(), _DTYPE[dy.dtype], x.data_ptr(), weight.data_ptr(),
+                                      _opt(z) if act else None, act, M, N, K, _opt(out.get("dx")),
+                                      _opt(out.get("d_weight")), _opt(out.get("d_bias")), ws.data_ptr(), ws.numel(),
+                                      _handle()), "mok_linear_bwd")
+    return out
+
+
+def linear_status() -> int:
+    """Synchronises and returns the projections' device status since the last
+    call: 0, or MOK_ERR_TIMEOUT when a bounded wait gave up."""
+    st = C.c_int32()
+    _lib.check(_lib.load().mok_linear_status(C.byref(st)), "mok_linear_status")
+    return st.value

@@ -171,7 +171,7 @@ def test_missing_gradients_empty_tensors_and_two_gradient_types():
     opt.step(gs)
     assert bool((ps[2] < 1).all())
     for p, g in zip(ps, gs):
-        p.grad = g
+        p.grad = g.to(p.dtype)
     opt.step()
     assert opt.step_count == 3
 
