@@ -11,28 +11,48 @@
 namespace mok {
 namespace {
 
-// bf16 [outer][inner] with a box of box_outer rows x 64 elements, 128-byte
-// swizzle; zeros outside.
-mok_status_t operand_map(CUtensorMap* m, const void* base, long long inner, long long outer, int box_outer) {
+// [outer][inner] of bf16 or fp32 with a box of box_outer rows x box_inner
+// elements, whose bytes (64 or 128) are the swizzle; zeros outside.
+mok_status_t make_box(CUtensorMap* m, const void* base, int f32, long long inner, long long outer, int box_inner, int box_outer) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(MOK_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const int size = f32 ? 4 : 2;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_outer)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * size};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box_inner * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(MOK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for [%lld x %lld]", static_cast<int>(r), outer, inner);
   return MOK_OK;
+}
+
+mok_status_t operand_map(CUtensorMap* m, const void* base, long long inner, long long outer, int box_outer) {
+  return make_box(m, base, 0, inner, outer, 64, box_outer);
+}
+
+// Lets `kern` take `bytes` of shared memory, once per device.
+template <class K>
+cudaError_t allow_smem(K kern, int bytes, bool* done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) done[dev] = true;
+  return err;
 }
 
 template <bool AMN, bool BMN, int BN, bool FWD>
 cudaError_t launch_split(const LinearMaps& maps, const LinearParams& p, cudaStream_t st) {
   using C = SplitCfg<AMN, BMN, BN>;
   auto kern = linear_split_kernel<AMN, BMN, BN, FWD>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static bool allowed[64] = {};
+  const cudaError_t err = allow_smem(kern, C::kSmemBytes, allowed);
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -53,12 +73,11 @@ cudaError_t launch_split(const LinearMaps& maps, const LinearParams& p, cudaStre
 
 __device__ int g_linear_status;   // first error since the last read
 
-// CTA pairs of the kernel that are resident at once, looked up once per device.
 template <bool AMN, bool BMN, bool FWD>
 cudaError_t launch_pair(const LinearMaps& maps, const LinearParams& p, int num_sms, cudaStream_t st) {
   using C = PairCfg<AMN, BMN>;
   auto kern = linear_pair_kernel<AMN, BMN, FWD>;
-  static int resident[64] = {};
+  static int resident[64] = {};   // CTA pairs that are resident at once, looked up once per device
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -114,6 +133,9 @@ mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sm
     p.l_tiles = static_cast<int>(lt);
     p.c_tiles = static_cast<int>(ct);
     p.group = 8;
+    s = make_box(&maps.out, p.out, p.out_f32, p.L, p.C, 32, 32);
+    if (!s && p.z) s = make_box(&maps.z, p.z, 0, p.L, p.C, 32, 32);
+    if (s) return s;
     MOK_CUDA((launch_pair<AMN, BMN, FWD>(maps, p, num_sms, st)));
     return MOK_OK;
   }
@@ -199,7 +221,19 @@ cudaError_t launch_dz(const DY* dy, const uint16_t* z, int act, long long M, int
 }  // namespace
 
 cudaError_t linear_status_word(int** word) {
-  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_linear_status);
+  static int* at[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!at[dev]) {
+    void* a = nullptr;
+    err = cudaGetSymbolAddress(&a, g_linear_status);
+    if (err != cudaSuccess) return err;
+    at[dev] = static_cast<int*>(a);
+  }
+  *word = at[dev];
+  return cudaSuccess;
 }
 
 mok_status_t run_linear(LinKind kind, const LinearOperands& o, const LinearParams& p, int num_sms, cudaStream_t st) {

@@ -2,25 +2,24 @@
 // mok_linear and mok_linear_bwd.
 //
 // All three products are written as D[c][l] = sum_k A[l][k] B[c][k], with l
-// the contiguous index of the row-major output.  l runs over the tensor
-// core's M (128 TMEM lanes per CTA) and c over its N, so that a warp of the
-// epilogue holds 32 neighbouring elements of an output row: its loads of the
-// residual and its stores are whole 64- or 128-byte segments straight from
-// registers, the bias is one value per lane, and a handful of tokens costs an
-// N of 16 rather than a padded M of 128.
+// the contiguous index of the row-major output:
 //   forward  l = n, c = m, k = k:  A = W [N][K],            B = x [M][K]
 //   dx       l = k, c = m, k = n:  A = W^T (W is [k][l]),   B = dz [M][N]
 //   dW       l = k, c = n, k = m:  A = x^T (x is [k][l]),   B = dz^T (dz is [k][c])
 // An operand that is stored [k][l] is read in place as an MN-major operand.
 // Sums are fp32 in TMEM; every edge (l, c and k) is cut by the tensor maps,
-// whose loads read zeros outside.
+// whose loads read zeros outside and whose stores write nothing there.
 //
-// Two kernels.  linear_pair_kernel: persistent CTA pairs (M = 256 over two
-// SMs, 256 columns, two accumulator buffers), for products with enough
-// 256 x 256 tiles to fill the GPU.  linear_split_kernel: one 128 x BN tile per
-// CTA, K split over a cluster of up to 8 CTAs that add their parts through
-// distributed shared memory in rank order, for everything smaller, where
-// the bytes of A have to come in through as many SMs as there are.
+// Two kernels.
+//   linear_pair_kernel: persistent CTA pairs (M = 256 rows c over two SMs, 256
+//   columns l, two accumulator buffers), for products with enough 256 x 256
+//   tiles to fill the GPU.  Each thread of the epilogue holds 32 neighbouring
+//   elements of an output row, which leave through TMA stores.
+//   linear_split_kernel: one 128 x BN tile per CTA, K split over a cluster of
+//   up to 8 CTAs that add their parts through distributed shared memory in
+//   rank order, for everything smaller, where the bytes of A have to come in
+//   through as many SMs as there are.  Here l runs over the tensor core's M,
+//   so that a handful of tokens costs an N of 16 rather than a padded M.
 #pragma once
 
 #include <cuda.h>
@@ -36,6 +35,8 @@ namespace mok {
 struct LinearMaps {
   CUtensorMap a;
   CUtensorMap b;
+  CUtensorMap out;   // pair kernel: 32 x 32 boxes of the output and of z
+  CUtensorMap z;
 };
 
 constexpr int kLinBK = 64;                 // K-block of a stage: one 128-byte swizzled row
@@ -43,11 +44,31 @@ constexpr int kLinChunk = 64 * 128;        // an MN-major 64 x 64 block
 constexpr int kLinABytes = 128 * kLinBK * 2;
 
 // ---------------------------------------------------------------- epilogue
+// Phi(z), the normal distribution function, and exp(-z^2/2): with t = 1 / (1 +
+// p |z| / sqrt 2), 1 - Phi(|z|) = 1/2 poly(t) exp(-z^2/2) (Abramowitz and
+// Stegun, 7.1.26; error in Phi below 7.5e-8).  Two special-function and about
+// ten other instructions, without a branch, where erff takes both of its
+// branches in nearly every warp.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  e = __expf(-0.5f * z * z);
+  float q = fmaf(t, 1.061405429f, -1.453152027f);
+  q = fmaf(t, q, 1.421413741f);
+  q = fmaf(t, q, -0.284496736f);
+  q = fmaf(t, q, 0.254829592f);
+  q *= 0.5f * t * e;
+  return z < 0.f ? q : 1.f - q;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == LIN_RELU) return z < 0.f ? 0.f : z;   // keeps a NaN
   if constexpr (ACT == LIN_SILU) return z * __fdividef(1.f, 1.f + __expf(-z));
-  if constexpr (ACT == LIN_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if constexpr (ACT == LIN_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   if constexpr (ACT == LIN_GELU_TANH)   // 0.5 z (1 + tanh u) = z / (1 + exp(-2u))
     return z * __fdividef(1.f, 1.f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
   return z;
@@ -61,8 +82,11 @@ __device__ __forceinline__ float act_slope(float z) {
     const float s = __fdividef(1.f, 1.f + __expf(-z));
     return s * (1.f + z * (1.f - s));
   }
-  if constexpr (ACT == LIN_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+  if constexpr (ACT == LIN_GELU) {
+    float e;
+    const float phi = normal_cdf(z, e);
+    return fmaf(z * 0.3989422804014327f, e, phi);
+  }
   if constexpr (ACT == LIN_GELU_TANH) {   // with s = 1 / (1 + exp(-2u)): s + 2 z s (1 - s) du/dz
     const float z2 = z * z;
     const float s = __fdividef(1.f, 1.f + __expf(-1.5957691216057308f * z * (1.f + 0.044715f * z2)));
@@ -71,60 +95,60 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.f;
 }
 
-__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
-
-// The output elements (row c + i, column l) for i < NC from the sums acc:
-// z = acc + bias, y = act(z) + residual.  Rows past p.C are left alone.
-template <int ACT, int NC>
-__device__ __forceinline__ void linear_store_act(const LinearParams& p, long long l, int c, float bias, const float* acc) {
-  const int n = min(NC, p.C - c);
-  const long long at = static_cast<long long>(c) * p.L + l;
-  float res[NC];
+// NV (4 or 8) consecutive values of a bf16 or fp32 array.
+template <int NV>
+__device__ __forceinline__ void load_vals(const void* base, int f32, long long at, float* f) {
+  if (f32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    res[i] = 0.f;
-    if (p.residual && i < n)
-      res[i] = p.residual_f32 ? __ldg(static_cast<const float*>(p.residual) + at + static_cast<long long>(i) * p.L)
-                              : bf16_value(__ldg(static_cast<const uint16_t*>(p.residual) + at + static_cast<long long>(i) * p.L));
-  }
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    if (i < n) {
-      const long long o = at + static_cast<long long>(i) * p.L;
-      const float z = acc[i] + bias;
-      if (p.z) p.z[o] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
-      const float y = act_value<ACT>(z) + res[i];
-      if (p.out_f32)
-        static_cast<float*>(p.out)[o] = y;
-      else
-        static_cast<uint16_t*>(p.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+    for (int i = 0; i < NV / 4; ++i) {
+      const float4 a = __ldg(p + i);
+      f[4 * i] = a.x, f[4 * i + 1] = a.y, f[4 * i + 2] = a.z, f[4 * i + 3] = a.w;
     }
-  }
-}
-
-template <bool FWD, int NC>
-__device__ __forceinline__ void linear_store(const LinearParams& p, long long l, int c, float bias, const float* acc) {
-  if (l >= p.L || c >= p.C) return;
-  if constexpr (!FWD) {
-    const int n = min(NC, p.C - c);
-    uint16_t* o = static_cast<uint16_t*>(p.out) + static_cast<long long>(c) * p.L + l;
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-      if (i < n) o[static_cast<long long>(i) * p.L] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i]));
   } else {
-    switch (p.act) {
-      case LIN_RELU: linear_store_act<LIN_RELU, NC>(p, l, c, bias, acc); break;
-      case LIN_SILU: linear_store_act<LIN_SILU, NC>(p, l, c, bias, acc); break;
-      case LIN_GELU: linear_store_act<LIN_GELU, NC>(p, l, c, bias, acc); break;
-      case LIN_GELU_TANH: linear_store_act<LIN_GELU_TANH, NC>(p, l, c, bias, acc); break;
-      default: linear_store_act<LIN_NONE, NC>(p, l, c, bias, acc); break;
+    uint32_t w[NV / 2];
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if constexpr (NV == 8) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    } else {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = a.x, w[1] = a.y;
+    }
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
 }
 
-__device__ __forceinline__ float lane_bias(const LinearParams& p, long long l) {
-  if (!p.bias || l >= p.L) return 0.f;
-  return p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + l) : bf16_value(__ldg(static_cast<const uint16_t*>(p.bias) + l));
+// Four output elements at index `at`: z = acc + bias, y = act(z) + residual.
+template <int ACT>
+__device__ __forceinline__ void store_four_act(const LinearParams& p, long long at, const float* bias, const float* acc) {
+  float z[4], y[4], r[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.residual) load_vals<4>(p.residual, p.residual_f32, at, r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    z[i] = acc[i] + bias[i];
+    y[i] = act_value<ACT>(z[i]) + r[i];
+  }
+  if (p.z) *reinterpret_cast<uint2*>(p.z + at) = make_uint2(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]));
+  if (p.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+}
+
+template <bool FWD>
+__device__ __forceinline__ void store_four(const LinearParams& p, long long at, const float* bias, const float* acc) {
+  switch (FWD ? p.act : LIN_NONE) {
+    case LIN_RELU: store_four_act<LIN_RELU>(p, at, bias, acc); break;
+    case LIN_SILU: store_four_act<LIN_SILU>(p, at, bias, acc); break;
+    case LIN_GELU: store_four_act<LIN_GELU>(p, at, bias, acc); break;
+    case LIN_GELU_TANH: store_four_act<LIN_GELU_TANH>(p, at, bias, acc); break;
+    default: store_four_act<LIN_NONE>(p, at, bias, acc); break;
+  }
 }
 
 // Descriptor of K-step kk (16 elements) of an operand block at shared address
@@ -142,16 +166,16 @@ struct SplitCfg {
   // as many stages as let two CTAs share an SM
   static constexpr int kStages = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256;
-  static constexpr int kTmemCols = BN < 32 ? 32 : BN;
+  static constexpr int kTmemCols = 2 * BN;   // two accumulators, for fp32 outputs
   static constexpr int kThreads = 192;
   static constexpr uint32_t kIdesc = idesc_bf16(128, BN, AMN, BMN);
   static_assert(BN * 128 * 4 <= kStages * kStageBytes, "the partial tile fits the stages");
   static_assert(!BMN || BN % 64 == 0, "MN-major B comes in 64-wide chunks");
 };
 
-__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
@@ -175,6 +199,10 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
   const int c0 = blockIdx.y * BN;
   const int kb0 = static_cast<int>(static_cast<long long>(p.nk) * rank / S);
   const int kb1 = static_cast<int>(static_cast<long long>(p.nk) * (rank + 1) / S);
+  // fp32 outputs: the K range in two accumulators, added in the epilogue, which
+  // halves the length of the tensor core's chain of truncating additions
+  const bool two = FWD && p.out_f32 && kb1 - kb0 > 1;
+  const int kbm = two ? (kb0 + kb1) / 2 : kb1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -248,7 +276,8 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
         const uint32_t a0 = smem_u32(smem + stage * C::kStageBytes), b0 = a0 + kLinABytes;
 #pragma unroll
         for (int kk = 0; kk < kLinBK / 16; ++kk)
-          umma_bf16(tmem_base, linear_desc<AMN>(a0, kk), linear_desc<BMN>(b0, kk), C::kIdesc, (kb > kb0 || kk) ? 1u : 0u);
+          umma_bf16(tmem_base + (kb >= kbm ? BN : 0), linear_desc<AMN>(a0, kk), linear_desc<BMN>(b0, kk), C::kIdesc,
+                    ((kb != kb0 && kb != kbm) || kk) ? 1u : 0u);
         umma_commit(&empty[stage]);
         if (++stage == C::kStages) stage = 0, phase ^= 1;
       }
@@ -258,56 +287,70 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
     }
   }
   __syncwarp();
-  const int q = warp & 3, row = q * 32 + lane;
-  const long long l = l0 + row;
-  bool ready = false;
-  float bias = 0.f;
   float* part = reinterpret_cast<float*>(smem);   // [BN][128], over the stages
   if (warp >= 2) {
-    if (FWD) bias = lane_bias(p, l);
-    int w = (lane == 0) ? (mbar_wait(tfull, 0, abort_flag, p.status) ? 1 : 0) : 0;
-    ready = __shfl_sync(0xffffffffu, w, 0) != 0;
-    tc_fence_after();
-    if (ready) {
+    const int q = warp & 3, row = q * 32 + lane;
+    const int w = (lane == 0) ? (mbar_wait(tfull, 0, abort_flag, p.status) ? 1 : 0) : 0;
+    if (__shfl_sync(0xffffffffu, w, 0)) {
+      tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
       for (int c = 0; c < BN; c += 16) {
         float v[16];
         tmem_ld16(tb + c, v);
-        if (S == 1) {
-          linear_store<FWD, 16>(p, l, c0 + c, bias, v);
-        } else {
+        if (two) {
+          float u[16];
+          tmem_ld16(tb + BN + c, u);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(c + i) * 128 + row] = v[i];
+          for (int i = 0; i < 16; ++i) v[i] += u[i];
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[(c + i) * 128 + row] = v[i];
       }
     }
-    tc_fence_before();
   }
-  if (S > 1) {
-    __syncwarp();
-    cluster_sync();   // every CTA's part is in its shared memory
-    if (warp >= 2) {
-      // this CTA's share of the columns: the parts of all ranks, in rank order
-      const int nc = BN / S;
+  __syncwarp();
+  // every CTA's part is in its shared memory; each now finishes its share of
+  // the columns, four elements of a row per thread
+  if (S > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  {
+    const int nc = BN / S, c_end = (rank + 1) * nc;
+    const long long l = l0 + lane * 4;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (l < p.L) {
+      if (FWD && p.bias) load_vals<4>(p.bias, p.bias_f32, l, bias);
       uint32_t peer[8];
 #pragma unroll
-      for (int s = 0; s < 8; ++s) peer[s] = s < S ? cluster_addr(part, s) : 0u;
-      for (int c = rank * nc; c < (rank + 1) * nc; c += 2) {
-        float v[2] = {0.f, 0.f};
+      for (int s = 0; s < 8; ++s) peer[s] = S > 1 && s < S ? cluster_addr(part, s) : smem_u32(part);
+      constexpr int kAtOnce = 4;
+      for (int c = rank * nc + warp; c < c_end; c += 6 * kAtOnce) {
+        float v[kAtOnce][4] = {};
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
+        for (int s = 0; s < 8; ++s) {   // in rank order
           if (s < S) {
-            v[0] += ld_shared_cluster(peer[s] + static_cast<uint32_t>(c * 128 + row) * 4u);
-            v[1] += ld_shared_cluster(peer[s] + static_cast<uint32_t>((c + 1) * 128 + row) * 4u);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+              const int cu = c + 6 * u;
+              if (cu < c_end) {
+                const float4 t = ld_shared_cluster4(peer[s] + static_cast<uint32_t>(cu * 128 + lane * 4) * 4u);
+                v[u][0] += t.x, v[u][1] += t.y, v[u][2] += t.z, v[u][3] += t.w;
+              }
+            }
           }
         }
-        linear_store<FWD, 2>(p, l, c0 + c, bias, v);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int cu = c + 6 * u;
+          if (cu < c_end && c0 + cu < p.C) store_four<FWD>(p, static_cast<long long>(c0 + cu) * p.L + l, bias, v[u]);
+        }
       }
     }
-    __syncwarp();
-    cluster_sync();   // nobody reads this CTA's shared memory any more
   }
+  __syncwarp();
+  if (S > 1) cluster_sync();   // nobody reads this CTA's shared memory any more
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -323,10 +366,12 @@ struct PairCfg {
   static constexpr int kBBytes = 128 * kLinBK * 2;   // this CTA's half of B
   static constexpr int kStageBytes = kLinABytes + kBBytes;
   static constexpr int kStages = 6;
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 512;
   static constexpr int kEpiWarps = 8;
+  static constexpr int kOutBytes = 4096;   // per epilogue warp: two bf16 blocks of 32 x 32, or one of fp32
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kOutBytes + 512;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr uint32_t kIdesc = idesc_bf16(256, BN, AMN, BMN);
+  static constexpr uint32_t kIdesc = idesc_bf16(256, BN, BMN, AMN);
 };
 
 // Tile idx of the grid of L tiles x C tiles (256 x 256 each): C tiles in
@@ -336,12 +381,63 @@ __device__ __forceinline__ void linear_tile(const LinearParams& p, int idx, int&
   unit_and_col(idx, p.c_tiles, p.l_tiles, p.group, ct, lt);
 }
 
+// 32 fp32 values of each lane's row into a 128-byte-swizzled 32 x 32 block,
+// and its TMA store to {col, row}.
+__device__ __forceinline__ void store_block_f32(const float* v, const CUtensorMap* map, int col, int row, uint8_t* stage, int lane) {
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+  float4* s = reinterpret_cast<float4*>(stage) + lane * 8;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j ^ (lane & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, stage, col, row);
+    bulk_commit();
+  }
+}
+
+// One 32 x 32 block of the forward: this lane's row c, columns l .. l + 31.
+template <int ACT>
+__device__ __forceinline__ void forward_block(const LinearParams& p, const LinearMaps& maps, const float* acc, int l, long long c,
+                                              int row0, uint8_t* stage, int& slot, int lane) {
+  float z[32];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (p.bias && l + 8 * j < p.L) load_vals<8>(p.bias, p.bias_f32, l + 8 * j, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[8 * j + i] = acc[8 * j + i] + b[i];
+  }
+  uint32_t w[16];
+  if (p.z) {
+    pack_bf16x32(z, w);
+    if (p.out_f32 && lane == 0) bulk_wait_read<0>();   // an fp32 block uses both halves of the stage
+    __syncwarp();
+    warp_store_tma(w, &maps.z, l, row0, stage, slot, lane);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (p.residual && l + 8 * j < p.L && c < p.C) load_vals<8>(p.residual, p.residual_f32, c * p.L + l + 8 * j, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[8 * j + i] = act_value<ACT>(z[8 * j + i]) + r[i];
+  }
+  if (p.out_f32) {
+    store_block_f32(z, &maps.out, l, row0, stage, lane);
+  } else {
+    pack_bf16x32(z, w);
+    warp_store_tma(w, &maps.out, l, row0, stage, slot, lane);
+  }
+}
+
 template <bool AMN, bool BMN, bool FWD>
 __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
   using C = PairCfg<AMN, BMN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+  uint8_t* out_stage = smem + C::kStages * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + C::kEpiWarps * C::kOutBytes);
   uint64_t* empty = full + C::kStages;
   uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + 2;
@@ -393,8 +489,9 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
-          uint8_t* sA = smem + stage * C::kStageBytes;
-          uint8_t* sB = sA + kLinABytes;
+          // the tensor core's rows are c: its first operand is b
+          uint8_t* sB = smem + stage * C::kStageBytes;
+          uint8_t* sA = sB + kLinABytes;
           const uint32_t bar = cluster_addr(&full[stage], 0);   // both CTAs' loads count on the leader's
           const int k0 = kb * kLinBK;
           if (AMN) {
@@ -436,10 +533,10 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + stage * C::kStageBytes), b0 = a0 + kLinABytes;
+          const uint32_t b0 = smem_u32(smem + stage * C::kStageBytes), a0 = b0 + kLinABytes;
 #pragma unroll
           for (int kk = 0; kk < kLinBK / 16; ++kk)
-            umma_bf16_pair(acc, linear_desc<AMN>(a0, kk), linear_desc<BMN>(b0, kk), C::kIdesc, (kb | kk) ? 1u : 0u);
+            umma_bf16_pair(acc, linear_desc<BMN>(b0, kk), linear_desc<AMN>(a0, kk), C::kIdesc, (kb | kk) ? 1u : 0u);
           umma_commit_pair(&empty[stage], 0x3);
           if (++stage == C::kStages) stage = 0, phase ^= 1;
         }
@@ -453,23 +550,41 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    int buf = 0;
+    uint8_t* stage = out_stage + (warp - 2) * C::kOutBytes;
+    int buf = 0, slot = 0;
     uint32_t bphase = 0;
     for (int idx = first; idx < items; idx += step) {
       int lt, ct;
       linear_tile(p, idx, lt, ct);
-      const long long l = static_cast<long long>(lt) * 256 + rank * 128 + q * 32 + lane;
-      const int c0 = ct * 256 + half * 128;
-      const float bias = FWD ? lane_bias(p, l) : 0.f;
+      const int l0 = lt * 256 + half * 128, row0 = ct * 256 + rank * 128 + q * 32;
+      const long long c = static_cast<long long>(row0) + lane;
+      if (FWD && p.residual && c < p.C) {   // into L2 while the accumulator fills
+        const long long size = p.residual_f32 ? 4 : 2, end = p.L - l0 < 128 ? p.L - l0 : 128;
+        const char* r = static_cast<const char*>(p.residual) + (c * p.L + l0) * size;
+        for (long long o = 0; o < end * size; o += 128) prefetch_l2(r + o);
+      }
       int w = (lane == 0) ? (mbar_wait(&tfull[buf], bphase, abort_flag, p.status) ? 1 : 0) : 0;
       if (!__shfl_sync(0xffffffffu, w, 0)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * C::BN + half * 128) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
+      for (int k = 0; k < 128 && l0 + k < p.L; k += 32) {
+        if (row0 >= p.C) break;
         float v[32];
-        tmem_ld32(tb + c, v);
-        linear_store<FWD, 32>(p, l, c0 + c, bias, v);
+        tmem_ld32(tb + k, v);
+        if constexpr (FWD) {
+          switch (p.act) {
+            case LIN_RELU: forward_block<LIN_RELU>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
+            case LIN_SILU: forward_block<LIN_SILU>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
+            case LIN_GELU: forward_block<LIN_GELU>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
+            case LIN_GELU_TANH: forward_block<LIN_GELU_TANH>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
+            default: forward_block<LIN_NONE>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
+          }
+        } else {
+          uint32_t wv[16];
+          pack_bf16x32(v, wv);
+          warp_store_tma(wv, &maps.out, l0 + k, row0, stage, slot, lane);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -482,6 +597,7 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
       buf ^= 1;
       if (buf == 0) bphase ^= 1;
     }
+    if (lane == 0) bulk_wait<0>();   // this warp's stores are complete before the CTA ends
   }
   __syncwarp();
   tc_fence_before();

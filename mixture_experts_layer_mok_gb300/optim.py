@@ -2,10 +2,13 @@
 marshalling only: the step is libmok's ``mok_adamw_step``)."""
 from __future__ import annotations
 
+import ctypes as C
+
+import numpy as np
 import torch
 
 from . import _lib
-from .ops import _DTYPE, _check, _handle, _on
+from .ops import _DTYPE, _check, _fail, _raw_stream
 
 _STATE = {"fp32": _lib.MOK_ADAMW_STATE_F32, "mxfp8": _lib.MOK_ADAMW_STATE_MXFP8}
 _KEPT = {"fp32": ("m", "v"), "mxfp8": ("m", "m_scale", "r", "r_scale")}
@@ -73,7 +76,9 @@ class AdamW:
                     raise ValueError(f"buffers[{name!r}][{i}]: expected {n} elements for a "
                                      f"{p.dtype} parameter of {p.numel()}, got {t.numel()}")
         self.buffers = {k: list(v) for k, v in buffers.items()}
-        # one launch list per parameter type (master copies belong to the bf16 ones)
+        # one launch list per parameter type (master copies belong to the bf16
+        # ones), with the fields that a step changes as arrays over it
+        self._shapes = [p.shape for p in self.params]
         self._groups = []
         for dtype in (torch.bfloat16, torch.float32):
             idx = [i for i, p in enumerate(self.params) if p.dtype == dtype]
@@ -85,7 +90,8 @@ class AdamW:
                 for name, ts in self.buffers.items():
                     if ts[i] is not None:
                         setattr(a, _FIELD[name], ts[i].data_ptr())
-            self._groups.append((dtype, idx, arr))
+            fields = np.frombuffer(arr, dtype=np.dtype(_lib.MokAdamwTensor))
+            self._groups.append((dtype, idx, arr, fields, fields["p"].tolist(), fields["n"].tolist()))
 
     def state_dict(self) -> dict:
         """The step count, the state kind and the state tensors themselves."""
@@ -115,41 +121,49 @@ class AdamW:
         ``grad_scale``: a one-element fp32 CUDA tensor that multiplies every
         gradient (clipping, loss scaling).  ``lr`` replaces the learning rate
         for this step."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.step(grads, grad_scale, lr)
         if grads is None:
             grads = [p.grad for p in self.params]
         if len(grads) != len(self.params):
             raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
+        scale = None
         if grad_scale is not None:
             _check(grad_scale, "grad_scale", None, (torch.float32,))
             if grad_scale.numel() != 1:
                 raise ValueError("grad_scale: expected one element")
+            scale = grad_scale.data_ptr()
         runs = []
-        for dtype, idx, arr in self._groups:
-            kinds = set()
-            for a, i in zip(arr, idx):
-                g, p = grads[i], self.params[i]
+        for dtype, idx, arr, fields, at, lengths in self._groups:
+            kinds = [None] * len(idx)   # each gradient's type
+            ptrs = [0] * len(idx)
+            for k, i in enumerate(idx):
+                g = grads[i]
                 if g is None:
-                    a.n = 0
                     continue
-                if g.shape != p.shape or g.dtype not in _DTYPE or not g.is_cuda or not g.is_contiguous():
-                    _check(g, f"grads[{i}]", p.shape, tuple(_DTYPE))
-                if (a.p or 0) != p.data_ptr():
+                kind = g.dtype
+                if kind not in _DTYPE or g.shape != self._shapes[i] or not g.is_cuda or not g.is_contiguous():
+                    _check(g, f"grads[{i}]", self._shapes[i], tuple(_DTYPE))
+                if self.params[i].data_ptr() != at[k]:
                     raise ValueError(f"params[{i}] moved to other memory: build the optimiser again")
-                a.n, a.g = g.numel(), g.data_ptr()
-                kinds.add(g.dtype)
-            for kind in kinds:
-                part = arr
-                if len(kinds) > 1:   # gradients of two types: a list for each
-                    sub = [a for a, i in zip(arr, idx) if grads[i] is not None and grads[i].dtype == kind]
-                    part = (_lib.MokAdamwTensor * len(sub))(*sub)
-                runs.append((dtype, kind, part))
-        lib = _lib.load()
+                kinds[k] = kind
+                ptrs[k] = g.data_ptr()
+            runs.append((dtype, arr, fields, kinds, ptrs, lengths))
+        fn = _lib.load().mok_adamw_step
         cfg = _lib.MokAdamwConfig(state=_STATE[self.state], lr=self.lr if lr is None else lr, beta1=self.betas[0],
                                   beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
                                   step=self.step_count + 1, seed=self.seed & (2 ** 64 - 1))
-        scale = None if grad_scale is None else grad_scale.data_ptr()
-        with _on(stream):
-            for dtype, kind, part in runs:
-                cfg.param_dtype, cfg.grad_dtype = _DTYPE[dtype], _DTYPE[kind]
-                _lib.check(lib.mok_adamw_step(cfg, part, len(part), scale, _handle()), "mok_adamw_step")
+        handle = _raw_stream(self.params[0].get_device()) if self.params else None
+        for dtype, arr, fields, kinds, ptrs, lengths in runs:
+            cfg.param_dtype = _DTYPE[dtype]
+            fields["g"] = ptrs
+            for kind in set(kinds) - {None}:
+                cfg.grad_dtype = _DTYPE[kind]
+                # a length of 0 leaves a tensor out: no gradient, or one of another type
+                fields["n"] = lengths if kinds.count(kind) == len(kinds) else [
+                    n if t is kind else 0 for n, t in zip(lengths, kinds)]
+                st = fn(C.byref(cfg), arr, len(arr), scale, handle)
+                if st:
+                    _fail(st, "mok_adamw_step")
         self.step_count += 1
