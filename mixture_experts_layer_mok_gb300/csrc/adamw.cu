@@ -114,12 +114,17 @@ __device__ __forceinline__ void load_codes8(const uint8_t* p, float scale, bool 
 // bits are added below the last kept place of the fp32 form and the rest is
 // cut off.  Below 2^-6 the grid is uniform (2^-9), as it is in [2^-6, 2^-5):
 // such a value is moved there and back.
-__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t rand16) {
-  const float a = fabsf(y);
-  const float off = a < 0.015625f ? 0.015625f : 0.f;
-  const float t = a + off;
-  const float q = __uint_as_float((__float_as_uint(t) + (rand16 << 4)) & 0xFFF00000u) - off;
-  return q;   // sign dropped
+// `below`: the 16 random bits in places 4 to 19, zeros elsewhere.
+__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t below) {
+  const float off = fabsf(y) < 0.015625f ? 0.015625f : 0.f;
+  return __uint_as_float((__float_as_uint(fabsf(y) + off) + below) & 0xFFF00000u) - off;   // sign dropped
+}
+
+// sqrt(x) in two instructions, good to 2^-23.
+__device__ __forceinline__ float fast_sqrt(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Writes 8 values as codes with the scale of their block of 32 (four
@@ -139,12 +144,11 @@ __device__ __forceinline__ void store_codes8(uint8_t* codes, uint8_t* scales, lo
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float y = v[i] * inv;
-    q[i] = e4m3_stochastic(y, R ? rand[i] & 0xFFFFu : rand[i] >> 16);
-    if (R) {
-      if (q[i] == 0.f && y > 0.f) q[i] = 0.001953125f;   // 2^-9, the smallest code
-    } else {
+    q[i] = e4m3_stochastic(y, R ? (rand[i] << 4) & 0xFFFF0u : (rand[i] >> 12) & 0xFFFF0u);
+    if (R)
+      q[i] = fmaxf(q[i], y > 0.f ? 0.001953125f : 0.f);   // 2^-9, the smallest code
+    else
       q[i] = copysignf(q[i], y);
-    }
   }
   uint32_t w[2];
 #pragma unroll
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Adam
     m[i] = fmaf(s.beta1, m[i], s.one_minus_beta1 * gi);
     const float v0 = MX ? v[i] * v[i] : v[i];
     v[i] = fmaf(s.beta2, v0, s.one_minus_beta2 * gi * gi);
-    r[i] = sqrtf(v[i]);
+    r[i] = fast_sqrt(v[i]);
     p[i] = fmaf(-s.step_size, __fdividef(m[i], fmaf(r[i], s.inv_sqrt_bc2, s.eps)), p[i] * s.decay);
   }
   if (MASTER) store8(t.master + i0, whole, left, p);

@@ -44,33 +44,47 @@ constexpr int kLinChunk = 64 * 128;        // an MN-major 64 x 64 block
 constexpr int kLinABytes = 128 * kLinBK * 2;
 
 // ---------------------------------------------------------------- epilogue
-// Phi(z), the normal distribution function, and exp(-z^2/2): with t = 1 / (1 +
-// p |z| / sqrt 2), 1 - Phi(|z|) = 1/2 poly(t) exp(-z^2/2) (Abramowitz and
-// Stegun, 7.1.26; error in Phi below 7.5e-8).  Two special-function and about
-// ten other instructions, without a branch, where erff takes both of its
-// branches in nearly every warp.
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-  e = __expf(-0.5f * z * z);
-  float q = fmaf(t, 1.061405429f, -1.453152027f);
-  q = fmaf(t, q, 1.421413741f);
-  q = fmaf(t, q, -0.284496736f);
-  q = fmaf(t, q, 0.254829592f);
-  q *= 0.5f * t * e;
-  return z < 0.f ? q : 1.f - q;
+// One special-function instruction each (subnormals flushed): 2^x and 1/x,
+// good to about 2^-22.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float logistic(float x) { return fast_rcp(1.f + fast_exp2(-kLog2e * x)); }
+
+// 1 - Phi(|z|), Phi the normal distribution function, and e = exp(-z^2/2):
+// with t = 1 / (1 + p |z| / sqrt 2) it is 1/2 poly(t) e (Abramowitz and Stegun,
+// 7.1.26; error below 7.5e-8).  A dozen instructions without a branch, where
+// erff takes both of its branches in nearly every warp.
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+  const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
+  e = fast_exp2(z * z * (-0.5f * kLog2e));
+  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  q = fmaf(t, q, 0.5f * 1.421413741f);
+  q = fmaf(t, q, 0.5f * -0.284496736f);
+  q = fmaf(t, q, 0.5f * 0.254829592f);
+  return q * (t * e);
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == LIN_RELU) return z < 0.f ? 0.f : z;   // keeps a NaN
-  if constexpr (ACT == LIN_SILU) return z * __fdividef(1.f, 1.f + __expf(-z));
+  if constexpr (ACT == LIN_SILU) return z * logistic(z);
   if constexpr (ACT == LIN_GELU) {
+    // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)); the last factor is 0 from 15 on
     float e;
-    return z * normal_cdf(z, e);
+    const float q = normal_tail(z, e);
+    return fmaf(-fminf(fabsf(z), 64.f), q, z < 0.f ? 0.f : z);
   }
   if constexpr (ACT == LIN_GELU_TANH)   // 0.5 z (1 + tanh u) = z / (1 + exp(-2u))
-    return z * __fdividef(1.f, 1.f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+    return z * logistic(1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.f));
   return z;
 }
 
@@ -79,18 +93,18 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == LIN_RELU) return z > 0.f ? 1.f : z == z ? 0.f : z;
   if constexpr (ACT == LIN_SILU) {
-    const float s = __fdividef(1.f, 1.f + __expf(-z));
-    return s * (1.f + z * (1.f - s));
+    const float s = logistic(z);
+    return s * fmaf(z, 1.f - s, 1.f);
   }
-  if constexpr (ACT == LIN_GELU) {
+  if constexpr (ACT == LIN_GELU) {   // Phi(z) + z phi(z)
     float e;
-    const float phi = normal_cdf(z, e);
-    return fmaf(z * 0.3989422804014327f, e, phi);
+    const float q = normal_tail(z, e);
+    return fmaf(z * 0.3989422804014327f, e, z < 0.f ? q : 1.f - q);
   }
-  if constexpr (ACT == LIN_GELU_TANH) {   // with s = 1 / (1 + exp(-2u)): s + 2 z s (1 - s) du/dz
+  if constexpr (ACT == LIN_GELU_TANH) {   // with s = 1 / (1 + exp(-2u)): s + z s (1 - s) d(2u)/dz
     const float z2 = z * z;
-    const float s = __fdividef(1.f, 1.f + __expf(-1.5957691216057308f * z * (1.f + 0.044715f * z2)));
-    return s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z2);
+    const float s = logistic(1.5957691216057308f * z * fmaf(0.044715f, z2, 1.f));
+    return fmaf(z * s * (1.f - s), 1.5957691216057308f * fmaf(0.134145f, z2, 1.f), s);
   }
   return 1.f;
 }
@@ -568,8 +582,7 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
       tc_fence_after();
       const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * C::BN + half * 128) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int k = 0; k < 128 && l0 + k < p.L; k += 32) {
-        if (row0 >= p.C) break;
+      for (int k = 0; k < 128 && l0 + k < p.L && row0 < p.C; k += 32) {
         float v[32];
         tmem_ld32(tb + k, v);
         if constexpr (FWD) {

@@ -256,21 +256,34 @@ __global__ void __launch_bounds__(MAXT) rms_norm_bwd_kernel(const NormBwdArgs a)
     if (c < nv) load_weight<V>(a.weight, a.weight_f32, c * V, w[i]);
   }
   const float inv_h = 1.f / static_cast<float>(a.H);
-  int odd = 0;
-  for (long long row = walker; row < a.rows; row += walkers, odd ^= 1) {
+  // one row ahead: the next row's loads are in flight while this one is summed
+  Raw<uint16_t, V> ndy[ITEMS];
+  Raw<HT, V> nh[ITEMS], ndh[ITEMS];
+  float nr = 0.f;
+  const auto fetch = [&](long long row) {
+    if (row >= a.rows) return;
     const long long base = row * a.H;
-    const float rstd = __ldg(a.rstd + row);
-    Raw<uint16_t, V> rdy[ITEMS];
-    Raw<HT, V> rh[ITEMS], rdh[ITEMS];
+    nr = __ldg(a.rstd + row);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * T;
       if (c < nv) {
-        rdy[i] = load_raw<uint16_t, V>(a.dy + base + c * V);
-        rh[i] = load_raw<HT, V>(static_cast<const HT*>(a.h) + base + c * V);
-        if (a.dh) rdh[i] = load_raw<HT, V>(static_cast<const HT*>(a.dh) + base + c * V);
+        ndy[i] = load_raw<uint16_t, V>(a.dy + base + c * V);
+        nh[i] = load_raw<HT, V>(static_cast<const HT*>(a.h) + base + c * V);
+        if (a.dh) ndh[i] = load_raw<HT, V>(static_cast<const HT*>(a.dh) + base + c * V);
       }
     }
+  };
+  fetch(walker);
+  int odd = 0;
+  for (long long row = walker; row < a.rows; row += walkers, odd ^= 1) {
+    const long long base = row * a.H;
+    const float rstd = nr;
+    Raw<uint16_t, V> rdy[ITEMS];
+    Raw<HT, V> rh[ITEMS], rdh[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) rdy[i] = ndy[i], rh[i] = nh[i], rdh[i] = ndh[i];
+    fetch(row + walkers);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
