@@ -20,12 +20,16 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "gemm.cuh"
 #include "internal.h"
 #include "ops.h"
 
 namespace mok {
 namespace {
+
+constexpr int kAdamwPerSm = 4;   // resident blocks on each of 152 SMs
 
 template <int CAP>
 struct AdamwList {
@@ -40,36 +44,58 @@ __device__ __forceinline__ uint32_t mix_bits(uint32_t i, uint32_t key) {
   return h ^ (h >> 16);
 }
 
+// Eight elements as they lie in memory.
 template <class T>
-__device__ __forceinline__ void load8(const T* p, bool whole, int left, float* f) {
-  if (whole) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
+struct Raw8 {
+  uint32_t w[2 * sizeof(T)];
+};
+
+// `left`: elements that exist (8: all, loaded as vectors; fewer: the end of a tensor).
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int left) {
+  Raw8<T> r;
+  if (left == 8) {
+    if constexpr (sizeof(T) == 1) {
+      const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
+      r.w[0] = a.x, r.w[1] = a.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 r = __ldcs(reinterpret_cast<const float4*>(p) + i);
-        f[4 * i] = r.x, f[4 * i + 1] = r.y, f[4 * i + 2] = r.z, f[4 * i + 3] = r.w;
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+        const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+        r.w[4 * i] = a.x, r.w[4 * i + 1] = a.y, r.w[4 * i + 2] = a.z, r.w[4 * i + 3] = a.w;
       }
     }
   } else {
 #pragma unroll
+    for (int i = 0; i < 2 * static_cast<int>(sizeof(T)); ++i) r.w[i] = 0u;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-      f[i] = 0.f;
       if (i < left) {
-        if constexpr (sizeof(T) == 2)
-          f[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+        if constexpr (sizeof(T) == 4)
+          r.w[i] = __float_as_uint(p[i]);
+        else if constexpr (sizeof(T) == 2)
+          r.w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
         else
-          f[i] = p[i];
+          r.w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
       }
     }
   }
+  return r;
+}
+__device__ __forceinline__ void values(const Raw8<float>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.w[i]);
+}
+__device__ __forceinline__ void values(const Raw8<uint16_t>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(r.w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void values(const Raw8<uint8_t>& r, float* f) {
+  e4m3x4_values(r.w[0], f);
+  e4m3x4_values(r.w[1], f + 4);
 }
 
 template <class T>
@@ -94,22 +120,6 @@ __device__ __forceinline__ void store8(T* p, bool whole, int left, const float* 
   }
 }
 
-__device__ __forceinline__ void load_codes8(const uint8_t* p, float scale, bool whole, int left, float* f) {
-  uint32_t w[2] = {0u, 0u};
-  if (whole) {
-    const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
-    w[0] = q.x, w[1] = q.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
-  }
-  e4m3x4_values(w[0], f);
-  e4m3x4_values(w[1], f + 4);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] *= scale;
-}
-
 // |y| <= 448 onto the E4M3 grid, rounded up or down by 16 random bits: the
 // bits are added below the last kept place of the fp32 form and the rest is
 // cut off.  Below 2^-6 the grid is uniform (2^-9), as it is in [2^-6, 2^-5):
@@ -120,10 +130,16 @@ __device__ __forceinline__ float e4m3_stochastic(float y, uint32_t below) {
   return __uint_as_float((__float_as_uint(fabsf(y) + off) + below) & 0xFFF00000u) - off;   // sign dropped
 }
 
-// sqrt(x) in two instructions, good to 2^-23.
+// sqrt(x) and 1/x, one instruction each, good to about 2^-22; subnormals (v
+// below 1e-38) count as zero.
 __device__ __forceinline__ float fast_sqrt(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -167,103 +183,127 @@ __device__ __forceinline__ void store_codes8(uint8_t* codes, uint8_t* scales, lo
   if ((threadIdx.x & 3) == 0 && left > 0) scales[block] = static_cast<uint8_t>(s + 127);
 }
 
-// One block of 256 threads per kAdamwBlock elements of one tensor, 8 per
-// thread.
+// What a thread reads of its eight elements.
+template <class PT, class GT, bool MASTER, bool MX>
+struct AdamwIn {
+  using P = std::conditional_t<MASTER, float, PT>;
+  using S = std::conditional_t<MX, uint8_t, float>;
+  Raw8<GT> g;
+  Raw8<P> p;
+  Raw8<S> m, v;
+  uint32_t ms, rs;   // MXFP8: the scales of the thread's block
+  long long i0;
+  int left, tensor;
+
+  // Chunk `c` of the launch, of the tensor that holds it (searched from `from` on).
+  template <class L>
+  __device__ __forceinline__ void load(const L& list, int c, int from) {
+    tensor = from;
+    while (tensor + 1 < list.n && list.t[tensor + 1].first <= c) ++tensor;
+    const AdamwTensor& t = list.t[tensor];
+    i0 = static_cast<long long>(c - t.first) * kAdamwBlock + threadIdx.x * 8;
+    const long long rest = t.n - i0;
+    left = rest >= 8 ? 8 : rest > 0 ? static_cast<int>(rest) : 0;
+    g = load8(static_cast<const GT*>(t.g) + i0, left);
+    p = load8(static_cast<const P*>(MASTER ? static_cast<const void*>(t.master) : t.p) + i0, left);
+    m = load8(static_cast<const S*>(t.m) + i0, left);
+    v = load8(static_cast<const S*>(t.v) + i0, left);
+    ms = rs = 0;
+    if (MX && left > 0) {
+      ms = t.m_scale[i0 >> 5];
+      rs = t.r_scale[i0 >> 5];
+    }
+  }
+};
+
+// Persistent blocks of 256 threads over chunks of kAdamwBlock elements, 8 per
+// thread, each chunk within one tensor; a block's next chunk is in flight
+// while it works on this one.
 template <class PT, class GT, bool MASTER, bool MX, int CAP>
-__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ AdamwList<CAP> list, const AdamwScalars s) {
+__global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
+    adamw_kernel(const __grid_constant__ AdamwList<CAP> list, const int chunks, const AdamwScalars s) {
+  using In = AdamwIn<PT, GT, MASTER, MX>;
   griddep_wait();
   griddep_launch_dependents();
-  // the tensor this block works on: the last one that begins at or before it
-  int lo = 0, hi = list.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (list.t[mid].first <= static_cast<int>(blockIdx.x))
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const AdamwTensor& t = list.t[lo];
-  const long long i0 = static_cast<long long>(blockIdx.x - t.first) * kAdamwBlock + threadIdx.x * 8;
-  const long long rest = t.n - i0;
-  const int left = rest >= 8 ? 8 : rest > 0 ? static_cast<int>(rest) : 0;
-  const bool whole = left == 8;
-  if (!MX && left == 0) return;
-  float g[8], p[8], m[8], v[8];
-  load8(static_cast<const GT*>(t.g) + i0, whole, left, g);
-  if (MASTER)
-    load8(t.master + i0, whole, left, p);
-  else
-    load8(static_cast<const PT*>(t.p) + i0, whole, left, p);
-  const long long block = i0 >> 5;
-  if (MX) {
-    float ms = 0.f, rs = 0.f;
-    if (left > 0) {
-      ms = e8m0_value(t.m_scale[block]);
-      rs = e8m0_value(t.r_scale[block]);
-    }
-    load_codes8(static_cast<const uint8_t*>(t.m) + i0, ms, whole, left, m);
-    load_codes8(static_cast<const uint8_t*>(t.v) + i0, rs, whole, left, v);
-  } else {
-    load8(static_cast<const float*>(t.m) + i0, whole, left, m);
-    load8(static_cast<const float*>(t.v) + i0, whole, left, v);
-  }
   const float gs = s.grad_scale ? __ldg(s.grad_scale) : 1.f;
-  float r[8];
+  In next;
+  next.load(list, blockIdx.x, 0);
+  for (int c = blockIdx.x; c < chunks;) {
+    const In in = next;
+    c += gridDim.x;
+    if (MX && c < chunks) next.load(list, c, in.tensor);
+    const AdamwTensor& t = list.t[in.tensor];
+    const int left = in.left;
+    if (!MX && left == 0) continue;
+    const bool whole = left == 8;
+    float g[8], p[8], m[8], v[8], r[8];
+    values(in.g, g);
+    values(in.p, p);
+    values(in.m, m);
+    values(in.v, v);
+    if (MX) {
+      const float ms = e8m0_value(in.ms), rs = e8m0_value(in.rs);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float gi = g[i] * gs;
-    m[i] = fmaf(s.beta1, m[i], s.one_minus_beta1 * gi);
-    const float v0 = MX ? v[i] * v[i] : v[i];
-    v[i] = fmaf(s.beta2, v0, s.one_minus_beta2 * gi * gi);
-    r[i] = fast_sqrt(v[i]);
-    p[i] = fmaf(-s.step_size, __fdividef(m[i], fmaf(r[i], s.inv_sqrt_bc2, s.eps)), p[i] * s.decay);
-  }
-  if (MASTER) store8(t.master + i0, whole, left, p);
-  store8(static_cast<PT*>(t.p) + i0, whole, left, p);
-  if (MX) {
-    uint32_t rand[8];
+      for (int i = 0; i < 8; ++i) m[i] *= ms, v[i] *= rs, v[i] *= v[i];
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rand[i] = mix_bits(static_cast<uint32_t>(i0) + i, t.key);
-    store_codes8<false>(static_cast<uint8_t*>(t.m) + i0, t.m_scale, block, whole, left, m, rand);
-    store_codes8<true>(static_cast<uint8_t*>(t.v) + i0, t.r_scale, block, whole, left, r, rand);
-  } else {
-    store8(static_cast<float*>(t.m) + i0, whole, left, m);
-    store8(static_cast<float*>(t.v) + i0, whole, left, v);
+    for (int i = 0; i < 8; ++i) {
+      const float gi = g[i] * gs;
+      m[i] = fmaf(s.beta1, m[i], s.one_minus_beta1 * gi);
+      v[i] = fmaf(s.beta2, v[i], s.one_minus_beta2 * gi * gi);
+      r[i] = fast_sqrt(v[i]);
+      p[i] = fmaf(-s.step_size, m[i] * fast_rcp(fmaf(r[i], s.inv_sqrt_bc2, s.eps)), p[i] * s.decay);
+    }
+    if (MASTER) store8(t.master + in.i0, whole, left, p);
+    store8(static_cast<PT*>(t.p) + in.i0, whole, left, p);
+    if (MX) {
+      const long long block = in.i0 >> 5;
+      uint32_t rand[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rand[i] = mix_bits(static_cast<uint32_t>(in.i0) + i, t.key);
+      store_codes8<false>(static_cast<uint8_t*>(t.m) + in.i0, t.m_scale, block, whole, left, m, rand);
+      store_codes8<true>(static_cast<uint8_t*>(t.v) + in.i0, t.r_scale, block, whole, left, r, rand);
+    } else {
+      store8(static_cast<float*>(t.m) + in.i0, whole, left, m);
+      store8(static_cast<float*>(t.v) + in.i0, whole, left, v);
+    }
   }
 }
 
 template <class PT, class GT, bool MASTER, bool MX, int CAP>
-cudaError_t launch_cap(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, cudaStream_t st) {
+cudaError_t launch_cap(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, cudaStream_t st) {
   AdamwList<CAP> list;
   memcpy(list.t, t, sizeof(AdamwTensor) * n);
   list.n = n;
-  return launch_dependent(adamw_kernel<PT, GT, MASTER, MX, CAP>, dim3(blocks), dim3(256), 0, st, list, s);
+  constexpr int kResident = 152 * kAdamwPerSm;
+  return launch_dependent(adamw_kernel<PT, GT, MASTER, MX, CAP>, dim3(MX && chunks > kResident ? kResident : chunks),
+                          dim3(256), 0, st, list, chunks, s);
 }
 
 template <class PT, class GT, bool MASTER, bool MX>
-cudaError_t launch_typed(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, cudaStream_t st) {
-  return n <= 16 ? launch_cap<PT, GT, MASTER, MX, 16>(t, n, blocks, s, st)
-                 : launch_cap<PT, GT, MASTER, MX, kAdamwMaxTensors>(t, n, blocks, s, st);
+cudaError_t launch_typed(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, cudaStream_t st) {
+  return n <= 16 ? launch_cap<PT, GT, MASTER, MX, 16>(t, n, chunks, s, st)
+                 : launch_cap<PT, GT, MASTER, MX, kAdamwMaxTensors>(t, n, chunks, s, st);
 }
 
 template <class PT, class GT, bool MASTER>
-cudaError_t launch_state(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, int mx, cudaStream_t st) {
-  return mx ? launch_typed<PT, GT, MASTER, true>(t, n, blocks, s, st)
-            : launch_typed<PT, GT, MASTER, false>(t, n, blocks, s, st);
+cudaError_t launch_state(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, int mx, cudaStream_t st) {
+  return mx ? launch_typed<PT, GT, MASTER, true>(t, n, chunks, s, st)
+            : launch_typed<PT, GT, MASTER, false>(t, n, chunks, s, st);
 }
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, int p_f32, int g_f32,
+cudaError_t launch_adamw(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, int p_f32, int g_f32,
                          int master, int mx, cudaStream_t st) {
   if (p_f32)
-    return g_f32 ? launch_state<float, float, false>(t, n, blocks, s, mx, st)
-                 : launch_state<float, uint16_t, false>(t, n, blocks, s, mx, st);
+    return g_f32 ? launch_state<float, float, false>(t, n, chunks, s, mx, st)
+                 : launch_state<float, uint16_t, false>(t, n, chunks, s, mx, st);
   if (master)
-    return g_f32 ? launch_state<uint16_t, float, true>(t, n, blocks, s, mx, st)
-                 : launch_state<uint16_t, uint16_t, true>(t, n, blocks, s, mx, st);
-  return g_f32 ? launch_state<uint16_t, float, false>(t, n, blocks, s, mx, st)
-               : launch_state<uint16_t, uint16_t, false>(t, n, blocks, s, mx, st);
+    return g_f32 ? launch_state<uint16_t, float, true>(t, n, chunks, s, mx, st)
+                 : launch_state<uint16_t, uint16_t, true>(t, n, chunks, s, mx, st);
+  return g_f32 ? launch_state<uint16_t, float, false>(t, n, chunks, s, mx, st)
+               : launch_state<uint16_t, uint16_t, false>(t, n, chunks, s, mx, st);
 }
 
 }  // namespace mok

@@ -116,7 +116,7 @@ struct AdamwTensor {
   uint8_t* r_scale;
   long long n;
   uint32_t key;     // seeds the tensor's rounding bits
-  int first;        // its first block of the launch
+  int first;        // its first chunk of the launch
 };
 struct AdamwScalars {
   float beta1, one_minus_beta1, beta2, one_minus_beta2;
@@ -126,10 +126,10 @@ struct AdamwScalars {
   float eps;
   const float* grad_scale;  // device scalar or NULL
 };
-constexpr int kAdamwBlock = 2048;   // elements per thread block
+constexpr int kAdamwBlock = 2048;   // elements per chunk, the work of one block at a time
 // Tensors one launch takes at most, and the launch itself; t[i].first is set.
 constexpr int kAdamwMaxTensors = 400;
-cudaError_t launch_adamw(const AdamwTensor* t, int n, int blocks, const AdamwScalars& s, int p_f32, int g_f32,
+cudaError_t launch_adamw(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, int p_f32, int g_f32,
                          int master, int mx, cudaStream_t st);
 
 }  // namespace mok
