@@ -48,13 +48,13 @@ mok_status_t mok_mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, i
   if (rows < 0 || K < 0 || (rows > 1 && K % 32))
     return fail(MOK_ERR_INVALID_ARG, "need rows, K >= 0, and K %% 32 == 0 for more than one row");
   if (rows == 0 || K == 0) return MOK_OK;
-  if (rows > (1ll << 46) / K) return fail(MOK_ERR_INVALID_ARG, "rows * K too large");
+  if (rows > (1ll << 42) / K) return fail(MOK_ERR_INVALID_ARG, "rows * K too large");
   if (!codes || !scales || !out) return fail(MOK_ERR_INVALID_ARG, "NULL argument");
   if (!aligned16(codes) || !aligned16(out)) return fail(MOK_ERR_INVALID_ARG, "misaligned pointer");
   int sms = 0;
   mok_status_t st = device_info(&sms);
   if (st) return st;
-  MOK_CUDA(launch_mx_dequantize(codes, scales, rows * K, out, sms, static_cast<cudaStream_t>(stream)));
+  MOK_CUDA(launch_mx_dequantize(codes, scales, rows * K, out, static_cast<cudaStream_t>(stream)));
   return MOK_OK;
 }
 

@@ -165,12 +165,36 @@ __device__ __forceinline__ void store_four(const LinearParams& p, long long at, 
   }
 }
 
-// Descriptor of K-step kk (16 elements) of an operand block at shared address
-// s: K-major rows of 128 bytes, or MN-major chunks of 64 x 64.
+// Descriptor of an operand block at shared address s (K-major rows of 128
+// bytes, or MN-major chunks of 64 x 64), and the same `bytes` further on: the
+// low word holds the address in units of 16 bytes.  The issuing thread's own
+// instructions are what a k-block of 512 tensor cycles has little room for
+// (rebuilt descriptors cost the pair kernel a fifth of its rate), so it only
+// adds constants to two low words.
 template <bool MN>
-__device__ __forceinline__ uint64_t linear_desc(uint32_t s, int kk) {
-  return MN ? smem_desc(s + kk * 16 * 128, kLinChunk, 1024, 2u) : smem_desc(s + kk * 32, 16, 1024, 2u);
+__device__ __forceinline__ uint64_t linear_desc(uint32_t s) {
+  return MN ? smem_desc(s, kLinChunk, 1024, 2u) : smem_desc(s, 16, 1024, 2u);
 }
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+  return (d & 0xFFFFFFFF00000000ull) | (static_cast<uint32_t>(d) + (bytes >> 4));
+}
+// The loops of the producer and of the MMA issuer run in whole warps, so that
+// their counters, addresses and descriptors are warp-uniform values (what the
+// instructions they issue take); one elected lane issues.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+// mbar_wait for a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+
+// Bytes from one K-step (16 elements) to the next.
+template <bool MN>
+constexpr uint32_t kStep = MN ? 16 * 128 : 32;
 
 // ---------------------------------------------------------------- split kernel
 template <bool AMN, bool BMN, int BN>
@@ -278,6 +302,7 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      const uint64_t ad = linear_desc<AMN>(smem_u32(smem)), bd = linear_desc<BMN>(smem_u32(smem) + kLinABytes);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -286,12 +311,11 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint32_t a0 = smem_u32(smem + stage * C::kStageBytes), b0 = a0 + kLinABytes;
+        const uint32_t at = stage * C::kStageBytes, acc = tmem_base + (kb >= kbm ? BN : 0);
+        umma_bf16(acc, desc_at(ad, at), desc_at(bd, at), C::kIdesc, kb != kb0 && kb != kbm);
 #pragma unroll
-        for (int kk = 0; kk < kLinBK / 16; ++kk)
-          umma_bf16(tmem_base + (kb >= kbm ? BN : 0), linear_desc<AMN>(a0, kk), linear_desc<BMN>(b0, kk), C::kIdesc,
-                    ((kb != kb0 && kb != kbm) || kk) ? 1u : 0u);
+        for (int kk = 1; kk < kLinBK / 16; ++kk)
+          umma_bf16(acc, desc_at(ad, at + kk * kStep<AMN>), desc_at(bd, at + kk * kStep<BMN>), C::kIdesc, 1u);
         umma_commit(&empty[stage]);
         if (++stage == C::kStages) stage = 0, phase ^= 1;
       }
@@ -379,9 +403,9 @@ struct PairCfg {
   static constexpr int BN = 256;
   static constexpr int kBBytes = 128 * kLinBK * 2;   // this CTA's half of B
   static constexpr int kStageBytes = kLinABytes + kBBytes;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = 5;
   static constexpr int kEpiWarps = 8;
-  static constexpr int kOutBytes = 4096;   // per epilogue warp: two bf16 blocks of 32 x 32, or one of fp32
+  static constexpr int kOutBytes = 8192;   // per epilogue warp: see forward_block
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kOutBytes + 512;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
@@ -395,54 +419,89 @@ __device__ __forceinline__ void linear_tile(const LinearParams& p, int idx, int&
   unit_and_col(idx, p.c_tiles, p.l_tiles, p.group, ct, lt);
 }
 
-// 32 fp32 values of each lane's row into a 128-byte-swizzled 32 x 32 block,
-// and its TMA store to {col, row}.
-__device__ __forceinline__ void store_block_f32(const float* v, const CUtensorMap* map, int col, int row, uint8_t* stage, int lane) {
-  if (lane == 0) bulk_wait_read<0>();
-  __syncwarp();
-  float4* s = reinterpret_cast<float4*>(stage) + lane * 8;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s[j ^ (lane & 7)] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_2d(map, stage, col, row);
-    bulk_commit();
-  }
+// 16-byte piece j of this lane's row in a staged 32 x 32 block, in the
+// swizzled layout of its tensor map: rows of 64 bytes (bf16) or 128 (fp32).
+template <bool F32>
+__device__ __forceinline__ uint4* stage_piece(uint8_t* block, int lane, int j) {
+  return reinterpret_cast<uint4*>(block) + (F32 ? lane * 8 + (j ^ (lane & 7)) : lane * 4 + (j ^ ((lane >> 1) & 3)));
 }
 
-// One 32 x 32 block of the forward: this lane's row c, columns l .. l + 31.
+// One 32 x 32 block of an output: this lane's row c, columns l .. l + 31, the
+// sums at TMEM address t.  16 columns at a time they become z and y in the
+// warp's stage, and leave by TMA stores of the whole block.  The stage's 8 KB
+// are two buffers, of y (2 KB in bf16, 4 KB in fp32) and with bf16 of z (2 KB),
+// so that a block is computed while the one before it is read; fp32 y with z
+// is one buffer of both.
+template <bool FWD, int ACT, bool F32>
+__device__ __forceinline__ void output_block(const LinearParams& p, const LinearMaps& maps, uint32_t t, int l, long long c,
+                                             int row0, uint8_t* stage, int& buf, int lane) {
+  const bool has_z = FWD && p.z;
+  const bool single = F32 && has_z;
+  uint8_t* y_block = stage + (single ? 0 : buf * 4096);
+  uint8_t* z_block = single ? stage + 4096 : y_block + 2048;
+  if (lane == 0) {   // the copies that last read this buffer are done reading
+    if (single)
+      bulk_wait_read<0>();
+    else
+      bulk_wait_read<1>();
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[16];
+    tmem_ld16(t + 16 * h, v);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float* z = v + 8 * j;
+      const int lj = l + 16 * h + 8 * j;
+      if constexpr (FWD) {
+        if (p.bias && lj < p.L) {
+          float b[8];
+          load_vals<8>(p.bias, p.bias_f32, lj, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] += b[i];
+        }
+        if (has_z)
+          *stage_piece<false>(z_block, lane, 2 * h + j) =
+              make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = act_value<ACT>(z[i]);
+        if (p.residual && lj < p.L && c < p.C) {
+          float r[8];
+          load_vals<8>(p.residual, p.residual_f32, c * p.L + lj, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] += r[i];
+        }
+      }
+      if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *stage_piece<true>(y_block, lane, 4 * h + 2 * j + i) =
+              make_uint4(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]), __float_as_uint(z[4 * i + 2]),
+                         __float_as_uint(z[4 * i + 3]));
+      } else {
+        *stage_piece<false>(y_block, lane, 2 * h + j) =
+            make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+      }
+    }
+  }
+  fence_proxy_async_smem();   // generic-proxy writes, then the async-proxy reads
+  __syncwarp();
+  if (lane == 0) {
+    if (has_z) tma_store_2d(&maps.z, z_block, l, row0);
+    tma_store_2d(&maps.out, y_block, l, row0);
+    bulk_commit();
+  }
+  buf ^= 1;
+}
+
 template <int ACT>
-__device__ __forceinline__ void forward_block(const LinearParams& p, const LinearMaps& maps, const float* acc, int l, long long c,
-                                              int row0, uint8_t* stage, int& slot, int lane) {
-  float z[32];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (p.bias && l + 8 * j < p.L) load_vals<8>(p.bias, p.bias_f32, l + 8 * j, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[8 * j + i] = acc[8 * j + i] + b[i];
-  }
-  uint32_t w[16];
-  if (p.z) {
-    pack_bf16x32(z, w);
-    if (p.out_f32 && lane == 0) bulk_wait_read<0>();   // an fp32 block uses both halves of the stage
-    __syncwarp();
-    warp_store_tma(w, &maps.z, l, row0, stage, slot, lane);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (p.residual && l + 8 * j < p.L && c < p.C) load_vals<8>(p.residual, p.residual_f32, c * p.L + l + 8 * j, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[8 * j + i] = act_value<ACT>(z[8 * j + i]) + r[i];
-  }
-  if (p.out_f32) {
-    store_block_f32(z, &maps.out, l, row0, stage, lane);
-  } else {
-    pack_bf16x32(z, w);
-    warp_store_tma(w, &maps.out, l, row0, stage, slot, lane);
-  }
+__device__ __forceinline__ void forward_block(const LinearParams& p, const LinearMaps& maps, uint32_t t, int l, long long c,
+                                              int row0, uint8_t* stage, int& buf, int lane) {
+  if (p.out_f32)
+    output_block<true, ACT, true>(p, maps, t, l, c, row0, stage, buf, lane);
+  else
+    output_block<true, ACT, false>(p, maps, t, l, c, row0, stage, buf, lane);
 }
 
 template <bool AMN, bool BMN, bool FWD>
@@ -533,34 +592,39 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const uint64_t bd = linear_desc<BMN>(smem_u32(smem)), ad = linear_desc<AMN>(smem_u32(smem) + kLinABytes);
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
       for (int idx = first; idx < items && ok; idx += step) {
-        if (!mbar_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) break;
+        if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) break;
         tc_fence_after();
         const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * C::BN);
         for (int kb = 0; kb < p.nk; ++kb) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) {
+          if (!warp_wait(&full[stage], phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t b0 = smem_u32(smem + stage * C::kStageBytes), a0 = b0 + kLinABytes;
+          const uint32_t at = stage * C::kStageBytes;
+          if (elect_one()) {
+            umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), C::kIdesc, kb != 0);
 #pragma unroll
-          for (int kk = 0; kk < kLinBK / 16; ++kk)
-            umma_bf16_pair(acc, linear_desc<BMN>(b0, kk), linear_desc<AMN>(a0, kk), C::kIdesc, (kb | kk) ? 1u : 0u);
-          umma_commit_pair(&empty[stage], 0x3);
+            for (int kk = 1; kk < kLinBK / 16; ++kk)
+              umma_bf16_pair(acc, desc_at(bd, at + kk * kStep<BMN>), desc_at(ad, at + kk * kStep<AMN>), C::kIdesc, 1u);
+            umma_commit_pair(&empty[stage], 0x3);
+            if (kb == p.nk - 1) umma_commit_pair(&tfull[buf], 0x3);
+          }
+          __syncwarp();
           if (++stage == C::kStages) stage = 0, phase ^= 1;
         }
-        if (!ok) break;
-        umma_commit_pair(&tfull[buf], 0x3);
         buf ^= 1;
         if (buf == 0) bphase ^= 1;
       }
-      umma_commit_pair(done, 0x1);
-      mbar_drain(done, 0);
+      if (elect_one()) {
+        umma_commit_pair(done, 0x1);
+        mbar_drain(done, 0);
+      }
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
@@ -583,20 +647,16 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
       const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * C::BN + half * 128) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
       for (int k = 0; k < 128 && l0 + k < p.L && row0 < p.C; k += 32) {
-        float v[32];
-        tmem_ld32(tb + k, v);
         if constexpr (FWD) {
           switch (p.act) {
-            case LIN_RELU: forward_block<LIN_RELU>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
-            case LIN_SILU: forward_block<LIN_SILU>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
-            case LIN_GELU: forward_block<LIN_GELU>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
-            case LIN_GELU_TANH: forward_block<LIN_GELU_TANH>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
-            default: forward_block<LIN_NONE>(p, maps, v, l0 + k, c, row0, stage, slot, lane); break;
+            case LIN_RELU: forward_block<LIN_RELU>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane); break;
+            case LIN_SILU: forward_block<LIN_SILU>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane); break;
+            case LIN_GELU: forward_block<LIN_GELU>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane); break;
+            case LIN_GELU_TANH: forward_block<LIN_GELU_TANH>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane); break;
+            default: forward_block<LIN_NONE>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane); break;
           }
         } else {
-          uint32_t wv[16];
-          pack_bf16x32(v, wv);
-          warp_store_tma(wv, &maps.out, l0 + k, row0, stage, slot, lane);
+          output_block<false, LIN_NONE, false>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane);
         }
       }
       tc_fence_before();

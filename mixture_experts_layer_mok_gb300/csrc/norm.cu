@@ -351,30 +351,32 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
   }
 }
 
-// E4M3 codes and E8M0 scales -> bf16: 8 codes per thread.
+// E4M3 codes and E8M0 scales -> bf16: 16 codes per thread, half a block.
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales, long long n,
                                                             uint16_t* __restrict__ out) {
   griddep_wait();
   griddep_launch_dependents();
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long c = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; c * 8 < n; c += step) {
-    const float s = e8m0_value(scales[c >> 2]);
-    if (c * 8 + 8 <= n) {
-      const uint2 q = __ldcs(reinterpret_cast<const uint2*>(codes) + c);
-      float f[8];
-      e4m3x4_values(q.x, f);
-      e4m3x4_values(q.y, f + 4);
+  const long long c = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x, at = c * 16;
+  if (at >= n) return;
+  if (at + 16 <= n) {
+    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(codes) + c);
+    const float s = e8m0_value(__ldg(scales + (c >> 1)));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    float f[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= s;
-      store_vals<8>(out + c * 8, f);
-    } else {
-      for (long long i = c * 8; i < n; ++i) {
-        float f[4];
-        e4m3x4_values(codes[i], f);
-        f[0] *= s;
-        store_vals<1>(out + i, f);
-      }
+    for (int i = 0; i < 4; ++i) e4m3x4_values(w[i], f + 4 * i);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] *= s;
+    store_vals<8>(out + at, f);
+    store_vals<8>(out + at + 8, f + 8);
+  } else {
+    const float s = e8m0_value(scales[c >> 1]);
+    for (long long i = at; i < n; ++i) {
+      float f[4];
+      e4m3x4_values(codes[i], f);
+      f[0] *= s;
+      store_vals<1>(out + i, f);
     }
   }
 }
@@ -454,10 +456,9 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight
   return launch_column_sum(a.part, walkers, a.H, d_weight, st);
 }
 
-cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out, int num_sms,
+cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out,
                                  cudaStream_t st) {
-  long long grid = (n / 8 + 256) / 256;
-  if (grid > 16ll * num_sms) grid = 16ll * num_sms;
+  const long long grid = (n + 16 * 256 - 1) / (16 * 256);
   return launch_dependent(mx_dequantize_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, codes, scales, n, out);
 }
 

@@ -63,8 +63,7 @@ cudaError_t launch_rms_norm(const NormArgs& a, int x_f32, int residual, cudaStre
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight, cudaStream_t st);
 // out[j] = sum over n rows of part[.][j], in a fixed order (n = 0: zeros).
 cudaError_t launch_column_sum(const float* part, int n, int H, float* out, cudaStream_t st);
-cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out, int num_sms,
-                                 cudaStream_t st);
+cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out, cudaStream_t st);
 
 // ---------------------------------------------------------------- dense projection
 enum LinAct : int { LIN_NONE = 0, LIN_RELU = 1, LIN_SILU = 2, LIN_GELU = 3, LIN_GELU_TANH = 4 };
