@@ -403,9 +403,9 @@ struct PairCfg {
   static constexpr int BN = 256;
   static constexpr int kBBytes = 128 * kLinBK * 2;   // this CTA's half of B
   static constexpr int kStageBytes = kLinABytes + kBBytes;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 6;
   static constexpr int kEpiWarps = 8;
-  static constexpr int kOutBytes = 8192;   // per epilogue warp: see forward_block
+  static constexpr int kOutBytes = 4096;   // per epilogue warp: see output_block
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kOutBytes + 512;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
@@ -426,19 +426,17 @@ __device__ __forceinline__ uint4* stage_piece(uint8_t* block, int lane, int j) {
   return reinterpret_cast<uint4*>(block) + (F32 ? lane * 8 + (j ^ (lane & 7)) : lane * 4 + (j ^ ((lane >> 1) & 3)));
 }
 
-// One 32 x 32 block of an output: this lane's row c, columns l .. l + 31, the
+// One 32 x 32 block of the outputs: this lane's row c, columns l .. l + 31, the
 // sums at TMEM address t.  16 columns at a time they become z and y in the
-// warp's stage, and leave by TMA stores of the whole block.  The stage's 8 KB
-// are two buffers, of y (2 KB in bf16, 4 KB in fp32) and with bf16 of z (2 KB),
-// so that a block is computed while the one before it is read; fp32 y with z
-// is one buffer of both.
+// warp's stage, and leave by TMA stores of the whole block.  The stage's 4 KB
+// hold two bf16 blocks, either one after the other (a block is computed while
+// the one before it is read) or y and z of one, or one fp32 block.
 template <bool FWD, int ACT, bool F32>
 __device__ __forceinline__ void output_block(const LinearParams& p, const LinearMaps& maps, uint32_t t, int l, long long c,
-                                             int row0, uint8_t* stage, int& buf, int lane) {
-  const bool has_z = FWD && p.z;
-  const bool single = F32 && has_z;
-  uint8_t* y_block = stage + (single ? 0 : buf * 4096);
-  uint8_t* z_block = single ? stage + 4096 : y_block + 2048;
+                                             int row0, uint8_t* stage, int& buf, int lane, bool has_z) {
+  const bool single = F32 || has_z;
+  uint8_t* y_block = stage + (single ? 0 : buf * 2048);
+  uint8_t* z_block = stage + 2048;
   if (lane == 0) {   // the copies that last read this buffer are done reading
     if (single)
       bulk_wait_read<0>();
@@ -495,13 +493,46 @@ __device__ __forceinline__ void output_block(const LinearParams& p, const Linear
   buf ^= 1;
 }
 
+// The pre-activations of one block alone.
+__device__ __forceinline__ void z_only_block(const LinearParams& p, const LinearMaps& maps, uint32_t t, int l, int row0,
+                                             uint8_t* stage, int lane) {
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[16];
+    tmem_ld16(t + 16 * h, v);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float* z = v + 8 * j;
+      const int lj = l + 16 * h + 8 * j;
+      if (p.bias && lj < p.L) {
+        float b[8];
+        load_vals<8>(p.bias, p.bias_f32, lj, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += b[i];
+      }
+      *stage_piece<false>(stage, lane, 2 * h + j) =
+          make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(&maps.z, stage, l, row0);
+    bulk_commit();
+  }
+}
+
 template <int ACT>
 __device__ __forceinline__ void forward_block(const LinearParams& p, const LinearMaps& maps, uint32_t t, int l, long long c,
                                               int row0, uint8_t* stage, int& buf, int lane) {
-  if (p.out_f32)
-    output_block<true, ACT, true>(p, maps, t, l, c, row0, stage, buf, lane);
-  else
-    output_block<true, ACT, false>(p, maps, t, l, c, row0, stage, buf, lane);
+  if (!p.out_f32) {
+    output_block<true, ACT, false>(p, maps, t, l, c, row0, stage, buf, lane, p.z != nullptr);
+    return;
+  }
+  if (p.z) z_only_block(p, maps, t, l, row0, stage, lane);   // the stage does not hold both
+  output_block<true, ACT, true>(p, maps, t, l, c, row0, stage, buf, lane, false);
 }
 
 template <bool AMN, bool BMN, bool FWD>
@@ -547,26 +578,27 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
   griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      long long fills = 0;
-      bool ok = true;
-      for (int idx = first; idx < items && ok; idx += step) {
-        int lt, ct;
-        linear_tile(p, idx, lt, ct);
-        const int l0 = lt * 256 + rank * 128, c0 = ct * 256 + rank * 128;
-        for (int kb = 0; kb < p.nk; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+    int stage = 0;
+    uint32_t phase = 0;
+    long long fills = 0;
+    bool ok = true;
+    const uint32_t lead_full = cluster_addr(full, 0);   // both CTAs' loads count on the leader's barriers
+    for (int idx = first; idx < items && ok; idx += step) {
+      int lt, ct;
+      linear_tile(p, idx, lt, ct);
+      const int l0 = lt * 256 + rank * 128, c0 = ct * 256 + rank * 128;
+      for (int kb = 0; kb < p.nk; ++kb) {
+        if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        // the tensor core's rows are c: its first operand is b
+        uint8_t* sB = smem + stage * C::kStageBytes;
+        uint8_t* sA = sB + kLinABytes;
+        const uint32_t bar = lead_full + stage * 8;
+        const int k0 = kb * kLinBK;
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
-          // the tensor core's rows are c: its first operand is b
-          uint8_t* sB = smem + stage * C::kStageBytes;
-          uint8_t* sA = sB + kLinABytes;
-          const uint32_t bar = cluster_addr(&full[stage], 0);   // both CTAs' loads count on the leader's
-          const int k0 = kb * kLinBK;
           if (AMN) {
             tma_load_2d_pair(sA, &maps.a, bar, l0, k0);
             tma_load_2d_pair(sA + kLinChunk, &maps.a, bar, l0 + 64, k0);
@@ -579,16 +611,17 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
           } else {
             tma_load_2d_pair(sB, &maps.b, bar, k0, c0);
           }
-          ++fills;
-          if (++stage == C::kStages) stage = 0, phase ^= 1;
         }
+        __syncwarp();
+        ++fills;
+        if (++stage == C::kStages) stage = 0, phase ^= 1;
       }
-      if (!ok && rank == 0) {
-        const int n = fills < C::kStages ? static_cast<int>(fills) : C::kStages;
-        for (int i = 0; i < n; ++i) {
-          if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
-          mbar_drain(&full[stage], phase);
-        }
+    }
+    if (!ok && rank == 0 && lane == 0) {   // no load may be in flight when the CTA ends
+      const int n = fills < C::kStages ? static_cast<int>(fills) : C::kStages;
+      for (int i = 0; i < n; ++i) {
+        if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
+        mbar_drain(&full[stage], phase);
       }
     }
   } else if (warp == 1) {
@@ -656,7 +689,7 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
             default: forward_block<LIN_NONE>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane); break;
           }
         } else {
-          output_block<false, LIN_NONE, false>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane);
+          output_block<false, LIN_NONE, false>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane, false);
         }
       }
       tc_fence_before();
