@@ -34,81 +34,117 @@ mok_status_t operand_map(CUtensorMap* m, const void* base, long long inner, long
   return make_box(m, base, 0, inner, outer, 64, box_outer);
 }
 
-// Lets `kern` take `bytes` of shared memory, once per device.
+// A kernel's launch attributes, and how many clusters of each size are
+// resident at once on a device (looked up once).  GB300's SMs come in groups
+// of different sizes, so that fewer large clusters fit than the SM count says:
+// of the pair split kernel 76 of 2 CTAs, 36 of 4, 23 of 6 and 15 of 8.
+struct KernelInfo {
+  int resident[64][9] = {};
+};
+
 template <class K>
-cudaError_t allow_smem(K kern, int bytes, bool* done) {
+cudaError_t resident_clusters(K kern, KernelInfo& info, int threads, int smem, int cluster, int* n) {
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (done[dev]) return cudaSuccess;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (err == cudaSuccess) done[dev] = true;
-  return err;
+  if (dev < 0 || dev >= 64 || cluster < 1 || cluster > 8) return cudaErrorInvalidValue;
+  int& at = info.resident[dev][cluster];
+  if (at == 0) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster * 1024);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int found = 0;
+    err = cudaOccupancyMaxActiveClusters(&found, kern, &cfg);
+    if (err != cudaSuccess) return err;
+    if (found <= 0) return cudaErrorInvalidConfiguration;
+    at = found;
+  }
+  *n = at;
+  return cudaSuccess;
 }
 
-template <bool AMN, bool BMN, int BN, bool FWD>
-cudaError_t launch_split(const LinearMaps& maps, const LinearParams& p, cudaStream_t st) {
-  using C = SplitCfg<AMN, BMN, BN>;
-  auto kern = linear_split_kernel<AMN, BMN, BN, FWD>;
-  static bool allowed[64] = {};
-  const cudaError_t err = allow_smem(kern, C::kSmemBytes, allowed);
-  if (err != cudaSuccess) return err;
+template <class K>
+cudaError_t launch_clusters(K kern, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, const LinearMaps& maps,
+                            const LinearParams& p) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.L + 127) / 128 * p.split), static_cast<unsigned>((p.C + BN - 1) / BN));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
 __device__ int g_linear_status;   // first error since the last read
 
+// The largest split of K, in powers of two, whose clusters are all resident
+// and whose CTAs each have at least four K-blocks.
+template <bool AMN, bool BMN, int BN, bool FWD>
+cudaError_t launch_split(const LinearMaps& maps, LinearParams& p, cudaStream_t st) {
+  using C = SplitCfg<AMN, BMN, BN>;
+  auto kern = linear_split_kernel<AMN, BMN, BN, FWD>;
+  static KernelInfo info;
+  const long long lt = (p.L + 127) / 128, ct = (static_cast<long long>(p.C) + BN - 1) / BN;
+  p.split = 1;
+  int n = 0;
+  cudaError_t err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 1, &n);
+  for (int s = 2; err == cudaSuccess && s <= 8 && p.nk / s >= 4; s *= 2) {
+    err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, s, &n);
+    if (lt * ct > n) break;
+    p.split = s;
+  }
+  if (err != cudaSuccess) return err;
+  return launch_clusters(kern, dim3(static_cast<unsigned>(lt * p.split), static_cast<unsigned>(ct)), C::kThreads, C::kSmemBytes,
+                         p.split, st, maps, p);
+}
+
+// The largest number of pairs along K, likewise.
 template <bool AMN, bool BMN, bool FWD>
-cudaError_t launch_pair(const LinearMaps& maps, const LinearParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_pair_split(const LinearMaps& maps, LinearParams& p, cudaStream_t st) {
+  using C = PairSplitCfg<AMN, BMN>;
+  auto kern = linear_pair_split_kernel<AMN, BMN, FWD>;
+  static KernelInfo info;
+  p.split = 1;
+  int n = 0;
+  cudaError_t err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2, &n);
+  for (int s = 2; err == cudaSuccess && s <= 4 && p.nk / s >= 4; ++s) {
+    err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2 * s, &n);
+    if (p.l_tiles * p.c_tiles > n) break;
+    p.split = s;
+  }
+  if (err != cudaSuccess) return err;
+  return launch_clusters(kern, dim3(static_cast<unsigned>(2 * p.split * p.l_tiles * p.c_tiles)), C::kThreads, C::kSmemBytes,
+                         2 * p.split, st, maps, p);
+}
+
+template <bool AMN, bool BMN, bool FWD>
+cudaError_t launch_pair(const LinearMaps& maps, const LinearParams& p, cudaStream_t st) {
   using C = PairCfg<AMN, BMN>;
   auto kern = linear_pair_kernel<AMN, BMN, FWD>;
-  static int resident[64] = {};   // CTA pairs that are resident at once, looked up once per device
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  static KernelInfo info;
+  int n = 0;
+  const cudaError_t err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2, &n);
   if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;   // the occupancy query takes the cluster shape only
-  if (resident[dev] == 0) {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-    if (err != cudaSuccess) return err;
-    cfg.gridDim = dim3(2 * (num_sms / 2));
-    int n = 0;
-    err = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-    if (err != cudaSuccess) return err;
-    if (n <= 0) return cudaErrorInvalidConfiguration;
-    resident[dev] = n;
-  }
-  const int items = p.l_tiles * p.c_tiles, pairs = items < resident[dev] ? items : resident[dev];
-  cfg.gridDim = dim3(2 * pairs);
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+  const int items = p.l_tiles * p.c_tiles, pairs = items < n ? items : n;
+  return launch_clusters(kern, dim3(2 * pairs), C::kThreads, C::kSmemBytes, 2, st, maps, p);
 }
 
 template <bool AMN, bool BMN, bool FWD>
@@ -117,7 +153,8 @@ mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sm
   p.nk = static_cast<int>((o.K + kLinBK - 1) / kLinBK);
   LinearMaps maps;
   const long long lt = (p.L + 255) / 256, ct = (static_cast<long long>(p.C) + 255) / 256;
-  const bool pair = lt * ct >= num_sms / 2;
+  const int pairs = num_sms / 2;
+  const bool pair = lt * ct >= pairs || (p.L > 128 && p.C > 128);
   int bn = 128;
   if (!pair) {
     if (!BMN && p.C <= 16) bn = 16;
@@ -132,17 +169,17 @@ mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sm
     if (lt * ct > 0x7fffffffll) return fail(MOK_ERR_INVALID_ARG, "product too large");
     p.l_tiles = static_cast<int>(lt);
     p.c_tiles = static_cast<int>(ct);
+    if (lt * ct < pairs) {
+      MOK_CUDA((launch_pair_split<AMN, BMN, FWD>(maps, p, st)));
+      return MOK_OK;
+    }
     p.group = 8;
     s = make_box(&maps.out, p.out, p.out_f32, p.L, p.C, 32, 32);
     if (!s && p.z) s = make_box(&maps.z, p.z, 0, p.L, p.C, 32, 32);
     if (s) return s;
-    MOK_CUDA((launch_pair<AMN, BMN, FWD>(maps, p, num_sms, st)));
+    MOK_CUDA((launch_pair<AMN, BMN, FWD>(maps, p, st)));
     return MOK_OK;
   }
-  const long long tiles = (p.L + 127) / 128 * ((p.C + bn - 1) / bn);
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * num_sms && p.nk / (split * 2) >= 4) split *= 2;
-  p.split = split;
   cudaError_t err = cudaSuccess;
   if (bn == 128) {
     err = launch_split<AMN, BMN, 128, FWD>(maps, p, st);

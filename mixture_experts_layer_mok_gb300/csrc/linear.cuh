@@ -10,16 +10,21 @@
 // Sums are fp32 in TMEM; every edge (l, c and k) is cut by the tensor maps,
 // whose loads read zeros outside and whose stores write nothing there.
 //
-// Two kernels.
+// Three kernels.
 //   linear_pair_kernel: persistent CTA pairs (M = 256 rows c over two SMs, 256
 //   columns l, two accumulator buffers), for products with enough 256 x 256
 //   tiles to fill the GPU.  Each thread of the epilogue holds 32 neighbouring
 //   elements of an output row, which leave through TMA stores.
+//   linear_pair_split_kernel: the same tile with K split over 1 to 4 pairs of a
+//   cluster, which add their parts through distributed shared memory in rank
+//   order, for products of fewer such tiles.  An SM takes in about 64 bytes a
+//   clock from L2, which bounds these: a pair loads 32 KB per CTA for 128 x
+//   256 outputs, half of what two 128 x 128 tiles would.
 //   linear_split_kernel: one 128 x BN tile per CTA, K split over a cluster of
-//   up to 8 CTAs that add their parts through distributed shared memory in
-//   rank order, for everything smaller, where the bytes of A have to come in
-//   through as many SMs as there are.  Here l runs over the tensor core's M,
-//   so that a handful of tokens costs an N of 16 rather than a padded M.
+//   up to 8 CTAs joined in the same way, where one side of the output is at
+//   most 128 wide.  Here l runs over the tensor core's M, so that a handful of
+//   tokens costs an N of 16 rather than a padded M, and the bytes of A come in
+//   through as many SMs as there are.
 #pragma once
 
 #include <cuda.h>
@@ -139,30 +144,19 @@ __device__ __forceinline__ void load_vals(const void* base, int f32, long long a
 
 // Four output elements at index `at`: z = acc + bias, y = act(z) + residual.
 template <int ACT>
-__device__ __forceinline__ void store_four_act(const LinearParams& p, long long at, const float* bias, const float* acc) {
-  float z[4], y[4], r[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.residual) load_vals<4>(p.residual, p.residual_f32, at, r);
+__device__ __forceinline__ void store_four(const LinearParams& p, long long at, const float* bias, const float* acc,
+                                           const float* res) {
+  float z[4], y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     z[i] = acc[i] + bias[i];
-    y[i] = act_value<ACT>(z[i]) + r[i];
+    y[i] = act_value<ACT>(z[i]) + res[i];
   }
   if (p.z) *reinterpret_cast<uint2*>(p.z + at) = make_uint2(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]));
   if (p.out_f32)
     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-}
-
-template <bool FWD>
-__device__ __forceinline__ void store_four(const LinearParams& p, long long at, const float* bias, const float* acc) {
-  switch (FWD ? p.act : LIN_NONE) {
-    case LIN_RELU: store_four_act<LIN_RELU>(p, at, bias, acc); break;
-    case LIN_SILU: store_four_act<LIN_SILU>(p, at, bias, acc); break;
-    case LIN_GELU: store_four_act<LIN_GELU>(p, at, bias, acc); break;
-    case LIN_GELU_TANH: store_four_act<LIN_GELU_TANH>(p, at, bias, acc); break;
-    default: store_four_act<LIN_NONE>(p, at, bias, acc); break;
-  }
 }
 
 // Descriptor of an operand block at shared address s (K-major rows of 128
@@ -213,8 +207,56 @@ struct SplitCfg {
 
 __device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr) {
   float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
+}
+
+// The join of a tile whose parts [BN][128] lie at `part` in the shared memory
+// of S CTAs: this CTA's share of the columns, summed in rank order, four
+// elements of a row per thread.  Several columns at a time, their residuals
+// and all ranks' parts in flight together: one at a time each would cost the
+// latency of a global and of a remote load.
+template <bool FWD, int ACT, int S, int BN>
+__device__ __forceinline__ void join_columns(const LinearParams& p, const float* part, int rank, long long l0, int c0, int warp,
+                                             int lane) {
+  constexpr int kShare = BN / S, kWarps = 6, kAtOnce = S == 8 ? 2 : 4;
+  const long long l = l0 + lane * 4;
+  if (l >= p.L) return;
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if (FWD && p.bias) load_vals<4>(p.bias, p.bias_f32, l, bias);
+  uint32_t peer[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) peer[s] = S > 1 ? cluster_addr(part, s) : smem_u32(part);
+  const int c_end = min((rank + 1) * kShare, p.C - c0);
+  for (int c = rank * kShare + warp; c < c_end; c += kWarps * kAtOnce) {
+    float r[kAtOnce][4] = {}, v[kAtOnce][4] = {};
+    float4 t[kAtOnce][S];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int cu = min(c + kWarps * u, c_end - 1);   // past the end: the last column again, not stored
+      if (FWD && p.residual) load_vals<4>(p.residual, p.residual_f32, static_cast<long long>(c0 + cu) * p.L + l, r[u]);
+#pragma unroll
+      for (int s = 0; s < S; ++s) t[u][s] = ld_shared_cluster4(peer[s] + static_cast<uint32_t>(cu * 128 + lane * 4) * 4u);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) v[u][0] += t[u][s].x, v[u][1] += t[u][s].y, v[u][2] += t[u][s].z, v[u][3] += t[u][s].w;
+      const int cu = c + kWarps * u;
+      if (cu < c_end) store_four<ACT>(p, static_cast<long long>(c0 + cu) * p.L + l, bias, v[u], r[u]);
+    }
+  }
+}
+
+template <bool FWD, int ACT, int BN>
+__device__ __forceinline__ void join_split(const LinearParams& p, const float* part, int rank, long long l0, int c0, int warp,
+                                           int lane) {
+  switch (p.split) {
+    case 1: join_columns<FWD, ACT, 1, BN>(p, part, rank, l0, c0, warp, lane); break;
+    case 2: join_columns<FWD, ACT, 2, BN>(p, part, rank, l0, c0, warp, lane); break;
+    case 4: join_columns<FWD, ACT, 4, BN>(p, part, rank, l0, c0, warp, lane); break;
+    default: join_columns<FWD, ACT, 8, BN>(p, part, rank, l0, c0, warp, lane); break;
+  }
 }
 
 // grid {S * L tiles, C tiles}, clusters of S CTAs along K.
@@ -264,19 +306,19 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
   griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0, fills = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
+    int stage = 0, fills = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      uint8_t* sA = smem + stage * C::kStageBytes;
+      uint8_t* sB = sA + kLinABytes;
+      const int k0 = kb * kLinBK;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
-        uint8_t* sA = smem + stage * C::kStageBytes;
-        uint8_t* sB = sA + kLinABytes;
-        const int k0 = kb * kLinBK;
         if (AMN) {
           tma_load_2d(sA, &maps.a, &full[stage], static_cast<int>(l0), k0);
           tma_load_2d(sA + kLinChunk, &maps.a, &full[stage], static_cast<int>(l0) + 64, k0);
@@ -289,37 +331,37 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
         } else {
           tma_load_2d(sB, &maps.b, &full[stage], k0, c0);
         }
-        ++fills;
-        if (++stage == C::kStages) stage = 0, phase ^= 1;
       }
-      if (!ok) {   // no load may be in flight when the CTA ends
-        const int n = min(fills, C::kStages);
-        for (int i = 0; i < n; ++i) {
-          if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
-          mbar_drain(&full[stage], phase);
-        }
+      __syncwarp();
+      ++fills;
+      if (++stage == C::kStages) stage = 0, phase ^= 1;
+    }
+    if (!ok && lane == 0) {   // no load may be in flight when the CTA ends
+      const int n = min(fills, C::kStages);
+      for (int i = 0; i < n; ++i) {
+        if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
+        mbar_drain(&full[stage], phase);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint64_t ad = linear_desc<AMN>(smem_u32(smem)), bd = linear_desc<BMN>(smem_u32(smem) + kLinABytes);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        const uint32_t at = stage * C::kStageBytes, acc = tmem_base + (kb >= kbm ? BN : 0);
+    const uint64_t ad = linear_desc<AMN>(smem_u32(smem)), bd = linear_desc<BMN>(smem_u32(smem) + kLinABytes);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_wait(&full[stage], phase, abort_flag, p.status)) break;
+      const uint32_t at = stage * C::kStageBytes, acc = tmem_base + (kb >= kbm ? BN : 0);
+      if (elect_one()) {
         umma_bf16(acc, desc_at(ad, at), desc_at(bd, at), C::kIdesc, kb != kb0 && kb != kbm);
 #pragma unroll
         for (int kk = 1; kk < kLinBK / 16; ++kk)
           umma_bf16(acc, desc_at(ad, at + kk * kStep<AMN>), desc_at(bd, at + kk * kStep<BMN>), C::kIdesc, 1u);
         umma_commit(&empty[stage]);
-        if (++stage == C::kStages) stage = 0, phase ^= 1;
+        if (kb == kb1 - 1) umma_commit(tfull);
       }
-      if (ok) umma_commit(tfull);
+      __syncwarp();
+      if (++stage == C::kStages) stage = 0, phase ^= 1;
+    }
+    if (elect_one()) {
       umma_commit(done);   // every MMA issued here ends before TMEM is released
       mbar_drain(done, 0);
     }
@@ -328,6 +370,13 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
   float* part = reinterpret_cast<float*>(smem);   // [BN][128], over the stages
   if (warp >= 2) {
     const int q = warp & 3, row = q * 32 + lane;
+    if (FWD && p.residual) {   // this CTA's share of it into L2 while the accumulator fills
+      const int size = p.residual_f32 ? 4 : 2, c1 = min((rank + 1) * (BN / S), p.C - c0);
+      const long long cols = p.L - l0 < 128 ? p.L - l0 : 128;
+      for (int c = rank * (BN / S) + q; c < c1; c += 4)
+        if (lane * 128 < cols * size)
+          prefetch_l2(static_cast<const char*>(p.residual) + (static_cast<long long>(c0 + c) * p.L + l0) * size + lane * 128);
+    }
     const int w = (lane == 0) ? (mbar_wait(tfull, 0, abort_flag, p.status) ? 1 : 0) : 0;
     if (__shfl_sync(0xffffffffu, w, 0)) {
       tc_fence_after();
@@ -354,38 +403,12 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
     cluster_sync();
   else
     __syncthreads();
-  {
-    const int nc = BN / S, c_end = (rank + 1) * nc;
-    const long long l = l0 + lane * 4;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (l < p.L) {
-      if (FWD && p.bias) load_vals<4>(p.bias, p.bias_f32, l, bias);
-      uint32_t peer[8];
-#pragma unroll
-      for (int s = 0; s < 8; ++s) peer[s] = S > 1 && s < S ? cluster_addr(part, s) : smem_u32(part);
-      constexpr int kAtOnce = 4;
-      for (int c = rank * nc + warp; c < c_end; c += 6 * kAtOnce) {
-        float v[kAtOnce][4] = {};
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {   // in rank order
-          if (s < S) {
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-              const int cu = c + 6 * u;
-              if (cu < c_end) {
-                const float4 t = ld_shared_cluster4(peer[s] + static_cast<uint32_t>(cu * 128 + lane * 4) * 4u);
-                v[u][0] += t.x, v[u][1] += t.y, v[u][2] += t.z, v[u][3] += t.w;
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const int cu = c + 6 * u;
-          if (cu < c_end && c0 + cu < p.C) store_four<FWD>(p, static_cast<long long>(c0 + cu) * p.L + l, bias, v[u]);
-        }
-      }
-    }
+  switch (FWD ? p.act : LIN_NONE) {
+    case LIN_RELU: join_split<FWD, FWD ? LIN_RELU : LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
+    case LIN_SILU: join_split<FWD, FWD ? LIN_SILU : LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
+    case LIN_GELU: join_split<FWD, FWD ? LIN_GELU : LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
+    case LIN_GELU_TANH: join_split<FWD, FWD ? LIN_GELU_TANH : LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
+    default: join_split<FWD, LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
   }
   __syncwarp();
   if (S > 1) cluster_sync();   // nobody reads this CTA's shared memory any more
@@ -535,6 +558,230 @@ __device__ __forceinline__ void forward_block(const LinearParams& p, const Linea
   output_block<true, ACT, true>(p, maps, t, l, c, row0, stage, buf, lane, false);
 }
 
+// ---------------------------------------------------------------- pair split kernel
+template <bool AMN, bool BMN>
+struct PairSplitCfg {
+  static constexpr int kStageBytes = PairCfg<AMN, BMN>::kStageBytes;
+  static constexpr int kStages = 6;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256;
+  static constexpr int kThreads = 320;   // producer, MMA issuer, 8 epilogue warps; all ten join
+  static constexpr uint32_t kIdesc = PairCfg<AMN, BMN>::kIdesc;
+  static_assert(128 * 256 * 4 <= kStages * kStageBytes, "the partial tile fits the stages");
+};
+
+// Where float4 column c4 of row r of a part [128][256] lies (in units of 16
+// bytes): neighbouring rows' same column falls into different banks.
+__device__ __forceinline__ int part_at(int r, int c4) { return r * 64 + (c4 ^ (r & 7)); }
+
+// The join of a pair tile: this CTA's share of its 128 rows, from the S CTAs
+// that hold parts of the same rows, in rank order.
+template <bool FWD, int ACT, int S>
+__device__ __forceinline__ void join_rows(const LinearParams& p, const float* part, int rank, long long l0, int c0, int warp,
+                                          int lane) {
+  constexpr int kWarps = 10, kAtOnce = 2;
+  const int share = rank >> 1, r_end = min(128 * (share + 1) / S, p.C - c0);
+  uint32_t peer[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) peer[s] = cluster_addr(part, 2 * s + (rank & 1));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const long long l = l0 + h * 128 + lane * 4;
+    if (l >= p.L) continue;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (FWD && p.bias) load_vals<4>(p.bias, p.bias_f32, l, bias);
+    for (int r = 128 * share / S + warp; r < r_end; r += kWarps * kAtOnce) {
+      float res[kAtOnce][4] = {}, v[kAtOnce][4] = {};
+      float4 t[kAtOnce][S];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int ru = min(r + kWarps * u, r_end - 1);   // past the end: the last row again, not stored
+        if (FWD && p.residual) load_vals<4>(p.residual, p.residual_f32, static_cast<long long>(c0 + ru) * p.L + l, res[u]);
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+          t[u][s] = ld_shared_cluster4(peer[s] + static_cast<uint32_t>(part_at(ru, h * 32 + lane)) * 16u);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) v[u][0] += t[u][s].x, v[u][1] += t[u][s].y, v[u][2] += t[u][s].z, v[u][3] += t[u][s].w;
+        const int ru = r + kWarps * u;
+        if (ru < r_end) store_four<ACT>(p, static_cast<long long>(c0 + ru) * p.L + l, bias, v[u], res[u]);
+      }
+    }
+  }
+}
+
+template <bool FWD, int ACT>
+__device__ __forceinline__ void join_pairs(const LinearParams& p, const float* part, int rank, long long l0, int c0, int warp,
+                                           int lane) {
+  switch (p.split) {
+    case 1: join_rows<FWD, ACT, 1>(p, part, rank, l0, c0, warp, lane); break;
+    case 2: join_rows<FWD, ACT, 2>(p, part, rank, l0, c0, warp, lane); break;
+    case 3: join_rows<FWD, ACT, 3>(p, part, rank, l0, c0, warp, lane); break;
+    default: join_rows<FWD, ACT, 4>(p, part, rank, l0, c0, warp, lane); break;
+  }
+}
+
+// grid {2 S x tiles}, clusters of S pairs along K.
+template <bool AMN, bool BMN, bool FWD>
+__global__ void __launch_bounds__(320, 1) linear_pair_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
+  using C = PairSplitCfg<AMN, BMN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;
+  uint64_t* done = tfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.split, rank = static_cast<int>(cluster_rank()), lead = rank & ~1;
+  const int tile = blockIdx.x / (2 * S), lt = tile % p.l_tiles, ct = tile / p.l_tiles;
+  const long long l0 = static_cast<long long>(lt) * 256;
+  const int c0 = ct * 256 + (rank & 1) * 128;   // this CTA's rows
+  const int kb0 = static_cast<int>(static_cast<long long>(p.nk) * (rank >> 1) / S);
+  const int kb1 = static_cast<int>(static_cast<long long>(p.nk) * ((rank >> 1) + 1) / S);
+  // fp32 outputs: the K range in two accumulators (see linear_split_kernel)
+  const bool two = FWD && p.out_f32 && kb1 - kb0 > 1;
+  const int kbm = two ? (kb0 + kb1) / 2 : kb1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();   // all barriers are there before any signal crosses
+  tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t tmem_base = *tmem_slot;
+  if (warp == 0) {
+    int stage = 0, fills = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t lead_full = cluster_addr(full, lead);
+    const int la = static_cast<int>(l0) + (rank & 1) * 128;   // this CTA's half of the columns' operand
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      uint8_t* sB = smem + stage * C::kStageBytes;
+      uint8_t* sA = sB + kLinABytes;
+      const uint32_t bar = lead_full + stage * 8;
+      const int k0 = kb * kLinBK;
+      if (elect_one()) {
+        if (rank == lead) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
+        if (AMN) {
+          tma_load_2d_pair(sA, &maps.a, bar, la, k0);
+          tma_load_2d_pair(sA + kLinChunk, &maps.a, bar, la + 64, k0);
+        } else {
+          tma_load_2d_pair(sA, &maps.a, bar, k0, la);
+        }
+        if (BMN) {
+          tma_load_2d_pair(sB, &maps.b, bar, c0, k0);
+          tma_load_2d_pair(sB + kLinChunk, &maps.b, bar, c0 + 64, k0);
+        } else {
+          tma_load_2d_pair(sB, &maps.b, bar, k0, c0);
+        }
+      }
+      __syncwarp();
+      ++fills;
+      if (++stage == C::kStages) stage = 0, phase ^= 1;
+    }
+    if (!ok && rank == lead && lane == 0) {   // no load may be in flight when the CTA ends
+      const int n = min(fills, C::kStages);
+      for (int i = 0; i < n; ++i) {
+        if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
+        mbar_drain(&full[stage], phase);
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == lead) {
+      const uint64_t bd = linear_desc<BMN>(smem_u32(smem)), ad = linear_desc<AMN>(smem_u32(smem) + kLinABytes);
+      const uint16_t both = static_cast<uint16_t>(3u << lead), me = static_cast<uint16_t>(1u << lead);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait(&full[stage], phase, abort_flag, p.status)) break;
+        const uint32_t at = stage * C::kStageBytes, acc = tmem_base + (kb >= kbm ? 256 : 0);
+        if (elect_one()) {
+          umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), C::kIdesc, kb != kb0 && kb != kbm);
+#pragma unroll
+          for (int kk = 1; kk < kLinBK / 16; ++kk)
+            umma_bf16_pair(acc, desc_at(bd, at + kk * kStep<BMN>), desc_at(ad, at + kk * kStep<AMN>), C::kIdesc, 1u);
+          umma_commit_pair(&empty[stage], both);
+          if (kb == kb1 - 1) umma_commit_pair(tfull, both);
+        }
+        __syncwarp();
+        if (++stage == C::kStages) stage = 0, phase ^= 1;
+      }
+      if (elect_one()) {
+        umma_commit_pair(done, me);
+        mbar_drain(done, 0);
+      }
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2, row = q * 32 + lane;
+    if (FWD && p.residual) {   // this CTA's share of it into L2 while the accumulator fills
+      const int size = p.residual_f32 ? 4 : 2, r1 = min(128 * ((rank >> 1) + 1) / S, p.C - c0);
+      const long long cols = p.L - l0 < 256 ? p.L - l0 : 256;
+      for (int r = 128 * (rank >> 1) / S + warp - 2; r < r1; r += 8)
+        for (long long o = lane * 128; o < cols * size; o += 32 * 128)
+          prefetch_l2(static_cast<const char*>(p.residual) + (static_cast<long long>(c0 + r) * p.L + l0) * size + o);
+    }
+    const int w = (lane == 0) ? (mbar_wait(tfull, 0, abort_flag, p.status) ? 1 : 0) : 0;
+    if (__shfl_sync(0xffffffffu, w, 0)) {
+      tc_fence_after();
+      const uint32_t tb = tmem_base + half * 128 + (static_cast<uint32_t>(q * 32) << 16);
+      float4* part = reinterpret_cast<float4*>(smem);
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 16) {
+        float v[16];
+        tmem_ld16(tb + c, v);
+        if (two) {
+          float u[16];
+          tmem_ld16(tb + 256 + c, u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += u[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          part[part_at(row, half * 32 + c / 4 + i)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync();   // every CTA's part is in its shared memory
+  const float* part = reinterpret_cast<const float*>(smem);
+  switch (FWD ? p.act : LIN_NONE) {
+    case LIN_RELU: join_pairs<FWD, FWD ? LIN_RELU : LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
+    case LIN_SILU: join_pairs<FWD, FWD ? LIN_SILU : LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
+    case LIN_GELU: join_pairs<FWD, FWD ? LIN_GELU : LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
+    case LIN_GELU_TANH: join_pairs<FWD, FWD ? LIN_GELU_TANH : LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
+    default: join_pairs<FWD, LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
+  }
+  __syncwarp();
+  cluster_sync();   // nobody reads this CTA's shared memory or writes its TMEM any more
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------- persistent pair kernel
 template <bool AMN, bool BMN, bool FWD>
 __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
   using C = PairCfg<AMN, BMN>;
