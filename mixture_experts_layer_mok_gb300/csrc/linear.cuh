@@ -199,7 +199,8 @@ struct SplitCfg {
   static constexpr int kStages = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256;
   static constexpr int kTmemCols = 2 * BN;   // two accumulators, for fp32 outputs
-  static constexpr int kThreads = 192;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr uint32_t kIdesc = idesc_bf16(128, BN, AMN, BMN);
   static_assert(BN * 128 * 4 <= kStages * kStageBytes, "the partial tile fits the stages");
   static_assert(!BMN || BN % 64 == 0, "MN-major B comes in 64-wide chunks");
@@ -216,10 +217,31 @@ __device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr) {
 // elements of a row per thread.  Several columns at a time, their residuals
 // and all ranks' parts in flight together: one at a time each would cost the
 // latency of a global and of a remote load.
+// 8 consecutive fp32 columns of this thread's TMEM lane, waited on.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// float4 at byte `off` of rank s's part: this CTA's own through plain shared
+// loads, which are several times as fast as through the cluster's window.
+template <int S>
+__device__ __forceinline__ float4 part_of(const float* mine, const uint32_t* peer, int s, int me, uint32_t off) {
+  if (S == 1 || s == me) return *reinterpret_cast<const float4*>(reinterpret_cast<const char*>(mine) + off);
+  return ld_shared_cluster4(peer[s] + off);
+}
+
 template <bool FWD, int ACT, int S, int BN>
 __device__ __forceinline__ void join_columns(const LinearParams& p, const float* part, int rank, long long l0, int c0, int warp,
                                              int lane) {
-  constexpr int kShare = BN / S, kWarps = 6, kAtOnce = S == 8 ? 2 : 4;
+  constexpr int kShare = BN / S, kWarps = 8, kAtOnce = S == 8 ? 2 : 4;
   const long long l = l0 + lane * 4;
   if (l >= p.L) return;
   float bias[4] = {0.f, 0.f, 0.f, 0.f};
@@ -236,7 +258,7 @@ __device__ __forceinline__ void join_columns(const LinearParams& p, const float*
       const int cu = min(c + kWarps * u, c_end - 1);   // past the end: the last column again, not stored
       if (FWD && p.residual) load_vals<4>(p.residual, p.residual_f32, static_cast<long long>(c0 + cu) * p.L + l, r[u]);
 #pragma unroll
-      for (int s = 0; s < S; ++s) t[u][s] = ld_shared_cluster4(peer[s] + static_cast<uint32_t>(cu * 128 + lane * 4) * 4u);
+      for (int s = 0; s < S; ++s) t[u][s] = part_of<S>(part, peer, s, rank, static_cast<uint32_t>(cu * 128 + lane * 4) * 4u);
     }
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
@@ -260,9 +282,10 @@ __device__ __forceinline__ void join_split(const LinearParams& p, const float* p
 }
 
 // grid {S * L tiles, C tiles}, clusters of S CTAs along K.
-// warp 0: TMA producer; warp 1: MMA issuer, TMEM owner; warps 2..5: epilogue.
+// warp 0: TMA producer; warp 1: MMA issuer, TMEM owner; the others: epilogue, two
+// warps for each quarter of the TMEM lanes.
 template <bool AMN, bool BMN, int BN, bool FWD>
-__global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
+__global__ void __launch_bounds__(SplitCfg<AMN, BMN, BN>::kThreads, 2) linear_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
   using C = SplitCfg<AMN, BMN, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -369,11 +392,11 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
   __syncwarp();
   float* part = reinterpret_cast<float*>(smem);   // [BN][128], over the stages
   if (warp >= 2) {
-    const int q = warp & 3, row = q * 32 + lane;
+    const int q = warp & 3, row = q * 32 + lane, col0 = ((warp - 2) >> 2) * (BN / 2);
     if (FWD && p.residual) {   // this CTA's share of it into L2 while the accumulator fills
       const int size = p.residual_f32 ? 4 : 2, c1 = min((rank + 1) * (BN / S), p.C - c0);
       const long long cols = p.L - l0 < 128 ? p.L - l0 : 128;
-      for (int c = rank * (BN / S) + q; c < c1; c += 4)
+      for (int c = rank * (BN / S) + warp - 2; c < c1; c += C::kEpiWarps)
         if (lane * 128 < cols * size)
           prefetch_l2(static_cast<const char*>(p.residual) + (static_cast<long long>(c0 + c) * p.L + l0) * size + lane * 128);
     }
@@ -382,19 +405,20 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 16) {
-        float v[16];
-        tmem_ld16(tb + c, v);
+      for (int c = col0; c < col0 + BN / 2; c += 8) {
+        float v[8];
+        tmem_ld8(tb + c, v);
         if (two) {
-          float u[16];
-          tmem_ld16(tb + BN + c, u);
+          float u[8];
+          tmem_ld8(tb + BN + c, u);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += u[i];
+          for (int i = 0; i < 8; ++i) v[i] += u[i];
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * 128 + row] = v[i];
+        for (int i = 0; i < 8; ++i) part[(c + i) * 128 + row] = v[i];
       }
     }
+    tc_fence_before();
   }
   __syncwarp();
   // every CTA's part is in its shared memory; each now finishes its share of
@@ -403,12 +427,12 @@ __global__ void __launch_bounds__(192, 2) linear_split_kernel(const __grid_const
     cluster_sync();
   else
     __syncthreads();
-  switch (FWD ? p.act : LIN_NONE) {
-    case LIN_RELU: join_split<FWD, FWD ? LIN_RELU : LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
-    case LIN_SILU: join_split<FWD, FWD ? LIN_SILU : LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
-    case LIN_GELU: join_split<FWD, FWD ? LIN_GELU : LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
-    case LIN_GELU_TANH: join_split<FWD, FWD ? LIN_GELU_TANH : LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
-    default: join_split<FWD, LIN_NONE, BN>(p, part, rank, l0, c0, warp, lane); break;
+  if (warp >= 2) switch (FWD ? p.act : LIN_NONE) {
+    case LIN_RELU: join_split<FWD, FWD ? LIN_RELU : LIN_NONE, BN>(p, part, rank, l0, c0, warp - 2, lane); break;
+    case LIN_SILU: join_split<FWD, FWD ? LIN_SILU : LIN_NONE, BN>(p, part, rank, l0, c0, warp - 2, lane); break;
+    case LIN_GELU: join_split<FWD, FWD ? LIN_GELU : LIN_NONE, BN>(p, part, rank, l0, c0, warp - 2, lane); break;
+    case LIN_GELU_TANH: join_split<FWD, FWD ? LIN_GELU_TANH : LIN_NONE, BN>(p, part, rank, l0, c0, warp - 2, lane); break;
+    default: join_split<FWD, LIN_NONE, BN>(p, part, rank, l0, c0, warp - 2, lane); break;
   }
   __syncwarp();
   if (S > 1) cluster_sync();   // nobody reads this CTA's shared memory any more
@@ -564,7 +588,9 @@ struct PairSplitCfg {
   static constexpr int kStageBytes = PairCfg<AMN, BMN>::kStageBytes;
   static constexpr int kStages = 6;
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256;
-  static constexpr int kThreads = 320;   // producer, MMA issuer, 8 epilogue warps; all ten join
+  // the epilogue and the join wait on latencies: 16 warps of them
+  static constexpr int kEpiWarps = 16;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr uint32_t kIdesc = PairCfg<AMN, BMN>::kIdesc;
   static_assert(128 * 256 * 4 <= kStages * kStageBytes, "the partial tile fits the stages");
 };
@@ -578,35 +604,34 @@ __device__ __forceinline__ int part_at(int r, int c4) { return r * 64 + (c4 ^ (r
 template <bool FWD, int ACT, int S>
 __device__ __forceinline__ void join_rows(const LinearParams& p, const float* part, int rank, long long l0, int c0, int warp,
                                           int lane) {
-  constexpr int kWarps = 10, kAtOnce = 2;
-  const int share = rank >> 1, r_end = min(128 * (share + 1) / S, p.C - c0);
+  constexpr int kWarps = 16, kAtOnce = S <= 2 ? 4 : 2;
+  const int share = rank >> 1, r0 = 128 * share / S, rows = min(128 * (share + 1) / S, p.C - c0) - r0;
   uint32_t peer[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) peer[s] = cluster_addr(part, 2 * s + (rank & 1));
+  // a warp's tasks: halves (128 columns) of rows, a fixed half for each warp
+  const int h = warp & 1;
+  const long long l = l0 + h * 128 + lane * 4;
+  if (l >= p.L) return;
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if (FWD && p.bias) load_vals<4>(p.bias, p.bias_f32, l, bias);
+  for (int r = warp >> 1; r < rows; r += kWarps / 2 * kAtOnce) {
+    float res[kAtOnce][4] = {}, v[kAtOnce][4] = {};
+    float4 t[kAtOnce][S];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const long long l = l0 + h * 128 + lane * 4;
-    if (l >= p.L) continue;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (FWD && p.bias) load_vals<4>(p.bias, p.bias_f32, l, bias);
-    for (int r = 128 * share / S + warp; r < r_end; r += kWarps * kAtOnce) {
-      float res[kAtOnce][4] = {}, v[kAtOnce][4] = {};
-      float4 t[kAtOnce][S];
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int ru = r0 + min(r + kWarps / 2 * u, rows - 1);   // past the end: the last row again, not stored
+      if (FWD && p.residual) load_vals<4>(p.residual, p.residual_f32, static_cast<long long>(c0 + ru) * p.L + l, res[u]);
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int ru = min(r + kWarps * u, r_end - 1);   // past the end: the last row again, not stored
-        if (FWD && p.residual) load_vals<4>(p.residual, p.residual_f32, static_cast<long long>(c0 + ru) * p.L + l, res[u]);
+      for (int s = 0; s < S; ++s)
+        t[u][s] = part_of<S>(part, peer, s, share, static_cast<uint32_t>(part_at(ru, h * 32 + lane)) * 16u);
+    }
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-          t[u][s] = ld_shared_cluster4(peer[s] + static_cast<uint32_t>(part_at(ru, h * 32 + lane)) * 16u);
-      }
+    for (int u = 0; u < kAtOnce; ++u) {
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) v[u][0] += t[u][s].x, v[u][1] += t[u][s].y, v[u][2] += t[u][s].z, v[u][3] += t[u][s].w;
-        const int ru = r + kWarps * u;
-        if (ru < r_end) store_four<ACT>(p, static_cast<long long>(c0 + ru) * p.L + l, bias, v[u], res[u]);
-      }
+      for (int s = 0; s < S; ++s) v[u][0] += t[u][s].x, v[u][1] += t[u][s].y, v[u][2] += t[u][s].z, v[u][3] += t[u][s].w;
+      const int ru = r + kWarps / 2 * u;
+      if (ru < rows) store_four<ACT>(p, static_cast<long long>(c0 + r0 + ru) * p.L + l, bias, v[u], res[u]);
     }
   }
 }
@@ -624,7 +649,7 @@ __device__ __forceinline__ void join_pairs(const LinearParams& p, const float* p
 
 // grid {2 S x tiles}, clusters of S pairs along K.
 template <bool AMN, bool BMN, bool FWD>
-__global__ void __launch_bounds__(320, 1) linear_pair_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
+__global__ void __launch_bounds__(PairSplitCfg<AMN, BMN>::kThreads, 1) linear_pair_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
   using C = PairSplitCfg<AMN, BMN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -733,21 +758,22 @@ __global__ void __launch_bounds__(320, 1) linear_pair_split_kernel(const __grid_
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2, row = q * 32 + lane;
+    constexpr int kCols = 256 * 4 / C::kEpiWarps;   // this warp's columns
+    const int q = warp & 3, col0 = ((warp - 2) >> 2) * kCols, row = q * 32 + lane;
     if (FWD && p.residual) {   // this CTA's share of it into L2 while the accumulator fills
       const int size = p.residual_f32 ? 4 : 2, r1 = min(128 * ((rank >> 1) + 1) / S, p.C - c0);
       const long long cols = p.L - l0 < 256 ? p.L - l0 : 256;
-      for (int r = 128 * (rank >> 1) / S + warp - 2; r < r1; r += 8)
+      for (int r = 128 * (rank >> 1) / S + warp - 2; r < r1; r += C::kEpiWarps)
         for (long long o = lane * 128; o < cols * size; o += 32 * 128)
           prefetch_l2(static_cast<const char*>(p.residual) + (static_cast<long long>(c0 + r) * p.L + l0) * size + o);
     }
     const int w = (lane == 0) ? (mbar_wait(tfull, 0, abort_flag, p.status) ? 1 : 0) : 0;
     if (__shfl_sync(0xffffffffu, w, 0)) {
       tc_fence_after();
-      const uint32_t tb = tmem_base + half * 128 + (static_cast<uint32_t>(q * 32) << 16);
+      const uint32_t tb = tmem_base + col0 + (static_cast<uint32_t>(q * 32) << 16);
       float4* part = reinterpret_cast<float4*>(smem);
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 16) {
+      for (int c = 0; c < kCols; c += 16) {
         float v[16];
         tmem_ld16(tb + c, v);
         if (two) {
@@ -758,7 +784,7 @@ __global__ void __launch_bounds__(320, 1) linear_pair_split_kernel(const __grid_
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          part[part_at(row, half * 32 + c / 4 + i)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          part[part_at(row, (col0 + c) / 4 + i)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       }
     }
     tc_fence_before();
@@ -766,12 +792,12 @@ __global__ void __launch_bounds__(320, 1) linear_pair_split_kernel(const __grid_
   __syncwarp();
   cluster_sync();   // every CTA's part is in its shared memory
   const float* part = reinterpret_cast<const float*>(smem);
-  switch (FWD ? p.act : LIN_NONE) {
-    case LIN_RELU: join_pairs<FWD, FWD ? LIN_RELU : LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
-    case LIN_SILU: join_pairs<FWD, FWD ? LIN_SILU : LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
-    case LIN_GELU: join_pairs<FWD, FWD ? LIN_GELU : LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
-    case LIN_GELU_TANH: join_pairs<FWD, FWD ? LIN_GELU_TANH : LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
-    default: join_pairs<FWD, LIN_NONE>(p, part, rank, l0, c0, warp, lane); break;
+  if (warp >= 2) switch (FWD ? p.act : LIN_NONE) {
+    case LIN_RELU: join_pairs<FWD, FWD ? LIN_RELU : LIN_NONE>(p, part, rank, l0, c0, warp - 2, lane); break;
+    case LIN_SILU: join_pairs<FWD, FWD ? LIN_SILU : LIN_NONE>(p, part, rank, l0, c0, warp - 2, lane); break;
+    case LIN_GELU: join_pairs<FWD, FWD ? LIN_GELU : LIN_NONE>(p, part, rank, l0, c0, warp - 2, lane); break;
+    case LIN_GELU_TANH: join_pairs<FWD, FWD ? LIN_GELU_TANH : LIN_NONE>(p, part, rank, l0, c0, warp - 2, lane); break;
+    default: join_pairs<FWD, LIN_NONE>(p, part, rank, l0, c0, warp - 2, lane); break;
   }
   __syncwarp();
   cluster_sync();   // nobody reads this CTA's shared memory or writes its TMEM any more
