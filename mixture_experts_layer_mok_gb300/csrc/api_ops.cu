@@ -202,22 +202,24 @@ mok_status_t mok_linear_bwd(const void* dy, int dy_dtype, const uint16_t* x, con
   float* part = d_bias ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dz_bytes(make_dz, M, N)) : nullptr;
   if (dz || part)
     MOK_CUDA(launch_linear_dz(dy, dy_dtype == MOK_DTYPE_F32, z, activation, M, N, dz, part, s));
-  if (d_bias) MOK_CUDA(launch_column_sum(part, dz_partials(M, N), N, d_bias, s));
   const uint16_t* g = make_dz ? dz : static_cast<const uint16_t*>(dy);
-  LinearParams p = {};
-  MOK_CUDA(linear_status_word(&p.status));
-  p.L = K;
-  if (d_weight) {
-    p.C = N;
-    p.out = d_weight;
-    st = run_linear(LIN_DW, {x, g, M}, p, sms, s);
-    if (st) return st;
-  }
-  if (dx) {
-    p.C = static_cast<int>(M);
-    p.out = dx;
-    st = run_linear(LIN_DX, {w, g, N}, p, sms, s);
-  }
+  LinearParams px = {};
+  MOK_CUDA(linear_status_word(&px.status));
+  px.L = K;
+  LinearParams pw = px;
+  px.C = static_cast<int>(M);
+  px.out = dx;
+  pw.C = N;
+  pw.out = d_weight;
+  const LinearOperands ox = {w, g, N}, ow = {x, g, M};
+  if (dx && d_weight)
+    st = run_linear_grads(ox, px, ow, pw, sms, s);
+  else if (d_weight)
+    st = run_linear(LIN_DW, ow, pw, sms, s);
+  else if (dx)
+    st = run_linear(LIN_DX, ox, px, sms, s);
+  // the bias's sums run in the products' last wave
+  if (!st && d_bias) MOK_CUDA(launch_column_sum(part, dz_partials(M, N), N, d_bias, dx || d_weight, s));
   return st;
 }
 

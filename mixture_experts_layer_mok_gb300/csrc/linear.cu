@@ -73,9 +73,8 @@ cudaError_t resident_clusters(K kern, KernelInfo& info, int threads, int smem, i
   return cudaSuccess;
 }
 
-template <class K>
-cudaError_t launch_clusters(K kern, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, const LinearMaps& maps,
-                            const LinearParams& p) {
+template <class K, class... A>
+cudaError_t launch_clusters(K kern, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, const A&... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -90,7 +89,7 @@ cudaError_t launch_clusters(K kern, dim3 grid, int threads, int smem, int cluste
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 __device__ int g_linear_status;   // first error since the last read
@@ -135,51 +134,71 @@ cudaError_t launch_pair_split(const LinearMaps& maps, LinearParams& p, cudaStrea
                          2 * p.split, st, maps, p);
 }
 
-template <bool AMN, bool BMN, bool FWD>
-cudaError_t launch_pair(const LinearMaps& maps, const LinearParams& p, cudaStream_t st) {
-  using C = PairCfg<AMN, BMN>;
-  auto kern = linear_pair_kernel<AMN, BMN, FWD>;
+template <int KIND>
+cudaError_t launch_pair(PairJob& job, cudaStream_t st) {
+  using C = PairCfg<KIND != LIN_FWD, false>;
+  auto kern = linear_pair_kernel<KIND>;
   static KernelInfo info;
   int n = 0;
   const cudaError_t err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2, &n);
   if (err != cudaSuccess) return err;
-  const int items = p.l_tiles * p.c_tiles, pairs = items < n ? items : n;
-  return launch_clusters(kern, dim3(2 * pairs), C::kThreads, C::kSmemBytes, 2, st, maps, p);
+  const long long n0 = static_cast<long long>(job.p[0].l_tiles) * job.p[0].c_tiles;
+  const long long n1 = job.problems > 1 ? static_cast<long long>(job.p[1].l_tiles) * job.p[1].c_tiles : 0;
+  const int pairs = n0 + n1 < n ? static_cast<int>(n0 + n1) : n;
+  job.extra = n1 > 0 && n0 % pairs ? (job.p[0].nk + job.p[1].nk / 2) / job.p[1].nk : 0;
+  return launch_clusters(kern, dim3(2 * pairs), C::kThreads, C::kSmemBytes, 2, st, job);
 }
 
-template <bool AMN, bool BMN, bool FWD>
-mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sms, cudaStream_t st) {
-  LinearParams p = q;
-  p.nk = static_cast<int>((o.K + kLinBK - 1) / kLinBK);
-  LinearMaps maps;
+// A product's operand and output maps for the pair kernels, and its tiles.
+mok_status_t pair_setup(bool a_mn, bool b_mn, const LinearOperands& o, LinearParams& p, LinearMaps* maps, bool store_maps) {
   const long long lt = (p.L + 255) / 256, ct = (static_cast<long long>(p.C) + 255) / 256;
+  if (lt * ct > 0x7fffffffll / 4) return fail(MOK_ERR_INVALID_ARG, "product too large");
+  p.nk = static_cast<int>((o.K + kLinBK - 1) / kLinBK);
+  p.l_tiles = static_cast<int>(lt);
+  p.c_tiles = static_cast<int>(ct);
+  p.group = 8;
+  mok_status_t s = a_mn ? operand_map(&maps->a, o.a, p.L, o.K, 64) : operand_map(&maps->a, o.a, o.K, p.L, 128);
+  if (!s) s = b_mn ? operand_map(&maps->b, o.b, p.C, o.K, 64) : operand_map(&maps->b, o.b, o.K, p.C, 128);
+  if (!s && store_maps) s = make_box(&maps->out, p.out, p.out_f32, p.L, p.C, 32, 32);
+  if (!s && store_maps && p.z) s = make_box(&maps->z, p.z, 0, p.L, p.C, 32, 32);
+  return s;
+}
+
+long long pair_tiles(const LinearParams& p) {
+  return (p.L + 255) / 256 * ((static_cast<long long>(p.C) + 255) / 256);
+}
+// Whether a product is for the pair kernels: both sides of its output wider
+// than one CTA's 128, or enough tiles to fill the GPU all the same.
+bool is_paired(const LinearParams& p, int pairs) { return (p.L > 128 && p.C > 128) || pair_tiles(p) >= pairs; }
+
+template <int KIND>
+mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sms, cudaStream_t st) {
+  constexpr bool FWD = KIND == LIN_FWD, AMN = KIND != LIN_FWD, BMN = KIND == LIN_DW;
+  LinearParams p = q;
   const int pairs = num_sms / 2;
-  const bool pair = lt * ct >= pairs || (p.L > 128 && p.C > 128);
-  int bn = 128;
-  if (!pair) {
-    if (!BMN && p.C <= 16) bn = 16;
-    else if (!BMN && p.C <= 32) bn = 32;
-    else if (p.C <= 64) bn = 64;
-  }
-  mok_status_t s = AMN ? operand_map(&maps.a, o.a, p.L, o.K, 64) : operand_map(&maps.a, o.a, o.K, p.L, 128);
-  if (s) return s;
-  s = BMN ? operand_map(&maps.b, o.b, p.C, o.K, 64) : operand_map(&maps.b, o.b, o.K, p.C, pair ? 128 : bn);
-  if (s) return s;
-  if (pair) {
-    if (lt * ct > 0x7fffffffll) return fail(MOK_ERR_INVALID_ARG, "product too large");
-    p.l_tiles = static_cast<int>(lt);
-    p.c_tiles = static_cast<int>(ct);
-    if (lt * ct < pairs) {
-      MOK_CUDA((launch_pair_split<AMN, BMN, FWD>(maps, p, st)));
-      return MOK_OK;
-    }
-    p.group = 8;
-    s = make_box(&maps.out, p.out, p.out_f32, p.L, p.C, 32, 32);
-    if (!s && p.z) s = make_box(&maps.z, p.z, 0, p.L, p.C, 32, 32);
+  if (is_paired(p, pairs)) {
+    const bool fills = pair_tiles(p) >= pairs;
+    PairJob job = {};
+    mok_status_t s = pair_setup(AMN, BMN, o, p, &job.maps[0], fills);
     if (s) return s;
-    MOK_CUDA((launch_pair<AMN, BMN, FWD>(maps, p, st)));
+    if (fills) {
+      job.p[0] = p;
+      job.problems = 1;
+      MOK_CUDA(launch_pair<KIND>(job, st));
+    } else {
+      MOK_CUDA((launch_pair_split<AMN, BMN, FWD>(job.maps[0], p, st)));
+    }
     return MOK_OK;
   }
+  int bn = 128;
+  if (!BMN && p.C <= 16) bn = 16;
+  else if (!BMN && p.C <= 32) bn = 32;
+  else if (p.C <= 64) bn = 64;
+  p.nk = static_cast<int>((o.K + kLinBK - 1) / kLinBK);
+  LinearMaps maps;
+  mok_status_t s = AMN ? operand_map(&maps.a, o.a, p.L, o.K, 64) : operand_map(&maps.a, o.a, o.K, p.L, 128);
+  if (!s) s = BMN ? operand_map(&maps.b, o.b, p.C, o.K, 64) : operand_map(&maps.b, o.b, o.K, p.C, bn);
+  if (s) return s;
   cudaError_t err = cudaSuccess;
   if (bn == 128) {
     err = launch_split<AMN, BMN, 128, FWD>(maps, p, st);
@@ -275,10 +294,30 @@ cudaError_t linear_status_word(int** word) {
 
 mok_status_t run_linear(LinKind kind, const LinearOperands& o, const LinearParams& p, int num_sms, cudaStream_t st) {
   switch (kind) {
-    case LIN_FWD: return run_kind<false, false, true>(o, p, num_sms, st);
-    case LIN_DX: return run_kind<true, false, false>(o, p, num_sms, st);
-    default: return run_kind<true, true, false>(o, p, num_sms, st);
+    case LIN_FWD: return run_kind<LIN_FWD>(o, p, num_sms, st);
+    case LIN_DX: return run_kind<LIN_DX>(o, p, num_sms, st);
+    default: return run_kind<LIN_DW>(o, p, num_sms, st);
   }
+}
+
+mok_status_t run_linear_grads(const LinearOperands& ox, const LinearParams& px, const LinearOperands& ow, const LinearParams& pw,
+                              int num_sms, cudaStream_t st) {
+  const int pairs = num_sms / 2;
+  if (!is_paired(px, pairs) || !is_paired(pw, pairs) || pair_tiles(px) + pair_tiles(pw) < pairs) {
+    const mok_status_t s = run_linear(LIN_DW, ow, pw, num_sms, st);
+    return s ? s : run_linear(LIN_DX, ox, px, num_sms, st);
+  }
+  PairJob job = {};
+  const int w = ow.K >= ox.K ? 0 : 1, x = 1 - w;   // the longer tiles first
+  job.p[w] = pw;
+  job.p[x] = px;
+  job.b_mn[w] = 1;
+  job.problems = 2;
+  mok_status_t s = pair_setup(true, true, ow, job.p[w], &job.maps[w], true);
+  if (!s) s = pair_setup(true, false, ox, job.p[x], &job.maps[x], true);
+  if (s) return s;
+  MOK_CUDA(launch_pair<LIN_GRADS>(job, st));
+  return MOK_OK;
 }
 
 int dz_partials(long long M, int N) {

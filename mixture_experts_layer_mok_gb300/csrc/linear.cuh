@@ -808,9 +808,45 @@ __global__ void __launch_bounds__(PairSplitCfg<AMN, BMN>::kThreads, 1) linear_pa
 }
 
 // ---------------------------------------------------------------- persistent pair kernel
-template <bool AMN, bool BMN, bool FWD>
-__global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
-  using C = PairCfg<AMN, BMN>;
+// The products of one launch: one, or the backward's two (the one with the
+// longer tiles first).
+struct PairJob {
+  LinearMaps maps[2];
+  LinearParams p[2];
+  int b_mn[2];    // the products' B is MN-major (LIN_GRADS)
+  int problems;
+  int extra;      // see pair_item
+};
+
+struct PairItem {
+  int w;       // the product
+  int lt, ct;  // its tile
+};
+
+// Work item s of pair `pair`.  The first product's n0 tiles go round the pairs
+// in turn, which leaves h = n0 % pairs of them a tile ahead.  Two products: the
+// other pairs first take `extra` tiles of the second, about as long as one of
+// the first, and what then remains goes round all pairs again, so that all end
+// together (two launches each end with pairs that stand still).
+__device__ __forceinline__ bool pair_item(const PairJob& job, int s, int pair, int pairs, PairItem& it) {
+  const int n0 = job.p[0].l_tiles * job.p[0].c_tiles;
+  int idx = pair + s * pairs;
+  it.w = 0;
+  if (idx >= n0) {
+    if (job.problems == 1) return false;
+    const int h = n0 % pairs, s2 = s - (n0 / pairs + (pair < h ? 1 : 0)), mine = pair < h ? 0 : job.extra;
+    idx = s2 < mine ? s2 * (pairs - h) + pair - h : job.extra * (pairs - h) + (s2 - mine) * pairs + pair;
+    if (idx >= job.p[1].l_tiles * job.p[1].c_tiles) return false;
+    it.w = 1;
+  }
+  linear_tile(job.p[it.w], idx, it.lt, it.ct);
+  return true;
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_constant__ PairJob job) {
+  constexpr bool AMN = KIND != LIN_FWD, FWD = KIND == LIN_FWD;
+  using C = PairCfg<AMN, false>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* out_stage = smem + C::kStages * C::kStageBytes;
@@ -823,8 +859,9 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  const int items = p.l_tiles * p.c_tiles;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  int* const status = job.p[0].status;
+  const auto b_is_mn = [&](int w) { return KIND == LIN_GRADS ? job.b_mn[w] != 0 : KIND == LIN_DW; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -837,8 +874,8 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&maps.a);
-    tma_prefetch_desc(&maps.b);
+    tma_prefetch_desc(&job.maps[0].a);
+    tma_prefetch_desc(&job.maps[0].b);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -856,12 +893,13 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
     long long fills = 0;
     bool ok = true;
     const uint32_t lead_full = cluster_addr(full, 0);   // both CTAs' loads count on the leader's barriers
-    for (int idx = first; idx < items && ok; idx += step) {
-      int lt, ct;
-      linear_tile(p, idx, lt, ct);
-      const int l0 = lt * 256 + rank * 128, c0 = ct * 256 + rank * 128;
-      for (int kb = 0; kb < p.nk; ++kb) {
-        if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, p.status)) {
+    PairItem it;
+    for (int s = 0; ok && pair_item(job, s, pair, pairs, it); ++s) {
+      const LinearMaps& maps = job.maps[it.w];
+      const bool b_mn = b_is_mn(it.w);
+      const int l0 = it.lt * 256 + rank * 128, c0 = it.ct * 256 + rank * 128, nk = job.p[it.w].nk;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, status)) {
           ok = false;
           break;
         }
@@ -878,7 +916,7 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
           } else {
             tma_load_2d_pair(sA, &maps.a, bar, k0, l0);
           }
-          if (BMN) {
+          if (b_mn) {
             tma_load_2d_pair(sB, &maps.b, bar, c0, k0);
             tma_load_2d_pair(sB + kLinChunk, &maps.b, bar, c0 + 64, k0);
           } else {
@@ -899,27 +937,33 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
     }
   } else if (warp == 1) {
     if (rank == 0) {
-      const uint64_t bd = linear_desc<BMN>(smem_u32(smem)), ad = linear_desc<AMN>(smem_u32(smem) + kLinABytes);
+      const uint64_t ad = linear_desc<AMN>(smem_u32(smem) + kLinABytes);
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
-      for (int idx = first; idx < items && ok; idx += step) {
-        if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) break;
+      PairItem it;
+      for (int s = 0; ok && pair_item(job, s, pair, pairs, it); ++s) {
+        if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, status)) break;
         tc_fence_after();
+        const bool b_mn = b_is_mn(it.w);
+        const uint64_t bd = b_mn ? linear_desc<true>(smem_u32(smem)) : linear_desc<false>(smem_u32(smem));
+        const uint32_t b_step = b_mn ? kStep<true> : kStep<false>;
+        const uint32_t idesc = b_mn ? idesc_bf16(256, C::BN, true, AMN) : idesc_bf16(256, C::BN, false, AMN);
+        const int nk = job.p[it.w].nk;
         const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * C::BN);
-        for (int kb = 0; kb < p.nk; ++kb) {
-          if (!warp_wait(&full[stage], phase, abort_flag, p.status)) {
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!warp_wait(&full[stage], phase, abort_flag, status)) {
             ok = false;
             break;
           }
           const uint32_t at = stage * C::kStageBytes;
           if (elect_one()) {
-            umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), C::kIdesc, kb != 0);
+            umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), idesc, kb != 0);
 #pragma unroll
             for (int kk = 1; kk < kLinBK / 16; ++kk)
-              umma_bf16_pair(acc, desc_at(bd, at + kk * kStep<BMN>), desc_at(ad, at + kk * kStep<AMN>), C::kIdesc, 1u);
+              umma_bf16_pair(acc, desc_at(bd, at + kk * b_step), desc_at(ad, at + kk * kStep<AMN>), idesc, 1u);
             umma_commit_pair(&empty[stage], 0x3);
-            if (kb == p.nk - 1) umma_commit_pair(&tfull[buf], 0x3);
+            if (kb == nk - 1) umma_commit_pair(&tfull[buf], 0x3);
           }
           __syncwarp();
           if (++stage == C::kStages) stage = 0, phase ^= 1;
@@ -937,17 +981,18 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
     uint8_t* stage = out_stage + (warp - 2) * C::kOutBytes;
     int buf = 0, slot = 0;
     uint32_t bphase = 0;
-    for (int idx = first; idx < items; idx += step) {
-      int lt, ct;
-      linear_tile(p, idx, lt, ct);
-      const int l0 = lt * 256 + half * 128, row0 = ct * 256 + rank * 128 + q * 32;
+    PairItem it;
+    for (int s = 0; pair_item(job, s, pair, pairs, it); ++s) {
+      const LinearMaps& maps = job.maps[it.w];
+      const LinearParams& p = job.p[it.w];
+      const int l0 = it.lt * 256 + half * 128, row0 = it.ct * 256 + rank * 128 + q * 32;
       const long long c = static_cast<long long>(row0) + lane;
       if (FWD && p.residual && c < p.C) {   // into L2 while the accumulator fills
         const long long size = p.residual_f32 ? 4 : 2, end = p.L - l0 < 128 ? p.L - l0 : 128;
         const char* r = static_cast<const char*>(p.residual) + (c * p.L + l0) * size;
         for (long long o = 0; o < end * size; o += 128) prefetch_l2(r + o);
       }
-      int w = (lane == 0) ? (mbar_wait(&tfull[buf], bphase, abort_flag, p.status) ? 1 : 0) : 0;
+      int w = (lane == 0) ? (mbar_wait(&tfull[buf], bphase, abort_flag, status) ? 1 : 0) : 0;
       if (!__shfl_sync(0xffffffffu, w, 0)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * C::BN + half * 128) + (static_cast<uint32_t>(q * 32) << 16);

@@ -331,11 +331,16 @@ __global__ void __launch_bounds__(MAXT) rms_norm_bwd_kernel(const NormBwdArgs a)
 }
 
 // Column sums of [n][H] fp32 partial rows, in a fixed order: 32 columns per
-// block, 32 rows in step, then the 32 running sums.
+// block, 32 rows in step, then the 32 running sums.  LATE: the kernel launched
+// before this one does not write `part` and waited itself for the one that
+// does, so that the sums may run beside it (it lets its dependents start only
+// after that wait); this kernel still ends after it, for what follows on the
+// stream.
+template <bool LATE>
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part, int n, int H,
                                                           float* __restrict__ out) {
   __shared__ float s[32][33];
-  griddep_wait();
+  if (!LATE) griddep_wait();
   griddep_launch_dependents();
   const int col = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
@@ -349,6 +354,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
     for (int i = 0; i < 32; ++i) v += s[i][threadIdx.x];
     out[col] = v;
   }
+  if (LATE) griddep_wait();
 }
 
 // E4M3 codes and E8M0 scales -> bf16: 16 codes per thread, half a block.
@@ -443,8 +449,9 @@ cudaError_t launch_rms_norm(const NormArgs& a, int x_f32, int residual, cudaStre
   return residual == 1 ? norm_launch<uint16_t, uint16_t>(a, st) : norm_launch<uint16_t, float>(a, st);
 }
 
-cudaError_t launch_column_sum(const float* part, int n, int H, float* out, cudaStream_t st) {
-  return launch_dependent(column_sum_kernel, dim3((H + 31) / 32), dim3(32, 32), 0, st, part, n, H, out);
+cudaError_t launch_column_sum(const float* part, int n, int H, float* out, bool late, cudaStream_t st) {
+  return launch_dependent(late ? column_sum_kernel<true> : column_sum_kernel<false>, dim3((H + 31) / 32), dim3(32, 32), 0, st,
+                          part, n, H, out);
 }
 
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight, cudaStream_t st) {
@@ -453,7 +460,7 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight
     const cudaError_t err = h_f32 ? norm_bwd_launch<float>(a, walkers, st) : norm_bwd_launch<uint16_t>(a, walkers, st);
     if (err != cudaSuccess) return err;
   }
-  return launch_column_sum(a.part, walkers, a.H, d_weight, st);
+  return launch_column_sum(a.part, walkers, a.H, d_weight, false, st);
 }
 
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out,

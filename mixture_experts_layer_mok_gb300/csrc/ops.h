@@ -62,7 +62,9 @@ int norm_bwd_walkers(long long rows, int H);
 cudaError_t launch_rms_norm(const NormArgs& a, int x_f32, int residual, cudaStream_t st);
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight, cudaStream_t st);
 // out[j] = sum over n rows of part[.][j], in a fixed order (n = 0: zeros).
-cudaError_t launch_column_sum(const float* part, int n, int H, float* out, cudaStream_t st);
+// late: the last kernel launched on the stream neither writes part nor started
+// before part was complete.
+cudaError_t launch_column_sum(const float* part, int n, int H, float* out, bool late, cudaStream_t st);
 cudaError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, long long n, uint16_t* out, cudaStream_t st);
 
 // ---------------------------------------------------------------- dense projection
@@ -95,8 +97,11 @@ struct LinearOperands {
 };
 // The device word that a bounded wait which gave up sets (current device).
 cudaError_t linear_status_word(int** word);
-enum LinKind : int { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2 };
+enum LinKind : int { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2, LIN_GRADS = 3 };
 mok_status_t run_linear(LinKind kind, const LinearOperands& o, const LinearParams& p, int num_sms, cudaStream_t st);
+// dx and dW of one projection, in one launch where both are large enough.
+mok_status_t run_linear_grads(const LinearOperands& ox, const LinearParams& px, const LinearOperands& ow, const LinearParams& pw,
+                              int num_sms, cudaStream_t st);
 
 // dz = dy act'(z) in bf16 (dz may be NULL) and the partial column sums of its
 // fp32 values ([dz_partials][N], part may be NULL).
