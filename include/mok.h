@@ -202,6 +202,13 @@ typedef struct {
                           bracket all windows (from the stage's start in the
                           first window to its end in the last), so their
                           intervals overlap.  Negative: MOK_ERR_INVALID_ARG. */
+  const uint8_t* x_codes;  /* MXFP8 forward modes, optional: x already quantised, as
+                          mok_rms_norm and mok_mxfp8_quantize make it (E4M3
+                          [T][H], scales E8M0 [T][H/32], both 16-byte aligned,
+                          both or neither).  The forward then reads these in
+                          place of quantising x; x itself is still needed, by
+                          the backward's weight gradients.  NULL: quantise x. */
+  const uint8_t* x_scales;
 } mok_config_t;
 
 /* The dispatch/combine schedule ([MoKEd] "The two API layers and the

@@ -312,7 +312,7 @@ def _config(mode, minibatch, debug, events=None, dispatch="auto", swiglu_limit=0
 
 def forward(x, router_w, sched: Schedule, weights: Weights, mode: str = "bf16", minibatch: int = 0,
             debug: int = 0, out=None, ctx_buf=None, stream=None, events=None, dispatch="auto",
-            swiglu_limit: float = 0.0, macrobatch: int = 0):
+            swiglu_limit: float = 0.0, macrobatch: int = 0, x_mx=None):
     """y = layer(x); returns (y, Context).  ``mode`` is "bf16", "mxfp8" or
     "mxfp8_full" (see ``MODES``; the backward follows the forward's mode);
     ``dispatch`` is "auto", "permute" or "fused" (same results, different kernels).
@@ -321,6 +321,9 @@ def forward(x, router_w, sched: Schedule, weights: Weights, mode: str = "bf16", 
     ``macrobatch`` > 0: rows of the token ring (mok_config_t.macrobatch_size):
     the routed experts run in windows of whole experts over scratch of that
     many rows, with the same result bits (reads the expert counts back once).
+    ``x_mx``: (codes, scales) of x, as ``rms_norm(mxfp8=True)`` or
+    ``mxfp8_quantize`` return them: the MXFP8 modes then use these instead of
+    quantising x.
     ``events``: optional list of 2 * MOK_NUM_STAGES torch.cuda.Event (timing); a
     None entry records nothing (each record costs a few microseconds on the
     device, so a timing run can watch one stage alone)."""
@@ -341,6 +344,11 @@ def forward(x, router_w, sched: Schedule, weights: Weights, mode: str = "bf16", 
     y = out if out is not None else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     c = _lib.MokCtx()
     cfg = _config(m, minibatch, debug, events, dispatch, swiglu_limit, macrobatch)
+    if x_mx is not None:
+        if mode == "bf16":
+            raise ValueError("x_mx goes with an MXFP8 mode")
+        cfg.x_codes = _need(x_mx[0], torch.uint8, (T, H), "x_mx codes").data_ptr()
+        cfg.x_scales = _need(x_mx[1], torch.uint8, (T, H // 32), "x_mx scales").data_ptr()
     _lib.check(lib.mok_forward(C.byref(cfg), _ptr(x), _ptr(router_w), C.byref(sched.c), C.byref(ws), _ptr(y),
                                _ptr(ctx_buf), ctx_buf.numel(), C.byref(c), _stream(stream)), "mok_forward")
     return y, Context(ctx_buf, c, m)

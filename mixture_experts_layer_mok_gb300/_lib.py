@@ -44,7 +44,7 @@ STAGE_NAMES = ["fwd_prep", "fwd_shared_gateup", "fwd_shared_down", "fwd_gateup",
 class MokConfig(C.Structure):
     _fields_ = [("mode", C.c_int), ("minibatch_size", C.c_int), ("debug_flags", C.c_int),
                 ("dispatch", C.c_int), ("num_events", C.c_int), ("events", C.POINTER(C.c_void_p)),
-                ("swiglu_limit", C.c_float), ("macrobatch_size", C.c_int64)]
+                ("swiglu_limit", C.c_float), ("macrobatch_size", C.c_int64), ("x_codes", P), ("x_scales", P)]
 
 
 class MokSchedule(C.Structure):

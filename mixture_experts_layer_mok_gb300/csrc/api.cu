@@ -945,6 +945,15 @@ mok_status_t forward_mxfp8(const mok_config_t* cfg, const uint16_t* x, const flo
   // gradient reads (a separate copy would contend for HBM with whichever GEMM
   // it overlapped).  Later windows skip the token-order copy.
   auto dispatch = [&](const Win& v, bool tokens) {
+    if (cfg->x_codes) {   // x came quantised: only rows to move
+      cudaError_t e = launch_permute_rows(reinterpret_cast<const uint16_t*>(cfg->x_codes), T, H / 2, k, s->slot_row, s->row_src,
+                                          s->header, v.r0, v.rows, reinterpret_cast<uint16_t*>(ctx->xq_perm), sms, cs);
+      if (e == cudaSuccess && ctx->x_perm)
+        e = launch_permute_rows(x, T, H, k, s->slot_row, s->row_src, s->header, v.r0, v.rows, ctx->x_perm, sms, cs);
+      if (e != cudaSuccess) return e;
+      return launch_mx_scale_gather(cfg->x_scales, T, H, k, s->row_src, s->header, v.r0, v.rows, ctx->xq_perm_sc,
+                                    tokens ? ctx->xq_sc : nullptr, cs);
+    }
     cudaError_t e = launch_mx_dispatch(x, T, H, k, s->slot_row, s->row_src, s->header, v.r0, v.rows,
                                        tokens ? ctx->xq : nullptr, X.xs, ctx->xq_perm, ctx->x_perm, sms, cs);
     if (e != cudaSuccess) return e;
@@ -1000,7 +1009,7 @@ mok_status_t forward_mxfp8(const mok_config_t* cfg, const uint16_t* x, const flo
   MOK_CUDA(mark(cfg, MOK_STAGE_FWD_SHARED_GATEUP, 0, cs));
   if (Is > 0) {
     MxMaps m;
-    if ((st = make_map_u8(&m.a, ctx->xq, H, T, 128)) || (st = make_map_u8(&m.b0, w->mxs_gate, H, Is, gu_box)) ||
+    if ((st = make_map_u8(&m.a, cfg->x_codes ? cfg->x_codes : ctx->xq, H, T, 128)) || (st = make_map_u8(&m.b0, w->mxs_gate, H, Is, gu_box)) ||
         (st = make_map_u8(&m.b1, w->mxs_up, H, Is, gu_box)) ||
         (st = make_map_sf(&m.sfa, ctx->xq_sc, t_atoms * (H / 128))) || (st = gu_sf_maps(m, X.wsg_sc, X.wsu_sc, Is)) ||
         (st = make_map_out(&m.o0, ctx->gu_s, 2ull * Is, T)) || (st = make_map_codes_out(&m.o1, ctx->hq_s, Is, T)))
@@ -1776,6 +1785,10 @@ mok_status_t mok_forward(const mok_config_t* cfg, const uint16_t* x, const float
     for (const void* q : mp)
       if (!aligned16(q)) return fail(MOK_ERR_INVALID_ARG, "misaligned MXFP8 weight pointer");
   }
+  if ((cfg->x_codes == nullptr) != (cfg->x_scales == nullptr) || (cfg->x_codes && !mx))
+    return fail(MOK_ERR_INVALID_ARG, "x_codes and x_scales go together, with an MXFP8 mode");
+  if (!aligned16(cfg->x_codes) || !aligned16(cfg->x_scales))
+    return fail(MOK_ERR_INVALID_ARG, "misaligned x_codes or x_scales");
   const void* ptrs[] = {x, router_w, y, ctx_buf, w->w_gate, w->w_up, w->w_down};
   for (const void* q : ptrs)
     if (!aligned16(q)) return fail(MOK_ERR_INVALID_ARG, "misaligned pointer");
