@@ -167,9 +167,11 @@ mok_status_t pair_setup(bool a_mn, bool b_mn, const LinearOperands& o, LinearPar
 long long pair_tiles(const LinearParams& p) {
   return (p.L + 255) / 256 * ((static_cast<long long>(p.C) + 255) / 256);
 }
-// Whether a product is for the pair kernels: both sides of its output wider
-// than one CTA's 128, or enough tiles to fill the GPU all the same.
-bool is_paired(const LinearParams& p, int pairs) { return (p.L > 128 && p.C > 128) || pair_tiles(p) >= pairs; }
+// Whether a product is for the pair kernels: more than 128 rows, and either
+// more than 128 columns or tiles enough to fill the GPU.  Measured, split and
+// pair kernel: 1 x 152064 x 4096 177 and 326 us, 128 x 28672 x 4096 44 and 49,
+// 1003 x 1416 x 2056 21.5 and 14.8, 100000 x 64 x 1024 46 and 40.
+bool is_paired(const LinearParams& p, int pairs) { return p.C > 128 && (p.L > 128 || pair_tiles(p) >= pairs); }
 
 template <int KIND>
 mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sms, cudaStream_t st) {

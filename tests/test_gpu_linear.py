@@ -213,6 +213,25 @@ def test_output_past_32_bit_offsets():
     assert m.linear_status() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 40000, 264), (3, 20000, 72), (100, 19600, 64), (19600, 64, 136), (20000, 8, 64),
+                                   (9000, 120, 72)])
+def test_one_long_side(M, N, K):
+    """Outputs with one side narrower than a CTA's tile and the other long, whichever kernel takes them."""
+    m = mok()
+    g = torch.Generator().manual_seed(M)
+    x, w, b, r = _rand(g, M, K), _rand(g, N, K, std=K ** -0.5), _rand(g, N), _rand(g, M, N)
+    y, _ = m.linear(x.cuda(), w.cuda(), bias=b.cuda(), residual=r.cuda())
+    y64 = x.double() @ w.double().t() + b.double() + r.double()
+    size = x.double().abs() @ w.double().abs().t() + b.double().abs() + r.double().abs()
+    _within(y, y64, _f(K) * size + U * y64.abs(), "y")
+    dy = _rand(g, M, N)
+    out = m.linear_backward(dy.cuda(), x.cuda(), w.cuda(), bias=True)
+    for key, a, c, k in (("dx", dy, w, N), ("d_weight", dy.t(), x, M)):
+        ref = a.double() @ c.double()
+        _within(out[key], ref, _f(k) * (a.double().abs() @ c.double().abs()) * 1.01 + U * ref.abs(), key)
+    assert m.linear_status() == 0
+
+
 def test_another_stream_gives_the_same():
     m = mok()
     g = torch.Generator().manual_seed(2)
