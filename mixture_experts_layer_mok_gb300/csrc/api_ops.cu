@@ -99,7 +99,8 @@ mok_status_t mok_rms_norm(const void* x, int x_dtype, const void* residual, int 
 
 size_t mok_rms_norm_bwd_workspace_bytes(int64_t rows, int H) {
   if (rows < 0 || rows > 0x7fffffffll || H < 1 || H > MOK_NORM_MAX_H) return 0;
-  return static_cast<size_t>(norm_bwd_walkers(rows, H)) * H * sizeof(float) + 256;
+  const int n = norm_bwd_walkers(rows, H, false), m = norm_bwd_walkers(rows, H, true);   // for either type of h
+  return static_cast<size_t>(n > m ? n : m) * H * sizeof(float) + 256;
 }
 
 mok_status_t mok_rms_norm_bwd(const uint16_t* dy, const void* h, int h_dtype, const void* weight, int weight_dtype,

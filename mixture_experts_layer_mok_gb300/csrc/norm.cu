@@ -234,18 +234,155 @@ __global__ void __launch_bounds__(MAXT) rms_norm_kernel(const NormArgs a) {
   }
 }
 
-// The backward: a grid of fixed size, each block (or warp) walking rows and
-// keeping its columns' share of dw in registers; `part` gets one row of sums
-// per walker, which norm_dw_kernel adds in order.
-template <class HT, int V, int ITEMS, bool WARP_ROW, int MAXT>
-__global__ void __launch_bounds__(MAXT) rms_norm_bwd_kernel(const NormBwdArgs a) {
+// The sums of R values over the W warps of a row, in a fixed order.  `red`: 32
+// slots of R; the caller alternates two of them, so that one barrier (of the
+// row's warps alone) serves R rows.
+template <int W, int R>
+__device__ __forceinline__ void row_sums(float (&s)[R], float (*red)[R]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) s[r] = warp_sum(s[r]);
+  if constexpr (W > 1) {
+    const int warp = threadIdx.x >> 5, first = warp / W * W;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) red[warp][r] = s[r];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "n"(32 * W) : "memory");
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s[r] += red[first + w][r];
+    }
+  }
+}
+
+// The backward: a grid of fixed size, W warps to a row and ITEMS x 8 of its
+// elements to a thread; each such group walks the rows, R at a time, and keeps
+// its columns' share of dw in registers.  `part` gets one row of sums per block,
+// which column_sum_kernel adds in order.
+//   acc_j += rstd (dy_j h_j),   s = sum_j w_j dy_j h_j,   k = -rstd^3 s / H,
+//   dx_j = rstd (w_j dy_j) + (k h_j + dh_j)
+template <class HT, int ITEMS, int R, int W, int THREADS>
+__global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int kGroups = THREADS / (32 * W), T = 32 * W;
+  __shared__ float red[2][32][R];
+  __shared__ float sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? T * ITEMS * 8 : 1];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int group = threadIdx.x / T, tid = threadIdx.x % T, nv = a.H / 8;
+  const long long step = static_cast<long long>(gridDim.x) * kGroups * R;
+  float acc[ITEMS][8];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  const float inv_h = 1.f / static_cast<float>(a.H);
+  int odd = 0;
+  for (long long row0 = (static_cast<long long>(blockIdx.x) * kGroups + group) * R; row0 < a.rows; row0 += step, odd ^= 1) {
+    Raw<uint16_t, 8> dy[R][ITEMS];
+    Raw<HT, 8> h[R][ITEMS], dh[R][ITEMS];
+    float rstd[R], dot[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool in = row0 + r < a.rows;
+      const long long base = (row0 + r) * a.H;
+      rstd[r] = in ? __ldg(a.rstd + row0 + r) : 0.f;
+      dot[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int c = tid + i * T;
+        dy[r][i] = {};
+        h[r][i] = {};
+        dh[r][i] = {};
+        if (in && c < nv) {
+          dy[r][i] = load_raw<uint16_t, 8>(a.dy + base + c * 8);
+          h[r][i] = load_raw<HT, 8>(static_cast<const HT*>(a.h) + base + c * 8);
+          if (a.dh) dh[r][i] = load_raw<HT, 8>(static_cast<const HT*>(a.dh) + base + c * 8);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = tid + i * T;
+      if (c < nv) {
+        float w[8];
+        load_weight<8>(a.weight, a.weight_f32, c * 8, w);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float y[8], x[8];
+          unpack(dy[r][i], y);
+          unpack(h[r][i], x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float t = y[j] * x[j];
+            acc[i][j] = fmaf(t, rstd[r], acc[i][j]);
+            dot[r] = fmaf(t, w[j], dot[r]);
+          }
+        }
+      }
+    }
+    row_sums<W, R>(dot, red[odd]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) dot[r] *= -inv_h * rstd[r] * rstd[r] * rstd[r];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = tid + i * T;
+      if (c < nv) {
+        float w[8];
+        load_weight<8>(a.weight, a.weight_f32, c * 8, w);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (row0 + r < a.rows) {
+            const long long at = (row0 + r) * a.H + c * 8;
+            float y[8], x[8], d[8];
+            unpack(dy[r][i], y);
+            unpack(h[r][i], x);
+            unpack(dh[r][i], d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] = fmaf(y[j] * w[j], rstd[r], fmaf(x[j], dot[r], d[j]));
+            store_vals<8>(static_cast<HT*>(a.dx) + at, d);
+            if (sizeof(HT) == 4 && a.dx16) store_vals<8>(a.dx16 + at, d);
+          }
+        }
+      }
+    }
+  }
+  float* part = a.part + static_cast<long long>(blockIdx.x) * a.H;
+  if constexpr (kGroups > 1) {   // the block's groups in order
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sums[group][(tid + i * T) * 8 + j] = acc[i][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.H; c += THREADS) {
+      float v = 0.f;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) v += sums[g][c];
+      part[c] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = tid + i * T;
+      if (c < nv) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[c * 8 + j] = acc[i][j];
+      }
+    }
+  }
+}
+
+// The same with a block to a row, the next row's values in registers: for middle
+// lengths, whose rows one block's threads hold in 8 elements each, and for
+// lengths that are not a multiple of 8 or above 16384.
+template <class HT, int V, int ITEMS, int MAXT>
+__global__ void __launch_bounds__(MAXT) rms_norm_bwd_block_kernel(const NormBwdArgs a) {
   __shared__ float red[2][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int T = WARP_ROW ? 32 : blockDim.x;
-  const int tid = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
-  const long long walkers = WARP_ROW ? static_cast<long long>(gridDim.x) * kWarpRows : gridDim.x;
-  const long long walker = WARP_ROW ? static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  const int T = blockDim.x, tid = threadIdx.x;
+  const long long walkers = gridDim.x, walker = blockIdx.x;
   const int nv = a.H / V;
   float acc[ITEMS][V], w[ITEMS][V];
 #pragma unroll
@@ -293,28 +430,23 @@ __global__ void __launch_bounds__(MAXT) rms_norm_bwd_kernel(const NormBwdArgs a)
         unpack(rh[i], h);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float t = dy[j] * (h[j] * rstd);
-          acc[i][j] += t;
+          const float t = dy[j] * h[j];
+          acc[i][j] = fmaf(t, rstd, acc[i][j]);
           dot = fmaf(t, w[i][j], dot);
         }
       }
     }
-    dot = row_sum<WARP_ROW>(dot, red[odd]) * inv_h;
+    const float k = row_sum<false>(dot, red[odd]) * (-inv_h * rstd * rstd * rstd);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * T;
       if (c < nv) {
-        float dy[V], h[V], d[V];
+        float dy[V], h[V], d[V] = {};
         unpack(rdy[i], dy);
         unpack(rh[i], h);
+        if (a.dh) unpack(rdh[i], d);
 #pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = rstd * fmaf(-h[j] * rstd, dot, dy[j] * w[i][j]);
-        if (a.dh) {
-          float r[V];
-          unpack(rdh[i], r);
-#pragma unroll
-          for (int j = 0; j < V; ++j) d[j] += r[j];
-        }
+        for (int j = 0; j < V; ++j) d[j] = fmaf(dy[j] * w[i][j], rstd, fmaf(h[j], k, d[j]));
         store_vals<V>(static_cast<HT*>(a.dx) + base + c * V, d);
         if (sizeof(HT) == 4 && a.dx16) store_vals<V>(a.dx16 + base + c * V, d);
       }
@@ -344,8 +476,10 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
   griddep_launch_dependents();
   const int col = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
-  if (col < H)
+  if (col < H) {
+#pragma unroll 8
     for (int r = threadIdx.y; r < n; r += 32) v += part[static_cast<long long>(r) * H + col];
+  }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   if (threadIdx.y == 0 && col < H) {
@@ -411,32 +545,43 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t st) {
   return launch_dependent(rms_norm_kernel<XT, RT, 8, 4, false, 1024>, dim3(rows), dim3(ceil32((nv + 3) / 4)), 0, st, a);
 }
 
+// The backward's kernel for a row length.  Measured (us; groups of warps, block
+// per row): 65536 x 512 bf16 45 and 47, 16384 x 2048 65 and 49, 16384 x 7168 162
+// and 173, in fp32 305 and 265, 1000 x 16384 bf16 40 and 108.
+bool bwd_groups(int H, bool f32) { return H % 8 == 0 && H <= 16384 && (H <= 512 || H > (f32 ? 8192 : 4096)); }
+
 template <class HT>
-cudaError_t norm_bwd_launch(const NormBwdArgs& a, int walkers, cudaStream_t st) {
-  const unsigned blocks = static_cast<unsigned>(walkers), wblocks = blocks / kWarpRows;
-  if (a.H % 8) {
-    if (a.H <= 4096)
-      return launch_dependent(rms_norm_bwd_kernel<HT, 1, 4, false, 1024>, dim3(blocks), dim3(ceil32((a.H + 3) / 4)), 0, st, a);
-    return launch_dependent(rms_norm_bwd_kernel<HT, 1, 32, false, 1024>, dim3(blocks), dim3(ceil32((a.H + 31) / 32)), 0, st, a);
+cudaError_t norm_bwd_launch(const NormBwdArgs& a, int blocks, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(blocks));
+  const int H = a.H, nv = H / 8;
+  if (bwd_groups(H, sizeof(HT) == 4)) {
+    if (H <= 256) return launch_dependent(rms_norm_bwd_kernel<HT, 1, 4, 1, 128>, grid, dim3(128), 0, st, a);
+    if (H <= 512) return launch_dependent(rms_norm_bwd_kernel<HT, 2, 2, 1, 128>, grid, dim3(128), 0, st, a);
+    if constexpr (sizeof(HT) == 2)
+      if (H <= 8192) return launch_dependent(rms_norm_bwd_kernel<HT, 4, 1, 8, 256>, grid, dim3(256), 0, st, a);
+    return launch_dependent(rms_norm_bwd_kernel<HT, 4, 1, 16, 512>, grid, dim3(512), 0, st, a);
   }
-  const int nv = a.H / 8;
-  if (nv <= 32) return launch_dependent(rms_norm_bwd_kernel<HT, 8, 1, true, 128>, dim3(wblocks), dim3(128), 0, st, a);
-  if (nv <= 64) return launch_dependent(rms_norm_bwd_kernel<HT, 8, 2, true, 128>, dim3(wblocks), dim3(128), 0, st, a);
-  if (nv <= 512)
-    return launch_dependent(rms_norm_bwd_kernel<HT, 8, 1, false, 512>, dim3(blocks), dim3(ceil32(nv)), 0, st, a);
-  if (nv <= 1024)
-    return launch_dependent(rms_norm_bwd_kernel<HT, 8, 2, false, 512>, dim3(blocks), dim3(ceil32((nv + 1) / 2)), 0, st, a);
-  return launch_dependent(rms_norm_bwd_kernel<HT, 8, 4, false, 1024>, dim3(blocks), dim3(ceil32((nv + 3) / 4)), 0, st, a);
+  if (H % 8) {
+    if (H <= 4096) return launch_dependent(rms_norm_bwd_block_kernel<HT, 1, 4, 1024>, grid, dim3(ceil32((H + 3) / 4)), 0, st, a);
+    return launch_dependent(rms_norm_bwd_block_kernel<HT, 1, 32, 1024>, grid, dim3(ceil32((H + 31) / 32)), 0, st, a);
+  }
+  if (H <= 4096) return launch_dependent(rms_norm_bwd_block_kernel<HT, 8, 1, 512>, grid, dim3(ceil32(nv)), 0, st, a);
+  if (H <= 8192) return launch_dependent(rms_norm_bwd_block_kernel<HT, 8, 2, 512>, grid, dim3(ceil32((nv + 1) / 2)), 0, st, a);
+  return launch_dependent(rms_norm_bwd_block_kernel<HT, 8, 4, 1024>, grid, dim3(ceil32((nv + 3) / 4)), 0, st, a);
 }
 
 }  // namespace
 
-int norm_bwd_walkers(long long rows, int H) {
-  const bool warp_row = H % 8 == 0 && H <= 512;
-  const long long most = warp_row ? 608 * kWarpRows : 608;   // 4 blocks on each of 152 SMs
-  long long n = rows < most ? rows : most;
-  if (warp_row) n = (n + kWarpRows - 1) / kWarpRows * kWarpRows;
-  return static_cast<int>(n);
+int norm_bwd_walkers(long long rows, int H, bool f32) {
+  long long each = 1, most = H % 8 == 0 && H <= 1024 ? 1216 : 608;   // rows that a block works on at a time; blocks
+  if (bwd_groups(H, f32)) {
+    each = H <= 256 ? 16 : H <= 512 ? 8 : 1;
+    most = H <= 512 ? 608 : H <= 8192 ? 304 : 152;
+  }
+  const long long groups = (rows + each - 1) / each;
+  if (groups == 0) return 0;
+  const long long turns = (groups + most - 1) / most;   // every block as many, but for the last
+  return static_cast<int>((groups + turns - 1) / turns);
 }
 
 cudaError_t launch_rms_norm(const NormArgs& a, int x_f32, int residual, cudaStream_t st) {
@@ -455,7 +600,7 @@ cudaError_t launch_column_sum(const float* part, int n, int H, float* out, bool 
 }
 
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight, cudaStream_t st) {
-  const int walkers = norm_bwd_walkers(a.rows, a.H);
+  const int walkers = norm_bwd_walkers(a.rows, a.H, h_f32 != 0);
   if (walkers > 0) {
     const cudaError_t err = h_f32 ? norm_bwd_launch<float>(a, walkers, st) : norm_bwd_launch<uint16_t>(a, walkers, st);
     if (err != cudaSuccess) return err;

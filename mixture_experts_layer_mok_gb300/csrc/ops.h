@@ -57,7 +57,7 @@ struct NormBwdArgs {
   int weight_f32;
 };
 // Partial rows of the weight gradient (part of the workspace's size).
-int norm_bwd_walkers(long long rows, int H);
+int norm_bwd_walkers(long long rows, int H, bool f32);
 // residual: 0 none, 1 bf16, 2 fp32.
 cudaError_t launch_rms_norm(const NormArgs& a, int x_f32, int residual, cudaStream_t st);
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight, cudaStream_t st);
