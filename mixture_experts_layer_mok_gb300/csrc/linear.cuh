@@ -241,7 +241,7 @@ __device__ __forceinline__ float4 part_of(const float* mine, const uint32_t* pee
 template <bool FWD, int ACT, int S, int BN>
 __device__ __forceinline__ void join_columns(const LinearParams& p, const float* part, int rank, long long l0, int c0, int warp,
                                              int lane) {
-  constexpr int kShare = BN / S, kWarps = 8, kAtOnce = S == 8 ? 2 : 4;
+  constexpr int kShare = BN / S, kWarps = 8, kAtOnce = 2;
   const long long l = l0 + lane * 4;
   if (l >= p.L) return;
   float bias[4] = {0.f, 0.f, 0.f, 0.f};
