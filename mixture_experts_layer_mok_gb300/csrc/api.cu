@@ -1624,7 +1624,7 @@ mok_status_t backward_bf16(const mok_config_t* cfg, const uint16_t* dy, const ui
 // ===========================================================================
 extern "C" {
 
-int mok_version(void) { return 1; }
+int mok_version(void) { return 2; }
 
 const char* mok_last_error(void) { return g_err; }
 

@@ -166,4 +166,7 @@ class AdamW:
                 st = fn(C.byref(cfg), arr, len(arr), scale, handle)
                 if st:
                     _fail(st, "mok_adamw_step")
+        # the parameters changed under autograd's eyes: a backward that saved
+        # them before this step has to notice
+        torch.autograd.graph.increment_version(self.params)
         self.step_count += 1

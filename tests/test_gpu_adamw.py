@@ -239,6 +239,16 @@ def test_a_nan_gradient_stays_in_its_block():
     assert not bool(r[:32].isnan().any()) and not bool(r[64:].isnan().any())
 
 
+def test_a_backward_notices_the_step():
+    m = mok()
+    w = torch.nn.Parameter(torch.ones(64, device="cuda"))
+    x = torch.ones(64, device="cuda", requires_grad=True)
+    loss = (w * w * x).sum()
+    m.AdamW([w]).step([torch.ones(64, device="cuda")])
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        loss.backward()
+
+
 def test_refusals():
     m = mok()
     p = torch.zeros(64, device="cuda")

@@ -131,3 +131,44 @@ def test_eight_bit_states_train_like_32_bit_ones():
     a, b = train_block.train(state="fp32", **kw), train_block.train(state="mxfp8", **kw)
     end_a, end_b = sum(a[-5:]) / 5, sum(b[-5:]) / 5
     assert abs(end_a - end_b) < 0.15 * sum(a[:3]) / 3, (end_a, end_b)
+
+
+def test_calls_in_a_cuda_graph():
+    """A captured sequence (norm, a token's and a batch's projections, their
+    gradients, a step) replays with new inputs in the same buffers."""
+    m = mok()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF16)  # noqa: E731
+    x, r, wn, w1, w2 = rand(300, 512), rand(300, 512), rand(512), rand(1024, 512), rand(64, 1024)
+    p = torch.randn(1000, generator=g, device="cuda")
+    opt = m.AdamW([p], lr=0.0, weight_decay=0.0, state="mxfp8")
+    gp = torch.ones(1000, device="cuda")
+
+    def work():
+        n = m.rms_norm(x, wn, residual=r, mxfp8=True)
+        y, z = m.linear(n.y, w1, activation="gelu", save_z=True)
+        one, _ = m.linear(y[:1], w2)
+        d = m.linear_backward(y, n.y, w1, z=z, activation="gelu", bias=True)
+        b = m.rms_norm_backward(d["dx"], n.h, wn, n.rstd, d_h=r)
+        opt.step([gp])
+        return [n.y, n.mx[0], y, one, d["d_weight"], d["d_bias"], b["dx"], b["d_weight"]]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):   # warm-up outside the capture
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for _ in range(2):
+        x.copy_(rand(300, 512))
+        r.copy_(rand(300, 512))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = work()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert m.linear_status() == 0
