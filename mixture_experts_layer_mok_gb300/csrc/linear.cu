@@ -136,7 +136,7 @@ cudaError_t launch_pair_split(const LinearMaps& maps, LinearParams& p, cudaStrea
 
 template <int KIND>
 cudaError_t launch_pair(PairJob& job, cudaStream_t st) {
-  using C = PairCfg<KIND != LIN_FWD, false>;
+  using C = PairKindCfg<KIND>;
   auto kern = linear_pair_kernel<KIND>;
   static KernelInfo info;
   int n = 0;
@@ -173,6 +173,13 @@ long long pair_tiles(const LinearParams& p) {
 // 1003 x 1416 x 2056 21.5 and 14.8, 100000 x 64 x 1024 46 and 40.
 bool is_paired(const LinearParams& p, int pairs) { return p.C > 128 && (p.L > 128 || pair_tiles(p) >= pairs); }
 
+// Up to how many K-blocks the forward runs with twice the epilogue warps for one
+// stage less.  Measured both ways (us; 8 and 16 epilogue warps), 8192 x 4864
+// outputs: K = 272 40 and 36 plain, 67 and 53 with bias and GELU, 79 and 65 with
+// a residual; K = 1024 50 and 50, 74 and 61, 87 and 73; K = 1536 66 and 68, 79
+// and 73, fp32 with bias 74 and 79; K = 2048 85 and 87, 91 and 91, fp32 92 and 98.
+constexpr int kShortK = 16;
+
 template <int KIND>
 mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sms, cudaStream_t st) {
   constexpr bool FWD = KIND == LIN_FWD, AMN = KIND != LIN_FWD, BMN = KIND == LIN_DW;
@@ -186,7 +193,10 @@ mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sm
     if (fills) {
       job.p[0] = p;
       job.problems = 1;
-      MOK_CUDA(launch_pair<KIND>(job, st));
+      if (FWD && p.nk <= kShortK)
+        MOK_CUDA(launch_pair<FWD ? LIN_FWD_SHORT : KIND>(job, st));
+      else
+        MOK_CUDA(launch_pair<KIND>(job, st));
     } else {
       MOK_CUDA((launch_pair_split<AMN, BMN, FWD>(job.maps[0], p, st)));
     }

@@ -190,6 +190,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 template <bool MN>
 constexpr uint32_t kStep = MN ? 16 * 128 : 32;
 
+// 8 consecutive fp32 columns of this thread's TMEM lane, waited on.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // ---------------------------------------------------------------- split kernel
 template <bool AMN, bool BMN, int BN>
 struct SplitCfg {
@@ -217,19 +230,6 @@ __device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr) {
 // elements of a row per thread.  Several columns at a time, their residuals
 // and all ranks' parts in flight together: one at a time each would cost the
 // latency of a global and of a remote load.
-// 8 consecutive fp32 columns of this thread's TMEM lane, waited on.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // float4 at byte `off` of rank s's part: this CTA's own through plain shared
 // loads, which are several times as fast as through the cluster's window.
 template <int S>
@@ -445,13 +445,15 @@ __global__ void __launch_bounds__(SplitCfg<AMN, BMN, BN>::kThreads, 2) linear_sp
 }
 
 // ---------------------------------------------------------------- pair kernel
-template <bool AMN, bool BMN>
+// SHORT: the forward over few K-blocks, whose epilogue takes longer than its
+// products: twice the epilogue warps, for one stage less.
+template <bool AMN, bool BMN, bool SHORT = false>
 struct PairCfg {
   static constexpr int BN = 256;
   static constexpr int kBBytes = 128 * kLinBK * 2;   // this CTA's half of B
   static constexpr int kStageBytes = kLinABytes + kBBytes;
-  static constexpr int kStages = 6;
-  static constexpr int kEpiWarps = 8;
+  static constexpr int kStages = SHORT ? 5 : 6;
+  static constexpr int kEpiWarps = SHORT ? 16 : 8;
   static constexpr int kOutBytes = 4096;   // per epilogue warp: see output_block
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpiWarps * kOutBytes + 512;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -474,7 +476,7 @@ __device__ __forceinline__ uint4* stage_piece(uint8_t* block, int lane, int j) {
 }
 
 // One 32 x 32 block of the outputs: this lane's row c, columns l .. l + 31, the
-// sums at TMEM address t.  16 columns at a time they become z and y in the
+// sums at TMEM address t.  8 columns at a time they become z and y in the
 // warp's stage, and leave by TMA stores of the whole block.  The stage's 4 KB
 // hold two bf16 blocks, either one after the other (a block is computed while
 // the one before it is read) or y and z of one, or one fp32 block.
@@ -843,10 +845,14 @@ __device__ __forceinline__ bool pair_item(const PairJob& job, int s, int pair, i
   return true;
 }
 
+// KIND: LIN_FWD, LIN_FWD_SHORT (the forward over few K-blocks), or a gradient.
 template <int KIND>
-__global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_constant__ PairJob job) {
-  constexpr bool AMN = KIND != LIN_FWD, FWD = KIND == LIN_FWD;
-  using C = PairCfg<AMN, false>;
+using PairKindCfg = PairCfg<KIND != LIN_FWD && KIND != LIN_FWD_SHORT, false, KIND == LIN_FWD_SHORT>;
+
+template <int KIND>
+__global__ void __launch_bounds__(PairKindCfg<KIND>::kThreads, 1) linear_pair_kernel(const __grid_constant__ PairJob job) {
+  constexpr bool FWD = KIND == LIN_FWD || KIND == LIN_FWD_SHORT, AMN = !FWD;
+  using C = PairKindCfg<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* out_stage = smem + C::kStages * C::kStageBytes;
@@ -977,7 +983,8 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    constexpr int kCols = C::BN * 4 / C::kEpiWarps;   // this warp's columns
+    const int q = warp & 3, col0 = ((warp - 2) >> 2) * kCols;
     uint8_t* stage = out_stage + (warp - 2) * C::kOutBytes;
     int buf = 0, slot = 0;
     uint32_t bphase = 0;
@@ -985,19 +992,19 @@ __global__ void __launch_bounds__(320, 1) linear_pair_kernel(const __grid_consta
     for (int s = 0; pair_item(job, s, pair, pairs, it); ++s) {
       const LinearMaps& maps = job.maps[it.w];
       const LinearParams& p = job.p[it.w];
-      const int l0 = it.lt * 256 + half * 128, row0 = it.ct * 256 + rank * 128 + q * 32;
+      const int l0 = it.lt * 256 + col0, row0 = it.ct * 256 + rank * 128 + q * 32;
       const long long c = static_cast<long long>(row0) + lane;
       if (FWD && p.residual && c < p.C) {   // into L2 while the accumulator fills
-        const long long size = p.residual_f32 ? 4 : 2, end = p.L - l0 < 128 ? p.L - l0 : 128;
+        const long long size = p.residual_f32 ? 4 : 2, end = p.L - l0 < kCols ? p.L - l0 : kCols;
         const char* r = static_cast<const char*>(p.residual) + (c * p.L + l0) * size;
         for (long long o = 0; o < end * size; o += 128) prefetch_l2(r + o);
       }
       int w = (lane == 0) ? (mbar_wait(&tfull[buf], bphase, abort_flag, status) ? 1 : 0) : 0;
       if (!__shfl_sync(0xffffffffu, w, 0)) break;
       tc_fence_after();
-      const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * C::BN + half * 128) + (static_cast<uint32_t>(q * 32) << 16);
+      const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * C::BN + col0) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-      for (int k = 0; k < 128 && l0 + k < p.L && row0 < p.C; k += 32) {
+      for (int k = 0; k < kCols && l0 + k < p.L && row0 < p.C; k += 32) {
         if constexpr (FWD) {
           switch (p.act) {
             case LIN_RELU: forward_block<LIN_RELU>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane); break;
