@@ -270,20 +270,33 @@ __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
   }
 }
 
+// The list is handed over by address: through the launch templates, which take
+// arguments by value, its 30 KB would be copied twice more.
 template <class PT, class GT, bool MASTER, bool MX, int CAP>
 cudaError_t launch_cap(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, cudaStream_t st) {
   AdamwList<CAP> list;
   memcpy(list.t, t, sizeof(AdamwTensor) * n);
   list.n = n;
   constexpr int kResident = 152 * kAdamwPerSm;
-  return launch_dependent(adamw_kernel<PT, GT, MASTER, MX, CAP>, dim3(MX && chunks > kResident ? kResident : chunks),
-                          dim3(256), 0, st, list, chunks, s);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(MX && chunks > kResident ? kResident : chunks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  AdamwScalars scalars = s;
+  void* args[] = {&list, &chunks, &scalars};
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(adamw_kernel<PT, GT, MASTER, MX, CAP>), args);
 }
 
 template <class PT, class GT, bool MASTER, bool MX>
 cudaError_t launch_typed(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, cudaStream_t st) {
-  return n <= 16 ? launch_cap<PT, GT, MASTER, MX, 16>(t, n, chunks, s, st)
-                 : launch_cap<PT, GT, MASTER, MX, kAdamwMaxTensors>(t, n, chunks, s, st);
+  if (n <= 16) return launch_cap<PT, GT, MASTER, MX, 16>(t, n, chunks, s, st);
+  if (n <= 128) return launch_cap<PT, GT, MASTER, MX, 128>(t, n, chunks, s, st);
+  return launch_cap<PT, GT, MASTER, MX, kAdamwMaxTensors>(t, n, chunks, s, st);
 }
 
 template <class PT, class GT, bool MASTER>

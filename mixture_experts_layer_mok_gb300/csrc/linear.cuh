@@ -476,7 +476,7 @@ __device__ __forceinline__ uint4* stage_piece(uint8_t* block, int lane, int j) {
 }
 
 // One 32 x 32 block of the outputs: this lane's row c, columns l .. l + 31, the
-// sums at TMEM address t.  8 columns at a time they become z and y in the
+// sums at TMEM address t.  16 columns at a time they become z and y in the
 // warp's stage, and leave by TMA stores of the whole block.  The stage's 4 KB
 // hold two bf16 blocks, either one after the other (a block is computed while
 // the one before it is read) or y and z of one, or one fp32 block.

@@ -3,6 +3,7 @@ marshalling only: the step is libmok's ``mok_adamw_step``)."""
 from __future__ import annotations
 
 import ctypes as C
+from operator import attrgetter
 
 import numpy as np
 import torch
@@ -13,6 +14,9 @@ from .ops import _DTYPE, _check, _fail, _raw_stream
 _STATE = {"fp32": _lib.MOK_ADAMW_STATE_F32, "mxfp8": _lib.MOK_ADAMW_STATE_MXFP8}
 _KEPT = {"fp32": ("m", "v"), "mxfp8": ("m", "m_scale", "r", "r_scale")}
 _FIELD = {"masters": "master", "m": "m", "v": "v", "r": "v", "m_scale": "m_scale", "r_scale": "v_scale"}
+# over a list, map() of these takes a third less time than a loop's body
+_data_ptr, _is_contiguous = torch.Tensor.data_ptr, torch.Tensor.is_contiguous
+_dtype, _shape, _is_cuda = attrgetter("dtype"), attrgetter("shape"), attrgetter("is_cuda")
 
 
 class AdamW:
@@ -78,7 +82,6 @@ class AdamW:
         self.buffers = {k: list(v) for k, v in buffers.items()}
         # one launch list per parameter type (master copies belong to the bf16
         # ones), with the fields that a step changes as arrays over it
-        self._shapes = [p.shape for p in self.params]
         self._groups = []
         for dtype in (torch.bfloat16, torch.float32):
             idx = [i for i, p in enumerate(self.params) if p.dtype == dtype]
@@ -91,7 +94,9 @@ class AdamW:
                     if ts[i] is not None:
                         setattr(a, _FIELD[name], ts[i].data_ptr())
             fields = np.frombuffer(arr, dtype=np.dtype(_lib.MokAdamwTensor))
-            self._groups.append((dtype, idx, arr, fields, fields["p"].tolist(), fields["n"].tolist()))
+            params = [self.params[i] for i in idx]
+            self._groups.append((dtype, idx, params, [p.shape for p in params], arr, fields, fields["p"].tolist(),
+                                 fields["n"].tolist()))
 
     def state_dict(self) -> dict:
         """The step count, the state kind and the state tensors themselves."""
@@ -115,6 +120,28 @@ class AdamW:
             mine.copy_(other.reshape(mine.shape))
         self.step_count, self.seed = int(sd["step"]), int(sd["seed"])
 
+    @staticmethod
+    def _gradients(grads, idx, params, shapes, at):
+        """The set of the gradients' types, and each one's type and address (None and 0: no gradient)."""
+        own = grads if len(idx) == len(grads) else [grads[i] for i in idx]
+        try:
+            kinds, ptrs = list(map(_dtype, own)), list(map(_data_ptr, own))
+            found = set(kinds)
+            if (found <= _DTYPE.keys() and list(map(_shape, own)) == shapes and all(map(_is_cuda, own))
+                    and all(map(_is_contiguous, own)) and list(map(_data_ptr, params)) == at):
+                return found, kinds, ptrs
+        except (AttributeError, TypeError):   # not all of them are tensors
+            pass
+        kinds, ptrs = [None] * len(idx), [0] * len(idx)
+        for k, (i, g) in enumerate(zip(idx, own)):
+            if g is None:
+                continue
+            _check(g, f"grads[{i}]", shapes[k], tuple(_DTYPE))
+            if params[k].data_ptr() != at[k]:
+                raise ValueError(f"params[{i}] moved to other memory: build the optimiser again")
+            kinds[k], ptrs[k] = g.dtype, g.data_ptr()
+        return set(kinds), kinds, ptrs
+
     def step(self, grads=None, grad_scale=None, lr: float | None = None, stream=None) -> None:
         """One step.  ``grads``: one gradient per parameter, of its shape, bf16
         or fp32 (default: each ``param.grad``); None entries are skipped.
@@ -135,34 +162,20 @@ class AdamW:
                 raise ValueError("grad_scale: expected one element")
             scale = grad_scale.data_ptr()
         runs = []
-        for dtype, idx, arr, fields, at, lengths in self._groups:
-            kinds = [None] * len(idx)   # each gradient's type
-            ptrs = [0] * len(idx)
-            for k, i in enumerate(idx):
-                g = grads[i]
-                if g is None:
-                    continue
-                kind = g.dtype
-                if kind not in _DTYPE or g.shape != self._shapes[i] or not g.is_cuda or not g.is_contiguous():
-                    _check(g, f"grads[{i}]", self._shapes[i], tuple(_DTYPE))
-                if self.params[i].data_ptr() != at[k]:
-                    raise ValueError(f"params[{i}] moved to other memory: build the optimiser again")
-                kinds[k] = kind
-                ptrs[k] = g.data_ptr()
-            runs.append((dtype, arr, fields, kinds, ptrs, lengths))
+        for dtype, idx, params, shapes, arr, fields, at, lengths in self._groups:
+            runs.append((dtype, arr, fields, lengths, *self._gradients(grads, idx, params, shapes, at)))
         fn = _lib.load().mok_adamw_step
         cfg = _lib.MokAdamwConfig(state=_STATE[self.state], lr=self.lr if lr is None else lr, beta1=self.betas[0],
                                   beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
                                   step=self.step_count + 1, seed=self.seed & (2 ** 64 - 1))
         handle = _raw_stream(self.params[0].get_device()) if self.params else None
-        for dtype, arr, fields, kinds, ptrs, lengths in runs:
+        for dtype, arr, fields, lengths, found, kinds, ptrs in runs:
             cfg.param_dtype = _DTYPE[dtype]
             fields["g"] = ptrs
-            for kind in set(kinds) - {None}:
+            for kind in found - {None}:
                 cfg.grad_dtype = _DTYPE[kind]
                 # a length of 0 leaves a tensor out: no gradient, or one of another type
-                fields["n"] = lengths if kinds.count(kind) == len(kinds) else [
-                    n if t is kind else 0 for n, t in zip(lengths, kinds)]
+                fields["n"] = lengths if len(found) == 1 else [n if t is kind else 0 for n, t in zip(lengths, kinds)]
                 st = fn(C.byref(cfg), arr, len(arr), scale, handle)
                 if st:
                     _fail(st, "mok_adamw_step")
