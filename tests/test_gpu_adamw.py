@@ -138,6 +138,48 @@ def test_mxfp8_states(pt, gt, master):
     assert close_calls <= 1e-3 * total + 3
 
 
+def _kept32(x, rand16, keep_positive):
+    """The codes and scales of fp32 x (whole blocks): E4M3 neighbours chosen by 16 random bits."""
+    b = x.reshape(-1, 32)
+    mant, e = np.frexp(np.abs(b).max(1))
+    s = np.where(mant <= 0.875, e - 9, e - 8).clip(-127, 127)
+    s = np.where(mant == 0, 0, s)
+    y = np.ldexp(b, -s[:, None]).astype(np.float32)
+    off = np.where(np.abs(y) < np.float32(2.0 ** -6), np.float32(2.0 ** -6), np.float32(0))
+    bits = (np.abs(y) + off).astype(np.float32).view(np.uint32) + (rand16.reshape(-1, 32).astype(np.uint32) << np.uint32(4))
+    q = (bits & np.uint32(0xFFF00000)).view(np.float32) - off
+    if keep_positive:
+        q = np.where((y > 0) & (q == 0), np.float32(2.0 ** -9), q)
+    return np.copysign(q, y).reshape(-1), s
+
+
+@pytest.mark.parametrize("seed", [5, 6])
+def test_mxfp8_states_are_those_of_separately_rounded_operations(seed):
+    """m, v and sqrt(v) are each operation rounded once to fp32, so that every
+    element falls on the same side of its random bits as in a restatement of
+    that kind: no code differs, over millions of elements."""
+    n = 1 << 21
+    (p,), b1, b2 = _tensors([n], F32, seed), *HYPER["betas"]
+    opt = mok().AdamW([p.cuda()], state="mxfp8", seed=seed, **HYPER)
+    f = np.float32
+    for step in range(1, 4):
+        g = (_tensors([n], F32, 10 * seed + step)[0] * 0.02)
+        kept = {k: opt.buffers[k][0].cpu().numpy() for k in ("m", "m_scale", "r", "r_scale")}
+        m0 = _decode(kept["m"], kept["m_scale"]).astype(f)
+        r0 = _decode(kept["r"], kept["r_scale"]).astype(f)
+        opt.step([g.cuda()])
+        g = g.numpy()
+        m1 = f(b1) * m0 + f(1 - b1) * g
+        r1 = np.sqrt(f(b2) * (r0 * r0) + f(1 - b2) * g * g)
+        assert m1.dtype == r1.dtype == f
+        bits = _random_bits(n, seed, step, 0)
+        for name, x, rand16 in (("m", m1, bits >> 16), ("r", r1, bits & 0xFFFF)):
+            want, s = _kept32(x, rand16, name == "r")
+            assert np.array_equal(opt.buffers[name + "_scale"][0].cpu().numpy(), s + 127), (step, name)
+            got = _grid_values(opt.buffers[name][0].cpu().numpy())
+            assert np.array_equal(got, want.astype(np.float64)), (step, name, int((got != want).sum()))
+
+
 def test_rounding_is_right_on_average():
     """Steps with a zero gradient shrink r by sqrt(b2) = 0.05% each, far below
     the grid's spacing: after 200 of them the mean has shrunk as it should.
