@@ -212,7 +212,12 @@ struct AdamwIn {
 
 // Persistent blocks of 256 threads over chunks of kAdamwBlock elements, 8 per
 // thread, each chunk within one tensor; a block's next chunk is in flight
-// while it works on this one.
+// while it works on this one.  32-bit states: a chunk to a block, bound by
+// memory; bf16 parameters with master copies, 402.7M elements, 1604 us (7.0
+// TB/s).  MXFP8 states: about 80 instructions an element keep the issue slots
+// busy 81% of the time beside 70% of the memory's peak; the same tensors 1115
+// us (5.8 TB/s).  16 elements a thread took fewer instructions but left fewer
+// warps, and were slower.
 template <class PT, class GT, bool MASTER, bool MX, int CAP>
 __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
     adamw_kernel(const __grid_constant__ AdamwList<CAP> list, const int chunks, const AdamwScalars s) {

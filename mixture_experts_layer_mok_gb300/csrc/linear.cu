@@ -226,6 +226,9 @@ mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sm
 // ---------------------------------------------------------------- dz
 constexpr int kDzRows = 8;   // rows in step in a block; 32 threads x 8 columns wide
 
+// dz = dy act'(z) in bf16, the products' operand type, and per block the column
+// sums of the unrounded values.  Bound by memory: 8192 x 4096 with GELU 31 us
+// for its 201 MB (6.5 TB/s).
 template <class DY, int ACT>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const DY* __restrict__ dy, const uint16_t* __restrict__ z,
                                                         long long M, int N, uint16_t* __restrict__ dz,
