@@ -193,7 +193,9 @@ mok_status_t run_kind(const LinearOperands& o, const LinearParams& q, int num_sm
     if (fills) {
       job.p[0] = p;
       job.problems = 1;
-      if (FWD && p.nk <= kShortK)
+      if (FWD && p.out_f32 && p.nk > kChunk)
+        MOK_CUDA(launch_pair<FWD ? LIN_FWD_F32 : KIND>(job, st));
+      else if (FWD && p.nk <= kShortK)
         MOK_CUDA(launch_pair<FWD ? LIN_FWD_SHORT : KIND>(job, st));
       else
         MOK_CUDA(launch_pair<KIND>(job, st));

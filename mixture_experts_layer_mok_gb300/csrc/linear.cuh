@@ -14,7 +14,8 @@
 //   linear_pair_kernel: persistent CTA pairs (M = 256 rows c over two SMs, 256
 //   columns l, two accumulator buffers), for products with enough 256 x 256
 //   tiles to fill the GPU.  Each thread of the epilogue holds 32 neighbouring
-//   elements of an output row, which leave through TMA stores.
+//   elements of an output row, which leave through TMA stores.  fp32 outputs
+//   are summed in chunks of K.
 //   linear_pair_split_kernel: the same tile with K split over 1 to 4 pairs of a
 //   cluster, which add their parts through distributed shared memory in rank
 //   order, for products of fewer such tiles.  An SM takes in about 64 bytes a
@@ -201,6 +202,19 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane, not waited on.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // ---------------------------------------------------------------- split kernel
@@ -462,6 +476,21 @@ struct PairCfg {
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr uint32_t kIdesc = idesc_bf16(256, BN, BMN, AMN);
 };
+
+// This thread's N columns at TMEM address t, in steps of 16: added to sum, or
+// with BACK the sums put in their place.
+template <int N, bool BACK = false>
+__device__ __forceinline__ void add_columns(uint32_t t, float (&sum)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; j += 16) {
+    float v[16];
+    tmem_ld16(t + j, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[j + i] += v[i];
+    if (BACK) tmem_st16(t + j, sum + j);
+  }
+  if (BACK) asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 
 // Tile idx of the grid of L tiles x C tiles (256 x 256 each): C tiles in
 // groups of p.group, L tiles inside the group's width, so that the CTAs at
@@ -853,13 +882,27 @@ __device__ __forceinline__ bool pair_item(const PairJob& job, int s, int pair, i
   return true;
 }
 
-// KIND: LIN_FWD, LIN_FWD_SHORT (the forward over few K-blocks), or a gradient.
+// KIND: the forward as LIN_FWD, LIN_FWD_SHORT (over few K-blocks) or
+// LIN_FWD_F32 (over more than kChunk of them into fp32), or a gradient.
 template <int KIND>
-using PairKindCfg = PairCfg<KIND != LIN_FWD && KIND != LIN_FWD_SHORT, false, KIND == LIN_FWD_SHORT>;
+constexpr bool kIsForward = KIND == LIN_FWD || KIND == LIN_FWD_SHORT || KIND == LIN_FWD_F32;
+template <int KIND>
+using PairKindCfg = PairCfg<!kIsForward<KIND>, false, KIND == LIN_FWD_SHORT>;
+
+// K-blocks that LIN_FWD_F32 sums in the tensor core before they are added to the
+// sums that the epilogue's registers hold.  The tensor core's additions
+// truncate, which shifts a sum by about 1e-9 of its size per k: in one go, the
+// outputs of K = 4096 are 4.4e-6 off and those of K = 16384 1.9e-5, in chunks
+// 7e-7 both (bf16 outputs, rounded at 2e-3, have no use for it).  What it costs:
+// while a tile's outputs are made, the products are at most a chunk ahead; 8192
+// x 4864 outputs, in one go and in chunks, K = 1024 61 and 69 us, K = 2048 91
+// and 103, K = 4096 168 and 183; 4096 x 8192 x 7168 271 to 298 and 279 to 289.
+// Sixteen epilogue warps: 73, 109 and 195 us.
+constexpr int kChunk = 12;
 
 template <int KIND>
 __global__ void __launch_bounds__(PairKindCfg<KIND>::kThreads, 1) linear_pair_kernel(const __grid_constant__ PairJob job) {
-  constexpr bool FWD = KIND == LIN_FWD || KIND == LIN_FWD_SHORT, AMN = !FWD;
+  constexpr bool FWD = kIsForward<KIND>, AMN = !FWD, CHUNKED = KIND == LIN_FWD_F32;
   using C = PairKindCfg<KIND>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -957,33 +1000,39 @@ __global__ void __launch_bounds__(PairKindCfg<KIND>::kThreads, 1) linear_pair_ke
       bool ok = true;
       PairItem it;
       for (int s = 0; ok && pair_item(job, s, pair, pairs, it); ++s) {
-        if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, status)) break;
-        tc_fence_after();
         const bool b_mn = b_is_mn(it.w);
         const uint64_t bd = b_mn ? linear_desc<true>(smem_u32(smem)) : linear_desc<false>(smem_u32(smem));
         const uint32_t b_step = b_mn ? kStep<true> : kStep<false>;
         const uint32_t idesc = b_mn ? idesc_bf16(256, C::BN, true, AMN) : idesc_bf16(256, C::BN, false, AMN);
         const int nk = job.p[it.w].nk;
-        const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * C::BN);
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!warp_wait(&full[stage], phase, abort_flag, status)) {
+        for (int first = 0; ok && first < nk; first += CHUNKED ? kChunk : nk) {
+          if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, status)) {
             ok = false;
             break;
           }
-          const uint32_t at = stage * C::kStageBytes;
-          if (elect_one()) {
-            umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), idesc, kb != 0);
+          tc_fence_after();
+          const int end = CHUNKED ? min(first + kChunk, nk) : nk;
+          const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * C::BN);
+          for (int kb = first; kb < end; ++kb) {
+            if (!warp_wait(&full[stage], phase, abort_flag, status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t at = stage * C::kStageBytes;
+            if (elect_one()) {
+              umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), idesc, kb != first);
 #pragma unroll
-            for (int kk = 1; kk < kLinBK / 16; ++kk)
-              umma_bf16_pair(acc, desc_at(bd, at + kk * b_step), desc_at(ad, at + kk * kStep<AMN>), idesc, 1u);
-            umma_commit_pair(&empty[stage], 0x3);
-            if (kb == nk - 1) umma_commit_pair(&tfull[buf], 0x3);
+              for (int kk = 1; kk < kLinBK / 16; ++kk)
+                umma_bf16_pair(acc, desc_at(bd, at + kk * b_step), desc_at(ad, at + kk * kStep<AMN>), idesc, 1u);
+              umma_commit_pair(&empty[stage], 0x3);
+              if (kb == end - 1) umma_commit_pair(&tfull[buf], 0x3);
+            }
+            __syncwarp();
+            if (++stage == C::kStages) stage = 0, phase ^= 1;
           }
-          __syncwarp();
-          if (++stage == C::kStages) stage = 0, phase ^= 1;
+          buf ^= 1;
+          if (buf == 0) bphase ^= 1;
         }
-        buf ^= 1;
-        if (buf == 0) bphase ^= 1;
       }
       if (elect_one()) {
         umma_commit_pair(done, 0x1);
@@ -1007,10 +1056,43 @@ __global__ void __launch_bounds__(PairKindCfg<KIND>::kThreads, 1) linear_pair_ke
         const char* r = static_cast<const char*>(p.residual) + (c * p.L + l0) * size;
         for (long long o = 0; o < end * size; o += 128) prefetch_l2(r + o);
       }
-      int w = (lane == 0) ? (mbar_wait(&tfull[buf], bphase, abort_flag, status) ? 1 : 0) : 0;
-      if (!__shfl_sync(0xffffffffu, w, 0)) break;
-      tc_fence_after();
-      const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * C::BN + col0) + (static_cast<uint32_t>(q * 32) << 16);
+      const auto wait_full = [&]() {
+        const int w = lane == 0 ? (mbar_wait(&tfull[buf], bphase, abort_flag, status) ? 1 : 0) : 0;
+        const bool got = __shfl_sync(0xffffffffu, w, 0) != 0;
+        tc_fence_after();
+        return got;
+      };
+      const auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank != 0)
+            mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
+          else
+            mbar_arrive(&tempty[buf]);
+        }
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1;
+      };
+      const auto own_columns = [&]() {
+        return tmem_base + static_cast<uint32_t>(buf * C::BN + col0) + (static_cast<uint32_t>(q * 32) << 16);
+      };
+      if constexpr (CHUNKED) {
+        // all chunks but the last in registers, then onto the last one's, in
+        // TMEM, from where the outputs are made
+        float sum[kCols] = {};
+        bool ok = true;
+        for (int first = 0; first + kChunk < p.nk; first += kChunk) {
+          if (!(ok = wait_full())) break;
+          add_columns<kCols>(own_columns(), sum);
+          release();
+        }
+        if (!ok || !wait_full()) break;
+        add_columns<kCols, true>(own_columns(), sum);
+      } else {
+        if (!wait_full()) break;
+      }
+      const uint32_t tb = own_columns();
 #pragma unroll 1
       for (int k = 0; k < kCols && l0 + k < p.L && row0 < p.C; k += 32) {
         if constexpr (FWD) {
@@ -1025,16 +1107,7 @@ __global__ void __launch_bounds__(PairKindCfg<KIND>::kThreads, 1) linear_pair_ke
           output_block<false, LIN_NONE, false>(p, maps, tb + k, l0 + k, c, row0, stage, slot, lane, false);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank != 0)
-          mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
-        else
-          mbar_arrive(&tempty[buf]);
-      }
-      buf ^= 1;
-      if (buf == 0) bphase ^= 1;
+      release();
     }
     if (lane == 0) bulk_wait<0>();   // this warp's stores are complete before the CTA ends
   }

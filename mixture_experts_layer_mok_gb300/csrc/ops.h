@@ -97,9 +97,9 @@ struct LinearOperands {
 };
 // The device word that a bounded wait which gave up sets (current device).
 cudaError_t linear_status_word(int** word);
-// LIN_GRADS and LIN_FWD_SHORT name kernels only: dx and dW together, and the
-// forward over few K-blocks.
-enum LinKind : int { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2, LIN_GRADS = 3, LIN_FWD_SHORT = 4 };
+// The last three name kernels only: dx and dW together, the forward over few
+// K-blocks, and the forward over many of them into fp32.
+enum LinKind : int { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2, LIN_GRADS = 3, LIN_FWD_SHORT = 4, LIN_FWD_F32 = 5 };
 mok_status_t run_linear(LinKind kind, const LinearOperands& o, const LinearParams& p, int num_sms, cudaStream_t st);
 // dx and dW of one projection, in one launch where both are large enough.
 mok_status_t run_linear_grads(const LinearOperands& ox, const LinearParams& px, const LinearOperands& ow, const LinearParams& pw,

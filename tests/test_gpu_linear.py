@@ -163,6 +163,35 @@ def test_gradient_against_differences():
         assert torch.linalg.norm(out[key].double().cpu() - num) <= 1.5e-2 * torch.linalg.norm(num), key
 
 
+@pytest.mark.parametrize("K", [776, 1536, 1600, 4096])
+@pytest.mark.parametrize("act,bias,res,save_z", [("none", None, None, False), ("gelu", F32, BF16, True)])
+def test_32_bit_outputs_do_not_lose_with_the_length(K, act, bias, res, save_z):
+    """A 2-norm bound that does not grow with K: at most 48 truncating additions
+    in a row, each of half of 2^-23 of the sum so far on average, whose size
+    over them averages two thirds of its last: 48/2 2^-23 2/3, below 2^-19; one
+    row with an infinity beside it."""
+    M, N = 2500, 2056
+    g = torch.Generator().manual_seed(K)
+    x, w = _rand(g, M, K), _rand(g, N, K, std=K ** -0.5)
+    x[7, K - 1] = float("inf")
+    b = None if bias is None else _rand(g, N, dtype=bias, std=0.1)
+    r = None if res is None else _rand(g, M, N, dtype=res)
+    y, z = mok().linear(x.cuda(), w.cuda(), bias=None if b is None else b.cuda(), activation=act,
+                        residual=None if r is None else r.cuda(), out_dtype=F32, save_z=save_z)
+    z64 = x.double().cuda() @ w.double().cuda().T
+    z64 = z64 if b is None else z64 + b.double().cuda()
+    y64 = act64(z64, act)
+    y64 = y64 if r is None else y64 + r.double().cuda()
+    rows = torch.arange(M, device="cuda") != 7
+    assert ((y[rows].double() - y64[rows]).norm() / y64[rows].norm()).item() <= 2.0 ** -19
+    assert torch.isinf(z64[7]).all() and not torch.isfinite(y[7]).all()
+    if save_z:
+        assert ((z[rows].double() - z64[rows]).norm() / z64[rows].norm()).item() <= 2.0 ** -9
+    again, _ = mok().linear(x.cuda(), w.cuda(), bias=None if b is None else b.cuda(), activation=act,
+                            residual=None if r is None else r.cuda(), out_dtype=F32, save_z=save_z)
+    assert torch.equal(again[rows], y[rows])
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 136, 200), (300, 264, 136), (2600, 2048, 72)])
 def test_infinities_and_nan_stay_in_their_rows(M, N, K):
     m = mok()
