@@ -174,10 +174,11 @@ long long pair_tiles(const LinearParams& p) {
 bool is_paired(const LinearParams& p, int pairs) { return p.C > 128 && (p.L > 128 || pair_tiles(p) >= pairs); }
 
 // Up to how many K-blocks the forward runs with twice the epilogue warps for one
-// stage less.  Measured both ways (us; 8 and 16 epilogue warps), 8192 x 4864
-// outputs: K = 272 40 and 36 plain, 67 and 53 with bias and GELU, 79 and 65 with
-// a residual; K = 1024 50 and 50, 74 and 61, 87 and 73; K = 1536 66 and 68, 79
-// and 73, fp32 with bias 74 and 79; K = 2048 85 and 87, 91 and 91, fp32 92 and 98.
+// stage less (fp32 outputs: up to kChunk).  Measured both ways (us; 8 and 16
+// epilogue warps), 8192 x 4864 outputs: K = 272 40 and 36 plain, 67 and 53 with
+// bias and GELU, 79 and 65 with a residual, 50 and 44 in fp32; K = 1024 50 and
+// 50, 74 and 61, 87 and 73; K = 1536 66 and 68, 79 and 73; K = 2048 85 and 87,
+// 91 and 91.
 constexpr int kShortK = 16;
 
 template <int KIND>
