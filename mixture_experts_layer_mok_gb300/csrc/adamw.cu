@@ -214,9 +214,9 @@ struct AdamwIn {
 // thread, each chunk within one tensor; a block's next chunk is in flight
 // while it works on this one.  32-bit states: a chunk to a block, bound by
 // memory; bf16 parameters with master copies, 402.7M elements, 1604 us (7.0
-// TB/s).  MXFP8 states: about 80 instructions an element keep the issue slots
-// busy 81% of the time beside 70% of the memory's peak; the same tensors 1115
-// us (5.8 TB/s).  16 elements a thread took fewer instructions but left fewer
+// TB/s).  MXFP8 states: 95 instructions an element keep the issue slots busy
+// 84% of the time beside 64 to 70% of the memory's peak; the same tensors 1158
+// us (5.6 TB/s).  16 elements a thread took fewer instructions but left fewer
 // warps, and were slower.
 template <class PT, class GT, bool MASTER, bool MX, int CAP>
 __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
     // What the states keep is formed by single roundings, no fused ones, and the
     // root rounded correctly: a last-bit difference would put one element in
     // 10^6 on the other side of its random bits, a whole code away from a
-    // restatement in 32 bits.  It costs no time (402.7M elements 1500 us with
-    // two readers either way).
+    // restatement in 32 bits.  With fused operations and an approximate root
+    // 402.7M elements take 1144 us, this way 1158.
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float gi = g[i] * gs;
