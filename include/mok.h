@@ -591,6 +591,22 @@ typedef struct {
 mok_status_t mok_adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
                             const float* grad_scale, void* stream);
 
+/* The step in a CUDA graph.  mok_adamw_step takes the step's number, the
+ * learning rate and the seed when it is called, so a graph that holds it would
+ * repeat that one step.  These two count on the device: mok_adamw_advance adds
+ * 1 to the counter, once a step, and mok_adamw_step_counted takes step number
+ * cfg->step (>= 0) + count.  A sequence of them does what mok_adamw_step does
+ * with the same numbers, called or replayed.
+ * counter: MOK_ADAMW_COUNTER_BYTES of device memory, 16-byte aligned, which
+ * the caller sets once and may change between steps: int64 count (0); double
+ * lr, which replaces cfg->lr where it is not NaN and fixed_lr is 0; uint64
+ * seed_change, which the seed is xor-ed with (0).  The rest is the library's.
+ * Betas, eps, weight_decay and the tensor list stay those of the call. */
+#define MOK_ADAMW_COUNTER_BYTES 64
+mok_status_t mok_adamw_advance(const mok_adamw_config_t* cfg, int fixed_lr, void* counter, void* stream);
+mok_status_t mok_adamw_step_counted(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
+                                    const float* grad_scale, const void* counter, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -85,6 +85,7 @@ MOK_NORM_MAX_H = 32768
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 MOK_ADAMW_STATE_F32 = 0
 MOK_ADAMW_STATE_MXFP8 = 1
+MOK_ADAMW_COUNTER_BYTES = 64
 
 
 class MokAdamwConfig(C.Structure):
@@ -131,6 +132,8 @@ SIGNATURES = {
                                  P]),
     "mok_linear_status": (C.c_int, [I32P]),
     "mok_adamw_step": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int, P, P]),
+    "mok_adamw_step_counted": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int, P, P, P]),
+    "mok_adamw_advance": (C.c_int, [C.POINTER(MokAdamwConfig), C.c_int, P, P]),
 }
 
 _lib = None

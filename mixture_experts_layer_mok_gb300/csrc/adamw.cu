@@ -218,13 +218,18 @@ struct AdamwIn {
 // 84% of the time beside 64 to 70% of the memory's peak; the same tensors 1158
 // us (5.6 TB/s).  16 elements a thread took fewer instructions but left fewer
 // warps, and were slower.
-template <class PT, class GT, bool MASTER, bool MX, int CAP>
+// COUNTED: what depends on the step count comes from device memory.
+template <class PT, class GT, bool MASTER, bool MX, int CAP, bool COUNTED>
 __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
-    adamw_kernel(const __grid_constant__ AdamwList<CAP> list, const int chunks, const AdamwScalars s) {
+    adamw_kernel(const __grid_constant__ AdamwList<CAP> list, const int chunks, const AdamwScalars s,
+                 const AdamwCounter* counter) {
   using In = AdamwIn<PT, GT, MASTER, MX>;
   griddep_wait();
   griddep_launch_dependents();
   const float gs = s.grad_scale ? __ldg(s.grad_scale) : 1.f;
+  const float decay = COUNTED ? counter->decay : s.decay, step_size = COUNTED ? counter->step_size : s.step_size;
+  const float inv_sqrt_bc2 = COUNTED ? counter->inv_sqrt_bc2 : s.inv_sqrt_bc2;
+  const uint32_t step_key = COUNTED ? counter->key : 0u;
   In next;
   next.load(list, blockIdx.x, 0);
   for (int c = blockIdx.x; c < chunks;) {
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
       m[i] = __fadd_rn(__fmul_rn(s.beta1, m[i]), __fmul_rn(s.one_minus_beta1, gi));
       v[i] = __fadd_rn(__fmul_rn(s.beta2, v[i]), __fmul_rn(__fmul_rn(s.one_minus_beta2, gi), gi));
       r[i] = __fsqrt_rn(v[i]);
-      p[i] = fmaf(-s.step_size, m[i] * fast_rcp(fmaf(r[i], s.inv_sqrt_bc2, s.eps)), p[i] * s.decay);
+      p[i] = fmaf(-step_size, m[i] * fast_rcp(fmaf(r[i], inv_sqrt_bc2, s.eps)), p[i] * decay);
     }
     if (MASTER) store8(t.master + in.i0, whole, left, p);
     store8(static_cast<PT*>(t.p) + in.i0, whole, left, p);
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
       const long long block = in.i0 >> 5;
       uint32_t rand[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rand[i] = mix_bits(static_cast<uint32_t>(in.i0) + i, t.key);
+      for (int i = 0; i < 8; ++i) rand[i] = mix_bits(static_cast<uint32_t>(in.i0) + i, t.key + step_key);
       store_codes8<false>(static_cast<uint8_t*>(t.m) + in.i0, t.m_scale, block, whole, left, m, rand);
       store_codes8<true>(static_cast<uint8_t*>(t.v) + in.i0, t.r_scale, block, whole, left, r, rand);
     } else {
@@ -276,8 +281,9 @@ __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
 
 // The list is handed over by address: through the launch templates, which take
 // arguments by value, its 30 KB would be copied twice more.
-template <class PT, class GT, bool MASTER, bool MX, int CAP>
-cudaError_t launch_cap(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, cudaStream_t st) {
+template <class PT, class GT, bool MASTER, bool MX, int CAP, bool COUNTED>
+cudaError_t launch_cap(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, const AdamwCounter* counter,
+                       cudaStream_t st) {
   AdamwList<CAP> list;
   memcpy(list.t, t, sizeof(AdamwTensor) * n);
   list.n = n;
@@ -292,35 +298,55 @@ cudaError_t launch_cap(const AdamwTensor* t, int n, int chunks, const AdamwScala
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   AdamwScalars scalars = s;
-  void* args[] = {&list, &chunks, &scalars};
-  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(adamw_kernel<PT, GT, MASTER, MX, CAP>), args);
+  void* args[] = {&list, &chunks, &scalars, &counter};
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(adamw_kernel<PT, GT, MASTER, MX, CAP, COUNTED>), args);
 }
 
 template <class PT, class GT, bool MASTER, bool MX>
-cudaError_t launch_typed(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, cudaStream_t st) {
-  if (n <= 16) return launch_cap<PT, GT, MASTER, MX, 16>(t, n, chunks, s, st);
-  if (n <= 128) return launch_cap<PT, GT, MASTER, MX, 128>(t, n, chunks, s, st);
-  return launch_cap<PT, GT, MASTER, MX, kAdamwMaxTensors>(t, n, chunks, s, st);
+cudaError_t launch_typed(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, const AdamwCounter* counter,
+                         cudaStream_t st) {
+  // a counted step's list is copied at its capture only: one size will do
+  if (counter) return launch_cap<PT, GT, MASTER, MX, kAdamwMaxTensors, true>(t, n, chunks, s, counter, st);
+  if (n <= 16) return launch_cap<PT, GT, MASTER, MX, 16, false>(t, n, chunks, s, nullptr, st);
+  if (n <= 128) return launch_cap<PT, GT, MASTER, MX, 128, false>(t, n, chunks, s, nullptr, st);
+  return launch_cap<PT, GT, MASTER, MX, kAdamwMaxTensors, false>(t, n, chunks, s, nullptr, st);
 }
 
 template <class PT, class GT, bool MASTER>
-cudaError_t launch_state(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, int mx, cudaStream_t st) {
-  return mx ? launch_typed<PT, GT, MASTER, true>(t, n, chunks, s, st)
-            : launch_typed<PT, GT, MASTER, false>(t, n, chunks, s, st);
+cudaError_t launch_state(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, const AdamwCounter* counter, int mx,
+                         cudaStream_t st) {
+  return mx ? launch_typed<PT, GT, MASTER, true>(t, n, chunks, s, counter, st)
+            : launch_typed<PT, GT, MASTER, false>(t, n, chunks, s, counter, st);
+}
+
+// One step more, and what depends on its number, in 64 bits as on the host.
+__global__ void adamw_advance_kernel(const AdamwAdvance a, AdamwCounter* c) {
+  griddep_wait();   // the step before this one has read what is written here
+  griddep_launch_dependents();
+  const long long count = ++c->count, step = a.step + count;
+  const double lr = a.fixed_lr || isnan(c->lr) ? a.lr : c->lr;
+  c->decay = static_cast<float>(1.0 - lr * a.weight_decay);
+  c->step_size = static_cast<float>(lr / (1.0 - pow(a.beta1, static_cast<double>(step))));
+  c->inv_sqrt_bc2 = static_cast<float>(1.0 / sqrt(1.0 - pow(a.beta2, static_cast<double>(step))));
+  c->key = adamw_step_key(a.seed ^ c->seed_change, step);
 }
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, int p_f32, int g_f32,
-                         int master, int mx, cudaStream_t st) {
+cudaError_t launch_adamw_advance(const AdamwAdvance& a, AdamwCounter* counter, cudaStream_t st) {
+  return launch_dependent(adamw_advance_kernel, dim3(1), dim3(1), 0, st, a, counter);
+}
+
+cudaError_t launch_adamw(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, const AdamwCounter* counter, int p_f32,
+                         int g_f32, int master, int mx, cudaStream_t st) {
   if (p_f32)
-    return g_f32 ? launch_state<float, float, false>(t, n, chunks, s, mx, st)
-                 : launch_state<float, uint16_t, false>(t, n, chunks, s, mx, st);
+    return g_f32 ? launch_state<float, float, false>(t, n, chunks, s, counter, mx, st)
+                 : launch_state<float, uint16_t, false>(t, n, chunks, s, counter, mx, st);
   if (master)
-    return g_f32 ? launch_state<uint16_t, float, true>(t, n, chunks, s, mx, st)
-                 : launch_state<uint16_t, uint16_t, true>(t, n, chunks, s, mx, st);
-  return g_f32 ? launch_state<uint16_t, float, false>(t, n, chunks, s, mx, st)
-               : launch_state<uint16_t, uint16_t, false>(t, n, chunks, s, mx, st);
+    return g_f32 ? launch_state<uint16_t, float, true>(t, n, chunks, s, counter, mx, st)
+                 : launch_state<uint16_t, uint16_t, true>(t, n, chunks, s, counter, mx, st);
+  return g_f32 ? launch_state<uint16_t, float, false>(t, n, chunks, s, counter, mx, st)
+               : launch_state<uint16_t, uint16_t, false>(t, n, chunks, s, counter, mx, st);
 }
 
 }  // namespace mok

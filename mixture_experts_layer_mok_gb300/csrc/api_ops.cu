@@ -238,18 +238,28 @@ mok_status_t mok_linear_status(int* status) {
 }
 
 // ---------------------------------------------------------------- AdamW
-mok_status_t mok_adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
-                            const float* grad_scale, void* stream) {
-  NvtxRange nvtx("mok_adamw_step");
+}  // extern "C"
+
+namespace {
+
+// counted: cfg->step is what is added to a count of at least 1.
+mok_status_t check_adamw(const mok_adamw_config_t* cfg, bool counted) {
   if (!cfg) return fail(MOK_ERR_INVALID_ARG, "NULL config");
-  if (num_tensors < 0 || (num_tensors > 0 && !tensors)) return fail(MOK_ERR_INVALID_ARG, "bad tensor list");
   if (!is_dtype(cfg->param_dtype) || !is_dtype(cfg->grad_dtype)) return fail(MOK_ERR_INVALID_ARG, "unknown dtype");
   if (cfg->state != MOK_ADAMW_STATE_F32 && cfg->state != MOK_ADAMW_STATE_MXFP8)
     return fail(MOK_ERR_INVALID_ARG, "unknown state kind");
   if (!std::isfinite(cfg->lr) || !(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) || !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) ||
       !(cfg->eps >= 0.0) || !std::isfinite(cfg->eps) || !std::isfinite(cfg->weight_decay))
     return fail(MOK_ERR_INVALID_ARG, "need finite lr, eps >= 0 and weight_decay, and betas in [0, 1)");
-  if (cfg->step < 1) return fail(MOK_ERR_INVALID_ARG, "step counts from 1");
+  if (cfg->step < (counted ? 0 : 1)) return fail(MOK_ERR_INVALID_ARG, "step counts from %d", counted ? 0 : 1);
+  return MOK_OK;
+}
+
+mok_status_t adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
+                        const float* grad_scale, const AdamwCounter* counter, void* stream) {
+  mok_status_t st = check_adamw(cfg, counter != nullptr);
+  if (st) return st;
+  if (num_tensors < 0 || (num_tensors > 0 && !tensors)) return fail(MOK_ERR_INVALID_ARG, "bad tensor list");
   const bool mx = cfg->state == MOK_ADAMW_STATE_MXFP8, p_f32 = cfg->param_dtype == MOK_DTYPE_F32;
   const bool master = num_tensors > 0 && tensors[0].master != nullptr;
   if (master && p_f32) return fail(MOK_ERR_INVALID_ARG, "master copies go with bf16 parameters");
@@ -265,27 +275,30 @@ mok_status_t mok_adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tenso
       return fail(MOK_ERR_INVALID_ARG, "tensor %d: misaligned pointer", i);
   }
   int sms = 0;
-  mok_status_t st = device_info(&sms);
+  st = device_info(&sms);
   if (st) return st;
-  const double bc1 = 1.0 - std::pow(cfg->beta1, static_cast<double>(cfg->step));
-  const double bc2 = 1.0 - std::pow(cfg->beta2, static_cast<double>(cfg->step));
   AdamwScalars s = {};
   s.beta1 = static_cast<float>(cfg->beta1);
   s.one_minus_beta1 = static_cast<float>(1.0 - cfg->beta1);
   s.beta2 = static_cast<float>(cfg->beta2);
   s.one_minus_beta2 = static_cast<float>(1.0 - cfg->beta2);
-  s.decay = static_cast<float>(1.0 - cfg->lr * cfg->weight_decay);
-  s.step_size = static_cast<float>(cfg->lr / bc1);
-  s.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
   s.eps = static_cast<float>(cfg->eps);
   s.grad_scale = grad_scale;
-  const uint32_t key0 = static_cast<uint32_t>(cfg->seed * 0x9E3779B1ull + static_cast<uint64_t>(cfg->step) * 0xB504F333ull);
+  uint32_t key0 = 0;
+  if (!counter) {
+    const double bc1 = 1.0 - std::pow(cfg->beta1, static_cast<double>(cfg->step));
+    const double bc2 = 1.0 - std::pow(cfg->beta2, static_cast<double>(cfg->step));
+    s.decay = static_cast<float>(1.0 - cfg->lr * cfg->weight_decay);
+    s.step_size = static_cast<float>(cfg->lr / bc1);
+    s.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
+    key0 = adamw_step_key(cfg->seed, cfg->step);
+  }
   AdamwTensor list[kAdamwMaxTensors];
   int n = 0;
   long long blocks = 0;
   const auto flush = [&]() {
     const cudaError_t err = n == 0 ? cudaSuccess
-                                   : launch_adamw(list, n, static_cast<int>(blocks), s, p_f32,
+                                   : launch_adamw(list, n, static_cast<int>(blocks), s, counter, p_f32,
                                                   cfg->grad_dtype == MOK_DTYPE_F32, master, mx,
                                                   static_cast<cudaStream_t>(stream));
     n = 0;
@@ -311,6 +324,43 @@ mok_status_t mok_adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tenso
     blocks += b;
   }
   MOK_CUDA(flush());
+  return MOK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mok_status_t mok_adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
+                            const float* grad_scale, void* stream) {
+  NvtxRange nvtx("mok_adamw_step");
+  return adamw_step(cfg, tensors, num_tensors, grad_scale, nullptr, stream);
+}
+
+mok_status_t mok_adamw_step_counted(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
+                                    const float* grad_scale, const void* counter, void* stream) {
+  NvtxRange nvtx("mok_adamw_step_counted");
+  if (!counter || !aligned16(counter)) return fail(MOK_ERR_INVALID_ARG, "counter: NULL or misaligned pointer");
+  return adamw_step(cfg, tensors, num_tensors, grad_scale, static_cast<const AdamwCounter*>(counter), stream);
+}
+
+mok_status_t mok_adamw_advance(const mok_adamw_config_t* cfg, int fixed_lr, void* counter, void* stream) {
+  NvtxRange nvtx("mok_adamw_advance");
+  mok_status_t st = check_adamw(cfg, true);
+  if (st) return st;
+  if (!counter || !aligned16(counter)) return fail(MOK_ERR_INVALID_ARG, "counter: NULL or misaligned pointer");
+  int sms = 0;
+  st = device_info(&sms);
+  if (st) return st;
+  AdamwAdvance a = {};
+  a.lr = cfg->lr;
+  a.weight_decay = cfg->weight_decay;
+  a.beta1 = cfg->beta1;
+  a.beta2 = cfg->beta2;
+  a.step = cfg->step;
+  a.seed = cfg->seed;
+  a.fixed_lr = fixed_lr;
+  MOK_CUDA(launch_adamw_advance(a, static_cast<AdamwCounter*>(counter), static_cast<cudaStream_t>(stream)));
   return MOK_OK;
 }
 

@@ -132,10 +132,32 @@ struct AdamwScalars {
   float eps;
   const float* grad_scale;  // device scalar or NULL
 };
+// What a counted step reads in place of the scalars above: in device memory,
+// so that a replayed graph takes the step that is due.
+struct AdamwCounter {
+  long long count;       // steps counted
+  double lr;             // NaN: the call's
+  uint64_t seed_change;  // the seed is the call's, exclusive-or this
+  float decay, step_size, inv_sqrt_bc2;   // written by launch_adamw_advance
+  uint32_t key;                           // the step's and the seed's share of the tensors' keys
+};
+static_assert(sizeof(AdamwCounter) <= MOK_ADAMW_COUNTER_BYTES, "the documented size");
+struct AdamwAdvance {
+  double lr, weight_decay, beta1, beta2;
+  long long step;   // added to the count
+  uint64_t seed;
+  int fixed_lr;     // lr as it is here, whatever the counter says
+};
+cudaError_t launch_adamw_advance(const AdamwAdvance& a, AdamwCounter* counter, cudaStream_t st);
+// The step's and the seed's share of a tensor's key, and the tensor's.
+__host__ __device__ constexpr uint32_t adamw_step_key(uint64_t seed, long long step) {
+  return static_cast<uint32_t>(seed * 0x9E3779B1ull + static_cast<uint64_t>(step) * 0xB504F333ull);
+}
 constexpr int kAdamwBlock = 2048;   // elements per chunk, the work of one block at a time
 // Tensors one launch takes at most, and the launch itself; t[i].first is set.
+// counter: NULL, or of a counted step (t[i].key is the tensor's share alone).
 constexpr int kAdamwMaxTensors = 400;
-cudaError_t launch_adamw(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, int p_f32, int g_f32,
-                         int master, int mx, cudaStream_t st);
+cudaError_t launch_adamw(const AdamwTensor* t, int n, int chunks, const AdamwScalars& s, const AdamwCounter* counter, int p_f32,
+                         int g_f32, int master, int mx, cudaStream_t st);
 
 }  // namespace mok

@@ -3,6 +3,7 @@ marshalling only: the step is libmok's ``mok_adamw_step``)."""
 from __future__ import annotations
 
 import ctypes as C
+import math
 from operator import attrgetter
 
 import numpy as np
@@ -14,6 +15,8 @@ from .ops import _DTYPE, _check, _fail, _raw_stream
 _STATE = {"fp32": _lib.MOK_ADAMW_STATE_F32, "mxfp8": _lib.MOK_ADAMW_STATE_MXFP8}
 _KEPT = {"fp32": ("m", "v"), "mxfp8": ("m", "m_scale", "r", "r_scale")}
 _FIELD = {"masters": "master", "m": "m", "v": "v", "r": "v", "m_scale": "m_scale", "r_scale": "v_scale"}
+_COUNT, _LR, _SEED_CHANGE = 0, 1, 2   # the counter's 64-bit fields
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 # over a list, map() of these takes a third less time than a loop's body
 _data_ptr, _is_contiguous = torch.Tensor.data_ptr, torch.Tensor.is_contiguous
 _dtype, _shape, _is_cuda = attrgetter("dtype"), attrgetter("shape"), attrgetter("is_cuda")
@@ -31,7 +34,13 @@ class AdamW:
 
     ``buffers`` hands in state tensors instead of fresh zeros: a dict of lists
     (one entry per parameter, None for a master of an fp32 parameter) with the
-    keys of ``state_dict()["buffers"]``; ``step`` is the count they stand at."""
+    keys of ``state_dict()["buffers"]``; ``step`` is the count they stand at.
+
+    A step may be captured in a CUDA graph: each replay is the step that is due,
+    and ``step_count`` and ``state_dict()`` (which then wait for the device)
+    count it.  Replays follow ``lr``, ``step_count``, ``seed`` and
+    ``load_state_dict`` as these are set between them; betas, eps, the weight
+    decay and an ``lr`` given to the captured ``step`` itself stay as they were."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                  state: str = "fp32", master: bool = False, seed: int = 0, step: int = 0, buffers: dict | None = None):
@@ -40,8 +49,16 @@ class AdamW:
             raise ValueError(f"state must be one of {sorted(_STATE)}")
         for i, p in enumerate(self.params):
             _check(p, f"params[{i}]", None, (torch.bfloat16, torch.float32))
-        self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
-        self.state, self.seed, self.step_count = state, int(seed), int(step)
+        # the host's share of what a step reads; from the first captured step on
+        # `_counter` on the device holds the count of the steps since, and what
+        # replaces lr and seed
+        self._base_lr, self._base_seed, self._base_step = lr, int(seed), int(step)
+        self._captured, self._device_lr, self._seed_change = False, None, 0
+        self._counter = None
+        if self.params:
+            self._counter = torch.zeros(_lib.MOK_ADAMW_COUNTER_BYTES // 8, dtype=torch.int64, device=self.params[0].device)
+            self._counter.view(torch.float64)[_LR].fill_(float("nan"))
+        self.betas, self.eps, self.weight_decay, self.state = tuple(betas), eps, weight_decay, state
         if buffers is None:
             buffers = self._fresh(master)
         self._take(buffers)
@@ -97,6 +114,44 @@ class AdamW:
             params = [self.params[i] for i in idx]
             self._groups.append((dtype, idx, params, [p.shape for p in params], arr, fields, fields["p"].tolist(),
                                  fields["n"].tolist()))
+
+    @property
+    def lr(self) -> float:
+        return self._base_lr if self._device_lr is None else self._device_lr
+
+    @lr.setter
+    def lr(self, value: float) -> None:
+        if self._captured:
+            if not math.isfinite(value):
+                raise ValueError("lr must be finite")
+            self._counter.view(torch.float64)[_LR].fill_(value)
+            self._device_lr = value
+        else:
+            self._base_lr = value
+
+    @property
+    def seed(self) -> int:
+        return self._base_seed ^ self._seed_change
+
+    @seed.setter
+    def seed(self, value: int) -> None:
+        if self._captured:
+            self._seed_change = self._base_seed ^ int(value)
+            low = self._seed_change & (2 ** 64 - 1)
+            self._counter[_SEED_CHANGE].fill_(low - 2 ** 64 if low >> 63 else low)
+        else:
+            self._base_seed = int(value)
+
+    @property
+    def step_count(self) -> int:
+        return self._base_step + (int(self._counter[_COUNT]) if self._captured else 0)
+
+    @step_count.setter
+    def step_count(self, value: int) -> None:
+        if self._captured:
+            self._counter[_COUNT].fill_(int(value) - self._base_step)
+        else:
+            self._base_step = int(value)
 
     def state_dict(self) -> dict:
         """The step count, the state kind and the state tensors themselves."""
@@ -164,11 +219,18 @@ class AdamW:
         runs = []
         for dtype, idx, params, shapes, arr, fields, at, lengths in self._groups:
             runs.append((dtype, arr, fields, lengths, *self._gradients(grads, idx, params, shapes, at)))
-        fn = _lib.load().mok_adamw_step
-        cfg = _lib.MokAdamwConfig(state=_STATE[self.state], lr=self.lr if lr is None else lr, beta1=self.betas[0],
+        lib = _lib.load()
+        if not self._captured and runs and _capturing():
+            self._captured = True   # for good: only the device knows how often the graph runs
+        counted = self._captured
+        cfg = _lib.MokAdamwConfig(state=_STATE[self.state], lr=self._base_lr if lr is None else lr, beta1=self.betas[0],
                                   beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
-                                  step=self.step_count + 1, seed=self.seed & (2 ** 64 - 1))
+                                  step=self._base_step + (not counted), seed=self._base_seed & (2 ** 64 - 1))
         handle = _raw_stream(self.params[0].get_device()) if self.params else None
+        if counted:
+            st = lib.mok_adamw_advance(C.byref(cfg), lr is not None, self._counter.data_ptr(), handle)
+            if st:
+                _fail(st, "mok_adamw_advance")
         for dtype, arr, fields, lengths, found, kinds, ptrs in runs:
             cfg.param_dtype = _DTYPE[dtype]
             fields["g"] = ptrs
@@ -176,10 +238,14 @@ class AdamW:
                 cfg.grad_dtype = _DTYPE[kind]
                 # a length of 0 leaves a tensor out: no gradient, or one of another type
                 fields["n"] = lengths if len(found) == 1 else [n if t is kind else 0 for n, t in zip(lengths, kinds)]
-                st = fn(C.byref(cfg), arr, len(arr), scale, handle)
+                if counted:
+                    st = lib.mok_adamw_step_counted(C.byref(cfg), arr, len(arr), scale, self._counter.data_ptr(), handle)
+                else:
+                    st = lib.mok_adamw_step(C.byref(cfg), arr, len(arr), scale, handle)
                 if st:
                     _fail(st, "mok_adamw_step")
         # the parameters changed under autograd's eyes: a backward that saved
         # them before this step has to notice
         torch.autograd.graph.increment_version(self.params)
-        self.step_count += 1
+        if not counted:
+            self._base_step += 1

@@ -319,3 +319,69 @@ def test_refusals():
     with pytest.raises(m.MokError):
         m.AdamW([torch.zeros(65, device="cuda")[1:]]).step([p])
     assert opt.step_count == 0 and bool((p == 0).all())
+
+
+def _graph_of(step):
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    return graph
+
+
+@pytest.mark.parametrize("state,master", [("fp32", False), ("mxfp8", False), ("mxfp8", True), ("fp32", True)])
+@pytest.mark.parametrize("warm", [0, 2])
+def test_a_captured_step_replays_the_step_that_is_due(state, master, warm):
+    """Replays, steps called in between, and changes of the learning rate, the
+    count, the seed and the state: every bit as in an optimiser that is never
+    captured."""
+    m = mok()
+    pt = BF16 if master else F32
+    lengths = [300, 2048, 33]
+
+    def fresh(**kw):
+        ps = [p.cuda() for p in _tensors(lengths, pt, 3)] + [torch.ones(70, device="cuda")]
+        return ps, m.AdamW(ps, state=state, master=master, **{**HYPER, "seed": 4, **kw})
+
+    (ps, opt), (qs, twin) = fresh(), fresh()
+    gs = [torch.empty(n, device="cuda") for n in lengths + [70]]
+    gs[1] = gs[1].to(BF16)                      # two gradient types: several launches a step
+    scale = torch.ones(1, device="cuda")
+    draws = iter(range(1000, 2000))
+
+    def both(one, **kw):
+        for t, r in zip(gs, _tensors(lengths + [70], F32, next(draws))):
+            t.copy_(0.02 * r)
+        one()
+        twin.step([t.clone() for t in gs], grad_scale=scale, **kw)
+        assert opt.step_count == twin.step_count
+        for a, b in zip(ps, qs):
+            assert torch.equal(a, b)
+        for name in opt.buffers:
+            assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(opt.buffers[name], twin.buffers[name]))
+
+    call = lambda: opt.step(gs, grad_scale=scale)  # noqa: E731
+    for _ in range(warm):
+        both(call)
+    graph = _graph_of(call)
+    assert opt.step_count == warm               # nothing ran yet
+    for _ in range(3):
+        both(graph.replay)
+    both(call)
+    opt.lr = twin.lr = 3e-3
+    both(graph.replay)
+    both(call)
+    fixed = _graph_of(lambda: opt.step(gs, grad_scale=scale, lr=0.1))
+    both(fixed.replay, lr=0.1)
+    both(graph.replay)
+    assert opt.lr == 3e-3
+    other = fresh(seed=2 ** 63 + 9, step=7)[1]
+    other.step([torch.ones_like(p) for p in other.params])
+    for o in (opt, twin):
+        o.load_state_dict(other.state_dict())
+    assert opt.step_count == 8 and opt.seed == 2 ** 63 + 9
+    both(graph.replay)
+    both(call)
+    assert opt.state_dict()["step"] == 10
+    with pytest.raises(ValueError):
+        opt.lr = float("nan")

@@ -129,3 +129,18 @@ def test_python_faces_refuse_cpu_tensors_and_wrong_shapes():
     assert opt.state_dict()["step"] == 0
     with pytest.raises(ValueError):
         opt.step([x])
+
+
+def test_counted_adamw_refusals(lib):
+    from mixture_experts_layer_mok_gb300 import _lib
+
+    def cfg(**kw):
+        c = dict(param_dtype=1, grad_dtype=1, state=0, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.0, step=0)
+        return _lib.MokAdamwConfig(**{**c, **kw})
+
+    t = (_lib.MokAdamwTensor * 1)(_lib.MokAdamwTensor(p=16, g=16, m=16, v=24, n=64))
+    for c, counter in ((cfg(), None), (cfg(), ODD), (cfg(step=-1), FAKE), (cfg(lr=float("inf")), FAKE), (cfg(beta2=1.0), FAKE)):
+        assert lib.mok_adamw_advance(C.byref(c), 0, counter, None) == BAD
+        assert lib.mok_adamw_step_counted(C.byref(c), t, 0, None, counter, None) == BAD
+    assert lib.mok_adamw_advance(None, 0, FAKE, None) == BAD
+    assert lib.mok_adamw_step_counted(C.byref(cfg()), t, 1, None, FAKE, None) == BAD     # v is misaligned
