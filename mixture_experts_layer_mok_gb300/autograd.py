@@ -8,12 +8,51 @@ mok_experts": ``_MoKRuntime.forward`` / ``backward``, ``GroupedExpertsMoK``).
 This module puts those two calls under torch.autograd, so that a model can
 call the layer like any other module.  It only marshals arguments: the
 schedule, forward and backward run in libmok's kernels through the binding.
+First derivatives only: differentiating a gradient raises RuntimeError.
 """
 from __future__ import annotations
+
+import functools
 
 import torch
 
 from . import Context, Schedule, Weights, backward, forward, ops, quantize_weights, schedule
+
+
+class _NoSecondDerivative(torch.autograd.Function):
+    """The identity, with a backward that refuses."""
+
+    @staticmethod
+    def forward(ctx, name, *grads):
+        ctx.name = name
+        return grads
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name}: the gradients come from a kernel and have no derivative of their own")
+
+
+def _first_order(backward):
+    """A backward whose gradients refuse to be differentiated.  Under
+    ``create_graph`` they would otherwise pass for constants, and what a loss
+    makes of them would be lost without a word; that holds even where the
+    incoming gradient needs none, as they depend on the saved tensors too."""
+
+    @functools.wraps(backward)
+    def wrapper(ctx, *args):
+        with torch.no_grad():
+            out = backward(ctx, *args)
+        if torch.is_grad_enabled():
+            at = [i for i, g in enumerate(out) if g is not None]
+            marked = _NoSecondDerivative.apply(type(ctx).__name__.removesuffix("Backward"),
+                                               *(out[i].detach().requires_grad_() for i in at))
+            out = list(out)
+            for i, g in zip(at, marked):
+                out[i] = g
+            out = tuple(out)
+        return out
+
+    return wrapper
 
 
 class MoKFunction(torch.autograd.Function):
@@ -40,6 +79,7 @@ class MoKFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x, router_w, sbuf, cbuf = ctx.saved_tensors
         smeta, cmeta, weights, minibatch, macrobatch, shared = ctx.mok
@@ -112,6 +152,7 @@ class RMSNormFunction(torch.autograd.Function):
         return out.y, x.view_as(x) if residual is None else out.h, codes, scales
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, dh, _codes, _scales):
         h, weight, rstd = ctx.saved_tensors
         x_type, res_type = ctx.types
@@ -162,6 +203,7 @@ class LinearFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x, weight, z = ctx.saved_tensors
         activation, bias_type, res_type = ctx.linear
