@@ -31,9 +31,20 @@ def _ptr(t):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+_current_device = torch._C._cuda_getDevice
+
+
 def _stream(stream):
+    if stream is not None and stream.device_index != _current_device():
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, but the current device is cuda:{_current_device()}")
     s = stream if stream is not None else torch.cuda.current_stream()
     return C.c_void_p(s.cuda_stream)
+
+
+def _on_current(t, name):
+    """Refuses a CUDA tensor of another device: the library launches on the current one."""
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{_current_device()}")
 
 
 def _need(t, dtype, shape, name):
@@ -42,6 +53,7 @@ def _need(t, dtype, shape, name):
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    _on_current(t, name)
     return t
 
 
@@ -216,6 +228,7 @@ def mxfp8_quantize(x: torch.Tensor, stream=None):
     lib = _lib.load()
     if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be contiguous CUDA bf16")
+    _on_current(x, "x")
     K = x.shape[-1]
     rows = x.numel() // K if K else 0
     codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
@@ -232,6 +245,7 @@ def mxfp8_quantize_t(x: torch.Tensor, stream=None):
     lib = _lib.load()
     if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.dim() not in (2, 3):
         raise ValueError("x must be a contiguous CUDA bf16 matrix or batch of matrices")
+    _on_current(x, "x")
     x3 = x if x.dim() == 3 else x.unsqueeze(0)
     B, R, Cc = x3.shape
     codes = torch.empty((B, Cc, R), dtype=torch.uint8, device=x.device)
@@ -250,6 +264,7 @@ def mxfp8_quantize_dual(x: torch.Tensor, stream=None):
     lib = _lib.load()
     if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.dim() not in (2, 3):
         raise ValueError("x must be a contiguous CUDA bf16 matrix or batch of matrices")
+    _on_current(x, "x")
     x3 = x if x.dim() == 3 else x.unsqueeze(0)
     B, R, Cc = x3.shape
     codes = torch.empty((B, R, Cc), dtype=torch.uint8, device=x.device)

@@ -10,7 +10,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from .ops import _DTYPE, _check, _fail, _raw_stream
+from .ops import _DTYPE, _check, _current_device, _fail, _raw_stream
 
 _STATE = {"fp32": _lib.MOK_ADAMW_STATE_F32, "mxfp8": _lib.MOK_ADAMW_STATE_MXFP8}
 _KEPT = {"fp32": ("m", "v"), "mxfp8": ("m", "m_scale", "r", "r_scale")}
@@ -18,13 +18,14 @@ _FIELD = {"masters": "master", "m": "m", "v": "v", "r": "v", "m_scale": "m_scale
 _COUNT, _LR, _SEED_CHANGE = 0, 1, 2   # the counter's 64-bit fields
 _capturing = torch._C._cuda_isCurrentStreamCapturing
 # over a list, map() of these takes a third less time than a loop's body
-_data_ptr, _is_contiguous = torch.Tensor.data_ptr, torch.Tensor.is_contiguous
-_dtype, _shape, _is_cuda = attrgetter("dtype"), attrgetter("shape"), attrgetter("is_cuda")
+_data_ptr, _is_contiguous, _device = torch.Tensor.data_ptr, torch.Tensor.is_contiguous, torch.Tensor.get_device
+_dtype, _shape = attrgetter("dtype"), attrgetter("shape")
 
 
 class AdamW:
-    """Decoupled-weight-decay Adam over ``params`` (contiguous CUDA tensors,
-    bf16 or fp32, updated in place), all of them in one launch per kind.
+    """Decoupled-weight-decay Adam over ``params`` (contiguous CUDA tensors of
+    one device, bf16 or fp32, updated in place), all of them in one launch per
+    kind.
 
     ``state``: "fp32" keeps m and v in 32 bits; "mxfp8" keeps m and
     r = sqrt(v) as E4M3 codes with one E8M0 scale per 32 elements, rounded
@@ -47,8 +48,9 @@ class AdamW:
         self.params = list(params)
         if state not in _STATE:
             raise ValueError(f"state must be one of {sorted(_STATE)}")
+        self._dev = None
         for i, p in enumerate(self.params):
-            _check(p, f"params[{i}]", None, (torch.bfloat16, torch.float32))
+            self._dev = _check(p, f"params[{i}]", None, (torch.bfloat16, torch.float32), self._dev)
         # the host's share of what a step reads; from the first captured step on
         # `_counter` on the device holds the count of the steps since, and what
         # replaces lr and seed
@@ -92,7 +94,7 @@ class AdamW:
                     continue
                 n = (p.numel() + 31) // 32 if name.endswith("_scale") else p.numel()
                 dtype = torch.float32 if name == "masters" or self.state == "fp32" else torch.uint8
-                _check(t, f"buffers[{name!r}][{i}]", None, (dtype,))
+                _check(t, f"buffers[{name!r}][{i}]", None, (dtype,), self._dev)
                 if t.numel() != n or (name == "masters" and p.dtype == torch.float32):
                     raise ValueError(f"buffers[{name!r}][{i}]: expected {n} elements for a "
                                      f"{p.dtype} parameter of {p.numel()}, got {t.numel()}")
@@ -175,14 +177,13 @@ class AdamW:
             mine.copy_(other.reshape(mine.shape))
         self.step_count, self.seed = int(sd["step"]), int(sd["seed"])
 
-    @staticmethod
-    def _gradients(grads, idx, params, shapes, at):
+    def _gradients(self, grads, idx, params, shapes, at):
         """The set of the gradients' types, and each one's type and address (None and 0: no gradient)."""
         own = grads if len(idx) == len(grads) else [grads[i] for i in idx]
         try:
             kinds, ptrs = list(map(_dtype, own)), list(map(_data_ptr, own))
             found = set(kinds)
-            if (found <= _DTYPE.keys() and list(map(_shape, own)) == shapes and all(map(_is_cuda, own))
+            if (found <= _DTYPE.keys() and list(map(_shape, own)) == shapes and set(map(_device, own)) == {self._dev}
                     and all(map(_is_contiguous, own)) and list(map(_data_ptr, params)) == at):
                 return found, kinds, ptrs
         except (AttributeError, TypeError):   # not all of them are tensors
@@ -191,7 +192,7 @@ class AdamW:
         for k, (i, g) in enumerate(zip(idx, own)):
             if g is None:
                 continue
-            _check(g, f"grads[{i}]", shapes[k], tuple(_DTYPE))
+            _check(g, f"grads[{i}]", shapes[k], tuple(_DTYPE), self._dev)
             if params[k].data_ptr() != at[k]:
                 raise ValueError(f"params[{i}] moved to other memory: build the optimiser again")
             kinds[k], ptrs[k] = g.dtype, g.data_ptr()
@@ -210,9 +211,12 @@ class AdamW:
             grads = [p.grad for p in self.params]
         if len(grads) != len(self.params):
             raise ValueError(f"expected {len(self.params)} gradients, got {len(grads)}")
+        if self.params and self._dev != _current_device():
+            raise ValueError(f"the parameters are on cuda:{self._dev}, but the current device (or the stream's) is "
+                             f"cuda:{_current_device()}")
         scale = None
         if grad_scale is not None:
-            _check(grad_scale, "grad_scale", None, (torch.float32,))
+            _check(grad_scale, "grad_scale", None, (torch.float32,), self._dev)
             if grad_scale.numel() != 1:
                 raise ValueError("grad_scale: expected one element")
             scale = grad_scale.data_ptr()
@@ -226,7 +230,7 @@ class AdamW:
         cfg = _lib.MokAdamwConfig(state=_STATE[self.state], lr=self._base_lr if lr is None else lr, beta1=self.betas[0],
                                   beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
                                   step=self._base_step + (not counted), seed=self._base_seed & (2 ** 64 - 1))
-        handle = _raw_stream(self.params[0].get_device()) if self.params else None
+        handle = _raw_stream(self._dev) if self.params else None
         if counted:
             st = lib.mok_adamw_advance(C.byref(cfg), lr is not None, self._counter.data_ptr(), handle)
             if st:
