@@ -591,6 +591,11 @@ typedef struct {
 mok_status_t mok_adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
                             const float* grad_scale, void* stream);
 
+/* The checks of a step's arguments alone (of a counted one's where cfg->step is
+ * 0): enqueues nothing and needs no device.  For a step made of several calls,
+ * one per type of parameter or gradient, which is to be refused as a whole. */
+mok_status_t mok_adamw_check(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors);
+
 /* The step in a CUDA graph.  mok_adamw_step takes the step's number, the
  * learning rate and the seed when it is called, so a graph that holds it would
  * repeat that one step.  These two count on the device: mok_adamw_advance adds

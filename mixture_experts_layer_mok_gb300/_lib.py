@@ -132,6 +132,7 @@ SIGNATURES = {
                                  P]),
     "mok_linear_status": (C.c_int, [I32P]),
     "mok_adamw_step": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int, P, P]),
+    "mok_adamw_check": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int]),
     "mok_adamw_step_counted": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int, P, P, P]),
     "mok_adamw_advance": (C.c_int, [C.POINTER(MokAdamwConfig), C.c_int, P, P]),
 }

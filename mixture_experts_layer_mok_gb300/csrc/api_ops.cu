@@ -243,7 +243,7 @@ mok_status_t mok_linear_status(int* status) {
 namespace {
 
 // counted: cfg->step is what is added to a count of at least 1.
-mok_status_t check_adamw(const mok_adamw_config_t* cfg, bool counted) {
+mok_status_t check_adamw_config(const mok_adamw_config_t* cfg, bool counted) {
   if (!cfg) return fail(MOK_ERR_INVALID_ARG, "NULL config");
   if (!is_dtype(cfg->param_dtype) || !is_dtype(cfg->grad_dtype)) return fail(MOK_ERR_INVALID_ARG, "unknown dtype");
   if (cfg->state != MOK_ADAMW_STATE_F32 && cfg->state != MOK_ADAMW_STATE_MXFP8)
@@ -255,9 +255,8 @@ mok_status_t check_adamw(const mok_adamw_config_t* cfg, bool counted) {
   return MOK_OK;
 }
 
-mok_status_t adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
-                        const float* grad_scale, const AdamwCounter* counter, void* stream) {
-  mok_status_t st = check_adamw(cfg, counter != nullptr);
+mok_status_t check_adamw(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors, bool counted) {
+  mok_status_t st = check_adamw_config(cfg, counted);
   if (st) return st;
   if (num_tensors < 0 || (num_tensors > 0 && !tensors)) return fail(MOK_ERR_INVALID_ARG, "bad tensor list");
   const bool mx = cfg->state == MOK_ADAMW_STATE_MXFP8, p_f32 = cfg->param_dtype == MOK_DTYPE_F32;
@@ -274,9 +273,18 @@ mok_status_t adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t*
     if (!aligned16(t.p) || !aligned16(t.master) || !aligned16(t.g) || !aligned16(t.m) || !aligned16(t.v))
       return fail(MOK_ERR_INVALID_ARG, "tensor %d: misaligned pointer", i);
   }
+  return MOK_OK;
+}
+
+mok_status_t adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
+                        const float* grad_scale, const AdamwCounter* counter, void* stream) {
+  mok_status_t st = check_adamw(cfg, tensors, num_tensors, counter != nullptr);
+  if (st) return st;
   int sms = 0;
   st = device_info(&sms);
   if (st) return st;
+  const bool mx = cfg->state == MOK_ADAMW_STATE_MXFP8, p_f32 = cfg->param_dtype == MOK_DTYPE_F32;
+  const bool master = num_tensors > 0 && tensors[0].master != nullptr;
   AdamwScalars s = {};
   s.beta1 = static_cast<float>(cfg->beta1);
   s.one_minus_beta1 = static_cast<float>(1.0 - cfg->beta1);
@@ -337,6 +345,10 @@ mok_status_t mok_adamw_step(const mok_adamw_config_t* cfg, const mok_adamw_tenso
   return adamw_step(cfg, tensors, num_tensors, grad_scale, nullptr, stream);
 }
 
+mok_status_t mok_adamw_check(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors) {
+  return check_adamw(cfg, tensors, num_tensors, true);
+}
+
 mok_status_t mok_adamw_step_counted(const mok_adamw_config_t* cfg, const mok_adamw_tensor_t* tensors, int num_tensors,
                                     const float* grad_scale, const void* counter, void* stream) {
   NvtxRange nvtx("mok_adamw_step_counted");
@@ -346,7 +358,7 @@ mok_status_t mok_adamw_step_counted(const mok_adamw_config_t* cfg, const mok_ada
 
 mok_status_t mok_adamw_advance(const mok_adamw_config_t* cfg, int fixed_lr, void* counter, void* stream) {
   NvtxRange nvtx("mok_adamw_advance");
-  mok_status_t st = check_adamw(cfg, true);
+  mok_status_t st = check_adamw_config(cfg, true);
   if (st) return st;
   if (!counter || !aligned16(counter)) return fail(MOK_ERR_INVALID_ARG, "counter: NULL or misaligned pointer");
   int sms = 0;

@@ -231,23 +231,30 @@ class AdamW:
                                   beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
                                   step=self._base_step + (not counted), seed=self._base_seed & (2 ** 64 - 1))
         handle = _raw_stream(self._dev) if self.params else None
-        if counted:
-            st = lib.mok_adamw_advance(C.byref(cfg), lr is not None, self._counter.data_ptr(), handle)
-            if st:
-                _fail(st, "mok_adamw_advance")
-        for dtype, arr, fields, lengths, found, kinds, ptrs in runs:
-            cfg.param_dtype = _DTYPE[dtype]
-            fields["g"] = ptrs
-            for kind in found - {None}:
-                cfg.grad_dtype = _DTYPE[kind]
+        launches = [(run, kind) for run in runs for kind in run[4] - {None}]
+
+        def each(fn, where, *args):
+            for (dtype, arr, fields, lengths, found, kinds, ptrs), kind in launches:
+                cfg.param_dtype, cfg.grad_dtype = _DTYPE[dtype], _DTYPE[kind]
+                fields["g"] = ptrs
                 # a length of 0 leaves a tensor out: no gradient, or one of another type
                 fields["n"] = lengths if len(found) == 1 else [n if t is kind else 0 for n, t in zip(lengths, kinds)]
-                if counted:
-                    st = lib.mok_adamw_step_counted(C.byref(cfg), arr, len(arr), scale, self._counter.data_ptr(), handle)
-                else:
-                    st = lib.mok_adamw_step(C.byref(cfg), arr, len(arr), scale, handle)
+                st = fn(C.byref(cfg), arr, len(arr), *args)
                 if st:
-                    _fail(st, "mok_adamw_step")
+                    _fail(st, where)
+
+        # several calls make one step: what any of them would refuse is refused
+        # before the first one moves anything
+        if counted or len(launches) > 1:
+            each(lib.mok_adamw_check, "mok_adamw_check")
+        if counted:
+            counter = self._counter.data_ptr()
+            st = lib.mok_adamw_advance(C.byref(cfg), lr is not None, counter, handle)
+            if st:
+                _fail(st, "mok_adamw_advance")
+            each(lib.mok_adamw_step_counted, "mok_adamw_step_counted", scale, counter, handle)
+        else:
+            each(lib.mok_adamw_step, "mok_adamw_step", scale, handle)
         # the parameters changed under autograd's eyes: a backward that saved
         # them before this step has to notice
         torch.autograd.graph.increment_version(self.params)

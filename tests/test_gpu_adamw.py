@@ -385,3 +385,30 @@ def test_a_captured_step_replays_the_step_that_is_due(state, master, warm):
     assert opt.state_dict()["step"] == 10
     with pytest.raises(ValueError):
         opt.lr = float("nan")
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("which", ["gradient", "parameter"])
+def test_a_refused_step_moves_nothing(which, captured):
+    """Two launches, the second of which is refused: a retry must not step the
+    first group twice."""
+    m = mok()
+    odd = torch.ones(65, device="cuda")[1:]
+    ps = [torch.ones(64, dtype=BF16, device="cuda"), torch.ones(64, device="cuda")]
+    good = [torch.ones(64, dtype=BF16, device="cuda"), torch.ones(64, device="cuda")]
+    opt = m.AdamW(ps, lr=0.1)
+    if captured:
+        _graph_of(lambda: opt.step(good))
+    if which == "parameter":
+        ps[1] = odd
+        opt = m.AdamW(ps, lr=0.1)
+    version = [p._version for p in ps]
+    with pytest.raises(m.MokError):
+        opt.step(good if which == "parameter" else [good[0], odd])
+    torch.cuda.synchronize()
+    assert all(bool((p == 1).all()) for p in ps) and opt.step_count == 0
+    assert all(bool((b == 0).all()) for name in ("m", "v") for b in opt.buffers[name])
+    assert [p._version for p in ps] == version
+    if which == "gradient":
+        opt.step(good)
+        assert opt.step_count == 1 and all(bool((p < 1).all()) for p in ps)

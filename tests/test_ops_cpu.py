@@ -144,3 +144,19 @@ def test_counted_adamw_refusals(lib):
         assert lib.mok_adamw_step_counted(C.byref(c), t, 0, None, counter, None) == BAD
     assert lib.mok_adamw_advance(None, 0, FAKE, None) == BAD
     assert lib.mok_adamw_step_counted(C.byref(cfg()), t, 1, None, FAKE, None) == BAD     # v is misaligned
+
+
+def test_adamw_check_is_the_steps_own(lib):
+    from mixture_experts_layer_mok_gb300 import _lib
+
+    def check(num=1, step=1, **kw):
+        c = dict(param_dtype=1, grad_dtype=1, lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=step)
+        t = dict(p=16, g=16, m=16, v=16, n=64)
+        c.update({k: v for k, v in kw.items() if k in c})
+        t.update({k: v for k, v in kw.items() if k not in c})
+        return lib.mok_adamw_check(C.byref(_lib.MokAdamwConfig(**c)), (_lib.MokAdamwTensor * 1)(_lib.MokAdamwTensor(**t)), num)
+
+    assert check() == 0 and check(step=0) == 0 and check(g=24, n=0) == 0
+    for bad in (dict(num=-1), dict(step=-1), dict(g=24), dict(p=24), dict(v=None), dict(master=16), dict(lr=float("inf")),
+                dict(beta1=1.0), dict(n=-1)):
+        assert check(**bad) == BAD, bad
