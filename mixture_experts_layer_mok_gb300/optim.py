@@ -256,7 +256,11 @@ class AdamW:
         else:
             each(lib.mok_adamw_step, "mok_adamw_step", scale, handle)
         # the parameters changed under autograd's eyes: a backward that saved
-        # them before this step has to notice
-        torch.autograd.graph.increment_version(self.params)
+        # them before this step has to notice (and only those: a parameter
+        # without a gradient is what it was)
+        for (_, _, params, *_), (_, _, _, _, found, kinds, _) in zip(self._groups, runs):
+            if None in found:
+                params = [p for p, kind in zip(params, kinds) if kind is not None]
+            torch.autograd.graph.increment_version(params)
         if not counted:
             self._base_step += 1

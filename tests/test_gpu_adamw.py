@@ -412,3 +412,17 @@ def test_a_refused_step_moves_nothing(which, captured):
     if which == "gradient":
         opt.step(good)
         assert opt.step_count == 1 and all(bool((p < 1).all()) for p in ps)
+
+
+def test_a_backward_does_not_mind_parameters_that_stayed():
+    """A parameter without a gradient is left alone, by its version too; of two
+    types, so that each launch's own are told apart."""
+    m = mok()
+    for dtype in (F32, BF16):
+        kept, moved = (torch.nn.Parameter(torch.ones(64, device="cuda", dtype=dtype)) for _ in range(2))
+        x = torch.ones(64, device="cuda", dtype=dtype, requires_grad=True)
+        loss = (kept * kept * x).sum()
+        before = moved._version
+        m.AdamW([kept, moved, torch.ones(8, device="cuda")]).step([None, torch.ones_like(moved), None])
+        loss.backward()
+        assert moved._version > before and bool((kept == 1).all()) and bool((x.grad == 1).all())
