@@ -564,6 +564,8 @@ mok_status_t mok_linear_status(int* status);
  *     flat index, key = seed 0x9E3779B1 + step 0xB504F333 + index 0xBB67AE85
  *     and mix(z): h = z 0x9E3779B1; h ^= h >> 15; h *= 0xB504F333;
  *     h ^= h >> 16, all modulo 2^32.  The same call gives the same bits.
+ *     An m or v that is not finite (from such a gradient) is kept as NaN, and
+ *     the scale is that of the block's finite values, which are kept as ever.
  * `tensors` is a HOST array; all pointers in it are device pointers, 16-byte
  * aligned but for the scales.  grad_scale: a device scalar (gradient clipping,
  * loss scaling) or NULL for 1. */

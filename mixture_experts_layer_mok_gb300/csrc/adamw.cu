@@ -120,7 +120,7 @@ __device__ __forceinline__ void store8(T* p, bool whole, int left, const float* 
   }
 }
 
-// |y| <= 448 onto the E4M3 grid, rounded up or down by 16 random bits: the
+// |y| <= 448 (not NaN) onto the E4M3 grid, rounded up or down by 16 random bits: the
 // bits are added below the last kept place of the fp32 form and the rest is
 // cut off.  Below 2^-6 the grid is uniform (2^-9), as it is in [2^-6, 2^-5):
 // such a value is moved there and back.
@@ -137,9 +137,17 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
+// The larger of two values; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Writes 8 values as codes with the scale of their block of 32 (four
-// neighbouring lanes); `v` are values before rounding, `rand` their bits
-// (m: the high half, r: the low one).
+// neighbouring lanes); `v` are values before rounding, none of them infinite,
+// `rand` their bits (m: the high half, r: the low one).  A NaN has no say in
+// the scale and stays NaN.
 template <bool R>
 __device__ __forceinline__ void store_codes8(uint8_t* codes, uint8_t* scales, long long block, bool whole, int left,
                                              const float* v, const uint32_t* rand) {
@@ -156,9 +164,9 @@ __device__ __forceinline__ void store_codes8(uint8_t* codes, uint8_t* scales, lo
     const float y = v[i] * inv;
     q[i] = e4m3_stochastic(y, R ? (rand[i] << 4) & 0xFFFF0u : (rand[i] >> 12) & 0xFFFF0u);
     if (R)
-      q[i] = fmaxf(q[i], y > 0.f ? 0.001953125f : 0.f);   // 2^-9, the smallest code
+      q[i] = max_nan(q[i], y > 0.f ? 0.001953125f : y);   // 2^-9, the smallest code
     else
-      q[i] = copysignf(q[i], y);
+      q[i] = fmaf(y, 0.f, copysignf(q[i], y));            // (the rounding loses a NaN)
   }
   uint32_t w[2];
 #pragma unroll
@@ -215,8 +223,8 @@ struct AdamwIn {
 // while it works on this one.  32-bit states: a chunk to a block, bound by
 // memory; bf16 parameters with master copies, 402.7M elements, 1604 us (7.0
 // TB/s).  MXFP8 states: 95 instructions an element keep the issue slots busy
-// 84% of the time beside 64 to 70% of the memory's peak; the same tensors 1158
-// us (5.6 TB/s).  16 elements a thread took fewer instructions but left fewer
+// 84% of the time beside 64 to 70% of the memory's peak; the same tensors 1187
+// us (5.5 TB/s).  16 elements a thread took fewer instructions but left fewer
 // warps, and were slower.
 // COUNTED: what depends on the step count comes from device memory.
 template <class PT, class GT, bool MASTER, bool MX, int CAP, bool COUNTED>
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
     // root rounded correctly: a last-bit difference would put one element in
     // 10^6 on the other side of its random bits, a whole code away from a
     // restatement in 32 bits.  With fused operations and an approximate root
-    // 402.7M elements take 1144 us, this way 1158.
+    // 402.7M elements took 1144 us, this way 1158.
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float gi = g[i] * gs;
@@ -267,6 +275,11 @@ __global__ void __launch_bounds__(256, MX ? kAdamwPerSm : 6)
     store8(static_cast<PT*>(t.p) + in.i0, whole, left, p);
     if (MX) {
       const long long block = in.i0 >> 5;
+      // An infinity becomes NaN, which E4M3 has: as the block's scale it would
+      // make each neighbour's smallest code 2^111.  These and the NaNs' way
+      // through the rounding cost 2% (402.7M elements 1160 us, so 1187).
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i] = fmaf(m[i], 0.f, m[i]), r[i] = fmaf(r[i], 0.f, r[i]);
       uint32_t rand[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) rand[i] = mix_bits(static_cast<uint32_t>(in.i0) + i, t.key + step_key);

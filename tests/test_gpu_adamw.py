@@ -426,3 +426,40 @@ def test_a_backward_does_not_mind_parameters_that_stayed():
         m.AdamW([kept, moved, torch.ones(8, device="cuda")]).step([None, torch.ones_like(moved), None])
         loss.backward()
         assert moved._version > before and bool((kept == 1).all()) and bool((x.grad == 1).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf"), 3e38])
+@pytest.mark.parametrize("at", [0, 40, 63, 255, 259])
+def test_a_gradient_that_is_not_finite_stays_in_its_element(bad, at):
+    """32-bit states hold such a value in one element.  So do MXFP8 states, as
+    NaN: every other element, its block's own among them, is to the bit what it
+    is in a run where that element's gradient is zero, in the step and in the
+    one after.  (3e38 has an infinite square and an m that is finite: it stays
+    m's, and sets the scale of its block of m as any value does.)"""
+    m = mok()
+    n = 260
+    g = torch.rand(n, generator=torch.Generator().manual_seed(at)) + 0.5
+
+    def run(value):
+        p = torch.ones(n, device="cuda")
+        opt = m.AdamW([p], state="mxfp8", seed=3)
+        for k in range(2):
+            gk = (1.0 + k) * g
+            gk[at] = value if k == 0 else gk[at] * 0
+            opt.step([gk.cuda()])
+            kept = {name: opt.buffers[name][0].cpu().numpy().copy() for name in ("m", "m_scale", "r", "r_scale")}
+            yield p.cpu().clone(), kept
+
+    others = np.arange(n) != at
+    block = np.arange(n) // 32 == at // 32
+    for (p, kept), (p0, kept0) in zip(run(bad), run(0.0)):
+        assert not np.isfinite(p[at].item()) or bad == 3e38
+        names = ("m", "r") if bad != 3e38 else ("r",)
+        for name in names:
+            value = _decode(kept[name], kept[name + "_scale"])
+            assert (kept[name][at] & 127) == 127            # E4M3's NaN
+            assert np.array_equal(value[others], _decode(kept0[name], kept0[name + "_scale"])[others]), name
+            assert np.array_equal(kept[name + "_scale"], kept0[name + "_scale"]), name
+        if bad == 3e38:
+            assert np.array_equal(kept["m"][~block], kept0["m"][~block]) and (kept["m"][at] & 127) != 127
+        assert torch.equal(p[others & ~block] if bad == 3e38 else p[others], p0[others & ~block] if bad == 3e38 else p0[others])
