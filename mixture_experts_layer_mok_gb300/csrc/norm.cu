@@ -264,8 +264,11 @@ __device__ __forceinline__ void row_sums(float (&s)[R], float (*red)[R]) {
 // elements to a thread; each such group walks the rows, R at a time, and keeps
 // its columns' share of dw in registers.  `part` gets one row of sums per block,
 // which column_sum_kernel adds in order.
-//   acc_j += rstd (dy_j h_j),   s = sum_j w_j dy_j h_j,   k = -rstd^3 s / H,
-//   dx_j = rstd (w_j dy_j) + (k h_j + dh_j)
+//   acc_j += rstd (dy_j h_j),   s = sum_j w_j dy_j h_j,   k = -(s rstd) / H,
+//   dx_j = rstd (w_j dy_j + k (h_j rstd)) + dh_j
+// k is the mean of g xhat and h_j rstd is xhat_j, of order 1 whatever the size
+// of h: with rstd^3 in one factor, one multiplication an element less, dx was
+// lost for rows of a root mean square above 1e12 or below 1e-13.
 template <class HT, int ITEMS, int R, int W, int THREADS>
 __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int kGroups = THREADS / (32 * W), T = 32 * W;
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
     }
     row_sums<W, R>(dot, red[odd]);
 #pragma unroll
-    for (int r = 0; r < R; ++r) dot[r] *= -inv_h * rstd[r] * rstd[r] * rstd[r];
+    for (int r = 0; r < R; ++r) dot[r] = dot[r] * rstd[r] * -inv_h;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * T;
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
             unpack(h[r][i], x);
             unpack(dh[r][i], d);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = fmaf(y[j] * w[j], rstd[r], fmaf(x[j], dot[r], d[j]));
+            for (int j = 0; j < 8; ++j) d[j] = fmaf(fmaf(x[j] * rstd[r], dot[r], y[j] * w[j]), rstd[r], d[j]);
             store_vals<8>(static_cast<HT*>(a.dx) + at, d);
             if (sizeof(HT) == 4 && a.dx16) store_vals<8>(a.dx16 + at, d);
           }
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_bwd_block_kernel(const NormBwdA
         }
       }
     }
-    const float k = row_sum<false>(dot, red[odd]) * (-inv_h * rstd * rstd * rstd);
+    const float k = row_sum<false>(dot, red[odd]) * rstd * -inv_h;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * T;
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_bwd_block_kernel(const NormBwdA
         unpack(rh[i], h);
         if (a.dh) unpack(rdh[i], d);
 #pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = fmaf(dy[j] * w[i][j], rstd, fmaf(h[j], k, d[j]));
+        for (int j = 0; j < V; ++j) d[j] = fmaf(fmaf(h[j] * rstd, k, dy[j] * w[i][j]), rstd, d[j]);
         store_vals<V>(static_cast<HT*>(a.dx) + base + c * V, d);
         if (sizeof(HT) == 4 && a.dx16) store_vals<V>(a.dx16 + base + c * V, d);
       }

@@ -242,3 +242,26 @@ def test_refusals():
     with pytest.raises(m.MokError):                            # K % 32 != 0 over several rows
         m.mxfp8_dequantize(torch.zeros(2, 40, dtype=torch.uint8, device="cuda"),
                            torch.zeros(2, 2, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("scale", [1e17, 1e13, 1e11, 1e-11, 1e-15, 1e-18])
+@pytest.mark.parametrize("rows,H", [(40, 256), (9, 512), (130, 2048), (64, 4096), (2, 8200), (3, 16384), (2, 17), (2, 4097)])
+@pytest.mark.parametrize("ht", ["bf16", "f32"])
+def test_backward_of_rows_of_any_size(rows, H, ht, scale):
+    """Rows over the range that the forward takes (their squares fit 32 bits),
+    eps = 0 where they are small: the usual bound."""
+    m = mok()
+    h, dh, w = _inputs(rows, H, ht, ht, "bf16", seed=13)
+    h = (h.double() * scale).to(TYPES[ht])
+    dy = _inputs(rows, H, "bf16", "none", "bf16", seed=15)[0]
+    out = m.rms_norm(h.cuda(), w.cuda(), eps=0.0 if scale < 1 else 1e-6)
+    _close(out.rstd, _ref(h, None, w, 0.0)[1], F * _ref(h, None, w, 0.0)[1], "rstd")
+    rstd = out.rstd.cpu()
+    r = rstd.double()[:, None]
+    dh = (dh.double() / scale).to(TYPES[ht])
+    xhat, g = h.double() * r, dy.double() * w.double()
+    dx = r * (g - xhat * (g * xhat).mean(-1, keepdim=True)) + dh.double()
+    got = m.rms_norm_backward(dy.cuda(), h.cuda(), w.cuda(), out.rstd, d_h=dh.cuda())
+    size = r * (g.abs() + xhat.abs() * (g * xhat).abs().mean(-1, keepdim=True)) + dh.double().abs()
+    _close(got["dx"], dx, F * size + (U * dx.abs() if ht == "bf16" else 0.0), "dx")
+    _close(got["d_weight"], (dy.double() * xhat).sum(0), F * (dy.double() * xhat).abs().sum(0) + 1e-30, "d_weight")
