@@ -55,6 +55,13 @@ def _first_order(backward):
     return wrapper
 
 
+def _incoming(grad):
+    """A gradient as the library takes it: contiguous, and 16-byte aligned, which
+    a contiguous one need not be (the backward of a ``cat`` hands on views)."""
+    grad = grad.contiguous()
+    return grad.clone() if grad.data_ptr() & 15 else grad
+
+
 class MoKFunction(torch.autograd.Function):
     """y = MoK layer(x, router_w, top_experts; routed and optional shared
     SwiGLU weights).  Differentiable in x, router_w and every weight; the
@@ -85,7 +92,7 @@ class MoKFunction(torch.autograd.Function):
         smeta, cmeta, weights, minibatch, macrobatch, shared = ctx.mok
         sched = Schedule.unflatten(sbuf, smeta)     # over wherever the hooks put the buffers
         mctx = Context.unflatten(cbuf, cmeta)
-        g = backward(dy.to(torch.bfloat16).contiguous(), x, router_w, sched, mctx, weights, minibatch=minibatch,
+        g = backward(_incoming(dy.to(torch.bfloat16)), x, router_w, sched, mctx, weights, minibatch=minibatch,
                      macrobatch=macrobatch)
         ctx.mok = None
         return (g["dx"], g["d_router_w"], None, g["d_w_gate"], g["d_w_up"], g["d_w_down"],
@@ -162,7 +169,7 @@ class RMSNormFunction(torch.autograd.Function):
         if dy is None:
             dx = dx16 = dh
         else:
-            g = ops.rms_norm_backward(dy.contiguous(), h, weight, rstd, None if dh is None else dh.contiguous(),
+            g = ops.rms_norm_backward(_incoming(dy), h, weight, rstd, None if dh is None else _incoming(dh),
                                       bf16_dx=x_type == torch.bfloat16)
             dx, d_weight = g["dx"], g["d_weight"].to(weight.dtype)
             dx16 = g.get("dx_bf16", dx)
@@ -211,7 +218,7 @@ class LinearFunction(torch.autograd.Function):
         g = {}
         if need_x or need_w or need_b:
             need = [n for n, on in (("dx", need_x), ("d_weight", need_w)) if on]
-            g = ops.linear_backward(dy.contiguous(), x, weight, z, activation, bias=bool(need_b), need=need)
+            g = ops.linear_backward(_incoming(dy), x, weight, z, activation, bias=bool(need_b), need=need)
         return (g.get("dx"), g.get("d_weight"), g["d_bias"].to(bias_type) if need_b else None,
                 dy.to(res_type) if need_r else None, None, None)
 

@@ -88,3 +88,45 @@ def test_the_layers_gradients_derivative_is_refused(restated):
     y = autograd.mok_layer(x, rw, ids, *w)
     y.float().sum().backward()
     assert x.grad is not None and w[0].grad is not None
+
+
+def _odd(t):
+    """t's values at an address that is not a multiple of 16 bytes."""
+    flat = torch.empty(t.numel() + 9, dtype=t.dtype)
+    at = next(i for i in range(1, 9) if flat[i:].data_ptr() % 16)
+    view = flat[at:at + t.numel()].view(t.shape)
+    view.copy_(t)
+    assert view.is_contiguous() and view.data_ptr() % 16
+    return view
+
+
+@pytest.mark.parametrize("which", ["norm", "norm's stream", "linear", "layer"])
+def test_a_gradient_at_an_odd_address_reaches_the_library_aligned(restated, monkeypatch, which):
+    """The library refuses such a tensor, which the middle of a backward is no
+    place for."""
+    seen = []
+
+    def watch(module, name):
+        inner = getattr(module, name)
+
+        def call(*a, **k):
+            seen.extend(t for t in (*a, *k.values()) if isinstance(t, torch.Tensor))
+            return inner(*a, **k)
+        monkeypatch.setattr(module, name, call)
+
+    for module, name in ((ops, "rms_norm_backward"), (ops, "linear_backward"), (autograd, "backward")):
+        watch(module, name)
+    g = torch.Generator().manual_seed(0)
+    t = lambda *s: torch.randn(*s, generator=g).requires_grad_()  # noqa: E731
+    x, w, e = t(4, 8), t(8), [t(2, 3, 8), t(2, 3, 8), t(2, 8, 3)]
+    if which == "layer":
+        y = autograd.mok_layer(x.bfloat16(), torch.ones(4, 1, requires_grad=True), torch.zeros(4, 1, dtype=torch.int64),
+                               *(v.bfloat16() for v in e))
+    elif which == "linear":
+        y = autograd.linear(x, e[0][0], out_dtype=F32)
+    else:
+        y, h = autograd.rms_norm(x, w, t(4, 8))
+        y = y if which == "norm" else y.sum() + h
+    dy = torch.randn(y.shape, generator=g).to(y.dtype)
+    y.backward(_odd(dy))
+    assert seen and all(v.data_ptr() % 16 == 0 for v in seen)

@@ -172,3 +172,26 @@ def test_calls_in_a_cuda_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert m.linear_status() == 0
+
+
+def test_gradients_at_odd_addresses():
+    """Rows of 17 behind a row of another tensor: the concatenation's backward
+    hands the norm a contiguous gradient that begins at an odd address."""
+    mok()
+    from mixture_experts_layer_mok_gb300.autograd import rms_norm
+
+    g = torch.Generator().manual_seed(4)
+    x, r, w, top = (torch.randn(*s, generator=g).to(BF16).cuda() for s in ((3, 17), (3, 17), (17,), (1, 17)))
+    c = torch.randn(4, 17, generator=g).to(BF16).cuda()
+
+    def grads(join):
+        leaves = [t.clone().requires_grad_() for t in (x, w, r)]
+        y, h = rms_norm(leaves[0], leaves[1], leaves[2])
+        if join:
+            y, h = torch.cat([top, y]) * c, torch.cat([top, h]) * c
+        else:
+            y, h = y * c[1:], h * c[1:]
+        (y.float().sum() + h.float().sum()).backward()
+        return [t.grad for t in leaves]
+
+    assert all(torch.equal(a, b) for a, b in zip(grads(True), grads(False)))
