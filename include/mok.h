@@ -512,6 +512,12 @@ size_t mok_rms_norm_bwd_workspace_bytes(int64_t rows, int H);
 mok_status_t mok_rms_norm_bwd(const uint16_t* dy, const void* h, int h_dtype, const void* weight, int weight_dtype,
                               const float* rstd, const void* dh, int64_t rows, int H, void* dx, uint16_t* dx_bf16,
                               float* d_weight, void* ws, size_t ws_bytes, void* stream);
+/* The same with dx in both types for either type of h: dx_other (or NULL) gets
+ * the unrounded dx in the type that h does not have, for an x of another type
+ * than the residual's. */
+mok_status_t mok_rms_norm_bwd_both(const uint16_t* dy, const void* h, int h_dtype, const void* weight, int weight_dtype,
+                                   const float* rstd, const void* dh, int64_t rows, int H, void* dx, void* dx_other,
+                                   float* d_weight, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- dense projection with bias, activation and residual ----------------
  *   z = x W^T + bias,   y = act(z) + residual.

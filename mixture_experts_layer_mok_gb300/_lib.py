@@ -126,6 +126,7 @@ SIGNATURES = {
     "mok_rms_norm": (C.c_int, [P, C.c_int, P, C.c_int, P, C.c_int, C.c_int64, C.c_int, C.c_float, P, P, P, P, P, P]),
     "mok_rms_norm_bwd_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int]),
     "mok_rms_norm_bwd": (C.c_int, [P, P, C.c_int, P, C.c_int, P, P, C.c_int64, C.c_int, P, P, P, P, C.c_size_t, P]),
+    "mok_rms_norm_bwd_both": (C.c_int, [P, P, C.c_int, P, C.c_int, P, P, C.c_int64, C.c_int, P, P, P, P, C.c_size_t, P]),
     "mok_linear": (C.c_int, [P, P, P, C.c_int, P, C.c_int, C.c_int, C.c_int64, C.c_int, C.c_int, P, C.c_int, P, P]),
     "mok_linear_bwd_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int]),
     "mok_linear_bwd": (C.c_int, [P, C.c_int, P, P, P, C.c_int, C.c_int64, C.c_int, C.c_int, P, P, P, P, C.c_size_t,

@@ -167,13 +167,14 @@ class RMSNormFunction(torch.autograd.Function):
             return None, None, None, None, None
         d_weight = None
         if dy is None:
-            dx = dx16 = dh
+            d_x = dx = dh
         else:
             g = ops.rms_norm_backward(_incoming(dy), h, weight, rstd, None if dh is None else _incoming(dh),
-                                      bf16_dx=x_type == torch.bfloat16)
+                                      bf16_dx=x_type == torch.bfloat16, f32_dx=x_type == torch.float32)
             dx, d_weight = g["dx"], g["d_weight"].to(weight.dtype)
-            dx16 = g.get("dx_bf16", dx)
-        d_x = (dx16 if x_type == torch.bfloat16 else dx).to(x_type)
+            # x's own, in x's type where that is not the stream's
+            d_x = g.get("dx_bf16" if x_type == torch.bfloat16 else "dx_f32", dx)
+        d_x = d_x.to(x_type)
         return d_x, d_weight, None if res_type is None else dx.to(res_type), None, None
 
 

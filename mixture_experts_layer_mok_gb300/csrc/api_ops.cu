@@ -106,15 +106,22 @@ size_t mok_rms_norm_bwd_workspace_bytes(int64_t rows, int H) {
 mok_status_t mok_rms_norm_bwd(const uint16_t* dy, const void* h, int h_dtype, const void* weight, int weight_dtype,
                               const float* rstd, const void* dh, int64_t rows, int H, void* dx, uint16_t* dx_bf16,
                               float* d_weight, void* ws, size_t ws_bytes, void* stream) {
+  if (dx_bf16 && h_dtype != MOK_DTYPE_F32) return fail(MOK_ERR_INVALID_ARG, "dx_bf16 goes with an fp32 h");
+  return mok_rms_norm_bwd_both(dy, h, h_dtype, weight, weight_dtype, rstd, dh, rows, H, dx, dx_bf16, d_weight, ws, ws_bytes,
+                               stream);
+}
+
+mok_status_t mok_rms_norm_bwd_both(const uint16_t* dy, const void* h, int h_dtype, const void* weight, int weight_dtype,
+                                   const float* rstd, const void* dh, int64_t rows, int H, void* dx, void* dx_other,
+                                   float* d_weight, void* ws, size_t ws_bytes, void* stream) {
   NvtxRange nvtx("mok_rms_norm_bwd");
   if (rows < 0 || rows > 0x7fffffffll || H < 1 || H > MOK_NORM_MAX_H)
     return fail(MOK_ERR_INVALID_ARG, "need 0 <= rows < 2^31 and 1 <= H <= %d", MOK_NORM_MAX_H);
   if (!is_dtype(h_dtype) || !is_dtype(weight_dtype)) return fail(MOK_ERR_INVALID_ARG, "unknown dtype");
-  if (dx_bf16 && h_dtype != MOK_DTYPE_F32) return fail(MOK_ERR_INVALID_ARG, "dx_bf16 goes with an fp32 h");
   if (!d_weight || !ws || !weight) return fail(MOK_ERR_INVALID_ARG, "NULL argument");
   if (rows > 0 && (!dy || !h || !rstd || !dx)) return fail(MOK_ERR_INVALID_ARG, "NULL argument");
   if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(rstd) || !aligned16(dh) || !aligned16(dx) ||
-      !aligned16(dx_bf16) || !aligned16(d_weight) || !aligned16(ws))
+      !aligned16(dx_other) || !aligned16(d_weight) || !aligned16(ws))
     return fail(MOK_ERR_INVALID_ARG, "misaligned pointer");
   if (ws_bytes < mok_rms_norm_bwd_workspace_bytes(rows, H))
     return fail(MOK_ERR_INVALID_ARG, "workspace too small: %zu < %zu", ws_bytes,
@@ -129,7 +136,7 @@ mok_status_t mok_rms_norm_bwd(const uint16_t* dy, const void* h, int h_dtype, co
   a.rstd = rstd;
   a.dh = dh;
   a.dx = dx;
-  a.dx16 = dx_bf16;
+  a.dx_other = dx_other;
   a.part = static_cast<float*>(ws);
   a.rows = rows;
   a.H = H;

@@ -14,6 +14,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gemm.cuh"
 #include "internal.h"
 #include "ops.h"
@@ -22,6 +24,9 @@ namespace mok {
 namespace {
 
 struct NoType {};
+// The other of the two types that a stream has.
+template <class T>
+using Other = std::conditional_t<sizeof(T) == 4, uint16_t, float>;
 
 // V consecutive values (8, or 1 where a row's length is not a multiple of 8)
 // as they lie in memory.
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[j] = fmaf(fmaf(x[j] * rstd[r], dot[r], y[j] * w[j]), rstd[r], d[j]);
             store_vals<8>(static_cast<HT*>(a.dx) + at, d);
-            if (sizeof(HT) == 4 && a.dx16) store_vals<8>(a.dx16 + at, d);
+            if (a.dx_other) store_vals<8>(static_cast<Other<HT>*>(a.dx_other) + at, d);
           }
         }
       }
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_bwd_block_kernel(const NormBwdA
 #pragma unroll
         for (int j = 0; j < V; ++j) d[j] = fmaf(fmaf(h[j] * rstd, k, dy[j] * w[i][j]), rstd, d[j]);
         store_vals<V>(static_cast<HT*>(a.dx) + base + c * V, d);
-        if (sizeof(HT) == 4 && a.dx16) store_vals<V>(a.dx16 + base + c * V, d);
+        if (a.dx_other) store_vals<V>(static_cast<Other<HT>*>(a.dx_other) + base + c * V, d);
       }
     }
   }

@@ -50,7 +50,7 @@ struct NormBwdArgs {
   const float* rstd;
   const void* dh;     // gradient of h from its other uses, or NULL
   void* dx;           // in h's type
-  uint16_t* dx16;     // fp32 h: also in bf16, or NULL
+  void* dx_other;     // the same unrounded values in the other type, or NULL
   float* part;        // [norm_bwd_walkers][H]
   long long rows;
   int H;

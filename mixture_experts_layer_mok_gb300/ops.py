@@ -136,15 +136,16 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, bf16: bool = True, mxf
     return NormOutput(y, mx, h, rstd)
 
 
-def rms_norm_backward(dy, h, weight, rstd, d_h=None, bf16_dx: bool = False, stream=None) -> dict:
+def rms_norm_backward(dy, h, weight, rstd, d_h=None, bf16_dx: bool = False, stream=None, f32_dx: bool = False) -> dict:
     """Gradients of ``rms_norm``: dy bf16 [..., H]; h, rstd from its output;
     ``d_h`` the gradient that reaches h from its other uses (the residual
     stream), in h's type.  Returns dx in h's type, the gradient of x and of
     the residual alike, and d_weight fp32 [H]; with ``bf16_dx`` and an fp32 h
-    also dx_bf16."""
+    also dx_bf16, with ``f32_dx`` and a bf16 h also dx_f32 (each rounded once,
+    for an x of another type than the residual's)."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return rms_norm_backward(dy, h, weight, rstd, d_h, bf16_dx)
+            return rms_norm_backward(dy, h, weight, rstd, d_h, bf16_dx, f32_dx=f32_dx)
     at = _check(h, "h", None, _BF16_F32)
     shape = h.shape
     if not shape or not shape[-1]:
@@ -161,14 +162,17 @@ def rms_norm_backward(dy, h, weight, rstd, d_h=None, bf16_dx: bool = False, stre
     if nbytes == 0:
         raise ValueError("shape outside the kernels' contract")
     out = {"dx": torch.empty_like(h), "d_weight": _empty((H,), dtype=_F32, device=dev)}
+    other = None
     if bf16_dx and h.dtype == _F32:
-        out["dx_bf16"] = _empty(shape, dtype=_BF16, device=dev)
+        other = out["dx_bf16"] = _empty(shape, dtype=_BF16, device=dev)
+    elif f32_dx and h.dtype == _BF16:
+        other = out["dx_f32"] = _empty(shape, dtype=_F32, device=dev)
     ws = _empty((nbytes,), dtype=_U8, device=dev)
-    st = lib.mok_rms_norm_bwd(dy.data_ptr(), h.data_ptr(), _DTYPE[h.dtype], weight.data_ptr(), _DTYPE[weight.dtype],
-                              rstd.data_ptr(), _opt(d_h), rows, H, out["dx"].data_ptr(), _opt(out.get("dx_bf16")),
-                              out["d_weight"].data_ptr(), ws.data_ptr(), nbytes, _raw_stream(at))
+    st = lib.mok_rms_norm_bwd_both(dy.data_ptr(), h.data_ptr(), _DTYPE[h.dtype], weight.data_ptr(), _DTYPE[weight.dtype],
+                                   rstd.data_ptr(), _opt(d_h), rows, H, out["dx"].data_ptr(), _opt(other),
+                                   out["d_weight"].data_ptr(), ws.data_ptr(), nbytes, _raw_stream(at))
     if st:
-        _fail(st, "mok_rms_norm_bwd")
+        _fail(st, "mok_rms_norm_bwd_both")
     return out
 
 

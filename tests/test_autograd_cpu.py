@@ -16,7 +16,7 @@ def _norm(x, weight, residual=None, eps=1e-6, mxfp8=False):
     return ops.NormOutput((h * rstd[..., None] * weight).to(x.dtype), None, h, rstd)
 
 
-def _norm_backward(dy, h, weight, rstd, d_h=None, bf16_dx=False):
+def _norm_backward(dy, h, weight, rstd, d_h=None, bf16_dx=False, f32_dx=False):
     xhat, g = h * rstd[..., None], dy * weight
     dx = rstd[..., None] * (g - xhat * (g * xhat).mean(-1, keepdim=True))
     return {"dx": dx if d_h is None else dx + d_h, "d_weight": (dy * xhat).sum(0)}

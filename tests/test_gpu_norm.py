@@ -265,3 +265,44 @@ def test_backward_of_rows_of_any_size(rows, H, ht, scale):
     size = r * (g.abs() + xhat.abs() * (g * xhat).abs().mean(-1, keepdim=True)) + dh.double().abs()
     _close(got["dx"], dx, F * size + (U * dx.abs() if ht == "bf16" else 0.0), "dx")
     _close(got["d_weight"], (dy.double() * xhat).sum(0), F * (dy.double() * xhat).abs().sum(0) + 1e-30, "d_weight")
+
+
+@pytest.mark.parametrize("rows,H", [(7, 40), (33, 256), (9, 512), (130, 2048), (3, 4104), (2, 8200), (2, 17), (2, 4097)])
+@pytest.mark.parametrize("with_dh", [True, False])
+def test_backward_in_fp32_of_a_bf16_stream(rows, H, with_dh):
+    """dx_f32 is the value that dx is the rounding of."""
+    m = mok()
+    h, dh, w = _inputs(rows, H, "bf16", "bf16", "bf16", seed=23)
+    dy = _inputs(rows, H, "bf16", "none", "bf16", seed=25)[0]
+    rstd = _ref(h, None, w, 1e-6)[1].float()
+    a = _cuda(dy, h, w, rstd, dh if with_dh else None)
+    out = m.rms_norm_backward(*a[:4], d_h=a[4], f32_dx=True)
+    plain = m.rms_norm_backward(*a[:4], d_h=a[4], bf16_dx=True)
+    assert set(plain) == {"dx", "d_weight"} and out["dx_f32"].dtype == F32
+    assert torch.equal(out["dx_f32"].to(BF16), out["dx"]) and torch.equal(out["dx"], plain["dx"])
+    r = rstd.double()[:, None]
+    xhat, g = h.double() * r, dy.double() * w.double()
+    dx = r * (g - xhat * (g * xhat).mean(-1, keepdim=True)) + (dh.double() if with_dh else 0.0)
+    size = r * (g.abs() + xhat.abs() * (g * xhat).abs().mean(-1, keepdim=True)) + (dh.double().abs() if with_dh else 0.0)
+    _close(out["dx_f32"], dx, F * size, "dx_f32")
+
+
+def test_an_fp32_x_beside_a_bf16_stream_gets_an_unrounded_gradient():
+    """Under autograd the gradient of x is fp32, as x is: within fp32's error of
+    the 64-bit gradient at the stream as it was stored, where the stream's own
+    gradient is rounded to bf16."""
+    mok()
+    from mixture_experts_layer_mok_gb300.autograd import rms_norm
+
+    x, r, w = _inputs(37, 96, "f32", "bf16", "bf16", seed=31)
+    dy, dh = (_inputs(37, 96, "bf16", "none", "bf16", seed=s)[0] for s in (33, 35))
+    gx, gr, gw = (t.cuda().requires_grad_() for t in (x, r, w))
+    y, h = rms_norm(gx, gw, gr, eps=1e-5)
+    torch.autograd.backward([y, h], [dy.cuda(), dh.cuda()])
+    rstd = _ref(x, r, w, 1e-5)[1][:, None]
+    xhat, g = h.detach().double().cpu() * rstd, dy.double() * w.double()
+    dx = rstd * (g - xhat * (g * xhat).mean(-1, keepdim=True)) + dh.double()
+    size = rstd * (g.abs() + xhat.abs() * (g * xhat).abs().mean(-1, keepdim=True)) + dh.double().abs()
+    assert gx.grad.dtype == F32 and gr.grad.dtype == BF16
+    _close(gx.grad, dx, F * size, "dx")
+    assert torch.equal(gx.grad.to(BF16), gr.grad)

@@ -160,3 +160,15 @@ def test_adamw_check_is_the_steps_own(lib):
     for bad in (dict(num=-1), dict(step=-1), dict(g=24), dict(p=24), dict(v=None), dict(master=16), dict(lr=float("inf")),
                 dict(beta1=1.0), dict(n=-1)):
         assert check(**bad) == BAD, bad
+
+
+def test_norm_backward_in_both_types_refusals(lib):
+    def bwd(dy=FAKE, h=FAKE, hd=0, w=FAKE, wd=0, rstd=FAKE, dh=None, rows=4, H=64, dx=FAKE, other=FAKE, dw=FAKE, ws=FAKE,
+            n=1 << 30):
+        return lib.mok_rms_norm_bwd_both(dy, h, hd, w, wd, rstd, dh, rows, H, dx, other, dw, ws, n, None)
+
+    for hd in (0, 1):
+        for bad in (dict(rows=-1), dict(H=0), dict(wd=3), dict(dw=None), dict(ws=None), dict(dy=None), dict(dx=None), dict(n=16),
+                    dict(other=ODD), dict(dh=ODD)):
+            assert bwd(hd=hd, **bad) == BAD, bad
+    assert bwd(hd=2) == BAD
