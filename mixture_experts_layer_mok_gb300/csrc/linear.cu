@@ -96,42 +96,79 @@ __device__ int g_linear_status;   // first error since the last read
 
 // The largest split of K, in powers of two, whose clusters are all resident
 // and whose CTAs each have at least four K-blocks.
+template <class K>
+cudaError_t choose_split(K kern, KernelInfo& info, int threads, int smem, long long tiles, LinearParams& p) {
+  p.split = 1;
+  int n = 0;
+  cudaError_t err = resident_clusters(kern, info, threads, smem, 1, &n);
+  for (int s = 2; err == cudaSuccess && s <= 8 && p.nk / s >= 4; s *= 2) {
+    err = resident_clusters(kern, info, threads, smem, s, &n);
+    if (tiles > n) break;
+    p.split = s;
+  }
+  return err;
+}
+
+// Whether the longest of the split's ranges of K is summed in chunks.
+bool needs_chunks(const LinearParams& p) { return p.out_f32 && (p.nk + p.split - 1) / p.split > 2 * kChunk; }
+
 template <bool AMN, bool BMN, int BN, bool FWD>
 cudaError_t launch_split(const LinearMaps& maps, LinearParams& p, cudaStream_t st) {
   using C = SplitCfg<AMN, BMN, BN>;
-  auto kern = linear_split_kernel<AMN, BMN, BN, FWD>;
-  static KernelInfo info;
   const long long lt = (p.L + 127) / 128, ct = (static_cast<long long>(p.C) + BN - 1) / BN;
-  p.split = 1;
-  int n = 0;
-  cudaError_t err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 1, &n);
-  for (int s = 2; err == cudaSuccess && s <= 8 && p.nk / s >= 4; s *= 2) {
-    err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, s, &n);
-    if (lt * ct > n) break;
-    p.split = s;
-  }
+  const auto launch = [&](auto kern) {
+    return launch_clusters(kern, dim3(static_cast<unsigned>(lt * p.split), static_cast<unsigned>(ct)), C::kThreads, C::kSmemBytes,
+                           p.split, st, maps, p);
+  };
+  auto kern = linear_split_kernel<AMN, BMN, BN, FWD, false>;
+  static KernelInfo info;
+  cudaError_t err = choose_split(kern, info, C::kThreads, C::kSmemBytes, lt * ct, p);
   if (err != cudaSuccess) return err;
-  return launch_clusters(kern, dim3(static_cast<unsigned>(lt * p.split), static_cast<unsigned>(ct)), C::kThreads, C::kSmemBytes,
-                         p.split, st, maps, p);
+  if constexpr (FWD) {
+    if (needs_chunks(p)) {
+      auto chunked = linear_split_kernel<AMN, BMN, BN, FWD, true>;
+      static KernelInfo chunked_info;
+      err = choose_split(chunked, chunked_info, C::kThreads, C::kSmemBytes, lt * ct, p);
+      return err != cudaSuccess ? err : launch(chunked);
+    }
+  }
+  return launch(kern);
 }
 
 // The largest number of pairs along K, likewise.
-template <bool AMN, bool BMN, bool FWD>
-cudaError_t launch_pair_split(const LinearMaps& maps, LinearParams& p, cudaStream_t st) {
-  using C = PairSplitCfg<AMN, BMN>;
-  auto kern = linear_pair_split_kernel<AMN, BMN, FWD>;
-  static KernelInfo info;
+template <class K>
+cudaError_t choose_pairs(K kern, KernelInfo& info, int threads, int smem, LinearParams& p) {
   p.split = 1;
   int n = 0;
-  cudaError_t err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2, &n);
+  cudaError_t err = resident_clusters(kern, info, threads, smem, 2, &n);
   for (int s = 2; err == cudaSuccess && s <= 4 && p.nk / s >= 4; ++s) {
-    err = resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2 * s, &n);
+    err = resident_clusters(kern, info, threads, smem, 2 * s, &n);
     if (p.l_tiles * p.c_tiles > n) break;
     p.split = s;
   }
+  return err;
+}
+
+template <bool AMN, bool BMN, bool FWD>
+cudaError_t launch_pair_split(const LinearMaps& maps, LinearParams& p, cudaStream_t st) {
+  using C = PairSplitCfg<AMN, BMN>;
+  const auto launch = [&](auto kern) {
+    return launch_clusters(kern, dim3(static_cast<unsigned>(2 * p.split * p.l_tiles * p.c_tiles)), C::kThreads, C::kSmemBytes,
+                           2 * p.split, st, maps, p);
+  };
+  auto kern = linear_pair_split_kernel<AMN, BMN, FWD, false>;
+  static KernelInfo info;
+  cudaError_t err = choose_pairs(kern, info, C::kThreads, C::kSmemBytes, p);
   if (err != cudaSuccess) return err;
-  return launch_clusters(kern, dim3(static_cast<unsigned>(2 * p.split * p.l_tiles * p.c_tiles)), C::kThreads, C::kSmemBytes,
-                         2 * p.split, st, maps, p);
+  if constexpr (FWD) {
+    if (needs_chunks(p)) {
+      auto chunked = linear_pair_split_kernel<AMN, BMN, FWD, true>;
+      static KernelInfo chunked_info;
+      err = choose_pairs(chunked, chunked_info, C::kThreads, C::kSmemBytes, p);
+      return err != cudaSuccess ? err : launch(chunked);
+    }
+  }
+  return launch(kern);
 }
 
 template <int KIND>

@@ -10,12 +10,11 @@
 // Sums are fp32 in TMEM; every edge (l, c and k) is cut by the tensor maps,
 // whose loads read zeros outside and whose stores write nothing there.
 //
-// Three kernels.
+// Three kernels, each of which sums fp32 outputs in chunks of K (kChunk).
 //   linear_pair_kernel: persistent CTA pairs (M = 256 rows c over two SMs, 256
 //   columns l, two accumulator buffers), for products with enough 256 x 256
 //   tiles to fill the GPU.  Each thread of the epilogue holds 32 neighbouring
-//   elements of an output row, which leave through TMA stores.  fp32 outputs
-//   are summed in chunks of K.
+//   elements of an output row, which leave through TMA stores.
 //   linear_pair_split_kernel: the same tile with K split over 1 to 4 pairs of a
 //   cluster, which add their parts through distributed shared memory in rank
 //   order, for products of fewer such tiles.  An SM takes in about 64 bytes a
@@ -217,6 +216,35 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
       : "memory");
 }
 
+// K-blocks that are summed in the tensor core for fp32 outputs before they are
+// added to the sums that the epilogue's registers hold.  The tensor core's
+// additions truncate, which shifts a sum by about 1e-9 of its size per k: in one
+// go, the outputs of K = 4096 are 4.4e-6 off and those of K = 16384 1.9e-5, in
+// chunks 7e-7 both, whichever kernel takes the product (bf16 outputs, rounded at
+// 2e-3, have no use for it).  The split kernels sum up to two chunks in their
+// two accumulators, and only longer ranges of K in registers.
+constexpr int kChunk = 12;
+
+// This thread's N columns at TMEM address t, in steps of 16 (or 8): added to
+// sum, or with BACK the sums put in their place.
+template <int N, bool BACK = false>
+__device__ __forceinline__ void add_columns(uint32_t t, float (&sum)[N]) {
+  constexpr int kStep = N % 16 == 0 ? 16 : 8;
+  static_assert(N % kStep == 0 && (kStep == 16 || !BACK), "whole steps");
+#pragma unroll
+  for (int j = 0; j < N; j += kStep) {
+    float v[kStep];
+    if constexpr (kStep == 16)
+      tmem_ld16(t + j, v);
+    else
+      tmem_ld8(t + j, v);
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) sum[j + i] += v[i];
+    if constexpr (BACK) tmem_st16(t + j, sum + j);
+  }
+  if (BACK) asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- split kernel
 template <bool AMN, bool BMN, int BN>
 struct SplitCfg {
@@ -300,15 +328,19 @@ __device__ __forceinline__ void join_split(const LinearParams& p, const float* p
 // warps for each quarter of the TMEM lanes.  Few rows are bound by the bytes of
 // the weight: one row, 152064 x 4096, 174 us (7.2 TB/s); 7168 x 2048, 7.3 us, of
 // which the launch and the first bytes take three.
-template <bool AMN, bool BMN, int BN, bool FWD>
+// CHUNKED: fp32 outputs over more than two chunks of K to a CTA; 100 x 152064 x
+// 4096 209 us so and 204 in two accumulators, 128 x 40000 x 16384 286 and 276, 1 x
+// 152064 x 4096 176 and 175 (errors 7e-7, and 2.1e-6 and 9.1e-6).
+template <bool AMN, bool BMN, int BN, bool FWD, bool CHUNKED>
 __global__ void __launch_bounds__(SplitCfg<AMN, BMN, BN>::kThreads, 2) linear_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
   using C = SplitCfg<AMN, BMN, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
   uint64_t* empty = full + C::kStages;
-  uint64_t* tfull = empty + C::kStages;
-  uint64_t* done = tfull + 1;
+  uint64_t* tfull = empty + C::kStages;   // (the second, and tempty: CHUNKED)
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -320,14 +352,17 @@ __global__ void __launch_bounds__(SplitCfg<AMN, BMN, BN>::kThreads, 2) linear_sp
   const int kb1 = static_cast<int>(static_cast<long long>(p.nk) * (rank + 1) / S);
   // fp32 outputs: the K range in two accumulators, added in the epilogue, which
   // halves the length of the tensor core's chain of truncating additions
-  const bool two = FWD && p.out_f32 && kb1 - kb0 > 1;
+  const bool two = FWD && !CHUNKED && p.out_f32 && kb1 - kb0 > 1;
   const int kbm = two ? (kb0 + kb1) / 2 : kb1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], C::kEpiWarps);
+    }
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -384,20 +419,30 @@ __global__ void __launch_bounds__(SplitCfg<AMN, BMN, BN>::kThreads, 2) linear_sp
     }
   } else if (warp == 1) {
     const uint64_t ad = linear_desc<AMN>(smem_u32(smem)), bd = linear_desc<BMN>(smem_u32(smem) + kLinABytes);
-    int stage = 0;
-    uint32_t phase = 0;
+    int stage = 0, buf = 0, in = 0;   // CHUNKED: the accumulator, and the block's place in its chunk
+    uint32_t phase = 0, bphase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
+      if (CHUNKED && in == 0) {
+        if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) break;
+        tc_fence_after();
+      }
       if (!warp_wait(&full[stage], phase, abort_flag, p.status)) break;
-      const uint32_t at = stage * C::kStageBytes, acc = tmem_base + (kb >= kbm ? BN : 0);
+      const uint32_t at = stage * C::kStageBytes, acc = tmem_base + (CHUNKED ? buf * BN : kb >= kbm ? BN : 0);
+      const bool last = CHUNKED ? in == kChunk - 1 || kb == kb1 - 1 : kb == kb1 - 1;
       if (elect_one()) {
-        umma_bf16(acc, desc_at(ad, at), desc_at(bd, at), C::kIdesc, kb != kb0 && kb != kbm);
+        umma_bf16(acc, desc_at(ad, at), desc_at(bd, at), C::kIdesc, CHUNKED ? in != 0 : kb != kb0 && kb != kbm);
 #pragma unroll
         for (int kk = 1; kk < kLinBK / 16; ++kk)
           umma_bf16(acc, desc_at(ad, at + kk * kStep<AMN>), desc_at(bd, at + kk * kStep<BMN>), C::kIdesc, 1u);
         umma_commit(&empty[stage]);
-        if (kb == kb1 - 1) umma_commit(tfull);
+        if (last) umma_commit(&tfull[CHUNKED ? buf : 0]);
       }
       __syncwarp();
+      if (CHUNKED && ++in == kChunk) {
+        in = 0;
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1;
+      }
       if (++stage == C::kStages) stage = 0, phase ^= 1;
     }
     if (elect_one()) {
@@ -416,10 +461,32 @@ __global__ void __launch_bounds__(SplitCfg<AMN, BMN, BN>::kThreads, 2) linear_sp
         if (lane * 128 < cols * size)
           prefetch_l2(static_cast<const char*>(p.residual) + (static_cast<long long>(c0 + c) * p.L + l0) * size + lane * 128);
     }
-    const int w = (lane == 0) ? (mbar_wait(tfull, 0, abort_flag, p.status) ? 1 : 0) : 0;
-    if (__shfl_sync(0xffffffffu, w, 0)) {
+    const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    const auto wait_full = [&](uint64_t* bar, uint32_t parity) {
+      const int w = lane == 0 ? (mbar_wait(bar, parity, abort_flag, p.status) ? 1 : 0) : 0;
+      const bool got = __shfl_sync(0xffffffffu, w, 0) != 0;
       tc_fence_after();
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      return got;
+    };
+    if constexpr (CHUNKED) {
+      float sum[BN / 2] = {};
+      bool ok = true;
+      int buf = 0;
+      uint32_t bphase = 0;
+      for (int first = kb0; first < kb1; first += kChunk) {
+        if (!(ok = wait_full(&tfull[buf], bphase))) break;
+        add_columns<BN / 2>(tb + buf * BN + col0, sum);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1;
+      }
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < BN / 2; ++c) part[(col0 + c) * 128 + row] = sum[c];
+      }
+    } else if (wait_full(tfull, 0)) {
 #pragma unroll 1
       for (int c = col0; c < col0 + BN / 2; c += 8) {
         float v[8];
@@ -476,21 +543,6 @@ struct PairCfg {
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr uint32_t kIdesc = idesc_bf16(256, BN, BMN, AMN);
 };
-
-// This thread's N columns at TMEM address t, in steps of 16: added to sum, or
-// with BACK the sums put in their place.
-template <int N, bool BACK = false>
-__device__ __forceinline__ void add_columns(uint32_t t, float (&sum)[N]) {
-#pragma unroll
-  for (int j = 0; j < N; j += 16) {
-    float v[16];
-    tmem_ld16(t + j, v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) sum[j + i] += v[i];
-    if (BACK) tmem_st16(t + j, sum + j);
-  }
-  if (BACK) asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
 
 // Tile idx of the grid of L tiles x C tiles (256 x 256 each): C tiles in
 // groups of p.group, L tiles inside the group's width, so that the CTAs at
@@ -683,15 +735,18 @@ __device__ __forceinline__ void join_pairs(const LinearParams& p, const float* p
 // grid {2 S x tiles}, clusters of S pairs along K.  4096 x 256 x 7168 in fp32:
 // 20.6 us, of which the products take 12 on the 96 SMs that clusters of six
 // fill, and the join 4; 1003 x 1416 x 2056 14.8 us.
-template <bool AMN, bool BMN, bool FWD>
+// CHUNKED: as for linear_split_kernel; 4096 x 256 x 7168 20.9 us so and 20.5 in two
+// accumulators, 1800 x 1800 x 4096 26.1 and 25.7.
+template <bool AMN, bool BMN, bool FWD, bool CHUNKED>
 __global__ void __launch_bounds__(PairSplitCfg<AMN, BMN>::kThreads, 1) linear_pair_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p) {
   using C = PairSplitCfg<AMN, BMN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
   uint64_t* empty = full + C::kStages;
-  uint64_t* tfull = empty + C::kStages;
-  uint64_t* done = tfull + 1;
+  uint64_t* tfull = empty + C::kStages;   // (the second, and tempty: CHUNKED)
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -702,14 +757,17 @@ __global__ void __launch_bounds__(PairSplitCfg<AMN, BMN>::kThreads, 1) linear_pa
   const int kb0 = static_cast<int>(static_cast<long long>(p.nk) * (rank >> 1) / S);
   const int kb1 = static_cast<int>(static_cast<long long>(p.nk) * ((rank >> 1) + 1) / S);
   // fp32 outputs: the K range in two accumulators (see linear_split_kernel)
-  const bool two = FWD && p.out_f32 && kb1 - kb0 > 1;
+  const bool two = FWD && !CHUNKED && p.out_f32 && kb1 - kb0 > 1;
   const int kbm = two ? (kb0 + kb1) / 2 : kb1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * C::kEpiWarps);   // the leader's counts both CTAs' warps
+    }
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -771,20 +829,30 @@ __global__ void __launch_bounds__(PairSplitCfg<AMN, BMN>::kThreads, 1) linear_pa
     if (rank == lead) {
       const uint64_t bd = linear_desc<BMN>(smem_u32(smem)), ad = linear_desc<AMN>(smem_u32(smem) + kLinABytes);
       const uint16_t both = static_cast<uint16_t>(3u << lead), me = static_cast<uint16_t>(1u << lead);
-      int stage = 0;
-      uint32_t phase = 0;
+      int stage = 0, buf = 0, in = 0;   // CHUNKED: the accumulator, and the block's place in its chunk
+      uint32_t phase = 0, bphase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
+        if (CHUNKED && in == 0) {
+          if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, p.status)) break;
+          tc_fence_after();
+        }
         if (!warp_wait(&full[stage], phase, abort_flag, p.status)) break;
-        const uint32_t at = stage * C::kStageBytes, acc = tmem_base + (kb >= kbm ? 256 : 0);
+        const uint32_t at = stage * C::kStageBytes, acc = tmem_base + (CHUNKED ? buf * 256 : kb >= kbm ? 256 : 0);
+        const bool last = CHUNKED ? in == kChunk - 1 || kb == kb1 - 1 : kb == kb1 - 1;
         if (elect_one()) {
-          umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), C::kIdesc, kb != kb0 && kb != kbm);
+          umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), C::kIdesc, CHUNKED ? in != 0 : kb != kb0 && kb != kbm);
 #pragma unroll
           for (int kk = 1; kk < kLinBK / 16; ++kk)
             umma_bf16_pair(acc, desc_at(bd, at + kk * kStep<BMN>), desc_at(ad, at + kk * kStep<AMN>), C::kIdesc, 1u);
           umma_commit_pair(&empty[stage], both);
-          if (kb == kb1 - 1) umma_commit_pair(tfull, both);
+          if (last) umma_commit_pair(&tfull[CHUNKED ? buf : 0], both);
         }
         __syncwarp();
+        if (CHUNKED && ++in == kChunk) {
+          in = 0;
+          buf ^= 1;
+          if (buf == 0) bphase ^= 1;
+        }
         if (++stage == C::kStages) stage = 0, phase ^= 1;
       }
       if (elect_one()) {
@@ -802,11 +870,39 @@ __global__ void __launch_bounds__(PairSplitCfg<AMN, BMN>::kThreads, 1) linear_pa
         for (long long o = lane * 128; o < cols * size; o += 32 * 128)
           prefetch_l2(static_cast<const char*>(p.residual) + (static_cast<long long>(c0 + r) * p.L + l0) * size + o);
     }
-    const int w = (lane == 0) ? (mbar_wait(tfull, 0, abort_flag, p.status) ? 1 : 0) : 0;
-    if (__shfl_sync(0xffffffffu, w, 0)) {
+    const uint32_t tb = tmem_base + col0 + (static_cast<uint32_t>(q * 32) << 16);
+    float4* part = reinterpret_cast<float4*>(smem);
+    const auto wait_full = [&](uint64_t* bar, uint32_t parity) {
+      const int w = lane == 0 ? (mbar_wait(bar, parity, abort_flag, p.status) ? 1 : 0) : 0;
+      const bool got = __shfl_sync(0xffffffffu, w, 0) != 0;
       tc_fence_after();
-      const uint32_t tb = tmem_base + col0 + (static_cast<uint32_t>(q * 32) << 16);
-      float4* part = reinterpret_cast<float4*>(smem);
+      return got;
+    };
+    if constexpr (CHUNKED) {
+      float sum[kCols] = {};
+      bool ok = true;
+      int buf = 0;
+      uint32_t bphase = 0;
+      for (int first = kb0; first < kb1; first += kChunk) {
+        if (!(ok = wait_full(&tfull[buf], bphase))) break;
+        add_columns<kCols>(tb + buf * 256, sum);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank != lead)
+            mbar_arrive_cluster(cluster_addr(&tempty[buf], lead));
+          else
+            mbar_arrive(&tempty[buf]);
+        }
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1;
+      }
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 4)
+          part[part_at(row, (col0 + c) / 4)] = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+      }
+    } else if (wait_full(tfull, 0)) {
 #pragma unroll 1
       for (int c = 0; c < kCols; c += 16) {
         float v[16];
@@ -889,17 +985,10 @@ constexpr bool kIsForward = KIND == LIN_FWD || KIND == LIN_FWD_SHORT || KIND == 
 template <int KIND>
 using PairKindCfg = PairCfg<!kIsForward<KIND>, false, KIND == LIN_FWD_SHORT>;
 
-// K-blocks that LIN_FWD_F32 sums in the tensor core before they are added to the
-// sums that the epilogue's registers hold.  The tensor core's additions
-// truncate, which shifts a sum by about 1e-9 of its size per k: in one go, the
-// outputs of K = 4096 are 4.4e-6 off and those of K = 16384 1.9e-5, in chunks
-// 7e-7 both (bf16 outputs, rounded at 2e-3, have no use for it).  What it costs:
-// while a tile's outputs are made, the products are at most a chunk ahead; 8192
-// x 4864 outputs, in one go and in chunks, K = 1024 61 and 69 us, K = 2048 91
-// and 103, K = 4096 168 and 183; 4096 x 8192 x 7168 271 to 298 and 279 to 289.
-// Sixteen epilogue warps: 73, 109 and 195 us.
-constexpr int kChunk = 12;
-
+// What the chunks cost here: while a tile's outputs are made, the products are at
+// most a chunk ahead; 8192 x 4864 outputs, in one go and in chunks, K = 1024 61
+// and 69 us, K = 2048 91 and 103, K = 4096 168 and 183; 4096 x 8192 x 7168 271 to
+// 298 and 279 to 289.  Sixteen epilogue warps: 73, 109 and 195 us.
 template <int KIND>
 __global__ void __launch_bounds__(PairKindCfg<KIND>::kThreads, 1) linear_pair_kernel(const __grid_constant__ PairJob job) {
   constexpr bool FWD = kIsForward<KIND>, AMN = !FWD, CHUNKED = KIND == LIN_FWD_F32;

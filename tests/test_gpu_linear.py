@@ -295,3 +295,28 @@ def test_refusals():
         m.linear(odd, w)
     with pytest.raises(m.MokError):
         m.linear_backward(dy, odd, w)
+
+
+@pytest.mark.parametrize("K", [1600, 4096, 16384])
+@pytest.mark.parametrize("M,N", [(1, 40000), (20, 40000), (60, 40000), (100, 40000), (128, 264), (1800, 1800), (4096, 256),
+                                 (1003, 1416), (40000, 64)])
+def test_32_bit_outputs_do_not_lose_with_the_length_in_any_kernel(M, N, K):
+    """The bound of the test above, whichever kernel takes the product and
+    however many CTAs share its K: a token or a few beside a large weight (each
+    tile width, K whole), fewer tiles than the GPU has pairs (K whole and
+    split), a narrow weight."""
+    g = torch.Generator(device="cuda").manual_seed(K + M)
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF16)
+    w = (torch.randn(N, K, generator=g, device="cuda") * K ** -0.5).to(BF16)
+    b = torch.randn(N, generator=g, device="cuda")
+    r = torch.randn(M, N, generator=g, device="cuda").to(BF16)
+    y, z = mok().linear(x, w, bias=b, residual=r, activation="silu", out_dtype=F32, save_z=True)
+    plain, _ = mok().linear(x, w, out_dtype=F32)
+    z64 = x.double() @ w.double().T
+    assert ((plain.double() - z64).norm() / z64.norm()).item() <= 2.0 ** -19
+    z64 += b.double()
+    y64 = act64(z64, "silu") + r.double()
+    assert ((y.double() - y64).norm() / y64.norm()).item() <= 2.0 ** -19
+    assert ((z.double() - z64).norm() / z64.norm()).item() <= 2.0 ** -9
+    again, _ = mok().linear(x, w, bias=b, residual=r, activation="silu", out_dtype=F32, save_z=True)
+    assert torch.equal(again, y) and mok().linear_status() == 0
