@@ -320,3 +320,38 @@ def test_32_bit_outputs_do_not_lose_with_the_length_in_any_kernel(M, N, K):
     assert ((z.double() - z64).norm() / z64.norm()).item() <= 2.0 ** -9
     again, _ = mok().linear(x, w, bias=b, residual=r, activation="silu", out_dtype=F32, save_z=True)
     assert torch.equal(again, y) and mok().linear_status() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 136, 200), (300, 264, 136), (300, 264, 2056), (2600, 2048, 72), (2600, 2048, 2056)])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_infinities_and_nan_arrive(M, N, K, act, out):
+    """A NaN in a row of x is in all of that row's outputs, an infinite weight
+    in its column with x's sign, an infinite residual in its element; nowhere
+    else."""
+    m = mok()
+    g = torch.Generator().manual_seed(8)
+    x, w, r = _rand(g, M, K), _rand(g, N, K, std=K ** -0.5), _rand(g, M, N)
+    assert bool((x[:, 0] != 0).all())
+    clean, _ = m.linear(x.cuda(), w.cuda(), residual=r.cuda(), activation=act, out_dtype=out)
+    x[1, K - 1] = float("nan")
+    w[N - 1, 0] = float("inf")
+    r[2, 0] = float("-inf")
+    y, z = m.linear(x.cuda(), w.cuda(), residual=r.cuda(), activation=act, out_dtype=out, save_z=True)
+    y, z, clean = y.cpu(), z.cpu(), clean.cpu()
+    keep = torch.ones(M, N, dtype=torch.bool)
+    keep[1], keep[:, N - 1], keep[2, 0] = False, False, False
+    assert torch.equal(y[keep], clean[keep])
+    assert bool(y[1].isnan().all()) and bool(z[1].isnan().all())
+    assert y[2, 0].item() == float("-inf") and bool(z[2, 0].isfinite())
+    rows = torch.arange(M) != 1
+    up, down = rows & (x[:, 0] > 0), rows & (x[:, 0] < 0)
+    assert bool((z[up, N - 1] == float("inf")).all()) and bool((z[down, N - 1] == float("-inf")).all())
+    assert bool((y[up, N - 1] == float("inf")).all())
+    if act == "none":
+        assert bool((y[down, N - 1] == float("-inf")).all())
+    elif act == "relu":
+        assert torch.equal(y[down, N - 1], r[down, N - 1].to(out))
+    else:   # their limit is 0, their formula -inf times 0
+        assert not bool(y[down, N - 1].isinf().any())
+    assert m.linear_status() == 0
