@@ -114,24 +114,30 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.f;
 }
 
-// NV (4 or 8) consecutive values of a bf16 or fp32 array.
-template <int NV>
+template <bool READ_ONLY, class T>
+__device__ __forceinline__ T load_as(const T* p) {
+  if constexpr (READ_ONLY) return __ldg(p);
+  return *p;
+}
+// NV (4 or 8) consecutive values of a bf16 or fp32 array.  READ_ONLY: nothing in
+// the launch writes it, as the residual may be, whose place the output can take.
+template <int NV, bool READ_ONLY = true>
 __device__ __forceinline__ void load_vals(const void* base, int f32, long long at, float* f) {
   if (f32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
 #pragma unroll
     for (int i = 0; i < NV / 4; ++i) {
-      const float4 a = __ldg(p + i);
+      const float4 a = load_as<READ_ONLY>(p + i);
       f[4 * i] = a.x, f[4 * i + 1] = a.y, f[4 * i + 2] = a.z, f[4 * i + 3] = a.w;
     }
   } else {
     uint32_t w[NV / 2];
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
     if constexpr (NV == 8) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 a = load_as<READ_ONLY>(reinterpret_cast<const uint4*>(p));
       w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     } else {
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 a = load_as<READ_ONLY>(reinterpret_cast<const uint2*>(p));
       w[0] = a.x, w[1] = a.y;
     }
 #pragma unroll
@@ -298,7 +304,7 @@ __device__ __forceinline__ void join_columns(const LinearParams& p, const float*
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int cu = min(c + kWarps * u, c_end - 1);   // past the end: the last column again, not stored
-      if (FWD && p.residual) load_vals<4>(p.residual, p.residual_f32, static_cast<long long>(c0 + cu) * p.L + l, r[u]);
+      if (FWD && p.residual) load_vals<4, false>(p.residual, p.residual_f32, static_cast<long long>(c0 + cu) * p.L + l, r[u]);
 #pragma unroll
       for (int s = 0; s < S; ++s) t[u][s] = part_of<S>(part, peer, s, rank, static_cast<uint32_t>(cu * 128 + lane * 4) * 4u);
     }
@@ -598,7 +604,7 @@ __device__ __forceinline__ void output_block(const LinearParams& p, const Linear
         for (int i = 0; i < 8; ++i) z[i] = act_value<ACT>(z[i]);
         if (p.residual && lj < p.L && c < p.C) {
           float r[8];
-          load_vals<8>(p.residual, p.residual_f32, c * p.L + lj, r);
+          load_vals<8, false>(p.residual, p.residual_f32, c * p.L + lj, r);
 #pragma unroll
           for (int i = 0; i < 8; ++i) z[i] += r[i];
         }
@@ -706,7 +712,7 @@ __device__ __forceinline__ void join_rows(const LinearParams& p, const float* pa
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int ru = r0 + min(r + kWarps / 2 * u, rows - 1);   // past the end: the last row again, not stored
-      if (FWD && p.residual) load_vals<4>(p.residual, p.residual_f32, static_cast<long long>(c0 + ru) * p.L + l, res[u]);
+      if (FWD && p.residual) load_vals<4, false>(p.residual, p.residual_f32, static_cast<long long>(c0 + ru) * p.L + l, res[u]);
 #pragma unroll
       for (int s = 0; s < S; ++s)
         t[u][s] = part_of<S>(part, peer, s, share, static_cast<uint32_t>(part_at(ru, h * 32 + lane)) * 16u);

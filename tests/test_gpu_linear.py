@@ -355,3 +355,21 @@ def test_infinities_and_nan_arrive(M, N, K, act, out):
     else:   # their limit is 0, their formula -inf times 0
         assert not bool(y[down, N - 1].isinf().any())
     assert m.linear_status() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 7168, 264), (3, 136, 200), (100, 19600, 64), (300, 264, 136), (300, 264, 2056),
+                                   (1003, 1416, 2056), (2600, 2056, 72), (2600, 2056, 1032)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_the_output_may_be_the_residual(M, N, K, dtype):
+    """y in the residual's place, through the C ABI: every bit as apart."""
+    m = mok()
+    from mixture_experts_layer_mok_gb300 import _lib
+
+    g = torch.Generator().manual_seed(M)
+    x, w, r = _rand(g, M, K).cuda(), _rand(g, N, K, std=K ** -0.5).cuda(), _rand(g, M, N, dtype=dtype).cuda()
+    want, _ = m.linear(x, w, residual=r, activation="gelu", out_dtype=dtype)
+    t = _lib.MOK_DTYPE_F32 if dtype == F32 else _lib.MOK_DTYPE_BF16
+    s = torch.cuda.current_stream().cuda_stream
+    st = _lib.load().mok_linear(x.data_ptr(), w.data_ptr(), None, 0, r.data_ptr(), t, _lib.ACTIVATIONS["gelu"], M, N, K,
+                                r.data_ptr(), t, None, s)
+    assert st == 0 and torch.equal(r, want) and m.linear_status() == 0

@@ -306,3 +306,49 @@ def test_an_fp32_x_beside_a_bf16_stream_gets_an_unrounded_gradient():
     assert gx.grad.dtype == F32 and gr.grad.dtype == BF16
     _close(gx.grad, dx, F * size, "dx")
     assert torch.equal(gx.grad.to(BF16), gr.grad)
+
+
+IN_PLACE = [(7, 40), (33, 256), (9, 512), (1300, 64), (130, 2048), (1217, 640), (3, 4104), (700, 8200), (2, 32768), (2, 17), (2, 4097)]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+@pytest.mark.parametrize("rows,H", IN_PLACE)
+@pytest.mark.parametrize("xt,rt,place", [("bf16", "bf16", "residual"), ("bf16", "f32", "residual"), ("f32", "f32", "x"),
+                                         ("bf16", "bf16", "x")])
+def test_the_stream_may_be_written_in_place(rows, H, xt, rt, place):
+    """h in the residual's or x's place, through the C ABI: every bit as apart."""
+    m = mok()
+    from mixture_experts_layer_mok_gb300 import _lib
+
+    x, r, w = _cuda(*_inputs(rows, H, xt, rt, "bf16", seed=41))
+    want = m.rms_norm(x, w, residual=r, eps=1e-5)
+    h = r if place == "residual" else x
+    y, rstd = torch.empty_like(want.y), torch.empty_like(want.rstd)
+    code = {"bf16": _lib.MOK_DTYPE_BF16, "f32": _lib.MOK_DTYPE_F32}
+    st = _lib.load().mok_rms_norm(_ptr(x), code[xt], _ptr(r), code[rt], _ptr(w), 0, rows, H, 1e-5, _ptr(h), _ptr(y), None, None,
+                                  _ptr(rstd), torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and torch.equal(h, want.h) and torch.equal(y, want.y) and torch.equal(rstd, want.rstd)
+
+
+@pytest.mark.parametrize("rows,H", IN_PLACE)
+@pytest.mark.parametrize("ht", ["bf16", "f32"])
+def test_the_streams_gradient_may_be_written_in_place(rows, H, ht):
+    """dx in dh's place, through the C ABI: every bit as apart."""
+    m = mok()
+    from mixture_experts_layer_mok_gb300 import _lib
+
+    h, dh, w = _cuda(*_inputs(rows, H, ht, ht, "bf16", seed=43))
+    dy = _inputs(rows, H, "bf16", "none", "bf16", seed=45)[0].cuda()
+    rstd = torch.rsqrt(h.float().square().mean(-1) + 1e-6)
+    want = m.rms_norm_backward(dy, h, w, rstd, d_h=dh, bf16_dx=True)
+    lib = _lib.load()
+    n = lib.mok_rms_norm_bwd_workspace_bytes(rows, H)
+    ws, dw = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(want["d_weight"])
+    d16 = torch.empty_like(want["dx_bf16"]) if ht == "f32" else None
+    st = lib.mok_rms_norm_bwd(_ptr(dy), _ptr(h), int(ht == "f32"), _ptr(w), 0, _ptr(rstd), _ptr(dh), rows, H, _ptr(dh), _ptr(d16),
+                              _ptr(dw), _ptr(ws), n, torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and torch.equal(dh, want["dx"]) and torch.equal(dw, want["d_weight"])
+    assert d16 is None or torch.equal(d16, want["dx_bf16"])
