@@ -66,8 +66,12 @@ __device__ __forceinline__ float logistic(float x) { return fast_rcp(1.f + fast_
 
 // 1 - Phi(|z|), Phi the normal distribution function, and e = exp(-z^2/2):
 // with t = 1 / (1 + p |z| / sqrt 2) it is 1/2 poly(t) e (Abramowitz and Stegun,
-// 7.1.26; error below 7.5e-8).  A dozen instructions without a branch, where
-// erff takes both of its branches in nearly every warp.
+// 7.1.26, whose own error is below 7.5e-8).  Evaluated in these 32-bit steps it is
+// off by up to 3e-7, and GELU, measured over [-12, 12], by 3.3e-7; for negative z
+// that is 3.3e-6 of the value at -2, 1.6e-3 at -5, 3.6e-3 at -6 and 4% at -8 (of
+// 6e-16), where 0.5 z (1 + erf) in 32 bits is off by 1.1e-6, 6% and, from -6 on,
+// all of it.  A dozen instructions without a branch, where erff takes both of
+// its branches in nearly every warp.
 __device__ __forceinline__ float normal_tail(float z, float& e) {
   const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
   e = fast_exp2(z * z * (-0.5f * kLog2e));

@@ -373,3 +373,17 @@ def test_the_output_may_be_the_residual(M, N, K, dtype):
     st = _lib.load().mok_linear(x.data_ptr(), w.data_ptr(), None, 0, r.data_ptr(), t, _lib.ACTIVATIONS["gelu"], M, N, K,
                                 r.data_ptr(), t, None, s)
     assert st == 0 and torch.equal(r, want) and m.linear_status() == 0
+
+
+def test_gelu_over_its_range():
+    """In 32 bits, from a bias alone: within 4e-7 (its values reach 12: half of
+    2^-21 of rounding) and, for negative z, within 4e-3 of the value down to -6."""
+    N = 1 << 18
+    z = torch.linspace(-12, 12, N, device="cuda")
+    x, w = torch.zeros(1, 8, device="cuda", dtype=BF16), torch.zeros(N, 8, device="cuda", dtype=BF16)
+    y = mok().linear(x, w, bias=z, activation="gelu", out_dtype=F32)[0][0].double()
+    ref = act64(z.double(), "gelu")
+    err = (y - ref).abs()
+    assert bool((err <= 4e-7 + 2.0 ** -24 * ref.abs()).all())
+    tail = (z < 0) & (z > -6)
+    assert bool((err[tail] <= 4e-3 * ref[tail].abs()).all())
