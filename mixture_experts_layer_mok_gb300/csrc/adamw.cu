@@ -130,13 +130,6 @@ __device__ __forceinline__ float e4m3_stochastic(float y, uint32_t below) {
   return __uint_as_float((__float_as_uint(fabsf(y) + off) + below) & 0xFFF00000u) - off;   // sign dropped
 }
 
-// 1/x in one instruction, good to about 2^-22.
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // The larger of two values; NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float m;

@@ -72,15 +72,7 @@ mok_status_t device_info(int* num_sms) {
   return MOK_OK;
 }
 
-}  // namespace mok
-
-namespace {
-
 // ---------------------------------------------------------------- TMA descriptors
-}  // namespace
-
-namespace mok {
-
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;

@@ -244,9 +244,9 @@ mok_status_t mok_linear_status(int* status) {
   return MOK_OK;
 }
 
-// ---------------------------------------------------------------- AdamW
 }  // extern "C"
 
+// ---------------------------------------------------------------- AdamW
 namespace {
 
 // counted: cfg->step is what is added to a count of at least 1.

@@ -49,18 +49,6 @@ constexpr int kLinChunk = 64 * 128;        // an MN-major 64 x 64 block
 constexpr int kLinABytes = 128 * kLinBK * 2;
 
 // ---------------------------------------------------------------- epilogue
-// One special-function instruction each (subnormals flushed): 2^x and 1/x,
-// good to about 2^-22.
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float logistic(float x) { return fast_rcp(1.f + fast_exp2(-kLog2e * x)); }
 

@@ -11,6 +11,19 @@
 
 namespace mok {
 
+// One special-function instruction each (subnormals flushed): 2^x and 1/x,
+// good to about 2^-22.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The value 2^(s - 127) of an E8M0 scale (255: NaN).
 __device__ __forceinline__ float e8m0_value(uint32_t s) {
   return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
