@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "api_util.h"
 #include "internal.h"
 #include "linear.cuh"
@@ -39,7 +41,7 @@ mok_status_t operand_map(CUtensorMap* m, const void* base, long long inner, long
 // of different sizes, so that fewer large clusters fit than the SM count says:
 // of the pair split kernel 76 of 2 CTAs, 36 of 4, 23 of 6 and 15 of 8.
 struct KernelInfo {
-  int resident[64][9] = {};
+  std::atomic<int> resident[64][9] = {};   // 0: not looked up yet; any thread may be the first
 };
 
 template <class K>
@@ -48,8 +50,9 @@ cudaError_t resident_clusters(K kern, KernelInfo& info, int threads, int smem, i
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64 || cluster < 1 || cluster > 8) return cudaErrorInvalidValue;
-  int& at = info.resident[dev][cluster];
-  if (at == 0) {
+  std::atomic<int>& at = info.resident[dev][cluster];
+  int found = at.load(std::memory_order_acquire);
+  if (found == 0) {
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[1];
@@ -63,13 +66,12 @@ cudaError_t resident_clusters(K kern, KernelInfo& info, int threads, int smem, i
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int found = 0;
     err = cudaOccupancyMaxActiveClusters(&found, kern, &cfg);
     if (err != cudaSuccess) return err;
     if (found <= 0) return cudaErrorInvalidConfiguration;
-    at = found;
+    at.store(found, std::memory_order_release);
   }
-  *n = at;
+  *n = found;
   return cudaSuccess;
 }
 
@@ -332,18 +334,19 @@ cudaError_t launch_dz(const DY* dy, const uint16_t* z, int act, long long M, int
 }  // namespace
 
 cudaError_t linear_status_word(int** word) {
-  static int* at[64] = {};
+  static std::atomic<int*> at[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!at[dev]) {
+  *word = at[dev].load(std::memory_order_acquire);
+  if (!*word) {
     void* a = nullptr;
     err = cudaGetSymbolAddress(&a, g_linear_status);
     if (err != cudaSuccess) return err;
-    at[dev] = static_cast<int*>(a);
+    *word = static_cast<int*>(a);
+    at[dev].store(*word, std::memory_order_release);
   }
-  *word = at[dev];
   return cudaSuccess;
 }
 

@@ -387,3 +387,33 @@ def test_gelu_over_its_range():
     assert bool((err <= 4e-7 + 2.0 ** -24 * ref.abs()).all())
     tail = (z < 0) & (z > -6)
     assert bool((err[tail] <= 4e-3 * ref[tail].abs()).all())
+
+
+def test_first_calls_from_several_threads():
+    """The launch parameters that are looked up once, first needed by threads at
+    the same time (a fresh process: nothing is looked up yet)."""
+    import os
+    import subprocess
+    import sys
+
+    mok()
+    code = """
+import threading, torch
+import mixture_experts_layer_mok_gb300 as m
+xs = [torch.randn(M, 512, device="cuda").bfloat16() for M in (1, 300, 9000)]
+w = torch.randn(2560, 512, device="cuda").bfloat16()
+out, gate = {}, threading.Barrier(8)
+def work(i):
+    gate.wait()
+    out[i] = [m.linear(x, w, activation="silu", stream=torch.cuda.Stream())[0] for x in xs]
+ts = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+[t.start() for t in ts]; [t.join() for t in ts]
+torch.cuda.synchronize()
+want = [m.linear(x, w, activation="silu")[0] for x in xs]
+assert len(out) == 8 and all(torch.equal(a, b) for o in out.values() for a, b in zip(o, want))
+assert m.linear_status() == 0
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and p.stdout.strip() == "ok", p.stderr[-2000:]
