@@ -153,9 +153,13 @@ constexpr int kWarpRows = 4;   // rows of a block in the one-warp-per-row kernel
 
 // XT: x's type; RT: the residual's (NoType: none).  V values per load, ITEMS
 // loads per thread; WARP_ROW: one warp per row, else one block.  Bound by
-// memory: bf16 with a bf16 residual, 65536 x 7168, 527 us (7.1 TB/s); an fp32
-// residual and MXFP8 out, 16384 x 4096, 102.5 us (7.2 TB/s); one row 5.6 us, a
-// launch and two trips to memory.
+// memory where lengths are a multiple of 8: bf16 with a bf16 residual, 65536 x
+// 7168, 526 us (7.1 TB/s); an fp32 residual and MXFP8 out, 16384 x 4096, 102.5 us
+// (7.2 TB/s), with bf16 out too 127 us (6.9 TB/s); 2048 x 32768 87 us (6.2 TB/s);
+// one row 5.6 us, a launch and two trips to memory.  Other lengths go an element
+// a load, bound by instructions: 67041 x 1001 146 us (3.7 TB/s), 16388 x 4095 186,
+// and above 4096, where a thread of 1024 spills up to 164 bytes, 16380 x 4097 251
+// us and 2048 x 32767 299 (2.1 and 1.8 TB/s).
 template <class XT, class RT, int V, int ITEMS, bool WARP_ROW, int MAXT>
 __global__ void __launch_bounds__(MAXT) rms_norm_kernel(const NormArgs a) {
   constexpr bool kRes = !std::is_same_v<RT, NoType>;
@@ -269,12 +273,12 @@ __device__ __forceinline__ void row_sums(float (&s)[R], float (*red)[R]) {
 // elements to a thread; each such group walks the rows, R at a time, and keeps
 // its columns' share of dw in registers.  `part` gets one row of sums per block,
 // which column_sum_kernel adds in order.
-//   acc_j += rstd (dy_j h_j),   s = sum_j w_j dy_j h_j,   k = -(s rstd) / H,
-//   dx_j = rstd (w_j dy_j + k (h_j rstd)) + dh_j
-// k is the mean of g xhat and h_j rstd is xhat_j, of order 1 whatever the size
-// of h: with rstd^3 in one factor, one multiplication an element less, dx was
-// lost for rows of a root mean square above 1e12 or below 1e-13.
-template <class HT, int ITEMS, int R, int W, int THREADS>
+//   acc_j += rstd (dy_j h_j),   s = sum_j w_j dy_j h_j,   k = -((s rstd) / H) rstd,
+//   dx_j = rstd (w_j dy_j + k h_j) + dh_j
+// (s rstd) / H is the mean of g xhat and k h_j that times xhat_j, of order 1
+// whatever the size of h; with rstd^3 in one factor dx would be lost for rows of
+// a root mean square above 1e12 or below 1e-13.
+template <class HT, bool BOTH, int ITEMS, int R, int W, int THREADS>
 __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs a) {
   constexpr int kGroups = THREADS / (32 * W), T = 32 * W;
   __shared__ float red[2][32][R];
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
     }
     row_sums<W, R>(dot, red[odd]);
 #pragma unroll
-    for (int r = 0; r < R; ++r) dot[r] = dot[r] * rstd[r] * -inv_h;
+    for (int r = 0; r < R; ++r) dot[r] = dot[r] * rstd[r] * -inv_h * rstd[r];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * T;
@@ -351,9 +355,9 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
             unpack(h[r][i], x);
             unpack(dh[r][i], d);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = fmaf(fmaf(x[j] * rstd[r], dot[r], y[j] * w[j]), rstd[r], d[j]);
+            for (int j = 0; j < 8; ++j) d[j] = fmaf(fmaf(x[j], dot[r], y[j] * w[j]), rstd[r], d[j]);
             store_vals<8>(static_cast<HT*>(a.dx) + at, d);
-            if (a.dx_other) store_vals<8>(static_cast<Other<HT>*>(a.dx_other) + at, d);
+            if (BOTH && a.dx_other) store_vals<8>(static_cast<Other<HT>*>(a.dx_other) + at, d);
           }
         }
       }
@@ -385,12 +389,16 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
 }
 
 // The same with a block to a row, the next row's values in registers: for middle
-// lengths, whose rows one block's threads hold in 8 elements each, and for
-// lengths that are not a multiple of 8 or above 16384.  Bound by memory, between
-// 5.4 TB/s (512 columns) and 6.2 (8192): a row's sum is a barrier, with one row
-// more in flight behind it.  Rings of asynchronous copies and several rows a
-// block were slower.
-template <class HT, int V, int ITEMS, int MAXT>
+// lengths, whose rows one block's threads hold in 8 elements each, bound by
+// memory, between 5.4 TB/s (512 columns) and 6.2 (8192): a row's sum is a barrier,
+// with one row more in flight behind it.  Rings of asynchronous copies and
+// several rows a block were slower.  And for the lengths that nothing was made
+// for.  Not a multiple of 8: an element a load, bound by instructions, 67041 x
+// 1001 152 us (3.5 TB/s), 16388 x 4095 171; above 4096 besides by the 1.3 to 3 KB
+// that a thread of 1024 spills, 16380 x 4097 1.78 ms (0.3 TB/s), 8193 x 8191 1.51,
+// 2048 x 32767 1.37; above 16384 likewise, 2048 x 32768 373 us in bf16 and 880 in
+// fp32 (1.4 and 1.1 TB/s).
+template <class HT, bool BOTH, int V, int ITEMS, int MAXT>
 __global__ void __launch_bounds__(MAXT) rms_norm_bwd_block_kernel(const NormBwdArgs a) {
   __shared__ float red[2][32];
   griddep_wait();
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_bwd_block_kernel(const NormBwdA
         }
       }
     }
-    const float k = row_sum<false>(dot, red[odd]) * rstd * -inv_h;
+    const float k = row_sum<false>(dot, red[odd]) * rstd * -inv_h * rstd;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * T;
@@ -460,9 +468,9 @@ __global__ void __launch_bounds__(MAXT) rms_norm_bwd_block_kernel(const NormBwdA
         unpack(rh[i], h);
         if (a.dh) unpack(rdh[i], d);
 #pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = fmaf(fmaf(h[j] * rstd, k, dy[j] * w[i][j]), rstd, d[j]);
+        for (int j = 0; j < V; ++j) d[j] = fmaf(fmaf(h[j], k, dy[j] * w[i][j]), rstd, d[j]);
         store_vals<V>(static_cast<HT*>(a.dx) + base + c * V, d);
-        if (a.dx_other) store_vals<V>(static_cast<Other<HT>*>(a.dx_other) + base + c * V, d);
+        if (BOTH && a.dx_other) store_vals<V>(static_cast<Other<HT>*>(a.dx_other) + base + c * V, d);
       }
     }
   }
@@ -565,24 +573,28 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t st) {
 // and 173, in fp32 305 and 265, 1000 x 16384 bf16 40 and 108.
 bool bwd_groups(int H, bool f32) { return H % 8 == 0 && H <= 16384 && (H <= 512 || H > (f32 ? 8192 : 4096)); }
 
-template <class HT>
+// BOTH: dx in the other type too, where the pointer says so.  For an fp32 h always
+// built in; a bf16 one has a form without: there the test alone takes the odd
+// lengths up to 4096 from 152 to 172 us (67041 x 1001) and those above 16384 from
+// 329 to 560 (4094 x 16392, whose registers spill).
+template <class HT, bool BOTH>
 cudaError_t norm_bwd_launch(const NormBwdArgs& a, int blocks, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(blocks));
   const int H = a.H, nv = H / 8;
   if (bwd_groups(H, sizeof(HT) == 4)) {
-    if (H <= 256) return launch_dependent(rms_norm_bwd_kernel<HT, 1, 4, 1, 128>, grid, dim3(128), 0, st, a);
-    if (H <= 512) return launch_dependent(rms_norm_bwd_kernel<HT, 2, 2, 1, 128>, grid, dim3(128), 0, st, a);
+    if (H <= 256) return launch_dependent(rms_norm_bwd_kernel<HT, BOTH, 1, 4, 1, 128>, grid, dim3(128), 0, st, a);
+    if (H <= 512) return launch_dependent(rms_norm_bwd_kernel<HT, BOTH, 2, 2, 1, 128>, grid, dim3(128), 0, st, a);
     if constexpr (sizeof(HT) == 2)
-      if (H <= 8192) return launch_dependent(rms_norm_bwd_kernel<HT, 4, 1, 8, 256>, grid, dim3(256), 0, st, a);
-    return launch_dependent(rms_norm_bwd_kernel<HT, 4, 1, 16, 512>, grid, dim3(512), 0, st, a);
+      if (H <= 8192) return launch_dependent(rms_norm_bwd_kernel<HT, BOTH, 4, 1, 8, 256>, grid, dim3(256), 0, st, a);
+    return launch_dependent(rms_norm_bwd_kernel<HT, BOTH, 4, 1, 16, 512>, grid, dim3(512), 0, st, a);
   }
   if (H % 8) {
-    if (H <= 4096) return launch_dependent(rms_norm_bwd_block_kernel<HT, 1, 4, 1024>, grid, dim3(ceil32((H + 3) / 4)), 0, st, a);
-    return launch_dependent(rms_norm_bwd_block_kernel<HT, 1, 32, 1024>, grid, dim3(ceil32((H + 31) / 32)), 0, st, a);
+    if (H <= 4096) return launch_dependent(rms_norm_bwd_block_kernel<HT, BOTH, 1, 4, 1024>, grid, dim3(ceil32((H + 3) / 4)), 0, st, a);
+    return launch_dependent(rms_norm_bwd_block_kernel<HT, BOTH, 1, 32, 1024>, grid, dim3(ceil32((H + 31) / 32)), 0, st, a);
   }
-  if (H <= 4096) return launch_dependent(rms_norm_bwd_block_kernel<HT, 8, 1, 512>, grid, dim3(ceil32(nv)), 0, st, a);
-  if (H <= 8192) return launch_dependent(rms_norm_bwd_block_kernel<HT, 8, 2, 512>, grid, dim3(ceil32((nv + 1) / 2)), 0, st, a);
-  return launch_dependent(rms_norm_bwd_block_kernel<HT, 8, 4, 1024>, grid, dim3(ceil32((nv + 3) / 4)), 0, st, a);
+  if (H <= 4096) return launch_dependent(rms_norm_bwd_block_kernel<HT, BOTH, 8, 1, 512>, grid, dim3(ceil32(nv)), 0, st, a);
+  if (H <= 8192) return launch_dependent(rms_norm_bwd_block_kernel<HT, BOTH, 8, 2, 512>, grid, dim3(ceil32((nv + 1) / 2)), 0, st, a);
+  return launch_dependent(rms_norm_bwd_block_kernel<HT, BOTH, 8, 4, 1024>, grid, dim3(ceil32((nv + 3) / 4)), 0, st, a);
 }
 
 }  // namespace
@@ -617,7 +629,9 @@ cudaError_t launch_column_sum(const float* part, int n, int H, float* out, bool 
 cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int h_f32, float* d_weight, cudaStream_t st) {
   const int walkers = norm_bwd_walkers(a.rows, a.H, h_f32 != 0);
   if (walkers > 0) {
-    const cudaError_t err = h_f32 ? norm_bwd_launch<float>(a, walkers, st) : norm_bwd_launch<uint16_t>(a, walkers, st);
+    const cudaError_t err = h_f32        ? norm_bwd_launch<float, true>(a, walkers, st)
+                            : a.dx_other ? norm_bwd_launch<uint16_t, true>(a, walkers, st)
+                                         : norm_bwd_launch<uint16_t, false>(a, walkers, st);
     if (err != cudaSuccess) return err;
   }
   return launch_column_sum(a.part, walkers, a.H, d_weight, false, st);
