@@ -220,47 +220,48 @@ class AdamW:
             if grad_scale.numel() != 1:
                 raise ValueError("grad_scale: expected one element")
             scale = grad_scale.data_ptr()
-        runs = []
+        # the launches: (parameter type, gradient type, list, its fields, addresses, lengths)
+        launches, changed = [], []
         for dtype, idx, params, shapes, arr, fields, at, lengths in self._groups:
-            runs.append((dtype, arr, fields, lengths, *self._gradients(grads, idx, params, shapes, at)))
+            found, kinds, ptrs = self._gradients(grads, idx, params, shapes, at)
+            if len(found) == 1 and None not in found:
+                launches.append((dtype, kinds[0], arr, fields, ptrs, lengths))
+            else:   # a length of 0 leaves a tensor out: no gradient, or one of another type
+                launches += [(dtype, kind, arr, fields, ptrs, [n if t is kind else 0 for n, t in zip(lengths, kinds)])
+                             for kind in found - {None}]
+                params = [p for p, kind in zip(params, kinds) if kind is not None]
+            changed += params
         lib = _lib.load()
-        if not self._captured and runs and _capturing():
+        if not self._captured and self.params and _capturing():
             self._captured = True   # for good: only the device knows how often the graph runs
         counted = self._captured
         cfg = _lib.MokAdamwConfig(state=_STATE[self.state], lr=self._base_lr if lr is None else lr, beta1=self.betas[0],
                                   beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
                                   step=self._base_step + (not counted), seed=self._base_seed & (2 ** 64 - 1))
         handle = _raw_stream(self._dev) if self.params else None
-        launches = [(run, kind) for run in runs for kind in run[4] - {None}]
-
-        def each(fn, where, *args):
-            for (dtype, arr, fields, lengths, found, kinds, ptrs), kind in launches:
-                cfg.param_dtype, cfg.grad_dtype = _DTYPE[dtype], _DTYPE[kind]
-                fields["g"] = ptrs
-                # a length of 0 leaves a tensor out: no gradient, or one of another type
-                fields["n"] = lengths if len(found) == 1 else [n if t is kind else 0 for n, t in zip(lengths, kinds)]
-                st = fn(C.byref(cfg), arr, len(arr), *args)
-                if st:
-                    _fail(st, where)
-
         # several calls make one step: what any of them would refuse is refused
         # before the first one moves anything
         if counted or len(launches) > 1:
-            each(lib.mok_adamw_check, "mok_adamw_check")
+            self._call(lib.mok_adamw_check, cfg, launches)
         if counted:
             counter = self._counter.data_ptr()
             st = lib.mok_adamw_advance(C.byref(cfg), lr is not None, counter, handle)
             if st:
                 _fail(st, "mok_adamw_advance")
-            each(lib.mok_adamw_step_counted, "mok_adamw_step_counted", scale, counter, handle)
+            self._call(lib.mok_adamw_step_counted, cfg, launches, scale, counter, handle)
         else:
-            each(lib.mok_adamw_step, "mok_adamw_step", scale, handle)
+            self._call(lib.mok_adamw_step, cfg, launches, scale, handle)
+            self._base_step += 1
         # the parameters changed under autograd's eyes: a backward that saved
         # them before this step has to notice (and only those: a parameter
         # without a gradient is what it was)
-        for (_, _, params, *_), (_, _, _, _, found, kinds, _) in zip(self._groups, runs):
-            if None in found:
-                params = [p for p, kind in zip(params, kinds) if kind is not None]
-            torch.autograd.graph.increment_version(params)
-        if not counted:
-            self._base_step += 1
+        torch.autograd.graph.increment_version(changed)
+
+    @staticmethod
+    def _call(fn, cfg, launches, *args):
+        for dtype, kind, arr, fields, ptrs, lengths in launches:
+            cfg.param_dtype, cfg.grad_dtype = _DTYPE[dtype], _DTYPE[kind]
+            fields["g"], fields["n"] = ptrs, lengths
+            st = fn(C.byref(cfg), arr, len(arr), *args)
+            if st:
+                _fail(st, fn.__name__)
