@@ -338,7 +338,7 @@ def forward(x, router_w, sched: Schedule, weights: Weights, mode: str = "bf16", 
     many rows, with the same result bits (reads the expert counts back once).
     ``x_mx``: (codes, scales) of x, as ``rms_norm(mxfp8=True)`` or
     ``mxfp8_quantize`` return them: the MXFP8 modes then use these instead of
-    quantising x.
+    quantising x (which saves a rounding, not time).
     ``events``: optional list of 2 * MOK_NUM_STAGES torch.cuda.Event (timing); a
     None entry records nothing (each record costs a few microseconds on the
     device, so a timing run can watch one stage alone)."""

@@ -215,8 +215,8 @@ struct AdamwIn {
 // thread, each chunk within one tensor; a block's next chunk is in flight
 // while it works on this one.  32-bit states: a chunk to a block, bound by
 // memory; bf16 parameters with master copies, 402.7M elements, 1604 us (7.0
-// TB/s).  MXFP8 states: 95 instructions an element keep the issue slots busy
-// 84% of the time beside 64 to 70% of the memory's peak; the same tensors 1187
+// TB/s).  MXFP8 states: 98 instructions an element keep the issue slots busy
+// 84% of the time beside 62 to 69% of the memory's peak; the same tensors 1187
 // us (5.5 TB/s).  16 elements a thread took fewer instructions but left fewer
 // warps, and were slower.
 // COUNTED: what depends on the step count comes from device memory.

@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(THREADS) rms_norm_bwd_kernel(const NormBwdArgs
 // with one row more in flight behind it.  Rings of asynchronous copies and
 // several rows a block were slower.  And for the lengths that nothing was made
 // for.  Not a multiple of 8: an element a load, bound by instructions, 67041 x
-// 1001 152 us (3.5 TB/s), 16388 x 4095 171; above 4096 besides by the 1.3 to 3 KB
+// 1001 152 us (3.5 TB/s), 16388 x 4095 171; above 4096 besides by the 1.3 to 2.5 KB
 // that a thread of 1024 spills, 16380 x 4097 1.78 ms (0.3 TB/s), 8193 x 8191 1.51,
 // 2048 x 32767 1.37; above 16384 likewise, 2048 x 32768 373 us in bf16 and 880 in
 // fp32 (1.4 and 1.1 TB/s).

@@ -30,7 +30,8 @@ class AdamW:
     ``state``: "fp32" keeps m and v in 32 bits; "mxfp8" keeps m and
     r = sqrt(v) as E4M3 codes with one E8M0 scale per 32 elements, rounded
     stochastically with bits that ``seed``, the step, the tensor's place in
-    ``params`` and the element's index determine.  ``master``: bf16 parameters
+    ``params`` and the element's index determine (give two
+    optimisers over one model two seeds).  ``master``: bf16 parameters
     also get an fp32 copy that takes the update; the parameter is its rounding.
 
     ``buffers`` hands in state tensors instead of fresh zeros: a dict of lists
