@@ -548,9 +548,96 @@ mok_status_t mok_linear_bwd(const void* dy, int dy_dtype, const uint16_t* x, con
                             int activation, int64_t M, int N, int K, uint16_t* dx, uint16_t* d_weight, float* d_bias,
                             void* ws, size_t ws_bytes, void* stream);
 /* Synchronises the current device and reads (and clears) the status word of
- * its projections: MOK_OK, or MOK_ERR_TIMEOUT once a bounded device-side wait
- * gave up since the last read (that call's outputs are then undefined). */
+ * its projections, the grouped and 4-bit ones below among them: MOK_OK, or the
+ * first error since the last read.  MOK_ERR_TIMEOUT: a bounded device-side wait
+ * gave up (that call's outputs are then undefined).  MOK_ERR_INDEX: rows
+ * counted beyond M or below 0 (mok_grouped_linear), or an expert id out of
+ * range (mok_int4_linear). */
 mok_status_t mok_linear_status(int* status);
+
+/* ---- router: logits -> experts and their weights --------------------------
+ * logits [T][E], bf16 or fp32.  s = softmax(logits) or sigmoid(logits), in fp32.
+ * The k experts of the largest s + bias (bias fp32 [E] or NULL; -inf logits
+ * last whatever the bias; ties to the lowest index, NaN above all), in that
+ * order, and for each the weight
+ *   normalize:  scale s_j / sum of the k chosen s      else:  scale s_j
+ * (0 where that sum is 0).  The bias decides the choice alone.
+ * experts int64 [T][k], weights fp32 [T][k]; lse fp32 [T] = log sum exp(logits),
+ * for a z loss (-inf for a row of -inf, whose softmax counts as zeros).  counts
+ * int32 [E], how often each expert was chosen, and mean_score fp32 [E], the mean
+ * of s over the tokens (0 for T = 0), for a balance loss: both or neither (then
+ * ws may be NULL).  No result depends on the order in which blocks run. */
+#define MOK_ROUTE_MAX_E 1024
+#define MOK_ROUTE_MAX_K 64
+#define MOK_SCORE_SOFTMAX 0
+#define MOK_SCORE_SIGMOID 1
+size_t mok_route_workspace_bytes(int64_t T, int E);
+mok_status_t mok_route(const void* logits, int logits_dtype, const float* bias, int64_t T, int E, int k, int score, int normalize,
+                       float scale, int64_t* experts, float* weights, float* lse, int32_t* counts, float* mean_score, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* The gradient of the logits (in their type) from those of weights, lse (may be
+ * NULL) and mean_score (may be NULL), for the experts that the forward chose;
+ * the choice itself has none.  An id outside [0, E) counts as no choice. */
+mok_status_t mok_route_bwd(const float* d_weights, const void* logits, int logits_dtype, const int64_t* experts, const float* d_lse,
+                           const float* d_mean_score, int64_t T, int E, int k, int score, int normalize, float scale, void* d_logits,
+                           void* stream);
+
+/* ---- projections grouped by expert -----------------------------------------
+ * E matrices, one for each group of rows: the rows of group e lie one after the
+ * other behind those of group e - 1, without padding, and counts (int32 [E], on
+ * the device) says how many there are; any may be 0.
+ *   z[r] = x[r] W_e^T + bias_e,   y = act(z)       for the rows r of group e
+ * x bf16 [M][K], w bf16 [E][N][K], bias [E][N] bf16 or fp32 or NULL, y [M][N]
+ * bf16 or fp32, z bf16 [M][N] or NULL, as for mok_linear.  Rows behind the last
+ * group get zeros in y and z.  N and K are multiples of 8.  A count below 0 is
+ * taken for 0 and rows counted beyond M for none; mok_linear_status then says
+ * MOK_ERR_INDEX. */
+#define MOK_GROUPED_MAX_E 1024
+mok_status_t mok_grouped_linear(const uint16_t* x, const uint16_t* w, const int32_t* counts, const void* bias, int bias_dtype,
+                                int activation, int64_t M, int E, int N, int K, void* y, int y_dtype, uint16_t* z, void* stream);
+
+/* Its backward, as mok_linear_bwd for each group: dx bf16 [M][K] (zeros behind
+ * the last group), d_weight bf16 [E][N][K] and d_bias fp32 [E][N] (zeros for a
+ * group without rows); a NULL one is not computed.  dy and z behind the last
+ * group are not read. */
+size_t mok_grouped_linear_bwd_workspace_bytes(int64_t M, int E, int N, int activation, int dy_dtype, int with_bias);
+mok_status_t mok_grouped_linear_bwd(const void* dy, int dy_dtype, const uint16_t* x, const uint16_t* w, const int32_t* counts,
+                                    const uint16_t* z, int activation, int64_t M, int E, int N, int K, uint16_t* dx,
+                                    uint16_t* d_weight, float* d_bias, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- 4-bit weights with group scales ----------------------------------------
+ * value[n][k] = (q[n][k] - zero[n][k / group]) scale[n][k / group], q in 0..15,
+ * scales bf16, zeros 0..15 or none (8); group 32, 64 or 128, K a multiple of it.
+ * The library keeps a weight (of one or several matrices) in its own layout,
+ * of the sizes that mok_int4_bytes gives (host pointers, each may be NULL).
+ * mok_int4_quantize rounds bf16 or fp32 values [matrices][N][K] to the nearest:
+ *   zeros NULL:  scale = bf16(max |w| / 7), q = clamp(round(w / scale) + 8)
+ *   else, over lo = min(w, 0) and hi = max(w, 0):  scale = bf16((hi - lo) / 15),
+ *     zero = clamp(round(-lo / scale)), q = clamp(round(w / scale) + zero)
+ * (clamped to 0..15; scale 0 where all of a group is 0).
+ * mok_int4_pack takes codes [matrices][N][K / 2], two to a byte, the even
+ * column's in the low half, scales [matrices][N][K / group] and zeros, a byte
+ * each (the low four bits).  mok_int4_dequantize gives the values in bf16. */
+mok_status_t mok_int4_bytes(int64_t matrices, int N, int K, int group, size_t* codes, size_t* scales, size_t* zeros);
+mok_status_t mok_int4_quantize(const void* w, int w_dtype, int64_t matrices, int N, int K, int group, uint8_t* codes, uint16_t* scales,
+                               uint8_t* zeros, void* stream);
+mok_status_t mok_int4_pack(const uint8_t* q, const uint16_t* q_scales, const uint8_t* q_zeros, int64_t matrices, int N, int K, int group,
+                           uint8_t* codes, uint16_t* scales, uint8_t* zeros, void* stream);
+mok_status_t mok_int4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t matrices, int N, int K,
+                                 int group, uint16_t* out, void* stream);
+
+/* y = act(x W^T + bias) for few rows: x bf16, y [rows][N] bf16 or fp32, bias
+ * [matrices][N] bf16 or fp32 or NULL.  The weights' values are not rounded: sums of
+ * a group are taken in fp32 and then scaled.
+ * experts NULL: one matrix, x [rows][K], rows_per_x 1.  Else int64 [rows]: row r
+ * of y is row r / rows_per_x of x times the matrix experts[r]; -1 stands for no
+ * expert and gives zeros, as does any other id outside, for which
+ * mok_linear_status says MOK_ERR_INDEX besides. */
+#define MOK_INT4_MAX_ROWS 65535
+mok_status_t mok_int4_linear(const uint16_t* x, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t matrices,
+                             int N, int K, int group, const int64_t* experts, int64_t rows, int rows_per_x, const void* bias,
+                             int bias_dtype, int activation, void* y, int y_dtype, void* stream);
 
 /* ---- AdamW over many tensors --------------------------------------------
  * For every element, t = cfg->step (from 1), g' = *grad_scale * g:

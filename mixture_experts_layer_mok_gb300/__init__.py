@@ -20,7 +20,8 @@ from ._lib import MokError  # noqa: F401
 __all__ = ["schedule", "schedule_noalloc", "mxfp8_quantize", "mxfp8_quantize_t", "mxfp8_quantize_dual", "forward",
            "backward", "Schedule", "Weights", "Context", "MokError", "quantize_weights", "macrobatch_plan", "MODES",
            "mxfp8_dequantize", "rms_norm", "rms_norm_backward", "NormOutput", "linear", "linear_backward",
-           "linear_status", "AdamW"]
+           "linear_status", "AdamW", "route", "route_backward", "Routing", "grouped_linear", "grouped_linear_backward",
+           "Int4Weight", "int4_quantize", "int4_pack", "int4_dequantize", "int4_linear"]
 
 # forward/backward precision: "bf16"; "mxfp8" (MXFP8 forward GEMMs, bf16
 # backward); "mxfp8_full" (MXFP8 forward and backward GEMMs)
@@ -409,4 +410,6 @@ def backward(dy, x, router_w, sched: Schedule, ctx: Context, weights: Weights, m
 # the operators around the layer
 from .ops import (NormOutput, linear, linear_backward, linear_status, mxfp8_dequantize, rms_norm,  # noqa: E402,F401
                   rms_norm_backward)
+from .experts import (Int4Weight, Routing, grouped_linear, grouped_linear_backward, int4_dequantize,  # noqa: E402,F401
+                      int4_linear, int4_pack, int4_quantize, route, route_backward)
 from .optim import AdamW  # noqa: E402,F401

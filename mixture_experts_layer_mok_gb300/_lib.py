@@ -82,6 +82,11 @@ class MokWeightGrads(C.Structure):
 MOK_DTYPE_BF16 = 0
 MOK_DTYPE_F32 = 1
 MOK_NORM_MAX_H = 32768
+SCORES = {"softmax": 0, "sigmoid": 1}
+MOK_ROUTE_MAX_E = 1024
+MOK_ROUTE_MAX_K = 64
+MOK_GROUPED_MAX_E = 1024
+MOK_INT4_MAX_ROWS = 65535
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 MOK_ADAMW_STATE_F32 = 0
 MOK_ADAMW_STATE_MXFP8 = 1
@@ -132,6 +137,20 @@ SIGNATURES = {
     "mok_linear_bwd": (C.c_int, [P, C.c_int, P, P, P, C.c_int, C.c_int64, C.c_int, C.c_int, P, P, P, P, C.c_size_t,
                                  P]),
     "mok_linear_status": (C.c_int, [I32P]),
+    "mok_route_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int]),
+    "mok_route": (C.c_int, [P, C.c_int, P, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_float, P, P, P, P, P, P, C.c_size_t,
+                            P]),
+    "mok_route_bwd": (C.c_int, [P, P, C.c_int, P, P, P, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_float, P, P]),
+    "mok_grouped_linear": (C.c_int, [P, P, P, P, C.c_int, C.c_int, C.c_int64, C.c_int, C.c_int, C.c_int, P, C.c_int, P, P]),
+    "mok_grouped_linear_bwd_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]),
+    "mok_grouped_linear_bwd": (C.c_int, [P, C.c_int, P, P, P, P, C.c_int, C.c_int64, C.c_int, C.c_int, C.c_int, P, P, P, P,
+                                         C.c_size_t, P]),
+    "mok_int4_bytes": (C.c_int, [C.c_int64, C.c_int, C.c_int, C.c_int] + [C.POINTER(C.c_size_t)] * 3),
+    "mok_int4_quantize": (C.c_int, [P, C.c_int, C.c_int64, C.c_int, C.c_int, C.c_int, P, P, P, P]),
+    "mok_int4_pack": (C.c_int, [P, P, P, C.c_int64, C.c_int, C.c_int, C.c_int, P, P, P, P]),
+    "mok_int4_dequantize": (C.c_int, [P, P, P, C.c_int64, C.c_int, C.c_int, C.c_int, P, P]),
+    "mok_int4_linear": (C.c_int, [P, P, P, P, C.c_int64, C.c_int, C.c_int, C.c_int, P, C.c_int64, C.c_int, P, C.c_int, C.c_int, P,
+                                  C.c_int, P]),
     "mok_adamw_step": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int, P, P]),
     "mok_adamw_check": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int]),
     "mok_adamw_step_counted": (C.c_int, [C.POINTER(MokAdamwConfig), C.POINTER(MokAdamwTensor), C.c_int, P, P, P]),

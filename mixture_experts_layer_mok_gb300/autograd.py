@@ -1,5 +1,6 @@
 """torch.autograd face of the layer (``MoKFunction``, ``MoKLayer``) and of the
-operators around it (``rms_norm``, ``MoKRMSNorm``; ``linear``, ``MoKLinear``).
+operators around it (``rms_norm``, ``MoKRMSNorm``; ``linear``, ``MoKLinear``;
+``route``, ``MoKRouter``; ``grouped_linear``, ``MoKGroupedLinear``).
 
 The pages' PyTorch-facing pieces are a runtime whose forward returns the
 output plus an opaque context and whose backward consumes it, returning
@@ -16,7 +17,7 @@ import functools
 
 import torch
 
-from . import Context, Schedule, Weights, backward, forward, ops, quantize_weights, schedule
+from . import Context, Schedule, Weights, backward, experts, forward, ops, quantize_weights, schedule
 
 
 class _NoSecondDerivative(torch.autograd.Function):
@@ -244,3 +245,93 @@ class MoKLinear(torch.nn.Module):
 
     def forward(self, x, residual=None):
         return linear(x, self.weight, self.bias, self.activation, residual, self.out_dtype)
+
+
+class RouteFunction(torch.autograd.Function):
+    """(experts, weights, lse, counts, mean_score) of router logits; the choice
+    and the counts are integers and get no gradient, nor does the bias, which
+    decides the choice alone."""
+
+    @staticmethod
+    def forward(ctx, logits, bias, k, score, normalize, scale, balance):
+        r = experts.route(logits, k, score, normalize, scale, bias, balance)
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(r.experts, *([r.counts] if balance else []))
+        ctx.save_for_backward(logits, r.experts)
+        ctx.route = (score, normalize, scale)
+        return r.experts, r.weights, r.lse, r.counts, r.mean_score
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, _experts, d_weights, d_lse, _counts, d_mean_score):
+        logits, chosen = ctx.saved_tensors
+        if d_weights is None and d_lse is None and d_mean_score is None:
+            return (None,) * 7
+        d_weights = torch.zeros(chosen.shape, device=chosen.device) if d_weights is None else _incoming(d_weights)
+        d = experts.route_backward(d_weights, logits, chosen, *ctx.route, None if d_lse is None else _incoming(d_lse),
+                                   None if d_mean_score is None else _incoming(d_mean_score))
+        return d, None, None, None, None, None, None
+
+
+def route(logits, k: int, score: str = "softmax", normalize: bool = True, scale: float = 1.0, bias=None, balance: bool = False):
+    """``experts.route`` under autograd: a ``Routing`` whose weights, lse and
+    mean_score are differentiable in the logits."""
+    return experts.Routing(*RouteFunction.apply(logits, bias, k, score, normalize, scale, balance))
+
+
+class MoKRouter(torch.nn.Module):
+    """The router: logits in 32 bits by the projection operator, and the choice.
+    Its ``Routing`` feeds ``MoKLayer``, or ``grouped_linear`` by its counts."""
+
+    def __init__(self, H: int, E: int, k: int, score: str = "softmax", normalize: bool = True, scale: float = 1.0,
+                 balance: bool = False, device=None, init_std: float = 0.02, generator=None):
+        super().__init__()
+        self.proj = MoKLinear(H, E, bias=False, out_dtype=torch.float32, device=device, init_std=init_std, generator=generator)
+        self.k, self.score, self.normalize, self.scale, self.balance = k, score, normalize, scale, balance
+
+    def forward(self, x, bias=None):
+        return route(self.proj(x), self.k, self.score, self.normalize, self.scale, bias, self.balance)
+
+
+class GroupedLinearFunction(torch.autograd.Function):
+    """y = act(x W_e^T + bias_e) for rows sorted by expert, the pre-activations
+    kept for the backward where an activation needs them."""
+
+    @staticmethod
+    def forward(ctx, x, weight, counts, bias, activation, out_dtype):
+        keep = activation != "none" and any(ctx.needs_input_grad)
+        y, z = experts.grouped_linear(x, weight, counts, bias, activation, out_dtype, save_z=keep)
+        ctx.save_for_backward(x, weight, counts, z)
+        ctx.linear = (activation, None if bias is None else bias.dtype)
+        return y
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dy):
+        x, weight, counts, z = ctx.saved_tensors
+        activation, bias_type = ctx.linear
+        need_x, need_w, _, need_b = ctx.needs_input_grad[:4]
+        need = [n for n, on in (("dx", need_x), ("d_weight", need_w)) if on]
+        g = experts.grouped_linear_backward(_incoming(dy), x, weight, counts, z, activation, bias=bool(need_b), need=need)
+        return g.get("dx"), g.get("d_weight"), None, g["d_bias"].to(bias_type) if need_b else None, None, None
+
+
+def grouped_linear(x, weight, counts, bias=None, activation: str = "none", out_dtype=torch.bfloat16):
+    """``experts.grouped_linear`` under autograd; returns y."""
+    return GroupedLinearFunction.apply(x, weight, counts, bias, activation, out_dtype)
+
+
+class MoKGroupedLinear(torch.nn.Module):
+    """E projections K -> N, one for each expert's rows."""
+
+    def __init__(self, E: int, K: int, N: int, bias: bool = True, activation: str = "none", out_dtype=torch.bfloat16, device=None,
+                 init_std: float = 0.02, generator=None):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.empty(E, N, K, dtype=torch.bfloat16, device=device))
+        with torch.no_grad():
+            self.weight.normal_(0.0, init_std, generator=generator)
+        self.bias = torch.nn.Parameter(torch.zeros(E, N, dtype=torch.float32, device=device)) if bias else None
+        self.activation, self.out_dtype = activation, out_dtype
+
+    def forward(self, x, counts):
+        return grouped_linear(x, self.weight, counts, self.bias, self.activation, self.out_dtype)

@@ -1616,7 +1616,7 @@ mok_status_t backward_bf16(const mok_config_t* cfg, const uint16_t* dy, const ui
 // ===========================================================================
 extern "C" {
 
-int mok_version(void) { return 3; }
+int mok_version(void) { return 4; }
 
 const char* mok_last_error(void) { return g_err; }
 

@@ -1,0 +1,130 @@
+// Internal launch interface of routed experts as operators of their own: the
+// router, the products grouped by expert, and the products with 4-bit weights.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mok.h"
+
+namespace mok {
+
+// ---------------------------------------------------------------- router
+struct RouteArgs {
+  const void* logits;    // [T][E]
+  const float* bias;     // [E] or NULL: added to the scores for the choice alone
+  long long T;
+  int E, k;
+  int sigmoid, normalize;
+  float scale;
+  int64_t* experts;      // [T][k]
+  float* weights;        // [T][k]
+  float* lse;            // [T]
+  // with the loads and mean scores (both or neither)
+  int* counts;           // [E]
+  float* mean_score;     // [E]
+  float* part;           // [route_blocks][E] sums of scores, then [route_blocks][E] counts
+};
+struct RouteBwdArgs {
+  const float* d_weights;  // [T][k]
+  const void* logits;
+  const int64_t* experts;
+  const float* d_lse;         // [T] or NULL
+  const float* d_mean_score;  // [E] or NULL
+  void* d_logits;             // in the logits' type
+  long long T;
+  int E, k;
+  int sigmoid, normalize;
+  float scale;
+};
+int route_blocks(long long T);
+cudaError_t launch_route(const RouteArgs& a, int f32, cudaStream_t st);
+cudaError_t launch_route_bwd(const RouteBwdArgs& a, int f32, cudaStream_t st);
+
+// ---------------------------------------------------------------- 4-bit weights
+// The layout of a matrix [N][K] (int4.cu): N in tiles of 16 rows, K in blocks of
+// 128, both padded.
+constexpr int kInt4Rows = 16, kInt4Block = 128;
+constexpr int kInt4TileBytes = kInt4Rows * kInt4Block / 2;
+struct Int4Shape {
+  long long matrices;
+  int N, K, group;
+  __host__ __device__ long long row_tiles() const { return (static_cast<long long>(N) + kInt4Rows - 1) / kInt4Rows; }
+  __host__ __device__ int blocks() const { return (K + kInt4Block - 1) / kInt4Block; }
+  __host__ __device__ long long tiles() const { return matrices * row_tiles() * blocks(); }
+  // scales (and zeros) of a tile: [16 rows][groups of a block]
+  __host__ __device__ int tile_scales() const { return kInt4Rows * (kInt4Block / group); }
+};
+struct Int4LinearArgs {
+  Int4Shape w;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;      // or NULL: 8
+  const uint16_t* x;
+  const int64_t* experts;    // [rows] or NULL
+  const void* bias;          // [matrices][N] or NULL
+  void* y;                   // [rows][N]
+  int rows;                  // of y
+  int x_div;                 // row r of y reads row r / x_div of x
+  int act;
+  int out_f32, bias_f32;
+  int* status;
+};
+cudaError_t launch_int4_quantize(const void* w, int f32, const Int4Shape& s, uint8_t* codes, uint16_t* scales, uint8_t* zeros,
+                                 cudaStream_t st);
+cudaError_t launch_int4_pack(const uint8_t* q, const uint16_t* qs, const uint8_t* qz, const Int4Shape& s, uint8_t* codes,
+                             uint16_t* scales, uint8_t* zeros, cudaStream_t st);
+cudaError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const Int4Shape& s,
+                                   uint16_t* out, cudaStream_t st);
+cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- products grouped by expert
+constexpr int kMaxGroups = MOK_GROUPED_MAX_E;
+// The products of grouped.cuh's rows kernel: the forward, and dx.
+struct GroupedRowsParams {
+  const int* counts;     // [E]
+  int E;
+  int L;                 // the output's contiguous length
+  int M;                 // its rows
+  int nk;                // K-blocks of 64
+  int l_tiles;           // tiles of 256
+  int act;
+  const void* bias;      // [E][L] or NULL
+  int bias_f32;
+  void* out;             // [M][L]
+  uint16_t* z;           // [M][L] bf16 or NULL
+  int* status;
+};
+struct GroupedRowsCall {
+  const uint16_t* w;     // [E][L][K], or [E][K][L] with w_mn
+  const uint16_t* x;     // [M][K]
+  int K;
+  bool w_mn, out_f32;
+};
+mok_status_t run_grouped_rows(const GroupedRowsCall& c, const GroupedRowsParams& p, cudaStream_t st);
+
+// The weight gradients: [E][N][K] from dz [M][N] and x [M][K].
+struct GroupedWeightCall {
+  const uint16_t* dz;
+  const uint16_t* x;
+  const int* counts;
+  int E, M, N, K;
+  uint16_t* out;
+  int* status;
+};
+// Part of the backward's workspace: the groups' first rows ([E + 1], 16-byte
+// multiple) and two tensor maps for each.
+size_t grouped_plan_bytes(int E);
+mok_status_t launch_grouped_plan(const GroupedWeightCall& c, bool maps, void* plan, cudaStream_t st);
+mok_status_t run_grouped_weights(const GroupedWeightCall& c, const void* plan, cudaStream_t st);
+
+// dz = dy act'(z) in bf16 (dz may be NULL) for the groups' rows, and the sums
+// of its fp32 values over each chunk of rows inside each group; then the
+// groups' sums in order.
+int grouped_dz_chunk(int M, int N);   // rows of a chunk
+inline long long grouped_dz_parts(int M, int N, int E) { return (static_cast<long long>(M) + grouped_dz_chunk(M, N) - 1) / grouped_dz_chunk(M, N) + E; }
+cudaError_t launch_grouped_dz(const void* dy, int dy_f32, const uint16_t* z, int act, const int* starts, int E, int M, int N,
+                              uint16_t* dz, float* part, cudaStream_t st);
+cudaError_t launch_grouped_bias(const float* part, const int* starts, int E, int M, int N, float* d_bias, cudaStream_t st);
+
+}  // namespace mok

@@ -1,0 +1,703 @@
+// Matrix products grouped by expert on tcgen05 / TMEM / TMA: the rows of each
+// group lie one after the other, without padding, and their counts are on the
+// device.
+//
+//   rows kernel    D[l][c] = sum_k A[l][k] B[c][k], c the rows of one group:
+//     forward  l = n, k = k:  A = W_e [N][K],                B = x rows
+//     dx       l = k, k = n:  A = W_e^T (W_e is [k][l]),     B = dz rows
+//   weight kernel  D[c][l] = sum_m dz[m][c] x[m][l], m the rows of one group.
+//
+// Both are persistent CTA pairs with two accumulator buffers.  In the rows
+// kernel the weights run over the tensor core's M (256 over two SMs) and a
+// group's rows over its N, which is any multiple of 32 up to 256: a group of 300
+// rows costs 320, not 512, and a group of two costs 32; one kernel serves the
+// decoded token, bound by the weights' bytes, and the long batch, bound by the
+// tensor core.  A group's rows are cut evenly into tiles of at most 256.
+// Rows that a tile's loads bring in from the next group fill columns that are
+// not stored.  The weight kernel contracts over the rows, where a neighbour's
+// row must not come in: it reads through tensor maps that end with the group
+// (grouped_plan_kernel writes them), so that the hardware fills in zeros.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "experts.h"
+#include "gemm.cuh"
+#include "linear.cuh"
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace mok {
+
+constexpr int kGroupedStages = 6;
+constexpr int kGroupedStageBytes = 2 * kLinABytes;   // 128 x 64 of A, up to 128 x 64 of B
+constexpr int kGroupedEpiWarps = 8;
+constexpr int kGroupedThreads = 64 + 32 * kGroupedEpiWarps;
+
+// ---------------------------------------------------------------- the groups
+struct GroupTable {
+  int start[kMaxGroups + 1];   // first row of each group, and the end of the last
+  int tile[kMaxGroups + 1];    // row tiles before each group, and all of them
+};
+
+// By one warp: the table from the counts.  Counts below 0 count as 0 and rows
+// behind M as none; returns whether there were any.
+__device__ __forceinline__ bool scan_groups(const int* counts, int E, int M, int* start, int* tile, int lane) {
+  const int each = (E + 31) / 32, e0 = min(lane * each, E), e1 = min(e0 + each, E);
+  long long sum = 0;
+  bool bad = false;
+  for (int e = e0; e < e1; ++e) {
+    const int c = __ldg(counts + e);
+    bad |= c < 0;
+    sum += max(c, 0);
+  }
+  long long before = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  bad |= before > M;
+  before -= sum;
+  int tiles = 0;
+  long long at = before;
+  for (int e = e0; e < e1; ++e) {
+    const int s = static_cast<int>(min(at, static_cast<long long>(M)));
+    at += max(__ldg(counts + e), 0);
+    const int n = static_cast<int>(min(at, static_cast<long long>(M))) - s;
+    start[e] = s;
+    tiles += (n + 255) / 256;
+  }
+  if (e1 == E && e0 < e1) start[E] = static_cast<int>(min(at, static_cast<long long>(M)));
+  if (tile) {
+    int t = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += v;
+    }
+    t -= tiles;
+    __syncwarp();
+    for (int e = e0; e < e1; ++e) {
+      tile[e] = t;
+      t += ((e + 1 < e1 ? start[e + 1] : static_cast<int>(min(at, static_cast<long long>(M)))) - start[e] + 255) / 256;
+    }
+    if (e1 == E && e0 < e1) tile[E] = t;
+  }
+  __syncwarp();
+  return __any_sync(0xffffffffu, bad);
+}
+
+// The last e with tab[e] <= q, for tab ascending with tab[0] = 0, by a warp.
+__device__ __forceinline__ int find_group(const int* tab, int E, int q, int lane) {
+  const int far = lane * 32;
+  const int seg = __popc(__ballot_sync(0xffffffffu, far < E && tab[far] <= q)) - 1;
+  const int near = seg * 32 + lane;
+  return seg * 32 + __popc(__ballot_sync(0xffffffffu, near < E && tab[near] <= q)) - 1;
+}
+
+// ---------------------------------------------------------------- rows kernel
+struct GroupedRowsMaps {
+  CUtensorMap w;      // [E][L][K], boxes 64 x 128, or [E][K][L], boxes 64 x 64
+  CUtensorMap x[4];   // [M][K], boxes of 64 x 16, 32, 64 and 128
+};
+
+struct GroupedRowsCfg {
+  static constexpr int kStageOut = 2048;   // an epilogue warp's 32 rows x 32 columns in bf16
+  static constexpr int kSmemBytes =
+      1024 + kGroupedStages * kGroupedStageBytes + kGroupedEpiWarps * kStageOut + static_cast<int>(sizeof(GroupTable)) + 256;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+struct RowsItem {
+  int e, l0, m0, rows, n;   // group, first l, first row, rows, and the tensor core's N
+};
+// Item idx of tile[E] x l_tiles: a group's items are neighbours, and inside a
+// group of 4 of its row tiles l goes on outside the rows, so that the CTAs at
+// work at one time share few rows of both operands.
+__device__ __forceinline__ bool rows_item(const GroupedRowsParams& p, const GroupTable& g, int idx, int lane, RowsItem& it) {
+  const int q = idx / p.l_tiles;
+  if (q >= g.tile[p.E]) return false;
+  it.e = find_group(g.tile, p.E, q, lane);
+  const int t0 = g.tile[it.e], tiles = g.tile[it.e + 1] - t0, first = g.start[it.e], count = g.start[it.e + 1] - first;
+  int ct, lt;
+  unit_and_col(idx - t0 * p.l_tiles, tiles, p.l_tiles, 4, ct, lt);
+  const int each = ((count + tiles - 1) / tiles + 31) & ~31;
+  it.l0 = lt * 256;
+  it.m0 = first + ct * each;
+  it.rows = min(each, count - ct * each);
+  it.n = (it.rows + 31) & ~31;
+  return true;
+}
+
+__device__ __forceinline__ void tma_load_rows_pair(uint8_t* dst, const CUtensorMap* maps, uint32_t bar, int k0, int row, int rows) {
+#pragma unroll
+  for (int b = 3; b >= 0; --b) {   // 128, 64, 32, 16: the bits of rows
+    const int box = 16 << b;
+    if (rows & box) {
+      tma_load_2d_pair(dst, &maps[b], bar, k0, row);
+      dst += box * 128;
+      row += box;
+    }
+  }
+}
+
+// 16 TMEM lanes x 8 N columns in the fragment layout: register 4 i + {0, 1}:
+// lane g = thread / 4, columns 8 i + 2 (thread % 4) + {0, 1}; + {2, 3}: lane g + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Four 8 x 8 blocks of bf16 from the fragment layout, each transposed; lane 8 i +
+// j names the address of block i's row j.
+__device__ __forceinline__ void st_matrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ float bias_at(const GroupedRowsParams& p, int e, int l) {
+  if (!p.bias || l >= p.L) return 0.f;
+  const long long at = static_cast<long long>(e) * p.L + l;
+  return p.bias_f32 ? __ldg(static_cast<const float*>(p.bias) + at)
+                    : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.bias) + at)) << 16);
+}
+
+// A staged block (32 rows of 64 bytes, 16-byte pieces swizzled) to rows row ..
+// row + rows - 1 of out, columns l .. l + 31 as far as there are: 64 bytes of a
+// row by four lanes.
+__device__ __forceinline__ void store_block(const uint8_t* stage, uint16_t* out, int L, int l, long long row, int rows, int lane) {
+  const int piece = lane & 3;
+  if (l + piece * 8 >= L) return;   // L % 8 == 0
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint4 v = reinterpret_cast<const uint4*>(stage)[r * 4 + (piece ^ ((r >> 1) & 3))];
+    if (r < rows) *reinterpret_cast<uint4*>(out + (row + r) * L + l + piece * 8) = v;
+  }
+}
+
+// 32 rows x 32 l's in bf16 from TMEM at taddr (this warp's lanes, 32 columns):
+// the fragments take bias and activation, and are transposed into the stage.
+template <int ACT>
+__device__ __forceinline__ void rows_block(const GroupedRowsParams& p, uint32_t taddr, const float (&bias)[4], int l, long long row,
+                                           int rows, uint8_t* stage, int lane) {
+  uint32_t r[2][16];
+  tmem_ld_16x256b_x4(taddr, r[0]);
+  tmem_ld_16x256b_x4(taddr + (16u << 16), r[1]);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  float v[2][16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      asm volatile("" : "+r"(r[h][i]));   // no use before the wait
+      v[h][i] = __uint_as_float(r[h][i]) + bias[2 * h + ((i >> 1) & 1)];
+    }
+  // block (rows 8 i .., l's 16 h + 8 u ..) holds registers 4 i + 2 u, 4 i + 2 u + 1 of half h; this lane's
+  // address: row 8 i + lane % 8 of the piece 2 h + u = lane / 8
+  const uint32_t at = smem_u32(stage);
+  const auto put = [&](auto value) {
+    __syncwarp();   // the stage's last readers are done
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int h = b >> 1, u = b & 1;
+        w[b] = pack_bf16(value(v[h][4 * i + 2 * u]), value(v[h][4 * i + 2 * u + 1]));
+      }
+      const int rr = 8 * i + (lane & 7), piece = lane >> 3;
+      st_matrix_trans(at + rr * 64 + ((piece ^ ((rr >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+  };
+  if (p.z) {
+    put([](float x) { return x; });
+    store_block(stage, p.z, p.L, l, row, rows, lane);
+  }
+  put([](float x) { return act_value<ACT>(x); });
+  store_block(stage, static_cast<uint16_t*>(p.out), p.L, l, row, rows, lane);
+}
+
+// 32 columns of this lane's l, in fp32: a warp's 32 l's of a row are 128 bytes.
+template <int ACT>
+__device__ __forceinline__ void rows_block_f32(const GroupedRowsParams& p, const float* v, float bias, int l, long long row, int rows) {
+  if (l >= p.L) return;
+  float* out = static_cast<float*>(p.out);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (i >= rows) break;
+    const float z = v[i] + bias;
+    if (p.z) p.z[(row + i) * p.L + l] = static_cast<uint16_t>(pack_bf16(z, 0.f) & 0xffffu);
+    out[(row + i) * p.L + l] = act_value<ACT>(z);
+  }
+}
+
+// AMN: A is stored [k][l] (dx).  F32: fp32 outputs, whose sums over more than
+// kChunk K-blocks are added in registers (linear.cuh).
+template <bool AMN, bool F32>
+__global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const __grid_constant__ GroupedRowsMaps maps, const GroupedRowsParams p) {
+  using C = GroupedRowsCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* out_stage = smem + kGroupedStages * kGroupedStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + kGroupedEpiWarps * C::kStageOut);
+  uint64_t* empty = full + kGroupedStages;
+  uint64_t* tfull = empty + kGroupedStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  GroupTable& table = *reinterpret_cast<GroupTable*>(tmem_slot + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  int* const status = p.status;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGroupedStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kGroupedEpiWarps);   // the leader's counts both CTAs' warps
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&maps.w);
+    for (int b = 0; b < 4; ++b) tma_prefetch_desc(&maps.x[b]);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 2) {
+    const bool bad = scan_groups(p.counts, p.E, p.M, table.start, table.tile, lane);
+    if (bad && blockIdx.x == 0 && lane == 0) atomicCAS(status, 0, MOK_ERR_INDEX);
+  }
+  tc_fence_before();
+  cluster_sync();   // both CTAs' barriers and tables are there before any signal crosses
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  if (warp == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    long long fills = 0;
+    bool ok = true;
+    const uint32_t lead_full = cluster_addr(full, 0);   // both CTAs' loads count on the leader's barriers
+    RowsItem it;
+    for (int idx = pair; ok && rows_item(p, table, idx, lane, it); idx += pairs) {
+      const int l0 = it.l0 + rank * 128, half = it.n >> 1, m0 = it.m0 + rank * half;
+      const uint32_t bytes = 2 * kLinABytes + it.n * 128;
+      for (int kb = 0; kb < p.nk; ++kb) {
+        if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sA = smem + stage * kGroupedStageBytes;
+        const uint32_t bar = lead_full + stage * 8;
+        const int k0 = kb * kLinBK;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+          if (AMN) {
+            tma_load_3d_pair(sA, &maps.w, bar, l0, k0, it.e);
+            tma_load_3d_pair(sA + kLinChunk, &maps.w, bar, l0 + 64, k0, it.e);
+          } else {
+            tma_load_3d_pair(sA, &maps.w, bar, k0, l0, it.e);
+          }
+          tma_load_rows_pair(sA + kLinABytes, maps.x, bar, k0, m0, half);
+        }
+        __syncwarp();
+        ++fills;
+        if (++stage == kGroupedStages) stage = 0, phase ^= 1;
+      }
+    }
+    if (!ok && rank == 0 && lane == 0) {   // no load may be in flight when the CTA ends
+      const int n = fills < kGroupedStages ? static_cast<int>(fills) : kGroupedStages;
+      for (int i = 0; i < n; ++i) {
+        if (--stage < 0) stage = kGroupedStages - 1, phase ^= 1;
+        mbar_drain(&full[stage], phase);
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint64_t ad = linear_desc<AMN>(smem_u32(smem)), bd = linear_desc<false>(smem_u32(smem) + kLinABytes);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      RowsItem it;
+      for (int idx = pair; ok && rows_item(p, table, idx, lane, it); idx += pairs) {
+        const uint32_t idesc = idesc_bf16(256, it.n, AMN, false);
+        for (int first = 0; ok && first < p.nk; first += F32 ? kChunk : p.nk) {
+          if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int end = F32 ? min(first + kChunk, p.nk) : p.nk;
+          const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * 256);
+          for (int kb = first; kb < end; ++kb) {
+            if (!warp_wait(&full[stage], phase, abort_flag, status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t at = stage * kGroupedStageBytes;
+            if (elect_one()) {
+              umma_bf16_pair(acc, desc_at(ad, at), desc_at(bd, at), idesc, kb != first);
+#pragma unroll
+              for (int kk = 1; kk < kLinBK / 16; ++kk)
+                umma_bf16_pair(acc, desc_at(ad, at + kk * kStep<AMN>), desc_at(bd, at + kk * kStep<false>), idesc, 1u);
+              umma_commit_pair(&empty[stage], 0x3);
+              if (kb == end - 1) umma_commit_pair(&tfull[buf], 0x3);
+            }
+            __syncwarp();
+            if (++stage == kGroupedStages) stage = 0, phase ^= 1;
+          }
+          buf ^= 1;
+          if (buf == 0) bphase ^= 1;
+        }
+      }
+      if (elect_one()) {
+        umma_commit_pair(done, 0x1);
+        mbar_drain(done, 0);
+      }
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stage = out_stage + (warp - 2) * C::kStageOut;
+    int buf = 0;
+    uint32_t bphase = 0;
+    bool ok = true;
+    RowsItem it;
+    const auto wait_full = [&]() {
+      const int w = lane == 0 ? (mbar_wait(&tfull[buf], bphase, abort_flag, status) ? 1 : 0) : 0;
+      const bool got = __shfl_sync(0xffffffffu, w, 0) != 0;
+      tc_fence_after();
+      return got;
+    };
+    const auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank != 0)
+          mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
+        else
+          mbar_arrive(&tempty[buf]);
+      }
+      buf ^= 1;
+      if (buf == 0) bphase ^= 1;
+    };
+    for (int idx = pair; rows_item(p, table, idx, lane, it); idx += pairs) {
+      const int l = it.l0 + rank * 128 + q * 32;   // this warp's l's
+      const auto lanes = [&]() { return tmem_base + static_cast<uint32_t>(buf * 256) + (static_cast<uint32_t>(q * 32) << 16); };
+      if constexpr (F32) {
+        float sum[4][32] = {};
+        for (int first = 0; first < p.nk; first += kChunk) {
+          if (!(ok = wait_full())) break;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if ((2 * b + half) * 32 < it.n) add_columns<32>(lanes() + (2 * b + half) * 32, sum[b]);
+          release();
+        }
+        if (!ok) break;
+        const float bias = bias_at(p, it.e, l + lane);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int c = (2 * b + half) * 32, rows = it.rows - c;
+          if (rows <= 0) continue;
+          const long long row = it.m0 + c;
+          switch (p.act) {
+            case LIN_RELU: rows_block_f32<LIN_RELU>(p, sum[b], bias, l + lane, row, rows); break;
+            case LIN_SILU: rows_block_f32<LIN_SILU>(p, sum[b], bias, l + lane, row, rows); break;
+            case LIN_GELU: rows_block_f32<LIN_GELU>(p, sum[b], bias, l + lane, row, rows); break;
+            case LIN_GELU_TANH: rows_block_f32<LIN_GELU_TANH>(p, sum[b], bias, l + lane, row, rows); break;
+            default: rows_block_f32<LIN_NONE>(p, sum[b], bias, l + lane, row, rows); break;
+          }
+        }
+      } else {
+        float bias[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bias[i] = bias_at(p, it.e, l + 8 * i + (lane >> 2));
+        if (!wait_full()) break;
+#pragma unroll 1
+        for (int c = half * 32; c < it.n && l < p.L; c += 64) {
+          const int rows = it.rows - c;
+          const long long row = it.m0 + c;
+          const uint32_t t = lanes() + c;
+          switch (AMN ? LIN_NONE : p.act) {
+            case LIN_RELU: rows_block<AMN ? LIN_NONE : LIN_RELU>(p, t, bias, l, row, rows, stage, lane); break;
+            case LIN_SILU: rows_block<AMN ? LIN_NONE : LIN_SILU>(p, t, bias, l, row, rows, stage, lane); break;
+            case LIN_GELU: rows_block<AMN ? LIN_NONE : LIN_GELU>(p, t, bias, l, row, rows, stage, lane); break;
+            case LIN_GELU_TANH: rows_block<AMN ? LIN_NONE : LIN_GELU_TANH>(p, t, bias, l, row, rows, stage, lane); break;
+            default: rows_block<LIN_NONE>(p, t, bias, l, row, rows, stage, lane); break;
+          }
+        }
+        release();
+      }
+    }
+    // zeros behind the last group, 16 bytes a lane
+    const long long first = static_cast<long long>(table.start[p.E]) * p.L, end = static_cast<long long>(p.M) * p.L;
+    const long long at = (static_cast<long long>(blockIdx.x) * kGroupedEpiWarps + warp - 2) * 32 + lane;
+    const long long step = static_cast<long long>(gridDim.x) * kGroupedEpiWarps * 32;
+    for (long long i = first + at * 8; i < end; i += step * 8) {   // L % 8 == 0
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      if (F32) {
+        reinterpret_cast<uint4*>(static_cast<float*>(p.out) + i)[0] = none;
+        reinterpret_cast<uint4*>(static_cast<float*>(p.out) + i)[1] = none;
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + i) = none;
+      }
+      if (p.z) *reinterpret_cast<uint4*>(p.z + i) = none;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();   // the leader's MMAs into both TMEMs are done
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------- weight kernel
+struct GroupedWeightMaps {
+  CUtensorMap out;    // [E][N][K], boxes of 32 x 32
+};
+struct GroupedWeightParams {
+  const int* starts;        // [E + 1]
+  const CUtensorMap* dz;    // [E] maps of dz's rows up to the group's end, boxes 64 x 64
+  const CUtensorMap* x;     // [E] of x's
+  int E, N, K;
+  int n_tiles, k_tiles;
+  int* status;
+};
+struct GroupedWeightCfg {
+  static constexpr int kOutBytes = 4096;   // an epilogue warp's two 32 x 32 blocks in bf16
+  static constexpr int kSmemBytes = 1024 + kGroupedStages * kGroupedStageBytes + kGroupedEpiWarps * kOutBytes + 256;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+// A tensor map in global memory that another kernel wrote: before its first use.
+__device__ __forceinline__ void tensormap_acquire(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+struct WeightItem {
+  int e, n0, k0, first, nk;
+};
+// Groups one after the other, k outside n inside groups of 8 n tiles.
+__device__ __forceinline__ bool weight_item(const GroupedWeightParams& p, int idx, WeightItem& it) {
+  const int per = p.n_tiles * p.k_tiles;
+  it.e = idx / per;
+  if (it.e >= p.E) return false;
+  int nt, kt;
+  unit_and_col(idx - it.e * per, p.n_tiles, p.k_tiles, 8, nt, kt);
+  it.n0 = nt * 256;
+  it.k0 = kt * 256;
+  it.first = __ldg(p.starts + it.e);
+  it.nk = (__ldg(p.starts + it.e + 1) - it.first + kLinBK - 1) / kLinBK;
+  return true;
+}
+
+// The pair kernel of linear.cuh with both operands MN-major, over the groups'
+// rows; a group without rows gets zeros.
+__global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(const __grid_constant__ GroupedWeightMaps maps, const GroupedWeightParams p) {
+  using C = GroupedWeightCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* out_stage = smem + kGroupedStages * kGroupedStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + kGroupedEpiWarps * C::kOutBytes);
+  uint64_t* empty = full + kGroupedStages;
+  uint64_t* tfull = empty + kGroupedStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  int* const status = p.status;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGroupedStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kGroupedEpiWarps);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&maps.out);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t tmem_base = *tmem_slot;
+  if (warp == 0) {
+    int stage = 0, e = -1;
+    uint32_t phase = 0;
+    long long fills = 0;
+    bool ok = true;
+    const uint32_t lead_full = cluster_addr(full, 0);
+    WeightItem it;
+    for (int idx = pair; ok && weight_item(p, idx, it); idx += pairs) {
+      if (it.nk > 0 && it.e != e) {   // (every lane: any may be elected)
+        e = it.e;
+        tensormap_acquire(p.dz + e);
+        tensormap_acquire(p.x + e);
+        __syncwarp();
+      }
+      const int c0 = it.n0 + rank * 128, l0 = it.k0 + rank * 128;
+      for (int kb = 0; kb < it.nk; ++kb) {
+        if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sB = smem + stage * kGroupedStageBytes;
+        uint8_t* sA = sB + kLinABytes;
+        const uint32_t bar = lead_full + stage * 8;
+        const int r0 = it.first + kb * kLinBK;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kGroupedStageBytes);
+          tma_load_2d_pair(sB, p.dz + e, bar, c0, r0);
+          tma_load_2d_pair(sB + kLinChunk, p.dz + e, bar, c0 + 64, r0);
+          tma_load_2d_pair(sA, p.x + e, bar, l0, r0);
+          tma_load_2d_pair(sA + kLinChunk, p.x + e, bar, l0 + 64, r0);
+        }
+        __syncwarp();
+        ++fills;
+        if (++stage == kGroupedStages) stage = 0, phase ^= 1;
+      }
+    }
+    if (!ok && rank == 0 && lane == 0) {
+      const int n = fills < kGroupedStages ? static_cast<int>(fills) : kGroupedStages;
+      for (int i = 0; i < n; ++i) {
+        if (--stage < 0) stage = kGroupedStages - 1, phase ^= 1;
+        mbar_drain(&full[stage], phase);
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint64_t bd = linear_desc<true>(smem_u32(smem)), ad = linear_desc<true>(smem_u32(smem) + kLinABytes);
+      constexpr uint32_t idesc = idesc_bf16(256, 256, true, true);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      WeightItem it;
+      for (int idx = pair; ok && weight_item(p, idx, it); idx += pairs) {
+        if (it.nk == 0) continue;
+        if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, status)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * 256);
+        for (int kb = 0; kb < it.nk; ++kb) {
+          if (!warp_wait(&full[stage], phase, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = stage * kGroupedStageBytes;
+          if (elect_one()) {
+            umma_bf16_pair(acc, desc_at(bd, at), desc_at(ad, at), idesc, kb != 0);
+#pragma unroll
+            for (int kk = 1; kk < kLinBK / 16; ++kk)
+              umma_bf16_pair(acc, desc_at(bd, at + kk * kStep<true>), desc_at(ad, at + kk * kStep<true>), idesc, 1u);
+            umma_commit_pair(&empty[stage], 0x3);
+            if (kb == it.nk - 1) umma_commit_pair(&tfull[buf], 0x3);
+          }
+          __syncwarp();
+          if (++stage == kGroupedStages) stage = 0, phase ^= 1;
+        }
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1;
+      }
+      if (elect_one()) {
+        umma_commit_pair(done, 0x1);
+        mbar_drain(done, 0);
+      }
+    }
+  } else {
+    const int q = warp & 3, col0 = ((warp - 2) >> 2) * 128;
+    uint8_t* stage = out_stage + (warp - 2) * C::kOutBytes;
+    int buf = 0, slot = 0;
+    uint32_t bphase = 0;
+    WeightItem it;
+    for (int idx = pair; weight_item(p, idx, it); idx += pairs) {
+      const int n = it.n0 + rank * 128 + q * 32, k = it.k0 + col0;
+      if (it.nk > 0) {
+        const int w = lane == 0 ? (mbar_wait(&tfull[buf], bphase, abort_flag, status) ? 1 : 0) : 0;
+        const bool got = __shfl_sync(0xffffffffu, w, 0) != 0;
+        tc_fence_after();
+        if (!got) break;
+      }
+      const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * 256 + col0) + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < 128 && k + c < p.K && n < p.N; c += 32) {
+        uint8_t* block = stage + slot * 2048;
+        if (lane == 0) bulk_wait_read<1>();   // the copy that last read this block is done reading
+        __syncwarp();
+        float v[32];
+        if (it.nk > 0) {
+          tmem_ld32(tb + c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *stage_piece<false>(block, lane, j) = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                                           pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&maps.out, block, k + c, n, it.e);
+          bulk_commit();
+        }
+        slot ^= 1;
+      }
+      if (it.nk > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank != 0)
+            mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
+          else
+            mbar_arrive(&tempty[buf]);
+        }
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1;
+      }
+    }
+    if (lane == 0) bulk_wait<0>();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+}  // namespace mok
