@@ -15,6 +15,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "api_util.h"
 #include "experts.h"
 #include "gemm.cuh"
@@ -138,70 +140,175 @@ dim3 tile_grid(long long tiles) {
 }
 
 // ---------------------------------------------------------------- products with few rows
-// The rows of x are the columns of a 16 x 8 x 16 tensor-core product whose rows
-// are 16 rows of w: at this size the weights' bytes bound the kernel, and what
+// The rows of x are the columns of 16 x 8 x 16 tensor-core products whose rows
+// are 16 rows of w: at this size the weights' bytes bound the kernels, and what
 // counts is how few instructions a code takes.  A word of 8 codes is 3 shifts, 4
 // masks and 4 subtractions (128 + q - 128 - zero: exact in bf16) and half of
 // two products; the sums of a group, exact products added in fp32, then take its
 // scale in fp32, so that no weight is rounded.
 // Since any order of k will do where both operands agree, lane (g, t)'s word j
 // meets the 16 bytes of x's columns 32 j + 8 t .. + 7 as they lie in memory.
+// Codes, scales and x come in through shared memory by asynchronous copies some
+// stages ahead: registers would hold too few bytes in flight.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The codes of columns 2 i, 2 i + 1 of a word less the zero, as bf16: z holds 128
-// + zero twice.
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i, __nv_bfloat162 z) {
-  const uint32_t u = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), z);
-  return *reinterpret_cast<const uint32_t*>(&v);
+// The same without sums to add to.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ uint4 load_once(const uint8_t* p) {   // codes are read once: not kept in L1
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+// The codes of columns 2 i, 2 i + 1 of a word less the zero, as bf16: z holds
+// -(128 + zero) twice.
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i, uint32_t z) {
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(0x43004300u));   // (a & b) | c
+  asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(z));
   return v;
 }
 
-constexpr int kInt4Warps = 8;
+constexpr int kInt4Warps = 8;   // of a block, at most
 
-// A tile's codes, scales and zeros as a lane holds them: rows g and g + 8.
-template <int GPB>
-struct Int4Frag {
-  uint4 c[2];
-  uint16_t s[2][GPB];
-  uint8_t z[2][GPB];
+// CH tiles of a row tile, neighbours along K, in shared memory: their codes, then
+// their scales, then their zeros.
+template <int GPB, bool ZEROS, int CH>
+struct Int4Chunk {
+  static constexpr int kScales = CH * kInt4TileBytes, kZeros = kScales + CH * 32 * GPB;
+  static constexpr int kBytes = kZeros + (ZEROS ? CH * 16 * GPB : 0);
+  static_assert(CH * 2 * GPB <= 16 && CH * GPB <= 16, "a warp copies scales and zeros at one go");
 };
-template <int GPB, bool ZEROS>
-__device__ __forceinline__ void load_frag(Int4Frag<GPB>& f, const Int4LinearArgs& a, long long tile, int lane) {
-  const uint8_t* c = a.codes + tile * kInt4TileBytes + lane * 16;
-  f.c[0] = load_once(c);
-  f.c[1] = load_once(c + 512);
-  const int g = lane >> 2;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint16_t* s = a.scales + tile * (kInt4Rows * GPB) + (g + 8 * h) * GPB;
-    if constexpr (GPB == 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
-      f.s[h][0] = v.x, f.s[h][1] = v.x >> 16, f.s[h][2] = v.y, f.s[h][3] = v.y >> 16;
-    } else if constexpr (GPB == 2) {
-      const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(s));
-      f.s[h][0] = v, f.s[h][1] = v >> 16;
-    } else {
-      f.s[h][0] = __ldg(s);
+// What a lane copies of a row tile, chunk by chunk: two pieces of each tile's
+// codes, and of the scales or zeros one or none.
+template <int GPB, bool ZEROS, int CH>
+struct Int4Source {
+  using L = Int4Chunk<GPB, ZEROS, CH>;
+  const uint8_t* codes;
+  const uint8_t* extra;
+  int extra_step, extra_at;   // extra_at: -1 for none
+  __device__ __forceinline__ void start(const Int4LinearArgs& a, long long tile, int lane) {
+    codes = a.codes + tile * kInt4TileBytes + lane * 16;
+    extra = nullptr, extra_step = 0, extra_at = -1;
+    if (lane < CH * 2 * GPB) {
+      extra = reinterpret_cast<const uint8_t*>(a.scales) + tile * (32 * GPB) + lane * 16;
+      extra_step = CH * 32 * GPB, extra_at = L::kScales + lane * 16;
+    } else if (ZEROS && lane >= 16 && lane < 16 + CH * GPB) {
+      extra = a.zeros + tile * (16 * GPB) + (lane - 16) * 16;
+      extra_step = CH * 16 * GPB, extra_at = L::kZeros + (lane - 16) * 16;
     }
-    if constexpr (ZEROS) {
-      const uint8_t* z = a.zeros + tile * (kInt4Rows * GPB) + (g + 8 * h) * GPB;
+  }
+  // n (1 .. CH) tiles into dst; then on by `step` chunks.
+  __device__ __forceinline__ void fetch(uint8_t* dst, int n, int step, int lane) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (i < n) {
+        cp_async16(dst + i * kInt4TileBytes + lane * 16, codes + i * kInt4TileBytes, 16);
+        cp_async16(dst + i * kInt4TileBytes + 512 + lane * 16, codes + i * kInt4TileBytes + 512, 16);
+      }
+    }
+    codes += step * (CH * kInt4TileBytes);
+    // (a piece lies in one tile: 16 bytes are a divisor of a tile's scales, and of its zeros)
+    if (extra_at >= 0 && (n == CH || (extra_at < L::kZeros ? lane < n * 2 * GPB : lane - 16 < n * GPB))) cp_async16(dst + extra_at, extra, 16);
+    extra += step * extra_step;
+  }
+};
+// A column of a chunk of x: 256 bytes for each block of K, and 64 more, so that
+// the eight lanes of a shared-memory access (two columns) meet all banks.
+template <int CH>
+constexpr int kXColumn = CH * 256 + 64;
+
+// A lane's rows g and g + 8 of tile i of a chunk; scales two to a word, zeros four.
+template <int GPB, bool ZEROS, int CH>
+struct Int4Frag {
+  using L = Int4Chunk<GPB, ZEROS, CH>;
+  uint4 c[2];
+  uint32_t s[2][(GPB + 1) / 2], z[2];
+  __device__ __forceinline__ void load(const uint8_t* chunk, int i, int lane) {
+    c[0] = *reinterpret_cast<const uint4*>(chunk + i * kInt4TileBytes + lane * 16);
+    c[1] = *reinterpret_cast<const uint4*>(chunk + i * kInt4TileBytes + 512 + lane * 16);
+    const int g = lane >> 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* at = chunk + L::kScales + g * (GPB * 2) + i * (32 * GPB) + h * (16 * GPB);
       if constexpr (GPB == 4) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(z));
-        f.z[h][0] = v, f.z[h][1] = v >> 8, f.z[h][2] = v >> 16, f.z[h][3] = v >> 24;
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        s[h][0] = v.x, s[h][1] = v.y;
       } else if constexpr (GPB == 2) {
-        const uint16_t v = __ldg(reinterpret_cast<const uint16_t*>(z));
-        f.z[h][0] = v, f.z[h][1] = v >> 8;
+        s[h][0] = *reinterpret_cast<const uint32_t*>(at);
       } else {
-        f.z[h][0] = __ldg(z);
+        s[h][0] = *reinterpret_cast<const uint16_t*>(at);
+      }
+      if constexpr (ZEROS) {
+        const uint8_t* zt = chunk + L::kZeros + g * GPB + i * (16 * GPB) + h * (8 * GPB);
+        if constexpr (GPB == 4)
+          z[h] = *reinterpret_cast<const uint32_t*>(zt);
+        else if constexpr (GPB == 2)
+          z[h] = *reinterpret_cast<const uint16_t*>(zt);
+        else
+          z[h] = *zt;
+      }
+    }
+  }
+  __device__ __forceinline__ float scale(int h, int gr) const {
+    const uint32_t v = s[h][gr >> 1];
+    return __uint_as_float(gr & 1 ? v & 0xFFFF0000u : v << 16);
+  }
+  // -(128 + zero) in bf16, twice: the bytes zero, 0xC3, zero, 0xC3.
+  __device__ __forceinline__ uint32_t zero(int h, int gr) const { return ZEROS ? __byte_perm(z[h], 0xC3u, 0x4040u + 0x0101u * gr) : 0xC308C308u; }
+};
+
+// acc += tile i of R chunks (step bytes apart) times that block of x's COLS
+// columns (2, or 8 NG): acc[.][c] holds rows g (0, 1) and g + 8 (2, 3) of the
+// columns 8 c + 2 t + {0, 1}.  COLS = 2: the others repeat them.
+template <int COLS, int NG, int R, int GPB, bool ZEROS, int CH>
+__device__ __forceinline__ void block_products(float (&acc)[R][NG][4], const uint8_t* chunk, int step, const uint8_t* x, int i, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  constexpr int kWords = 4 / GPB;   // words of a group
+  Int4Frag<GPB, ZEROS, CH> f[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) f[r].load(chunk + r * step, i, lane);
+  x += (g & (COLS - 1)) * kXColumn<CH> + t * 16 + i * 256;
+#pragma unroll
+  for (int gr = 0; gr < GPB; ++gr) {
+    float sum[R][NG][4];
+#pragma unroll
+    for (int jj = 0; jj < kWords; ++jj) {
+      const int j = gr * kWords + jj;
+      uint4 b[NG];
+#pragma unroll
+      for (int c = 0; c < NG; ++c) b[c] = *reinterpret_cast<const uint4*>(x + c * 8 * kXColumn<CH> + j * 64);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint32_t lo = j == 0 ? f[r].c[0].x : j == 1 ? f[r].c[0].y : j == 2 ? f[r].c[0].z : f[r].c[0].w;
+        const uint32_t hi = j == 0 ? f[r].c[1].x : j == 1 ? f[r].c[1].y : j == 2 ? f[r].c[1].z : f[r].c[1].w;
+        uint32_t wl[4], wh[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wl[i] = pair_of(lo, i, f[r].zero(0, gr)), wh[i] = pair_of(hi, i, f[r].zero(1, gr));
+#pragma unroll
+        for (int c = 0; c < NG; ++c) {
+          if (jj == 0)
+            mma_16816_first(sum[r][c], wl[0], wh[0], wl[1], wh[1], b[c].x, b[c].y);
+          else
+            mma_16816(sum[r][c], wl[0], wh[0], wl[1], wh[1], b[c].x, b[c].y);
+        }
+#pragma unroll
+        for (int c = 0; c < NG; ++c) mma_16816(sum[r][c], wl[2], wh[2], wl[3], wh[3], b[c].z, b[c].w);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float sl = f[r].scale(0, gr), sh = f[r].scale(1, gr);
+#pragma unroll
+      for (int c = 0; c < NG; ++c) {
+        acc[r][c][0] = fmaf(sl, sum[r][c][0], acc[r][c][0]);
+        acc[r][c][1] = fmaf(sl, sum[r][c][1], acc[r][c][1]);
+        acc[r][c][2] = fmaf(sh, sum[r][c][2], acc[r][c][2]);
+        acc[r][c][3] = fmaf(sh, sum[r][c][3], acc[r][c][3]);
       }
     }
   }
@@ -217,6 +324,11 @@ __device__ __forceinline__ float act_of(float z, int act) {
   }
 }
 
+__device__ __forceinline__ float int4_bias(const Int4LinearArgs& a, long long at) {
+  if (!a.bias) return 0.f;
+  return a.bias_f32 ? __ldg(static_cast<const float*>(a.bias) + at)
+                    : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.bias) + at)) << 16);
+}
 __device__ __forceinline__ void store_out(const Int4LinearArgs& a, long long row, int n, float v) {
   const long long at = row * a.w.N + n;
   if (a.out_f32)
@@ -225,79 +337,124 @@ __device__ __forceinline__ void store_out(const Int4LinearArgs& a, long long row
     static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
 }
 
-// grid {groups of R row tiles, rows of x in steps of 8 NG; with experts: rows of
-// y}.  A block makes 16 R outputs of up to 8 NG rows; its warps take the blocks of
-// K in turn, each with its next codes in flight, and add their sums in order.
+// ---- warps that share K: few rows of w to a block
+// grid {groups of R row tiles, rows of x in steps of COLS; with experts: rows of
+// y}, 4 or 8 warps.  A block makes 16 R outputs of up to COLS rows; each warp
+// takes a part of K through stages of its own, and their sums are added in order.
 // With experts the block of a row whose expert no earlier row has serves all
 // rows of that expert, and the others' blocks end at once: an expert's weights
 // are read once.
-template <int NG, int R, int GPB, bool ZEROS, bool EXPERTS>
-__global__ void __launch_bounds__(32 * kInt4Warps) int4_linear_kernel(const Int4LinearArgs a) {
-  constexpr int kCols = 8 * NG, kRows = 16 * R;
-  __shared__ float part[kInt4Warps][kCols][kRows + 1];
-  __shared__ int list[kCols];
-  __shared__ int found, next;
+template <int COLS, int R, int GPB, bool ZEROS>
+struct Int4SplitCfg {
+  static constexpr int kCols = COLS, kRows = 16 * R, kGroups = COLS < 8 ? 1 : COLS / 8;
+  static constexpr int kChunk = COLS == 2 ? 2 : 1;   // blocks of K to a stage
+  static constexpr int kStages = COLS == 2 || COLS == 32 ? 2 : 3;
+  static constexpr int kTiles = Int4Chunk<GPB, ZEROS, kChunk>::kBytes;
+  static constexpr int kStageBytes = R * kTiles + kCols * kXColumn<kChunk>;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static_assert(kCols * (kRows + 1) * 4 <= kWarpBytes, "the parts fit the stages");
+  static_assert(kInt4Warps * kWarpBytes + 4096 <= 227 * 1024, "shared memory");
+};
+
+template <int COLS, int R, int GPB, bool ZEROS, bool EXPERTS>
+__global__ void __launch_bounds__(32 * kInt4Warps, COLS <= 8 ? 4 : 1) int4_split_kernel(const Int4LinearArgs a) {
+  using C = Int4SplitCfg<COLS, R, GPB, ZEROS>;
+  constexpr int kCols = C::kCols, kRows = C::kRows, NG = C::kGroups, D = C::kStages, CH = C::kChunk;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int lists[kInt4Warps][kCols];   // each warp its own: rows of y
+  __shared__ const uint16_t* x_rows[kInt4Warps][kCols];   // and of x
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const long long rt0 = static_cast<long long>(blockIdx.x) * R;
   const int n0 = static_cast<int>(rt0) * kInt4Rows, nb = a.w.blocks();
   long long matrix = 0;
+  unsigned same = 0;   // up to 32 rows: those of this block's expert
+  const bool few = EXPERTS && a.rows <= 32;
   if constexpr (EXPERTS) {
     const int r = blockIdx.y;
-    matrix = __ldg(a.experts + r);
+    const long long id = few ? (lane < a.rows ? __ldg(a.experts + lane) : -2) : __ldg(a.experts + r);
+    matrix = few ? __shfl_sync(0xffffffffu, id, r) : id;
     if (matrix < 0 || matrix >= a.w.matrices) {   // no expert: zeros; any id but -1 is an error besides
       if (matrix != -1 && threadIdx.x == 0 && blockIdx.x == 0 && a.status) atomicCAS(a.status, 0, MOK_ERR_INDEX);
       for (int n = n0 + threadIdx.x; n < min(n0 + kRows, a.w.N); n += blockDim.x) store_out(a, r, n, 0.f);
       return;
     }
-    int earlier = 0;
-    for (int i = threadIdx.x; i < r; i += blockDim.x) earlier |= __ldg(a.experts + i) == matrix;
-    if (__syncthreads_or(earlier)) return;
-    if (threadIdx.x == 0) next = r;
+    if (few) {   // each warp for itself
+      same = __ballot_sync(0xffffffffu, id == matrix);
+      if (same & ((1u << r) - 1u)) return;
+    } else {
+      int earlier = 0;
+      for (int i = threadIdx.x; i < r; i += blockDim.x) earlier |= __ldg(a.experts + i) == matrix;
+      if (__syncthreads_or(earlier)) return;
+    }
   }
+  const int warps = blockDim.x >> 5;
+  uint8_t* const stages = smem + warp * C::kWarpBytes;
+  int* const list = lists[warp];
   const long long tile0 = (matrix * a.w.row_tiles() + rt0) * nb;
   const int tiles = static_cast<int>(min(static_cast<long long>(R), a.w.row_tiles() - rt0));
+  // this warp's blocks of K
+  const int each = nb / warps, more = nb - each * warps;
+  const int kb0 = each * warp + min(warp, more), kb1 = kb0 + each + (warp < more ? 1 : 0);
+  int next = EXPERTS ? blockIdx.y : 0;
   for (;;) {
     // the rows of y that this pass makes
     int cols;
     if constexpr (EXPERTS) {
-      __syncthreads();
-      if (warp == 0) {
-        int at = next, n = 0;
-        while (at < a.rows && n < kCols) {
-          const bool hit = at + lane < a.rows && __ldg(a.experts + at + lane) == matrix;
-          const unsigned m = __ballot_sync(0xffffffffu, hit);
-          const int mine = n + __popc(m & ((1u << lane) - 1u));
-          if (hit && mine < kCols) list[mine] = at + lane;
-          const int all = n + __popc(m);
-          if (all > kCols) {   // the next pass begins with the first that did not fit
-            const unsigned over = __ballot_sync(0xffffffffu, hit && mine == kCols);
-            at += __ffs(over) - 1;
-            n = kCols;
-            break;
-          }
-          n = all;
-          at += 32;
+      cols = 0;
+      while (next < a.rows && cols < kCols) {
+        const bool hit = next + lane < a.rows && (few ? (same >> (next + lane)) & 1u : __ldg(a.experts + next + lane) == matrix);
+        const unsigned m = __ballot_sync(0xffffffffu, hit);
+        const int at = cols + __popc(m & ((1u << lane) - 1u)), all = cols + __popc(m);
+        if (hit && at < kCols) list[at] = next + lane;
+        if (all > kCols) {   // the next pass begins with the first that did not fit
+          next += __ffs(__ballot_sync(0xffffffffu, hit && at == kCols)) - 1;
+          cols = kCols;
+          break;
         }
-        if (lane == 0) found = n, next = at;
+        cols = all;
+        next += 32;
       }
-      __syncthreads();
-      cols = found;
       if (cols == 0) return;
     } else {
       cols = min(kCols, a.rows - static_cast<int>(blockIdx.y) * kCols);
+      for (int i = lane; i < cols; i += 32) list[i] = blockIdx.y * kCols + i;
     }
-    const uint16_t* xp[NG];
+    __syncwarp();
+    for (int i = lane; i < cols; i += 32) x_rows[warp][i] = a.x + static_cast<long long>(list[i] / a.x_div) * a.w.K;
+    __syncwarp();
+    Int4Source<GPB, ZEROS, CH> src[R];
 #pragma unroll
-    for (int c = 0; c < NG; ++c) {
-      const int col = c * 8 + g;
-      xp[c] = nullptr;
-      if (col < cols) {
-        const int r = EXPERTS ? list[col] : static_cast<int>(blockIdx.y) * kCols + col;
-        xp[c] = a.x + static_cast<long long>(r / a.x_div) * a.w.K + t * 8;
+    for (int r = 0; r < R; ++r) src[r].start(a, tile0 + (r < tiles ? r : 0) * static_cast<long long>(nb) + kb0, lane);   // (behind the last row tile: the first again)
+    // a lane's piece of the columns of x: all of one column (CH = 2), or half of two
+    constexpr int kLanes = CH * 16;
+    const int p = lane % kLanes, odd = lane / kLanes;
+    const uint16_t* const xp = odd < cols ? x_rows[warp][odd] + p * 8 : nullptr;
+    int ahead = kb0, to = 0;   // the next block that is fetched, and its stage
+    const auto fetch = [&]() {
+      if (ahead < kb1) {
+        uint8_t* st = stages + to * C::kStageBytes;
+        const int n = min(CH, kb1 - ahead), k = ahead * kInt4Block;
+#pragma unroll
+        for (int r = 0; r < R; ++r) src[r].fetch(st + r * C::kTiles, n, 1, lane);
+        const uint32_t in = k + p * 8 < a.w.K ? 16u : 0u;   // zeros behind the last column
+        const int from = in ? k : -p * 8;
+        if (p < 16 * n) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32 / kLanes) {   // columns without a row hold anything: theirs are not stored
+            if (c >= cols) break;
+            if (c + odd < cols)
+              cp_async16(st + R * C::kTiles + (c + odd) * kXColumn<CH> + p * 16, (c == 0 ? xp : x_rows[warp][c + odd] + p * 8) + from, in);
+          }
+        }
+        ahead += CH;
+        if (++to == D) to = 0;
       }
-    }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) fetch();
     float acc[R][NG][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -305,114 +462,181 @@ __global__ void __launch_bounds__(32 * kInt4Warps) int4_linear_kernel(const Int4
       for (int c = 0; c < NG; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[r][c][i] = 0.f;
-    Int4Frag<GPB> now[R], ahead[R];
-    int kb = warp;
-    if (kb < nb) {
+    int at = 0;
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1; kb += CH) {
+      cp_async_wait<D - 2>();
+      __syncwarp();   // every lane's copies are there, and the stage that is filled next has been read
+      fetch();
+      const uint8_t* st = stages + at * C::kStageBytes;
 #pragma unroll
-      for (int r = 0; r < R; ++r) load_frag<GPB, ZEROS>(now[r], a, tile0 + static_cast<long long>(min(r, tiles - 1)) * nb + kb, lane);
+      for (int i = 0; i < CH; ++i)
+        if (kb + i < kb1) block_products<kCols, NG, R, GPB, ZEROS, CH>(acc, st, C::kTiles, st + R * C::kTiles, i, lane);
+      if (++at == D) at = 0;
     }
-    for (; kb < nb; kb += kInt4Warps) {
-      if (kb + kInt4Warps < nb) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          load_frag<GPB, ZEROS>(ahead[r], a, tile0 + static_cast<long long>(min(r, tiles - 1)) * nb + kb + kInt4Warps, lane);
-      }
-      constexpr int kWords = 4 / GPB;   // words of a group
-#pragma unroll
-      for (int gr = 0; gr < GPB; ++gr) {
-        float sum[R][NG][4];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int c = 0; c < NG; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[r][c][i] = 0.f;
-        __nv_bfloat162 zero[R][2];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t z = 0x43004300u | (ZEROS ? now[r].z[h][gr] * 0x00010001u : 0x00080008u);
-            zero[r][h] = *reinterpret_cast<const __nv_bfloat162*>(&z);
-          }
-#pragma unroll
-        for (int jj = 0; jj < kWords; ++jj) {
-          const int j = gr * kWords + jj, k = kb * kInt4Block + 32 * j;
-          uint4 b[NG];
-#pragma unroll
-          for (int c = 0; c < NG; ++c) {
-            b[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (xp[c] && k < a.w.K) b[c] = __ldg(reinterpret_cast<const uint4*>(xp[c] + k));   // K % 32 == 0
-          }
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const uint32_t lo = j == 0 ? now[r].c[0].x : j == 1 ? now[r].c[0].y : j == 2 ? now[r].c[0].z : now[r].c[0].w;
-            const uint32_t hi = j == 0 ? now[r].c[1].x : j == 1 ? now[r].c[1].y : j == 2 ? now[r].c[1].z : now[r].c[1].w;
-            uint32_t wl[4], wh[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) wl[i] = pair_of(lo, i, zero[r][0]), wh[i] = pair_of(hi, i, zero[r][1]);
-#pragma unroll
-            for (int c = 0; c < NG; ++c) {
-              mma_16816(sum[r][c], wl[0], wh[0], wl[1], wh[1], b[c].x, b[c].y);
-              mma_16816(sum[r][c], wl[2], wh[2], wl[3], wh[3], b[c].z, b[c].w);
-            }
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float sl = __uint_as_float(static_cast<uint32_t>(now[r].s[0][gr]) << 16);
-          const float sh = __uint_as_float(static_cast<uint32_t>(now[r].s[1][gr]) << 16);
-#pragma unroll
-          for (int c = 0; c < NG; ++c) {
-            acc[r][c][0] = fmaf(sl, sum[r][c][0], acc[r][c][0]);
-            acc[r][c][1] = fmaf(sl, sum[r][c][1], acc[r][c][1]);
-            acc[r][c][2] = fmaf(sh, sum[r][c][2], acc[r][c][2]);
-            acc[r][c][3] = fmaf(sh, sum[r][c][3], acc[r][c][3]);
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) now[r] = ahead[r];
-    }
+    cp_async_wait<0>();
+    __syncthreads();   // the parts lie over the stages
+    float* part = reinterpret_cast<float*>(smem);   // [warp][kCols][kRows + 1]
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int c = 0; c < NG; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[warp][c * 8 + 2 * t + (i & 1)][r * 16 + g + 8 * (i >> 1)] = acc[r][c][i];
+        for (int i = 0; i < 4; ++i)
+          if (kCols >= 8 || t == 0) part[(warp * kCols + c * 8 + 2 * t + (i & 1)) * (kRows + 1) + r * 16 + g + 8 * (i >> 1)] = acc[r][c][i];
     __syncthreads();
     for (int i = threadIdx.x; i < cols * kRows; i += blockDim.x) {
       const int c = i / kRows, m = i % kRows, n = n0 + m;
       if (n >= a.w.N) continue;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kInt4Warps; ++w) v += part[w][c][m];
-      if (a.bias) {
-        const long long at = matrix * a.w.N + n;
-        v += a.bias_f32 ? __ldg(static_cast<const float*>(a.bias) + at)
-                        : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(a.bias) + at)) << 16);
-      }
-      store_out(a, EXPERTS ? list[c] : blockIdx.y * kCols + c, n, act_of(v, a.act));
+      for (int w = 0; w < kInt4Warps; ++w)
+        if (w < warps) v += part[(w * kCols + c) * (kRows + 1) + m];
+      v += int4_bias(a, matrix * a.w.N + n);
+      store_out(a, list[c], n, act_of(v, a.act));
     }
     if constexpr (!EXPERTS) return;
+    __syncthreads();   // the parts have been read
   }
 }
 
-template <int NG, int R, int GPB, bool ZEROS>
-cudaError_t int4_launch(const Int4LinearArgs& a, cudaStream_t st) {
-  const unsigned x = static_cast<unsigned>((a.w.row_tiles() + R - 1) / R);
-  if (a.experts)
-    return launch_dependent(int4_linear_kernel<NG, R, GPB, ZEROS, true>, dim3(x, a.rows), dim3(32 * kInt4Warps), 0, st, a);
-  return launch_dependent(int4_linear_kernel<NG, R, GPB, ZEROS, false>, dim3(x, (a.rows + 8 * NG - 1) / (8 * NG)),
-                          dim3(32 * kInt4Warps), 0, st, a);
+// ---- warps that share x: many rows of w
+// grid {groups of 16 row tiles, rows of x in steps of 8 NG}, one matrix.  A warp
+// makes 32 rows of w over all of K; the block's warps go through K together, so
+// that a block of x is fetched once for 256 rows of w.
+template <int NG, int GPB, bool ZEROS>
+struct Int4WideCfg {
+  static constexpr int kCols = 8 * NG, kRowTiles = 2 * kInt4Warps;
+  static constexpr int kStages = 3;
+  static constexpr int kTile = Int4Chunk<GPB, ZEROS, 1>::kBytes;
+  static constexpr int kStageBytes = kRowTiles * kTile + kCols * kXColumn<1>;
+  static constexpr int kSmemBytes = kStages * kStageBytes;
+  static_assert(kInt4Warps * kCols * 33 * 4 <= kSmemBytes, "the outputs fit the stages");
+  static_assert(kSmemBytes <= 112 * 1024, "two blocks to an SM");
+};
+
+template <int NG, int GPB, bool ZEROS>
+__global__ void __launch_bounds__(32 * kInt4Warps, 2) int4_wide_kernel(const Int4LinearArgs a) {
+  using C = Int4WideCfg<NG, GPB, ZEROS>;
+  constexpr int kCols = C::kCols, D = C::kStages;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int nb = a.w.blocks(), row_tiles = static_cast<int>(a.w.row_tiles());
+  const int rt = static_cast<int>(blockIdx.x) * C::kRowTiles + 2 * warp;   // this warp's first row tile
+  const int c0 = static_cast<int>(blockIdx.y) * kCols, cols = min(kCols, a.rows - c0);
+  Int4Source<GPB, ZEROS, 1> src[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) src[r].start(a, static_cast<long long>(min(rt + r, row_tiles - 1)) * nb, lane);
+  // this thread's pieces of x: columns tid / 16 and + 16 (those without a row are not stored)
+  const int p = threadIdx.x & 15, col = threadIdx.x >> 4;
+  const uint16_t* xp[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) xp[i] = a.x + static_cast<long long>(c0 + min(col + 16 * i, cols - 1)) * a.w.K;
+  int ahead = 0;
+  const auto fetch = [&]() {
+    if (ahead < nb) {
+      uint8_t* st = smem + ahead % D * C::kStageBytes;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) src[r].fetch(st + (2 * warp + r) * C::kTile, 1, 1, lane);
+      const int k = ahead * kInt4Block + p * 8, from = k < a.w.K ? k : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (col + 16 * i < cols) cp_async16(st + C::kRowTiles * C::kTile + (col + 16 * i) * kXColumn<1> + p * 16, xp[i] + from, k < a.w.K ? 16u : 0u);
+      ++ahead;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) fetch();
+  float acc[2][NG][4];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[r][c][i] = 0.f;
+#pragma unroll 1
+  for (int kb = 0; kb < nb; ++kb) {
+    cp_async_wait<D - 2>();
+    __syncthreads();   // every thread's copies are there, and the stage that is filled next has been read
+    fetch();
+    const uint8_t* st = smem + kb % D * C::kStageBytes;
+    block_products<kCols, NG, 2, GPB, ZEROS, 1>(acc, st + 2 * warp * C::kTile, C::kTile, st + C::kRowTiles * C::kTile, 0, lane);
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  float* out = reinterpret_cast<float*>(smem) + warp * kCols * 33;   // [kCols][33] of this warp's 32 rows of w
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[(c * 8 + 2 * t + (i & 1)) * 33 + r * 16 + g + 8 * (i >> 1)] = acc[r][c][i];
+  __syncwarp();
+  const int n = rt * kInt4Rows + lane;
+  if (n >= a.w.N) return;
+  const float bias = int4_bias(a, n);
+#pragma unroll 4
+  for (int c = 0; c < cols; ++c) store_out(a, c0 + c, n, act_of(out[c * 33 + lane] + bias, a.act));
 }
 
-template <int NG, int R>
-cudaError_t int4_group(const Int4LinearArgs& a, cudaStream_t st) {
+// The kernels' shared memory is above the default limit, which is raised once per
+// kernel and device.
+struct SmemLimit {
+  std::atomic<bool> done[64] = {};   // any thread may be the first
+  template <class K>
+  cudaError_t raise(K kern, int bytes) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return err;
+  }
+};
+
+template <int COLS, int R, int GPB, bool ZEROS, bool EXPERTS>
+cudaError_t split_launch(const Int4LinearArgs& a, int num_sms, cudaStream_t st) {
+  using C = Int4SplitCfg<COLS, R, GPB, ZEROS>;
+  auto kern = int4_split_kernel<COLS, R, GPB, ZEROS, EXPERTS>;
+  static SmemLimit limit;
+  const cudaError_t err = limit.raise(kern, kInt4Warps * C::kWarpBytes);
+  if (err != cudaSuccess) return err;
+  const unsigned x = static_cast<unsigned>((a.w.row_tiles() + R - 1) / R);
+  const unsigned y = EXPERTS ? a.rows : (a.rows + C::kCols - 1) / C::kCols;
+  // 4 warps to a block, 8 where an SM would have fewer than ten warps.  Measured with 2, 4 and 8: one row times 7168 x 2048
+  // 4.2, 3.5 and 4.1 us, 8 experts of 2048 x 7168 20.4, 17.7 and 19.5.
+  const int warps = static_cast<long long>(x) * y * 4 < 10ll * num_sms ? 8 : 4;
+  return launch_dependent(kern, dim3(x, y), dim3(32 * warps), warps * C::kWarpBytes, st, a);
+}
+template <int NG, int GPB, bool ZEROS>
+cudaError_t wide_launch(const Int4LinearArgs& a, cudaStream_t st) {
+  using C = Int4WideCfg<NG, GPB, ZEROS>;
+  auto kern = int4_wide_kernel<NG, GPB, ZEROS>;
+  static SmemLimit limit;
+  const cudaError_t err = limit.raise(kern, C::kSmemBytes);
+  if (err != cudaSuccess) return err;
+  const unsigned x = static_cast<unsigned>((a.w.row_tiles() + C::kRowTiles - 1) / C::kRowTiles);
+  return launch_dependent(kern, dim3(x, (a.rows + C::kCols - 1) / C::kCols), dim3(32 * kInt4Warps), C::kSmemBytes, st, a);
+}
+
+// COLS columns of x at a time; wide: shared x.
+template <int COLS, int GPB, bool ZEROS>
+cudaError_t int4_kind(const Int4LinearArgs& a, bool wide, int num_sms, cudaStream_t st) {
+  if (wide) return wide_launch<(COLS < 8 ? 1 : COLS / 8), GPB, ZEROS>(a, st);
+  constexpr int R = COLS > 8 ? 2 : 1;   // two row tiles to a block halve the bytes of x
+  return a.experts ? split_launch<COLS, R, GPB, ZEROS, true>(a, num_sms, st) : split_launch<COLS, R, GPB, ZEROS, false>(a, num_sms, st);
+}
+template <int COLS>
+cudaError_t int4_group(const Int4LinearArgs& a, bool wide, int num_sms, cudaStream_t st) {
   const bool z = a.zeros != nullptr;
-  if (a.w.group == 32) return z ? int4_launch<NG, R, 4, true>(a, st) : int4_launch<NG, R, 4, false>(a, st);
-  if (a.w.group == 64) return z ? int4_launch<NG, R, 2, true>(a, st) : int4_launch<NG, R, 2, false>(a, st);
-  return z ? int4_launch<NG, R, 1, true>(a, st) : int4_launch<NG, R, 1, false>(a, st);
+  if (a.w.group == 32) return z ? int4_kind<COLS, 4, true>(a, wide, num_sms, st) : int4_kind<COLS, 4, false>(a, wide, num_sms, st);
+  if (a.w.group == 64) return z ? int4_kind<COLS, 2, true>(a, wide, num_sms, st) : int4_kind<COLS, 2, false>(a, wide, num_sms, st);
+  return z ? int4_kind<COLS, 1, true>(a, wide, num_sms, st) : int4_kind<COLS, 1, false>(a, wide, num_sms, st);
 }
 
 }  // namespace
@@ -440,11 +664,13 @@ cudaError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales,
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t st) {
   // columns of the product: what there are, or with experts the rows that one has on average
   const double per = a.experts ? static_cast<double>(a.rows) / static_cast<double>(a.w.matrices) : static_cast<double>(a.rows);
-  // two row tiles to a warp halve its loads of x; one, where there would be few blocks
-  const long long blocks = (a.w.row_tiles() + 1) / 2 * (a.experts ? a.rows : 1);
-  if (per > 16) return int4_group<4, 2>(a, st);
-  if (per > 8) return int4_group<2, 2>(a, st);
-  return blocks >= 4ll * num_sms ? int4_group<1, 2>(a, st) : int4_group<1, 1>(a, st);
+  const int cols = per > 16 ? 32 : per > 8 ? 16 : per > 2 ? 8 : 2;
+  // rows of w enough for 256 to a block
+  const bool wide = !a.experts && a.w.row_tiles() / (2 * kInt4Warps) * ((a.rows + cols - 1) / cols) >= num_sms;
+  if (cols == 32) return int4_group<32>(a, wide, num_sms, st);
+  if (cols == 16) return int4_group<16>(a, wide, num_sms, st);
+  if (cols == 8) return int4_group<8>(a, wide, num_sms, st);
+  return int4_group<2>(a, wide, num_sms, st);
 }
 
 }  // namespace mok

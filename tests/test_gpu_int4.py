@@ -92,9 +92,12 @@ def _check(y, z64, size, act, K, group, out):
 ONE = [(1, 8, 32, 32), (1, 7168, 2048, 128), (1, 1000, 4096, 64), (2, 17, 96, 32), (3, 1, 128, 64), (7, 264, 160, 32), (8, 513, 1024, 128),
        (9, 40, 384, 128), (16, 2056, 512, 64), (17, 136, 7168, 128), (31, 33, 224, 32), (32, 4096, 256, 128), (33, 100, 640, 64),
        (64, 520, 1152, 128), (100, 24, 192, 64), (1000, 72, 320, 32)]
+# rows of w enough for the variant whose warps share x
+WIDE = [(1, 39169, 96, 32), (5, 39168, 640, 128), (12, 41000, 192, 64), (16, 39200, 1024, 32), (31, 40007, 704, 64), (33, 30000, 128, 128),
+        (64, 39168, 256, 64)]
 
 
-@pytest.mark.parametrize("rows,N,K,group", ONE)
+@pytest.mark.parametrize("rows,N,K,group", ONE + WIDE)
 @pytest.mark.parametrize("zeros,bias,act,out", [(False, None, "none", BF16), (True, F32, "gelu", F32), (True, BF16, "silu", BF16),
                                                 (False, F32, "relu", F32), (False, None, "gelu_tanh", BF16)])
 def test_one_matrix(rows, N, K, group, zeros, bias, act, out):
