@@ -39,7 +39,7 @@ extern "C" {
 
 size_t mok_route_workspace_bytes(int64_t T, int E) {
   if (T < 0 || T > 0x7fffffffll || E < 1 || E > MOK_ROUTE_MAX_E) return 0;
-  return 2 * static_cast<size_t>(route_blocks(T)) * E * sizeof(float) + 256;
+  return 2 * static_cast<size_t>(route_blocks(T, E)) * E * sizeof(float) + 256;
 }
 
 mok_status_t mok_route(const void* logits, int logits_dtype, const float* bias, int64_t T, int E, int k, int score, int normalize,
@@ -210,7 +210,7 @@ mok_status_t mok_grouped_linear_bwd(const void* dy, int dy_dtype, const uint16_t
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~static_cast<uintptr_t>(255));
   uint16_t* dz = make_dz ? reinterpret_cast<uint16_t*>(base + at.dz) : nullptr;
   float* part = d_bias ? reinterpret_cast<float*>(base + at.part) : nullptr;
-  const int* starts = reinterpret_cast<const int*>(base);   // the plan's first part
+  const GroupedBias bias = {part, d_bias, grouped_dz_chunk(static_cast<int>(M), N)};
   GroupedWeightCall c = {};
   c.dz = make_dz ? dz : static_cast<const uint16_t*>(dy);
   c.x = x;
@@ -221,12 +221,10 @@ mok_status_t mok_grouped_linear_bwd(const void* dy, int dy_dtype, const uint16_t
   c.K = K;
   c.out = d_weight;
   c.status = status;
-  st = launch_grouped_plan(c, d_weight != nullptr, base, s);
+  st = run_grouped_dz(c, {dy, dy_dtype == MOK_DTYPE_F32, z, activation, dz, part}, d_weight != nullptr, base, s);
   if (st) return st;
-  if (dz || part)
-    MOK_CUDA(launch_grouped_dz(dy, dy_dtype == MOK_DTYPE_F32, z, activation, starts, E, c.M, N, dz, part, s));
-  if (d_weight) {
-    st = run_grouped_weights(c, base, s);
+  if (d_weight) {   // and the bias's sums
+    st = run_grouped_weights(c, base, bias, s);
     if (st) return st;
   }
   if (dx) {
@@ -238,6 +236,7 @@ mok_status_t mok_grouped_linear_bwd(const void* dy, int dy_dtype, const uint16_t
     p.M = c.M;
     p.act = MOK_ACT_NONE;
     p.out = dx;
+    p.beside_last = d_weight != nullptr;
     GroupedRowsCall r = {};
     r.w = w;
     r.x = c.dz;
@@ -247,7 +246,7 @@ mok_status_t mok_grouped_linear_bwd(const void* dy, int dy_dtype, const uint16_t
     st = run_grouped_rows(r, p, s);
     if (st) return st;
   }
-  if (d_bias) MOK_CUDA(launch_grouped_bias(part, starts, E, c.M, N, d_bias, s));
+  if (d_bias && !d_weight) MOK_CUDA(launch_grouped_bias(bias, base, E, N, s));
   return MOK_OK;
 }
 

@@ -37,7 +37,7 @@ struct RouteBwdArgs {
   int sigmoid, normalize;
   float scale;
 };
-int route_blocks(long long T);
+int route_blocks(long long T, int E);
 cudaError_t launch_route(const RouteArgs& a, int f32, cudaStream_t st);
 cudaError_t launch_route_bwd(const RouteBwdArgs& a, int f32, cudaStream_t st);
 
@@ -93,6 +93,9 @@ struct GroupedRowsParams {
   int bias_f32;
   void* out;             // [M][L]
   uint16_t* z;           // [M][L] bf16 or NULL
+  // the kernel before it on the stream is one that waited for all before itself, and whose results this one does not read:
+  // it starts as that one's CTAs leave, and waits for it at its end
+  int beside_last;
   int* status;
 };
 struct GroupedRowsCall {
@@ -112,19 +115,32 @@ struct GroupedWeightCall {
   uint16_t* out;
   int* status;
 };
+// The bias's gradient [E][N] from the sums of dz over each chunk of rows inside
+// each group: part [grouped_dz_parts][N], out NULL for none.
+struct GroupedBias {
+  const float* part;
+  float* out;
+  int chunk;
+};
 // Part of the backward's workspace: the groups' first rows ([E + 1], 16-byte
 // multiple) and two tensor maps for each.
 size_t grouped_plan_bytes(int E);
-mok_status_t launch_grouped_plan(const GroupedWeightCall& c, bool maps, void* plan, cudaStream_t st);
-mok_status_t run_grouped_weights(const GroupedWeightCall& c, const void* plan, cudaStream_t st);
 
-// dz = dy act'(z) in bf16 (dz may be NULL) for the groups' rows, and the sums
-// of its fp32 values over each chunk of rows inside each group; then the
-// groups' sums in order.
+// The backward's first pass: the plan, with the groups' maps of dz and x where
+// `maps`; and where dz or part is wanted, dz = dy act'(z) in bf16 for the groups'
+// rows, and the sums of its fp32 values over each chunk of rows inside each group.
+struct GroupedDzCall {
+  const void* dy;
+  int dy_f32;
+  const uint16_t* z;
+  int act;
+  uint16_t* dz;       // or NULL
+  float* part;        // or NULL
+};
 int grouped_dz_chunk(int M, int N);   // rows of a chunk
 inline long long grouped_dz_parts(int M, int N, int E) { return (static_cast<long long>(M) + grouped_dz_chunk(M, N) - 1) / grouped_dz_chunk(M, N) + E; }
-cudaError_t launch_grouped_dz(const void* dy, int dy_f32, const uint16_t* z, int act, const int* starts, int E, int M, int N,
-                              uint16_t* dz, float* part, cudaStream_t st);
-cudaError_t launch_grouped_bias(const float* part, const int* starts, int E, int M, int N, float* d_bias, cudaStream_t st);
+mok_status_t run_grouped_dz(const GroupedWeightCall& c, const GroupedDzCall& d, bool maps, void* plan, cudaStream_t st);
+mok_status_t run_grouped_weights(const GroupedWeightCall& c, const void* plan, const GroupedBias& bias, cudaStream_t st);
+cudaError_t launch_grouped_bias(const GroupedBias& b, const void* plan, int E, int N, cudaStream_t st);
 
 }  // namespace mok

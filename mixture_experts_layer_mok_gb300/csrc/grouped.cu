@@ -31,41 +31,44 @@ mok_status_t make_map(CUtensorMap* m, const void* base, long long inner, long lo
 
 template <bool AMN, bool F32>
 mok_status_t launch_rows(const GroupedRowsMaps& maps, const GroupedRowsParams& p, cudaStream_t st) {
+  using C = GroupedRowsCfg<F32>;
   auto kern = grouped_rows_kernel<AMN, F32>;
   static KernelInfo info;
   int n = 0;
-  MOK_CUDA(resident_clusters(kern, info, kGroupedThreads, GroupedRowsCfg::kSmemBytes, 2, &n));
+  MOK_CUDA(resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2, &n));
   const long long items = (static_cast<long long>(p.M) / 256 + (p.E < p.M ? p.E : p.M)) * p.l_tiles;   // at most
   const int pairs = items < n ? static_cast<int>(items) : n;
-  MOK_CUDA(launch_clusters(kern, dim3(2 * pairs), kGroupedThreads, GroupedRowsCfg::kSmemBytes, 2, st, maps, p));
+  MOK_CUDA(launch_clusters(kern, dim3(2 * pairs), C::kThreads, C::kSmemBytes, 2, st, maps, p));
   return MOK_OK;
 }
 
-// ---------------------------------------------------------------- plan
-struct PlanMaps {
-  CUtensorMap dz, x;
+// ---------------------------------------------------------------- plan and dz
+struct Plan {
+  CUtensorMap dz, x;   // of the whole tensors
+  const int* counts;
+  int E, M;
+  int* starts;
+  CUtensorMap *to_dz, *to_x;   // or NULL
+  int* status;
 };
 constexpr size_t plan_starts_bytes(int E) { return (static_cast<size_t>(E + 1) * sizeof(int) + 127) / 128 * 128; }
 
-// One block: the groups' first rows; and each group's maps, which are the whole
-// tensors' but for their length, which is the group's end.
-__global__ void __launch_bounds__(1024) grouped_plan_kernel(const __grid_constant__ PlanMaps whole, const int* counts, int E, int M, int* starts,
-                                                            CUtensorMap* dz, CUtensorMap* x, int* status) {
-  __shared__ int start[kMaxGroups + 1];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    const bool bad = scan_groups(counts, E, M, start, nullptr, lane);
-    if (bad && lane == 0) atomicCAS(status, 0, MOK_ERR_INDEX);
+// By a block: the groups' first rows into start (shared memory), and by one that
+// is to `write` them, the plan: each group's maps are the whole tensors' but for
+// their length, which is the group's end.
+__device__ __forceinline__ void make_plan(const Plan& p, int* start, bool write, int thread, int threads) {
+  if (thread < 32) {
+    const bool bad = scan_groups(p.counts, p.E, p.M, start, nullptr, thread);
+    if (bad && write && thread == 0) atomicCAS(p.status, 0, MOK_ERR_INDEX);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) starts[e] = start[e];
-  if (!dz) return;
-  for (int i = threadIdx.x; i < 2 * E; i += blockDim.x) {
+  if (!write) return;
+  for (int e = thread; e <= p.E; e += threads) p.starts[e] = start[e];
+  if (!p.to_dz) return;
+  for (int i = thread; i < 2 * p.E; i += threads) {
     const int e = i >> 1;
-    const uint4* from = reinterpret_cast<const uint4*>(i & 1 ? &whole.x : &whole.dz);
-    CUtensorMap* to = (i & 1 ? x : dz) + e;
+    const uint4* from = reinterpret_cast<const uint4*>(i & 1 ? &p.x : &p.dz);
+    CUtensorMap* to = (i & 1 ? p.to_x : p.to_dz) + e;
 #pragma unroll
     for (int j = 0; j < 8; ++j) reinterpret_cast<uint4*>(to)[j] = from[j];
     const uint32_t rows = max(start[e + 1], 1);   // (a group that begins and ends at 0 is never read)
@@ -74,50 +77,73 @@ __global__ void __launch_bounds__(1024) grouped_plan_kernel(const __grid_constan
   asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
 }
 
-// ---------------------------------------------------------------- dz
+// The plan alone, by one block.
+__global__ void __launch_bounds__(1024) grouped_plan_kernel(const __grid_constant__ Plan plan) {
+  __shared__ int start[kMaxGroups + 1];
+  griddep_wait();
+  griddep_launch_dependents();
+  make_plan(plan, start, true, threadIdx.x, blockDim.x);
+}
+
 constexpr int kDzRows = 8;   // rows in step in a block; 32 threads x 8 columns wide
+
+// One row's 8 columns at `at`: dy act'(z).
+template <class DY, int ACT>
+struct DzPiece {
+  uint4 dy[sizeof(DY) == 4 ? 2 : 1], z;
+  __device__ __forceinline__ void load(const DY* __restrict__ d, const uint16_t* __restrict__ zp, long long at) {
+    dy[0] = __ldcs(reinterpret_cast<const uint4*>(d + at));
+    if constexpr (sizeof(DY) == 4) dy[1] = __ldcs(reinterpret_cast<const uint4*>(d + at) + 1);
+    if constexpr (ACT != LIN_NONE) z = __ldcs(reinterpret_cast<const uint4*>(zp + at));
+  }
+  __device__ __forceinline__ void value(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = sizeof(DY) == 4 ? __uint_as_float(reinterpret_cast<const uint32_t*>(dy)[i]) : bf16_at(dy, i);
+      if constexpr (ACT != LIN_NONE) v[i] *= act_slope<ACT>(bf16_at(&z, i));
+    }
+  }
+};
 
 // Chunks of rows are cut without regard to the groups; part[chunk + e] holds the
 // sums over the rows of group e in a chunk: from one pair (chunk, e) to the next
-// at least one of the two grows, so that no two share a place.
+// at least one of the two grows, so that no two share a place.  The first block
+// also writes the plan.
+// Bound by memory.
 template <class DY, int ACT>
-__global__ void __launch_bounds__(256) grouped_dz_kernel(const DY* __restrict__ dy, const uint16_t* __restrict__ z,
-                                                         const int* __restrict__ starts, int E, int N, int chunk,
-                                                         uint16_t* __restrict__ dz, float* __restrict__ part) {
+__global__ void __launch_bounds__(256) grouped_dz_kernel(const __grid_constant__ Plan plan, const DY* __restrict__ dy,
+                                                         const uint16_t* __restrict__ z, int N, int chunk, uint16_t* __restrict__ dz,
+                                                         float* __restrict__ part) {
+  __shared__ int start[kMaxGroups + 1];
   __shared__ float s[kDzRows][32][9];
   griddep_wait();
   griddep_launch_dependents();
-  const int col = (blockIdx.x * 32 + threadIdx.x) * 8;
+  make_plan(plan, start, blockIdx.x == 0 && blockIdx.y == 0, threadIdx.y * 32 + threadIdx.x, 256);
+  const int E = plan.E, col = (blockIdx.x * 32 + threadIdx.x) * 8;
   int r0 = blockIdx.y * chunk;
-  const int r1 = min(r0 + chunk, __ldg(starts + E));
+  const int r1 = min(r0 + chunk, start[E]);
   if (r0 >= r1) return;
-  for (int e = find_group(starts, E, r0, threadIdx.x); r0 < r1; ++e) {
-    const int end = min(__ldg(starts + e + 1), r1);
+  for (int e = part ? find_group(start, E, r0, threadIdx.x) : 0; r0 < r1; ++e) {
+    const int end = part ? min(start[e + 1], r1) : r1;   // without sums the groups do not matter
     if (end <= r0) continue;   // an empty group
     float sum[8] = {};
     if (col < N) {
-      for (int r = r0 + threadIdx.y; r < end; r += kDzRows) {
-        const long long at = static_cast<long long>(r) * N + col;
-        float d[8];
-        if constexpr (sizeof(DY) == 4) {
-          const float4 a = __ldcs(reinterpret_cast<const float4*>(dy + at));
-          const float4 b = __ldcs(reinterpret_cast<const float4*>(dy + at) + 1);
-          d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
-        } else {
-          const uint4 a = __ldcs(reinterpret_cast<const uint4*>(dy + at));
+      constexpr int kAtOnce = 4;   // rows whose loads are in flight together
+      for (int r = r0 + threadIdx.y; r < end; r += kAtOnce * kDzRows) {
+        DzPiece<DY, ACT> in[kAtOnce];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = bf16_at(&a, i);
+        for (int u = 0; u < kAtOnce; ++u) in[u].load(dy, z, static_cast<long long>(min(r + u * kDzRows, end - 1)) * N + col);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          if (r + u * kDzRows >= end) break;
+          float d[8];
+          in[u].value(d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] += d[i];
+          if (dz)   // read again at once by the products: kept in L2
+            *reinterpret_cast<uint4*>(dz + static_cast<long long>(r + u * kDzRows) * N + col) =
+                make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
         }
-        if constexpr (ACT != LIN_NONE) {
-          const uint4 a = __ldcs(reinterpret_cast<const uint4*>(z + at));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] *= act_slope<ACT>(bf16_at(&a, i));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += d[i];
-        if (dz)   // read again at once by the products: kept in L2
-          *reinterpret_cast<uint4*>(dz + at) =
-              make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
       }
     }
     r0 = end;
@@ -135,42 +161,25 @@ __global__ void __launch_bounds__(256) grouped_dz_kernel(const DY* __restrict__ 
   }
 }
 
-// A group's parts in order: 32 columns a block, 8 parts in step.
-__global__ void __launch_bounds__(256) grouped_bias_kernel(const float* __restrict__ part, const int* __restrict__ starts, int N, int chunk,
-                                                           float* __restrict__ d_bias) {
-  __shared__ float s[8][33];
+__global__ void __launch_bounds__(256) grouped_bias_kernel(const GroupedBias b, const int* starts, int E, int N) {
   griddep_wait();
   griddep_launch_dependents();
-  const int e = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x;
-  const int r0 = __ldg(starts + e), r1 = __ldg(starts + e + 1);
-  float v = 0.f;
-  if (col < N && r0 < r1) {
-    const int last = (r1 - 1) / chunk;
-#pragma unroll 4
-    for (int c = r0 / chunk + threadIdx.y; c <= last; c += 8) v += part[(static_cast<long long>(c) + e) * N + col];
-  }
-  s[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.y == 0 && col < N) {
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v += s[i][threadIdx.x];
-    d_bias[static_cast<long long>(e) * N + col] = v;
-  }
+  grouped_bias_sums(b, starts, E, N, static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x,
+                    static_cast<long long>(gridDim.x) * blockDim.x);
 }
 
 template <class DY>
-cudaError_t dz_launch(const DY* dy, const uint16_t* z, int act, const int* starts, int E, int M, int N, uint16_t* dz, float* part,
-                      cudaStream_t st) {
-  const int chunk = grouped_dz_chunk(M, N);
-  const dim3 grid((N + 255) / 256, (M + chunk - 1) / chunk), block(32, kDzRows);
-  switch (act) {
-    case LIN_RELU: return launch_dependent(grouped_dz_kernel<DY, LIN_RELU>, grid, block, 0, st, dy, z, starts, E, N, chunk, dz, part);
-    case LIN_SILU: return launch_dependent(grouped_dz_kernel<DY, LIN_SILU>, grid, block, 0, st, dy, z, starts, E, N, chunk, dz, part);
-    case LIN_GELU: return launch_dependent(grouped_dz_kernel<DY, LIN_GELU>, grid, block, 0, st, dy, z, starts, E, N, chunk, dz, part);
-    case LIN_GELU_TANH:
-      return launch_dependent(grouped_dz_kernel<DY, LIN_GELU_TANH>, grid, block, 0, st, dy, z, starts, E, N, chunk, dz, part);
-    default: return launch_dependent(grouped_dz_kernel<DY, LIN_NONE>, grid, block, 0, st, dy, z, starts, E, N, chunk, dz, part);
+cudaError_t dz_launch(const Plan& plan, const GroupedDzCall& d, int N, cudaStream_t st) {
+  const DY* dy = static_cast<const DY*>(d.dy);
+  const int chunk = grouped_dz_chunk(plan.M, N);
+  const dim3 grid((N + 255) / 256, (plan.M + chunk - 1) / chunk), block(32, kDzRows);
+  const auto launch = [&](auto kern) { return launch_dependent(kern, grid, block, 0, st, plan, dy, d.z, N, chunk, d.dz, d.part); };
+  switch (d.act) {
+    case LIN_RELU: return launch(grouped_dz_kernel<DY, LIN_RELU>);
+    case LIN_SILU: return launch(grouped_dz_kernel<DY, LIN_SILU>);
+    case LIN_GELU: return launch(grouped_dz_kernel<DY, LIN_GELU>);
+    case LIN_GELU_TANH: return launch(grouped_dz_kernel<DY, LIN_GELU_TANH>);
+    default: return launch(grouped_dz_kernel<DY, LIN_NONE>);
   }
 }
 
@@ -191,22 +200,29 @@ mok_status_t run_grouped_rows(const GroupedRowsCall& c, const GroupedRowsParams&
 
 size_t grouped_plan_bytes(int E) { return plan_starts_bytes(E) + 2 * static_cast<size_t>(E) * sizeof(CUtensorMap); }
 
-mok_status_t launch_grouped_plan(const GroupedWeightCall& c, bool maps, void* plan, cudaStream_t st) {
-  PlanMaps whole = {};
-  CUtensorMap *dz = nullptr, *x = nullptr;
+mok_status_t run_grouped_dz(const GroupedWeightCall& c, const GroupedDzCall& d, bool maps, void* at, cudaStream_t st) {
+  Plan plan = {};
   if (maps) {
-    mok_status_t s = make_map(&whole.dz, c.dz, c.N, c.M, 0, 64, 64);
-    if (!s) s = make_map(&whole.x, c.x, c.K, c.M, 0, 64, 64);
+    mok_status_t s = make_map(&plan.dz, c.dz, c.N, c.M, 0, 64, 64);
+    if (!s) s = make_map(&plan.x, c.x, c.K, c.M, 0, 64, 64);
     if (s) return s;
-    dz = reinterpret_cast<CUtensorMap*>(static_cast<uint8_t*>(plan) + plan_starts_bytes(c.E));
-    x = dz + c.E;
+    plan.to_dz = reinterpret_cast<CUtensorMap*>(static_cast<uint8_t*>(at) + plan_starts_bytes(c.E));
+    plan.to_x = plan.to_dz + c.E;
   }
-  MOK_CUDA(launch_dependent(grouped_plan_kernel, dim3(1), dim3(1024), 0, st, whole, c.counts, c.E, c.M, static_cast<int*>(plan), dz, x,
-                            c.status));
+  plan.counts = c.counts;
+  plan.E = c.E;
+  plan.M = c.M;
+  plan.starts = static_cast<int*>(at);
+  plan.status = c.status;
+  if (!d.dz && !d.part)
+    MOK_CUDA(launch_dependent(grouped_plan_kernel, dim3(1), dim3(1024), 0, st, plan));
+  else
+    MOK_CUDA(d.dy_f32 ? dz_launch<float>(plan, d, c.N, st) : dz_launch<uint16_t>(plan, d, c.N, st));
   return MOK_OK;
 }
 
-mok_status_t run_grouped_weights(const GroupedWeightCall& c, const void* plan, cudaStream_t st) {
+mok_status_t run_grouped_weights(const GroupedWeightCall& c, const void* plan, const GroupedBias& bias, cudaStream_t st) {
+  using C = GroupedWeightCfg;
   GroupedWeightParams p = {};
   p.starts = static_cast<const int*>(plan);
   p.dz = reinterpret_cast<const CUtensorMap*>(static_cast<const uint8_t*>(plan) + plan_starts_bytes(c.E));
@@ -216,17 +232,18 @@ mok_status_t run_grouped_weights(const GroupedWeightCall& c, const void* plan, c
   p.K = c.K;
   p.n_tiles = (c.N + 255) / 256;
   p.k_tiles = (c.K + 255) / 256;
+  p.bias = bias;
   p.status = c.status;
   const long long items = static_cast<long long>(p.E) * p.n_tiles * p.k_tiles;
   if (items > 0x7fffffffll / 4) return fail(MOK_ERR_INVALID_ARG, "product too large");
   GroupedWeightMaps maps;
-  const mok_status_t s = make_map(&maps.out, c.out, c.K, c.N, c.E, 32, 32);
+  const mok_status_t s = make_map(&maps.out, c.out, c.K, c.N, c.E, 64, 32);
   if (s) return s;
   static KernelInfo info;
   int n = 0;
-  MOK_CUDA(resident_clusters(grouped_weight_kernel, info, kGroupedThreads, GroupedWeightCfg::kSmemBytes, 2, &n));
+  MOK_CUDA(resident_clusters(grouped_weight_kernel, info, C::kThreads, C::kSmemBytes, 2, &n));
   const int pairs = items < n ? static_cast<int>(items) : n;
-  MOK_CUDA(launch_clusters(grouped_weight_kernel, dim3(2 * pairs), kGroupedThreads, GroupedWeightCfg::kSmemBytes, 2, st, maps, p));
+  MOK_CUDA(launch_clusters(grouped_weight_kernel, dim3(2 * pairs), C::kThreads, C::kSmemBytes, 2, st, maps, p));
   return MOK_OK;
 }
 
@@ -237,15 +254,10 @@ int grouped_dz_chunk(int M, int N) {
   return rows < 4 * kDzRows ? 4 * kDzRows : rows;
 }
 
-cudaError_t launch_grouped_dz(const void* dy, int dy_f32, const uint16_t* z, int act, const int* starts, int E, int M, int N,
-                              uint16_t* dz, float* part, cudaStream_t st) {
-  return dy_f32 ? dz_launch(static_cast<const float*>(dy), z, act, starts, E, M, N, dz, part, st)
-                : dz_launch(static_cast<const uint16_t*>(dy), z, act, starts, E, M, N, dz, part, st);
-}
-
-cudaError_t launch_grouped_bias(const float* part, const int* starts, int E, int M, int N, float* d_bias, cudaStream_t st) {
-  return launch_dependent(grouped_bias_kernel, dim3((N + 31) / 32, E), dim3(32, 8), 0, st, part, starts, N, grouped_dz_chunk(M, N),
-                          d_bias);
+cudaError_t launch_grouped_bias(const GroupedBias& b, const void* plan, int E, int N, cudaStream_t st) {
+  const long long blocks = (static_cast<long long>(E) * N + 255) / 256;
+  return launch_dependent(grouped_bias_kernel, dim3(static_cast<unsigned>(blocks < 4864 ? blocks : 4864)), dim3(256), 0, st, b,
+                          static_cast<const int*>(plan), E, N);
 }
 
 }  // namespace mok

@@ -31,10 +31,7 @@
 
 namespace mok {
 
-constexpr int kGroupedStages = 6;
 constexpr int kGroupedStageBytes = 2 * kLinABytes;   // 128 x 64 of A, up to 128 x 64 of B
-constexpr int kGroupedEpiWarps = 8;
-constexpr int kGroupedThreads = 64 + 32 * kGroupedEpiWarps;
 
 // ---------------------------------------------------------------- the groups
 struct GroupTable {
@@ -104,10 +101,14 @@ struct GroupedRowsMaps {
   CUtensorMap x[4];   // [M][K], boxes of 64 x 16, 32, 64 and 128
 };
 
+// fp32 outputs leave from registers: room for twice the epilogue warps, whose
+// activations and stores are what the last tile of a pair ends with.
+template <bool F32>
 struct GroupedRowsCfg {
-  static constexpr int kStageOut = 2048;   // an epilogue warp's 32 rows x 32 columns in bf16
+  static constexpr int kStages = 6, kEpiWarps = F32 ? 16 : 8, kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kStageOut = F32 ? 0 : 2048;   // an epilogue warp's 32 rows x 32 columns in bf16
   static constexpr int kSmemBytes =
-      1024 + kGroupedStages * kGroupedStageBytes + kGroupedEpiWarps * kStageOut + static_cast<int>(sizeof(GroupTable)) + 256;
+      1024 + kStages * kGroupedStageBytes + kEpiWarps * kStageOut + static_cast<int>(sizeof(GroupTable)) + 256;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -242,14 +243,14 @@ __device__ __forceinline__ void rows_block_f32(const GroupedRowsParams& p, const
 // AMN: A is stored [k][l] (dx).  F32: fp32 outputs, whose sums over more than
 // kChunk K-blocks are added in registers (linear.cuh).
 template <bool AMN, bool F32>
-__global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const __grid_constant__ GroupedRowsMaps maps, const GroupedRowsParams p) {
-  using C = GroupedRowsCfg;
+__global__ void __launch_bounds__(GroupedRowsCfg<F32>::kThreads, 1) grouped_rows_kernel(const __grid_constant__ GroupedRowsMaps maps, const GroupedRowsParams p) {
+  using C = GroupedRowsCfg<F32>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* out_stage = smem + kGroupedStages * kGroupedStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + kGroupedEpiWarps * C::kStageOut);
-  uint64_t* empty = full + kGroupedStages;
-  uint64_t* tfull = empty + kGroupedStages;
+  uint8_t* out_stage = smem + C::kStages * kGroupedStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + C::kEpiWarps * C::kStageOut);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -260,13 +261,13 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   int* const status = p.status;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kGroupedStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kGroupedEpiWarps);   // the leader's counts both CTAs' warps
+      mbar_init(&tempty[b], 2 * C::kEpiWarps);   // the leader's counts both CTAs' warps
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
-  griddep_wait();
+  if (!p.beside_last) griddep_wait();
   griddep_launch_dependents();
   if (warp == 2) {
     const bool bad = scan_groups(p.counts, p.E, p.M, table.start, table.tile, lane);
@@ -318,13 +319,13 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
         }
         __syncwarp();
         ++fills;
-        if (++stage == kGroupedStages) stage = 0, phase ^= 1;
+        if (++stage == C::kStages) stage = 0, phase ^= 1;
       }
     }
     if (!ok && rank == 0 && lane == 0) {   // no load may be in flight when the CTA ends
-      const int n = fills < kGroupedStages ? static_cast<int>(fills) : kGroupedStages;
+      const int n = fills < C::kStages ? static_cast<int>(fills) : C::kStages;
       for (int i = 0; i < n; ++i) {
-        if (--stage < 0) stage = kGroupedStages - 1, phase ^= 1;
+        if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
         mbar_drain(&full[stage], phase);
       }
     }
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
               if (kb == end - 1) umma_commit_pair(&tfull[buf], 0x3);
             }
             __syncwarp();
-            if (++stage == kGroupedStages) stage = 0, phase ^= 1;
+            if (++stage == C::kStages) stage = 0, phase ^= 1;
           }
           buf ^= 1;
           if (buf == 0) bphase ^= 1;
@@ -372,7 +373,9 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    // a quarter of the TMEM lanes, and of each kEpiWarps / 4 blocks of 32 columns one
+    constexpr int kSide = C::kEpiWarps / 4, kBlocks = 8 / kSide;
+    const int q = warp & 3, side = (warp - 2) >> 2;
     uint8_t* stage = out_stage + (warp - 2) * C::kStageOut;
     int buf = 0;
     uint32_t bphase = 0;
@@ -400,19 +403,19 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
       const int l = it.l0 + rank * 128 + q * 32;   // this warp's l's
       const auto lanes = [&]() { return tmem_base + static_cast<uint32_t>(buf * 256) + (static_cast<uint32_t>(q * 32) << 16); };
       if constexpr (F32) {
-        float sum[4][32] = {};
+        float sum[kBlocks][32] = {};
         for (int first = 0; first < p.nk; first += kChunk) {
           if (!(ok = wait_full())) break;
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if ((2 * b + half) * 32 < it.n) add_columns<32>(lanes() + (2 * b + half) * 32, sum[b]);
+          for (int b = 0; b < kBlocks; ++b)
+            if ((kSide * b + side) * 32 < it.n) add_columns<32>(lanes() + (kSide * b + side) * 32, sum[b]);
           release();
         }
         if (!ok) break;
         const float bias = bias_at(p, it.e, l + lane);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int c = (2 * b + half) * 32, rows = it.rows - c;
+        for (int b = 0; b < kBlocks; ++b) {
+          const int c = (kSide * b + side) * 32, rows = it.rows - c;
           if (rows <= 0) continue;
           const long long row = it.m0 + c;
           switch (p.act) {
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
         for (int i = 0; i < 4; ++i) bias[i] = bias_at(p, it.e, l + 8 * i + (lane >> 2));
         if (!wait_full()) break;
 #pragma unroll 1
-        for (int c = half * 32; c < it.n && l < p.L; c += 64) {
+        for (int c = side * 32; c < it.n && l < p.L; c += 32 * kSide) {
           const int rows = it.rows - c;
           const long long row = it.m0 + c;
           const uint32_t t = lanes() + c;
@@ -446,8 +449,8 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
     }
     // zeros behind the last group, 16 bytes a lane
     const long long first = static_cast<long long>(table.start[p.E]) * p.L, end = static_cast<long long>(p.M) * p.L;
-    const long long at = (static_cast<long long>(blockIdx.x) * kGroupedEpiWarps + warp - 2) * 32 + lane;
-    const long long step = static_cast<long long>(gridDim.x) * kGroupedEpiWarps * 32;
+    const long long at = (static_cast<long long>(blockIdx.x) * C::kEpiWarps + warp - 2) * 32 + lane;
+    const long long step = static_cast<long long>(gridDim.x) * C::kEpiWarps * 32;
     for (long long i = first + at * 8; i < end; i += step * 8) {   // L % 8 == 0
       const uint4 none = make_uint4(0u, 0u, 0u, 0u);
       if (F32) {
@@ -466,11 +469,12 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_rows_kernel(const 
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);
   }
+  if (p.beside_last) griddep_wait();   // what follows this kernel follows that one too
 }
 
 // ---------------------------------------------------------------- weight kernel
 struct GroupedWeightMaps {
-  CUtensorMap out;    // [E][N][K], boxes of 32 x 32
+  CUtensorMap out;    // [E][N][K], boxes of 32 x 64
 };
 struct GroupedWeightParams {
   const int* starts;        // [E + 1]
@@ -478,11 +482,16 @@ struct GroupedWeightParams {
   const CUtensorMap* x;     // [E] of x's
   int E, N, K;
   int n_tiles, k_tiles;
+  GroupedBias bias;
   int* status;
 };
+// 16 epilogue warps, each of which stores a block of 128-byte rows.  Bound by
+// memory where groups are short: 64 groups of 1024 x 2048 take 70 us with one
+// row each, as a memset of the 268 MB would (4.05 TB/s), and 110 with 512.
 struct GroupedWeightCfg {
-  static constexpr int kOutBytes = 4096;   // an epilogue warp's two 32 x 32 blocks in bf16
-  static constexpr int kSmemBytes = 1024 + kGroupedStages * kGroupedStageBytes + kGroupedEpiWarps * kOutBytes + 256;
+  static constexpr int kStages = 5, kEpiWarps = 16, kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kOutBytes = 4096;   // an epilogue warp's 32 x 64 block in bf16
+  static constexpr int kSmemBytes = 1024 + kStages * kGroupedStageBytes + kEpiWarps * kOutBytes + 256;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -498,32 +507,52 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 }
 
 struct WeightItem {
-  int e, n0, k0, first, nk;
+  int e, n0, k0, first, end;
+  __device__ __forceinline__ int nk() const { return (end - first + kLinBK - 1) / kLinBK; }
 };
-// Groups one after the other, k outside n inside groups of 8 n tiles.
-__device__ __forceinline__ bool weight_item(const GroupedWeightParams& p, int idx, WeightItem& it) {
+// Groups one after the other, k outside n inside groups of 8 n tiles.  The rows
+// come from global memory: an item is looked up one ahead of its use.
+__device__ __forceinline__ WeightItem weight_item(const GroupedWeightParams& p, int idx) {
+  WeightItem it = {};
   const int per = p.n_tiles * p.k_tiles;
   it.e = idx / per;
-  if (it.e >= p.E) return false;
+  if (it.e >= p.E) return it;
   int nt, kt;
   unit_and_col(idx - it.e * per, p.n_tiles, p.k_tiles, 8, nt, kt);
   it.n0 = nt * 256;
   it.k0 = kt * 256;
   it.first = __ldg(p.starts + it.e);
-  it.nk = (__ldg(p.starts + it.e + 1) - it.first + kLinBK - 1) / kLinBK;
-  return true;
+  it.end = __ldg(p.starts + it.e + 1);
+  return it;
+}
+
+// The bias's gradient from the parts that grouped_dz_kernel left (grouped.cu), a
+// group's in order; thread `at` of `threads`.
+__device__ __forceinline__ void grouped_bias_sums(const GroupedBias& b, const int* starts, int E, int N, long long at, long long threads) {
+  for (long long i = at; i < static_cast<long long>(E) * N; i += threads) {
+    const int e = static_cast<int>(i / N), col = static_cast<int>(i - static_cast<long long>(e) * N);
+    const int r0 = __ldg(starts + e), r1 = __ldg(starts + e + 1);
+    float v = 0.f;
+    if (r0 < r1) {
+      const float* part = b.part + (static_cast<long long>(r0 / b.chunk) + e) * N + col;
+      const int n = (r1 - 1) / b.chunk - r0 / b.chunk + 1;
+#pragma unroll 4
+      for (int c = 0; c < n; ++c) v += part[static_cast<long long>(c) * N];
+    }
+    b.out[i] = v;
+  }
 }
 
 // The pair kernel of linear.cuh with both operands MN-major, over the groups'
 // rows; a group without rows gets zeros.
-__global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(const __grid_constant__ GroupedWeightMaps maps, const GroupedWeightParams p) {
+__global__ void __launch_bounds__(GroupedWeightCfg::kThreads, 1) grouped_weight_kernel(const __grid_constant__ GroupedWeightMaps maps, const GroupedWeightParams p) {
   using C = GroupedWeightCfg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* out_stage = smem + kGroupedStages * kGroupedStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + kGroupedEpiWarps * C::kOutBytes);
-  uint64_t* empty = full + kGroupedStages;
-  uint64_t* tfull = empty + kGroupedStages;
+  uint8_t* out_stage = smem + C::kStages * kGroupedStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + C::kEpiWarps * C::kOutBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -533,13 +562,13 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(cons
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   int* const status = p.status;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kGroupedStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kGroupedEpiWarps);
+      mbar_init(&tempty[b], 2 * C::kEpiWarps);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -562,16 +591,19 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(cons
     long long fills = 0;
     bool ok = true;
     const uint32_t lead_full = cluster_addr(full, 0);
-    WeightItem it;
-    for (int idx = pair; ok && weight_item(p, idx, it); idx += pairs) {
-      if (it.nk > 0 && it.e != e) {   // (every lane: any may be elected)
+    WeightItem it, next = weight_item(p, pair);
+    for (int idx = pair; ok && next.e < p.E; idx += pairs) {
+      it = next;
+      const int nk = it.nk();
+      next = weight_item(p, idx + pairs);
+      if (nk > 0 && it.e != e) {   // (every lane: any may be elected)
         e = it.e;
         tensormap_acquire(p.dz + e);
         tensormap_acquire(p.x + e);
         __syncwarp();
       }
       const int c0 = it.n0 + rank * 128, l0 = it.k0 + rank * 128;
-      for (int kb = 0; kb < it.nk; ++kb) {
+      for (int kb = 0; kb < nk; ++kb) {
         if (!warp_wait(&empty[stage], phase ^ 1, abort_flag, status)) {
           ok = false;
           break;
@@ -589,13 +621,13 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(cons
         }
         __syncwarp();
         ++fills;
-        if (++stage == kGroupedStages) stage = 0, phase ^= 1;
+        if (++stage == C::kStages) stage = 0, phase ^= 1;
       }
     }
     if (!ok && rank == 0 && lane == 0) {
-      const int n = fills < kGroupedStages ? static_cast<int>(fills) : kGroupedStages;
+      const int n = fills < C::kStages ? static_cast<int>(fills) : C::kStages;
       for (int i = 0; i < n; ++i) {
-        if (--stage < 0) stage = kGroupedStages - 1, phase ^= 1;
+        if (--stage < 0) stage = C::kStages - 1, phase ^= 1;
         mbar_drain(&full[stage], phase);
       }
     }
@@ -606,13 +638,16 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(cons
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
-      WeightItem it;
-      for (int idx = pair; ok && weight_item(p, idx, it); idx += pairs) {
-        if (it.nk == 0) continue;
+      WeightItem it, next = weight_item(p, pair);
+      for (int idx = pair; ok && next.e < p.E; idx += pairs) {
+        it = next;
+        const int nk = it.nk();
+        next = weight_item(p, idx + pairs);
+        if (nk == 0) continue;
         if (!warp_wait(&tempty[buf], bphase ^ 1, abort_flag, status)) break;
         tc_fence_after();
         const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * 256);
-        for (int kb = 0; kb < it.nk; ++kb) {
+        for (int kb = 0; kb < nk; ++kb) {
           if (!warp_wait(&full[stage], phase, abort_flag, status)) {
             ok = false;
             break;
@@ -624,10 +659,10 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(cons
             for (int kk = 1; kk < kLinBK / 16; ++kk)
               umma_bf16_pair(acc, desc_at(bd, at + kk * kStep<true>), desc_at(ad, at + kk * kStep<true>), idesc, 1u);
             umma_commit_pair(&empty[stage], 0x3);
-            if (kb == it.nk - 1) umma_commit_pair(&tfull[buf], 0x3);
+            if (kb == nk - 1) umma_commit_pair(&tfull[buf], 0x3);
           }
           __syncwarp();
-          if (++stage == kGroupedStages) stage = 0, phase ^= 1;
+          if (++stage == C::kStages) stage = 0, phase ^= 1;
         }
         buf ^= 1;
         if (buf == 0) bphase ^= 1;
@@ -638,45 +673,38 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(cons
       }
     }
   } else {
-    const int q = warp & 3, col0 = ((warp - 2) >> 2) * 128;
+    const int q = warp & 3, col0 = ((warp - 2) >> 2) * 64;   // this warp's rows and columns of the tile
     uint8_t* stage = out_stage + (warp - 2) * C::kOutBytes;
-    int buf = 0, slot = 0;
+    int buf = 0;
     uint32_t bphase = 0;
-    WeightItem it;
-    for (int idx = pair; weight_item(p, idx, it); idx += pairs) {
+    WeightItem it, next = weight_item(p, pair);
+    if (p.bias.out)   // while the first tile is made
+      grouped_bias_sums(p.bias, p.starts, p.E, p.N, (blockIdx.x * C::kEpiWarps + warp - 2) * 32 + lane, gridDim.x * C::kEpiWarps * 32);
+    for (int idx = pair; next.e < p.E; idx += pairs) {
+      it = next;
+      const int nk = it.nk();
+      next = weight_item(p, idx + pairs);
       const int n = it.n0 + rank * 128 + q * 32, k = it.k0 + col0;
-      if (it.nk > 0) {
-        const int w = lane == 0 ? (mbar_wait(&tfull[buf], bphase, abort_flag, status) ? 1 : 0) : 0;
-        const bool got = __shfl_sync(0xffffffffu, w, 0) != 0;
+      const bool in = n < p.N && k < p.K;
+      uint32_t w[32];
+      if (nk > 0) {
+        const int got = lane == 0 ? (mbar_wait(&tfull[buf], bphase, abort_flag, status) ? 1 : 0) : 0;
+        const bool ok = __shfl_sync(0xffffffffu, got, 0) != 0;
         tc_fence_after();
-        if (!got) break;
-      }
-      const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * 256 + col0) + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < 128 && k + c < p.K && n < p.N; c += 32) {
-        uint8_t* block = stage + slot * 2048;
-        if (lane == 0) bulk_wait_read<1>();   // the copy that last read this block is done reading
-        __syncwarp();
-        float v[32];
-        if (it.nk > 0) {
-          tmem_ld32(tb + c, v);
-        } else {
+        if (!ok) break;
+        if (in) {
+          const uint32_t tb = tmem_base + static_cast<uint32_t>(buf * 256 + col0) + (static_cast<uint32_t>(q * 32) << 16);
+          const uint32_t at[2] = {tb, tb + 32};
+          float v[64];
+          tmem_ld32_multi<2>(at, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          for (int i = 0; i < 32; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
         }
+      } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *stage_piece<false>(block, lane, j) = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                                                           pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&maps.out, block, k + c, n, it.e);
-          bulk_commit();
-        }
-        slot ^= 1;
+        for (int i = 0; i < 32; ++i) w[i] = 0u;
       }
-      if (it.nk > 0) {
+      if (nk > 0) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -687,6 +715,19 @@ __global__ void __launch_bounds__(kGroupedThreads, 1) grouped_weight_kernel(cons
         }
         buf ^= 1;
         if (buf == 0) bphase ^= 1;
+      }
+      if (in) {
+        if (lane == 0) bulk_wait_read<0>();   // the copy that last read the block is done reading
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)   // rows of 128 bytes, 16-byte pieces swizzled by the row
+          reinterpret_cast<uint4*>(stage)[lane * 8 + (j ^ (lane & 7))] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&maps.out, stage, k, n, it.e);
+          bulk_commit();
+        }
       }
     }
     if (lane == 0) bulk_wait<0>();

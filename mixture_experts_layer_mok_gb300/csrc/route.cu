@@ -1,11 +1,20 @@
 // The router: each token's k experts and their weights from its logits, what
 // the balance and z losses need, and the gradient of the logits.
 //
-// A warp to a token; lane l holds the V consecutive logits from l V on, so that
-// the lowest lane of several with the same largest value holds the lowest
-// index.  The k largest are taken one after the other: each lane keeps the
-// largest of what is left of its own, one warp reduction finds the largest of
-// those, and only the lane that held it looks for its next.
+// G lanes to a token, 32 / G tokens to a warp at a time; lane l of a token holds
+// the V consecutive logits from l V on, so that the lowest lane of several with the
+// same largest value holds the lowest index.  V is 8 up to 256 experts: fewer
+// lanes to a token of few experts, because a token's cost is in its reductions.
+//
+// The choice.  A whole warp to a token: the k-th largest of the lanes' largest
+// bounds the choice from below; the few logits that reach it (about k + 4 of 256
+// for k = 8) are put side by side, one to a lane, and ranked by comparing each
+// with all.  Where more than 32 reach it (ties, or k above 32), and for part of a
+// warp, the largest are taken one after the other: each lane keeps the largest of
+// what is left of its own, and only the lane that held the last one looks for its
+// next.
+//
+// Bound by instructions: per token of 256 experts some 400 for a warp.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -13,20 +22,27 @@
 #include "experts.h"
 #include "gemm.cuh"
 #include "internal.h"
+#include "linear.cuh"
+#include "ops.h"
 #include "ptx.cuh"
 
 namespace mok {
 namespace {
 
-constexpr int kRouteWarps = 8;
+// Warps of a block, at most: fewer where a lane holds more.
+template <int V>
+constexpr int kRouteWarps = V > 8 ? 8 : 16;
+constexpr int kSumRows = 4;   // warps' sums of scores that a block keeps at a time
 constexpr unsigned kAll = 0xffffffffu;
 
-// Unsigned integers in the order of the values: -0 as 0, NaN above all, and
-// above 0, which stands for nothing.
+// Unsigned integers in the order of the values: -0 as 0, NaN (which the addition
+// makes 0x7fffffff) above all, and above 0, which stands for nothing.
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
-  if (x != x) return 0xffffffffu;
   return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k ^ (static_cast<uint32_t>(static_cast<int>(~k) >> 31) | 0x80000000u));
 }
 
 // Lane l's V logits; -inf behind the last.
@@ -87,40 +103,140 @@ __device__ __forceinline__ float logit_at(const LT* row, long long i) {
   return __uint_as_float(static_cast<uint32_t>(__ldg(row + i)) << 16);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Over a token's G lanes.
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  for (int o = G / 2; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int G>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (G == 32) return __reduce_max_sync(kAll, v);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  for (int o = G / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
   return v;
+}
+template <int G>
+__device__ __forceinline__ float lanes_max(float v) {
+  return key_value(lanes_max<G>(order_key(v)));
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
-// The row's largest logit (0 where it is -inf: exp(x - 0) is then 0 for all)
-// and e[i] = exp(x[i] - it); returns the sum of e.
-template <int V>
+// The token's largest logit (0 where it is -inf: exp(x - 0) is then 0 for all)
+// and e[i] = exp(x[i] - it), good to 2^-21 or so; returns the sum of e.
+template <int G, int V>
 __device__ __forceinline__ float exps(const float (&x)[V], float (&e)[V], float& top) {
   float m = x[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
-  m = warp_max(m);
+  m = lanes_max<G>(m);
   top = m == -INFINITY ? 0.f : m;
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) sum += e[i] = expf(x[i] - top);
-  return warp_sum(sum);
+  for (int i = 0; i < V; ++i) sum += e[i] = fast_exp2((x[i] - top) * kLog2e);
+  return lanes_sum<G>(sum);
 }
 
-template <class LT, int V>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a) {
-  extern __shared__ float shared[];   // with counts: [E] counts, then [kRouteWarps][E] sums of scores
+// Picks that each of a token's P lanes holds (the j-th is slot j / P of lane j %
+// P): one where there are no more than lanes, which keeps the code short, else as
+// many as there can be.
+template <int P, int G, int V, bool MANY>
+constexpr int kSlots = MANY ? (G * V < MOK_ROUTE_MAX_K ? G * V : MOK_ROUTE_MAX_K) / P : 1;
+
+struct Pick {
+  int id;
+  uint32_t key;
+};
+// A warp's scratch in shared memory, for a round of 32 / P tokens.
+template <int P, int V, int G>
+struct RouteScratch {
+  static constexpr int kTokens = 32 / P;
+  Pick picks[kTokens][G * V < MOK_ROUTE_MAX_K ? G * V : MOK_ROUTE_MAX_K];
+  float top[kTokens], total[kTokens];
+  uint4 list[G == 32 ? 17 : 1];   // what reaches the bound: two of (key, index) each, one key of 0 behind; the rest of too many
+  int found;
+};
+
+// The k largest keys of a token, largest first, into its picks.
+template <int G, int V, class Scratch>
+__device__ __forceinline__ void choose(uint32_t (&key)[V], int k, int lane, Scratch& scratch, Pick* picks) {
+  const int l = lane % G;
+  uint32_t most = key[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) most = max(most, key[i]);
+  if (G == 32 && k <= 32) {
+    uint2* const list = reinterpret_cast<uint2*>(scratch.list);
+    uint32_t left = most, least = 0;
+#pragma unroll 2
+    for (int j = 0; j < k; ++j) {   // (equal ones go at one time: the bound is then lower than it need be)
+      least = lanes_max<G>(left);
+      if (left == least) left = 0;
+    }
+    uint32_t in = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) in |= key[i] >= least ? 1u << i : 0u;
+    if (lane == 0) scratch.found = 0;
+    __syncwarp();
+    if (in) {   // in any order: the ranks below do not depend on it
+      int at = atomicAdd(&scratch.found, __popc(in));
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if ((in >> i) & 1u) list[min(at++, 33)] = make_uint2(key[i], lane * V + i);
+    }
+    __syncwarp();
+    const int all = scratch.found;
+    if (all <= 32) {
+      if (lane == 0) list[all].x = 0;
+      __syncwarp();
+      const uint2 me = list[lane];
+      int rank = 0;
+#pragma unroll 2
+      for (int j = 0; j < all; j += 2) {
+        const uint4 v = scratch.list[j / 2];
+        rank += (v.x > me.x ? 1 : 0) + (v.z > me.x ? 1 : 0);
+      }
+      if (lane >= all) rank = 0;
+      if (__reduce_add_sync(kAll, rank) != all * (all - 1) / 2 && lane < all) {   // equal ones: in the order of their indices
+        for (int j = 0; j < all; ++j) rank += list[j].x == me.x && list[j].y < me.y ? 1 : 0;
+      }
+      if (lane < all && rank < k) picks[rank] = Pick{static_cast<int>(me.y), me.x};
+      __syncwarp();
+      return;
+    }
+  }
+  for (int j = 0; j < k; ++j) {
+    const uint32_t best = lanes_max<G>(most);
+    const unsigned hit = (__ballot_sync(kAll, most == best) >> (lane - l)) & (kAll >> (32 - G));
+    if (l == __ffs(hit) - 1) {
+      most = 0;
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const bool it = !found && key[i] == best;
+        if (it) picks[j] = Pick{l * V + i, best}, key[i] = 0;
+        found = found || it;
+        most = max(most, key[i]);
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// A round of a warp is 32 / P tokens: first G lanes to each in G / P passes, which
+// leave the picks and the sums in shared memory, then P lanes to each, which make
+// the weights of all of them at a time.
+template <class LT, int G, int V, bool MANY>
+__global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteArgs a) {
+  constexpr int P = G < 8 ? G : 8, S = kSlots<P, G, V, MANY>;
+  using Scratch = RouteScratch<P, V, G>;
+  extern __shared__ float shared[];   // with counts: [E] counts, then [kSumRows][E] sums of scores
+  __shared__ __align__(16) Scratch scratches[kRouteWarps<V>];
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31, l = lane % G;
+  Scratch& scratch = scratches[warp];
   const bool balance = a.counts != nullptr;
   int* cnt = reinterpret_cast<int*>(shared);
   if (balance) {
@@ -130,103 +246,115 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
   float mean[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) mean[i] = 0.f;
-  const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
-  for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp; t < a.T; t += step) {
-    float x[V], s[V], top;
-    load_logits<LT, V>(static_cast<const LT*>(a.logits) + t * a.E, a.E, lane, x);
-    const float total = exps<V>(x, s, top);
-    if (lane == 0) a.lse[t] = top == INFINITY ? top : top + logf(total);
-    const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
-    if (a.sigmoid) {
-      if (balance || a.bias) {
+  const long long step = static_cast<long long>(gridDim.x) * warps * (32 / P);
+  for (long long t0 = (static_cast<long long>(blockIdx.x) * warps + warp) * (32 / P); t0 < a.T; t0 += step) {
+#pragma unroll 1
+    for (int pass = 0; pass < G / P && t0 + pass * (32 / G) < a.T; ++pass) {
+      const int at = pass * (32 / G) + lane / G;   // the token's place in the round
+      const bool live = t0 + at < a.T;
+      const LT* row = static_cast<const LT*>(a.logits) + (live ? t0 + at : t0) * a.E;   // (behind the last token: the first again)
+      float x[V], s[V], top;
+      load_logits<LT, V>(row, a.E, l, x);
+      const float total = exps<G, V>(x, s, top);
+      if (l == 0) scratch.top[at] = top, scratch.total[at] = total;
+      if (a.sigmoid) {
+        if (balance || a.bias) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = sigmoid(x[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] *= inv;
-    }
-    if (balance) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) mean[i] += s[i];
-    }
-    // the choice: by the logits, in whose order the scores are, or by score + bias
-    uint32_t key[V], most = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      float by = x[i];
-      if (a.bias && e < a.E && x[i] != -INFINITY) by = s[i] + __ldg(a.bias + e);
-      key[i] = e < a.E ? order_key(by) : 0u;
-      most = max(most, key[i]);
-    }
-    int id[2] = {0, 0};
-    float picked[2] = {-INFINITY, -INFINITY};   // the logits of the picked, lane j's j-th and (j + 32)-th
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t best = __reduce_max_sync(kAll, most);
-      const int src = __ffs(__ballot_sync(kAll, most == best)) - 1;
-      int at = 0;
-      float val = 0.f;
-      if (lane == src) {
-        most = 0;
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const bool it = !found && key[i] == best;
-          if (it) at = lane * V + i, val = x[i], key[i] = 0;
-          found = found || it;
-          most = max(most, key[i]);
+          for (int i = 0; i < V; ++i) s[i] = a.bias ? sigmoid(x[i]) : logistic(x[i]);   // (a choice is by the exact ones)
         }
+      } else if (balance || a.bias) {
+        const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] *= inv;
       }
-      at = __shfl_sync(kAll, at, src);
-      val = __shfl_sync(kAll, val, src);
-      if (lane == (j & 31)) {
-        if (j < 32)
-          id[0] = at, picked[0] = val;
-        else
-          id[1] = at, picked[1] = val;
+      if (balance && live) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) mean[i] += s[i];
+      }
+      // the choice: by the logits, in whose order the scores are, or by score + bias; what lies behind the last expert is -inf
+      // and behind everything
+      uint32_t key[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = l * V + i;
+        float by = x[i];
+        if (a.bias && e < a.E && x[i] != -INFINITY) by = s[i] + __ldg(a.bias + e);
+        key[i] = order_key(by);
+      }
+      choose<G, V>(key, a.k, lane, scratch, scratch.picks[at]);
+    }
+    __syncwarp();
+    const int p = lane % P, at = lane / P;
+    const long long t = t0 + at;
+    const bool live = t < a.T;
+    const float top = live ? scratch.top[at] : 0.f, total = live ? scratch.total[at] : 1.f;
+    if (p == 0 && live) a.lse[t] = top == INFINITY ? top : top + logf(total);
+    const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
+    int id[S];
+    float w[S], logit[S], sum = 0.f, first = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < S; ++h) {
+      id[h] = -1, logit[h] = -INFINITY;
+      if (P * h >= a.k) continue;
+      if (p + P * h < a.k && live) {
+        const Pick pick = scratch.picks[at][p + P * h];
+        id[h] = pick.id;
+        logit[h] = a.bias ? logit_at(static_cast<const LT*>(a.logits) + t * a.E, pick.id) : key_value(pick.key);
+        first = fmaxf(first, logit[h]);
       }
     }
-    float w[2], sum = 0.f, first = -INFINITY;
+    __syncwarp();   // the scratch has been read
     if (!a.sigmoid && a.normalize) {   // from the largest of the picked, whatever the others sum to
-      first = warp_max(fmaxf(picked[0], picked[1]));
+      first = lanes_max<P>(first);
       if (first == -INFINITY) first = 0.f;
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool have = lane + 32 * h < a.k;
+    for (int h = 0; h < S; ++h) {
+      w[h] = 0.f;
+      if (P * h >= a.k) continue;
       if (a.sigmoid)
-        w[h] = have ? sigmoid(picked[h]) : 0.f;
+        w[h] = sigmoid(logit[h]);   // (0 where there is no pick)
       else
-        w[h] = have ? (a.normalize ? expf(picked[h] - first) : expf(picked[h] - top) * inv) : 0.f;
+        w[h] = a.normalize ? expf(logit[h] - first) : expf(logit[h] - top) * inv;
       sum += w[h];
     }
+    float by = 1.f;
     if (a.normalize) {
-      sum = warp_sum(sum);
-      const float by = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      w[0] *= by, w[1] *= by;
+      sum = lanes_sum<P>(sum);
+      by = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = lane + 32 * h;
-      if (j < a.k) {
+    for (int h = 0; h < S; ++h) {
+      const int j = p + P * h;
+      if (P * h >= a.k) continue;
+      if (j < a.k && live) {
         a.experts[t * a.k + j] = id[h];
-        a.weights[t * a.k + j] = w[h] * a.scale;
+        a.weights[t * a.k + j] = w[h] * by * a.scale;
         if (balance) atomicAdd(cnt + id[h], 1);   // whole numbers: any order
       }
     }
   }
   if (!balance) return;
+#pragma unroll
+  for (int o = G; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < V; ++i) mean[i] += __shfl_xor_sync(kAll, mean[i], o);
   float* sums = shared + a.E;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (lane * V + i < a.E) sums[warp * a.E + lane * V + i] = mean[i];
-  __syncthreads();
+  for (int w0 = kRouteWarps<V> - kSumRows; w0 >= 0; w0 -= kSumRows) {   // the last warps' first
+    if (warp >= w0 && warp < w0 + kSumRows && lane < G) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = l * V + i;
+        if (e < a.E) sums[(warp - w0) * a.E + e] = mean[i] + (warp + kSumRows < warps ? sums[(warp - w0) * a.E + e] : 0.f);
+      }
+    }
+    __syncthreads();
+  }
   int* part_cnt = reinterpret_cast<int*>(a.part + static_cast<long long>(gridDim.x) * a.E);
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRouteWarps; ++w) v += sums[w * a.E + e];
+    for (int w = 0; w < min(warps, kSumRows); ++w) v += sums[w * a.E + e];
     a.part[static_cast<long long>(blockIdx.x) * a.E + e] = v;
     part_cnt[static_cast<long long>(blockIdx.x) * a.E + e] = cnt[e];
   }
@@ -269,82 +397,99 @@ __global__ void __launch_bounds__(1024) route_join_kernel(const float* __restric
 //   mean score b / T, softmax:  s_i (b_i - sum s b) / T;   sigmoid: b_i s_i (1 - s_i) / T
 //   lse:           p_i dlse
 // u comes from the picked logits alone, so that it holds where s underflows.
-template <class LT, int V>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const RouteBwdArgs a) {
+template <class LT, int G, int V, bool MANY>
+__global__ void __launch_bounds__(32 * kRouteWarps<V>) route_bwd_kernel(const RouteBwdArgs a) {
+  constexpr int S = kSlots<G, G, V, MANY>;
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31, l = lane % G;
+  const long long step = static_cast<long long>(gridDim.x) * warps * (32 / G);
   const bool dense_softmax = !a.sigmoid && (!a.normalize || a.d_mean_score);
   const float inv_t = 1.f / static_cast<float>(a.T);
-  for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp; t < a.T; t += step) {
+  for (long long t0 = (static_cast<long long>(blockIdx.x) * warps + warp) * (32 / G); t0 < a.T; t0 += step) {
+    const long long t = min(t0 + lane / G, a.T - 1);   // (behind the last token: that one again, not stored)
     const LT* row = static_cast<const LT*>(a.logits) + t * a.E;
     float d[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.f;
-    // the picks: lane j's j-th and (j + 32)-th
-    int id[2];
-    float l[2], g[2], c[2];
+    int id[S];
+    float lg[S], g[S], c[S];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = lane + 32 * h;
+    for (int h = 0; h < S; ++h) {
+      const int j = l + G * h;
       const long long e = j < a.k ? __ldg(a.experts + t * a.k + j) : -1;
       const bool in = e >= 0 && e < a.E;   // an id outside is no expert's
       id[h] = in ? static_cast<int>(e) : -1;
-      l[h] = in ? logit_at(row, e) : -INFINITY;
+      lg[h] = in ? logit_at(row, e) : -INFINITY;
       g[h] = in ? __ldg(a.d_weights + t * a.k + j) * a.scale : 0.f;
+      c[h] = 0.f;
     }
     float x[V], p[V], top = 0.f, inv = 0.f;
-    if (dense_softmax || a.d_lse || (a.sigmoid && a.d_mean_score)) load_logits<LT, V>(row, a.E, lane, x);
+    if (dense_softmax || a.d_lse || (a.sigmoid && a.d_mean_score)) load_logits<LT, V>(row, a.E, l, x);
     if (dense_softmax || a.d_lse) {
-      const float total = exps<V>(x, p, top);
+      const float total = exps<G, V>(x, p, top);
       inv = total > 0.f || total != total ? 1.f / total : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) p[i] *= inv;
     }
     float q = 0.f;   // sum of s x (the gradients that reach the scores)
     if (a.normalize) {
-      float u[2], first = 0.f;
+      float first = 0.f, sum = 0.f, mean = 0.f;
       if (!a.sigmoid) {
-        first = warp_max(fmaxf(l[0], l[1]));
+        first = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < S; ++h) first = fmaxf(first, lg[h]);
+        first = lanes_max<G>(first);
         if (first == -INFINITY) first = 0.f;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) u[h] = id[h] < 0 ? 0.f : a.sigmoid ? sigmoid(l[h]) : expf(l[h] - first);
-      const float sum = warp_sum(u[0] + u[1]);
-      const float by = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-      u[0] *= by, u[1] *= by;
-      const float mean = warp_sum(u[0] * g[0] + u[1] * g[1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        c[h] = u[h] * (g[h] - mean);
-        if (a.sigmoid) c[h] *= sigmoid(-l[h]);
+      for (int h = 0; h < S; ++h) {
+        if (G * h >= a.k) break;
+        c[h] = id[h] < 0 ? 0.f : a.sigmoid ? sigmoid(lg[h]) : expf(lg[h] - first);
+        sum += c[h];
       }
-    } else if (a.sigmoid) {
+      sum = lanes_sum<G>(sum);
+      const float by = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) c[h] = id[h] < 0 ? 0.f : g[h] * sigmoid(l[h]) * sigmoid(-l[h]);
+      for (int h = 0; h < S; ++h) c[h] *= by, mean += c[h] * g[h];
+      mean = lanes_sum<G>(mean);
+#pragma unroll
+      for (int h = 0; h < S; ++h) {
+        if (G * h >= a.k) break;
+        c[h] *= g[h] - mean;
+        if (a.sigmoid) c[h] *= sigmoid(-lg[h]);
+      }
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) c[h] = id[h] < 0 ? 0.f : g[h] * (expf(l[h] - top) * inv);
-      q = warp_sum(c[0] + c[1]);
+      for (int h = 0; h < S; ++h) {
+        if (G * h >= a.k) break;
+        if (id[h] < 0) continue;
+        c[h] = a.sigmoid ? g[h] * sigmoid(lg[h]) * sigmoid(-lg[h]) : g[h] * (expf(lg[h] - top) * inv);
+        q += c[h];
+      }
+      q = a.sigmoid ? 0.f : lanes_sum<G>(q);
     }
     // to the lanes that hold the picks' logits, one after the other
-    for (int j = 0; j < a.k; ++j) {
-      const int e = __shfl_sync(kAll, j < 32 ? id[0] : id[1], j & 31);
-      const float v = __shfl_sync(kAll, j < 32 ? c[0] : c[1], j & 31);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e == lane * V + i) d[i] += v;
+    for (int h = 0; h < S; ++h) {
+#pragma unroll 4
+      for (int j = 0; j < G && G * h + j < a.k; ++j) {
+        const int e = __shfl_sync(kAll, id[h], j, G) - l * V;
+        const float v = __shfl_sync(kAll, c[h], j, G);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (e == i) d[i] += v;
+      }
     }
     float b[V];
     if (a.d_mean_score) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) b[i] = lane * V + i < a.E ? __ldg(a.d_mean_score + lane * V + i) * inv_t : 0.f;
+      for (int i = 0; i < V; ++i) b[i] = l * V + i < a.E ? __ldg(a.d_mean_score + l * V + i) * inv_t : 0.f;
       if (!a.sigmoid) {
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) m += p[i] * b[i];
-        q += warp_sum(m);
+        q += lanes_sum<G>(m);
       }
     }
     const float dl = a.d_lse ? __ldg(a.d_lse + t) : 0.f;
@@ -360,9 +505,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const Route
 #pragma unroll
       for (int i = 0; i < V; ++i) d[i] += p[i] * dl;
     }
-    LT* out = static_cast<LT*>(a.d_logits) + t * a.E + lane * V;
+    if (t0 + lane / G >= a.T) continue;
+    LT* out = static_cast<LT*>(a.d_logits) + t * a.E + l * V;
     constexpr int kVec = sizeof(LT) == 4 ? (V < 4 ? V : 4) : (V < 8 ? V : 8);
-    const int left = a.E - lane * V;
+    const int left = a.E - l * V;
     if (kVec > 1 && a.E % kVec == 0) {
 #pragma unroll
       for (int i = 0; i < V; i += kVec) {
@@ -394,43 +540,64 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_bwd_kernel(const Route
   }
 }
 
-int route_grid(long long T) {
-  const long long want = (T + kRouteWarps - 1) / kRouteWarps;
-  return static_cast<int>(want < 608 ? want : 608);
+// Warps to a block, and blocks: fewer warps where that spreads few tokens over more
+// SMs; at most 32 warps to each of 152 SMs.
+struct RouteGrid {
+  int warps, blocks;
+};
+RouteGrid route_grid(long long T, int E) {
+  const int each = E <= 32 ? 8 : 4;   // tokens of a warp's round
+  const long long all = (T + each - 1) / each;
+  const int warps = all <= 4 * 152 ? 1 : all <= 16 * 152 ? 4 : E <= 256 ? kRouteWarps<8> : kRouteWarps<16>;
+  const long long want = (all + warps - 1) / warps;
+  const long long most = 32 / warps * 152;
+  return {warps, static_cast<int>(want < most ? want : most)};
 }
 
+template <class LT, int G, int V>
+cudaError_t route_lanes(const RouteArgs& a, RouteGrid r, size_t smem, cudaStream_t st) {
+  const dim3 g(r.blocks), b(32 * r.warps);
+  return a.k <= (G < 8 ? G : 8) ? launch_dependent(route_kernel<LT, G, V, false>, g, b, smem, st, a)
+                                : launch_dependent(route_kernel<LT, G, V, true>, g, b, smem, st, a);
+}
 template <class LT>
-cudaError_t route_typed(const RouteArgs& a, int grid, size_t smem, cudaStream_t st) {
-  const dim3 g(grid), b(32 * kRouteWarps);
-  if (a.E <= 32) return launch_dependent(route_kernel<LT, 1>, g, b, smem, st, a);
-  if (a.E <= 64) return launch_dependent(route_kernel<LT, 2>, g, b, smem, st, a);
-  if (a.E <= 128) return launch_dependent(route_kernel<LT, 4>, g, b, smem, st, a);
-  if (a.E <= 256) return launch_dependent(route_kernel<LT, 8>, g, b, smem, st, a);
-  if (a.E <= 512) return launch_dependent(route_kernel<LT, 16>, g, b, smem, st, a);
-  return launch_dependent(route_kernel<LT, 32>, g, b, smem, st, a);
+cudaError_t route_typed(const RouteArgs& a, RouteGrid r, size_t smem, cudaStream_t st) {
+  if (a.E <= 32) return route_lanes<LT, 4, 8>(a, r, smem, st);
+  if (a.E <= 64) return route_lanes<LT, 8, 8>(a, r, smem, st);
+  if (a.E <= 128) return route_lanes<LT, 16, 8>(a, r, smem, st);
+  if (a.E <= 256) return route_lanes<LT, 32, 8>(a, r, smem, st);
+  if (a.E <= 512) return route_lanes<LT, 32, 16>(a, r, smem, st);
+  return route_lanes<LT, 32, 32>(a, r, smem, st);
 }
 
+template <class LT, int G, int V>
+cudaError_t route_bwd_lanes(const RouteBwdArgs& a, cudaStream_t st) {
+  // four warps to a block: a warp has few tokens, and small blocks spread and end evenly
+  const long long warps = (a.T + 32 / G - 1) / (32 / G), blocks = (warps + 3) / 4;
+  const dim3 g(static_cast<unsigned>(blocks < 8 * 152 ? blocks : 8 * 152)), b(128);
+  return a.k <= G ? launch_dependent(route_bwd_kernel<LT, G, V, false>, g, b, 0, st, a)
+                  : launch_dependent(route_bwd_kernel<LT, G, V, true>, g, b, 0, st, a);
+}
 template <class LT>
 cudaError_t route_bwd_typed(const RouteBwdArgs& a, cudaStream_t st) {
-  const dim3 g(route_grid(a.T) < 608 ? route_grid(a.T) : 1216), b(32 * kRouteWarps);
-  if (a.E <= 32) return launch_dependent(route_bwd_kernel<LT, 1>, g, b, 0, st, a);
-  if (a.E <= 64) return launch_dependent(route_bwd_kernel<LT, 2>, g, b, 0, st, a);
-  if (a.E <= 128) return launch_dependent(route_bwd_kernel<LT, 4>, g, b, 0, st, a);
-  if (a.E <= 256) return launch_dependent(route_bwd_kernel<LT, 8>, g, b, 0, st, a);
-  if (a.E <= 512) return launch_dependent(route_bwd_kernel<LT, 16>, g, b, 0, st, a);
-  return launch_dependent(route_bwd_kernel<LT, 32>, g, b, 0, st, a);
+  if (a.E <= 32) return route_bwd_lanes<LT, 4, 8>(a, st);
+  if (a.E <= 64) return route_bwd_lanes<LT, 8, 8>(a, st);
+  if (a.E <= 128) return route_bwd_lanes<LT, 16, 8>(a, st);
+  if (a.E <= 256) return route_bwd_lanes<LT, 32, 8>(a, st);
+  if (a.E <= 512) return route_bwd_lanes<LT, 32, 16>(a, st);
+  return route_bwd_lanes<LT, 32, 32>(a, st);
 }
 
 }  // namespace
 
-int route_blocks(long long T) { return route_grid(T); }
+int route_blocks(long long T, int E) { return route_grid(T, E).blocks; }
 
 cudaError_t launch_route(const RouteArgs& a, int f32, cudaStream_t st) {
-  const int grid = route_grid(a.T);
-  const size_t smem = a.counts ? static_cast<size_t>(1 + kRouteWarps) * a.E * sizeof(float) : 0;   // at most 36 KB
-  const cudaError_t err = grid == 0 ? cudaSuccess : f32 ? route_typed<float>(a, grid, smem, st) : route_typed<uint16_t>(a, grid, smem, st);
+  const RouteGrid r = route_grid(a.T, a.E);
+  const size_t smem = a.counts ? static_cast<size_t>(1 + kSumRows) * a.E * sizeof(float) : 0;   // at most 20 KB
+  const cudaError_t err = r.blocks == 0 ? cudaSuccess : f32 ? route_typed<float>(a, r, smem, st) : route_typed<uint16_t>(a, r, smem, st);
   if (err != cudaSuccess || !a.counts) return err;
-  return launch_dependent(route_join_kernel, dim3((a.E + 31) / 32), dim3(32, 32), 0, st, static_cast<const float*>(a.part), grid,
+  return launch_dependent(route_join_kernel, dim3((a.E + 31) / 32), dim3(32, 32), 0, st, static_cast<const float*>(a.part), r.blocks,
                           a.E, a.T > 0 ? 1.f / static_cast<float>(a.T) : 0.f, a.counts, a.mean_score);
 }
 

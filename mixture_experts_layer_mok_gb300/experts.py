@@ -10,6 +10,7 @@ contiguous tensors on the current GPU, 16-byte aligned.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -198,7 +199,10 @@ class Int4Weight:
     group: int
 
 
-def _int4_sizes(lib, matrices, N, K, group):
+@functools.lru_cache(maxsize=1024)
+def _int4_sizes(matrices, N, K, group):
+    """Elements of a weight's codes, scales and zeros."""
+    lib = _lib.load()
     n = [C.c_size_t() for _ in range(3)]
     st = lib.mok_int4_bytes(matrices, N, K, group, *(C.byref(v) for v in n))
     if st:
@@ -210,7 +214,7 @@ def _int4_new(shape, group, zeros, dev):
     if len(shape) not in (2, 3):
         raise ValueError(f"expected [N, K] or [matrices, N, K], got {tuple(shape)}")
     matrices = shape[0] if len(shape) == 3 else 1
-    nc, ns, nz = _int4_sizes(_lib.load(), matrices, shape[-2], shape[-1], group)
+    nc, ns, nz = _int4_sizes(matrices, shape[-2], shape[-1], group)
     w = Int4Weight(ops._empty((nc,), dtype=_U8, device=dev), ops._empty((ns,), dtype=_BF16, device=dev),
                    ops._empty((nz,), dtype=_U8, device=dev) if zeros else None, tuple(shape), group)
     return w, matrices
@@ -221,7 +225,7 @@ def _int4_args(weight):
     if not isinstance(weight, Int4Weight):
         raise ValueError(f"weight: expected an Int4Weight, got {type(weight).__name__}")
     matrices, (N, K) = weight.shape[0] if len(weight.shape) == 3 else 1, weight.shape[-2:]
-    nc, ns, nz = _int4_sizes(_lib.load(), matrices, N, K, weight.group)
+    nc, ns, nz = _int4_sizes(matrices, N, K, weight.group)
     at = _check(weight.codes, "weight.codes", (nc,), (_U8,))
     _check(weight.scales, "weight.scales", (ns,), (_BF16,), at)
     if weight.zeros is not None:
