@@ -20,6 +20,32 @@ from .ops import _BF16, _BF16_F32, _DTYPE, _F32, _U8, _check, _fail, _opt
 
 _I32, _I64 = torch.int32, torch.int64
 
+# A contiguous tensor on the current device.  A call here makes up to six, and a
+# small kernel takes less time than torch.empty's argument parsing does; the
+# allocation underneath is the same.
+_strided = getattr(getattr(torch._C._dynamo, "guards", None), "_empty_strided_cuda", None)
+
+
+def _new(shape, dtype, dev):
+    if _strided is None:
+        return ops._empty(shape, dtype=dtype, device=dev)
+    shape = tuple(shape)   # (not a torch.Size)
+    n = len(shape)
+    if n == 1:
+        return _strided(shape, (1,), dtype)
+    if n == 2:
+        return _strided(shape, (max(shape[1], 1), 1), dtype)
+    stride, at = [], 1
+    for size in shape[::-1]:
+        stride.append(at)
+        at *= max(size, 1)
+    return _strided(shape, tuple(stride[::-1]), dtype)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace(name, *sizes):
+    return getattr(_lib.load(), name)(*sizes)
+
 
 # ---------------------------------------------------------------- router
 @dataclass
@@ -59,16 +85,16 @@ def route(logits, k: int, score: str = "softmax", normalize: bool = True, scale:
     if bias is not None:
         _check(bias, "bias", (E,), (_F32,), at)
     lib, dev = _lib.load(), logits.device
-    experts = ops._empty((*lead, k), dtype=_I64, device=dev)
-    weights = ops._empty((*lead, k), dtype=_F32, device=dev)
-    lse = ops._empty(lead, dtype=_F32, device=dev)
+    experts = _new((*lead, k), _I64, dev)
+    weights = _new((*lead, k), _F32, dev)
+    lse = _new(lead, _F32, dev)
     counts = mean = ws = None
     nbytes = 0
     if balance:
-        counts = ops._empty((E,), dtype=_I32, device=dev)
-        mean = ops._empty((E,), dtype=_F32, device=dev)
-        nbytes = lib.mok_route_workspace_bytes(T, E)
-        ws = ops._empty((nbytes,), dtype=_U8, device=dev)
+        counts = _new((E,), _I32, dev)
+        mean = _new((E,), _F32, dev)
+        nbytes = _workspace("mok_route_workspace_bytes", T, E)
+        ws = _new((nbytes,), _U8, dev)
     st = lib.mok_route(logits.data_ptr(), _DTYPE[logits.dtype], _opt(bias), T, E, k, s, bool(normalize), scale, experts.data_ptr(),
                        weights.data_ptr(), lse.data_ptr(), _opt(counts), _opt(mean), _opt(ws), nbytes, ops._raw_stream(at))
     if st:
@@ -94,7 +120,7 @@ def route_backward(d_weights, logits, experts, score: str = "softmax", normalize
         _check(d_lse, "d_lse", lead, (_F32,), at)
     if d_mean_score is not None:
         _check(d_mean_score, "d_mean_score", (E,), (_F32,), at)
-    out = torch.empty_like(logits)
+    out = _new(logits.shape, logits.dtype, logits.device)
     st = _lib.load().mok_route_bwd(d_weights.data_ptr(), logits.data_ptr(), _DTYPE[logits.dtype], experts.data_ptr(), _opt(d_lse),
                                    _opt(d_mean_score), T, E, k, s, bool(normalize), scale, out.data_ptr(), ops._raw_stream(at))
     if st:
@@ -140,8 +166,8 @@ def grouped_linear(x, weight, counts, bias=None, activation: str = "none", out_d
     if bias is not None:
         _check(bias, "bias", (E, N), _BF16_F32, at)
         bias_type = _DTYPE[bias.dtype]
-    y = ops._empty((M, N), dtype=out_dtype, device=x.device)
-    z = ops._empty((M, N), dtype=_BF16, device=x.device) if save_z else None
+    y = _new((M, N), out_dtype, x.device)
+    z = _new((M, N), _BF16, x.device) if save_z else None
     st = _lib.load().mok_grouped_linear(x.data_ptr(), weight.data_ptr(), counts.data_ptr(), _opt(bias), bias_type, act, M, E, N, K,
                                         y.data_ptr(), out_type, _opt(z), ops._raw_stream(at))
     if st:
@@ -164,20 +190,20 @@ def grouped_linear_backward(dy, x, weight, counts, z=None, activation: str = "no
     if act:
         _check(z, "z", (M, N), dev=at)
     lib, dev, dy_type = _lib.load(), x.device, _DTYPE[dy.dtype]
-    nbytes = lib.mok_grouped_linear_bwd_workspace_bytes(M, E, N, act, dy_type, bool(bias))
+    nbytes = _workspace("mok_grouped_linear_bwd_workspace_bytes", M, E, N, act, dy_type, bool(bias))
     if nbytes == 0:
         raise ValueError("shape outside the kernels' contract")
     out = {}
     for name in need:
         if name == "dx":
-            out[name] = torch.empty_like(x)
+            out[name] = _new((M, K), _BF16, dev)
         elif name == "d_weight":
-            out[name] = torch.empty_like(weight)
+            out[name] = _new((E, N, K), _BF16, dev)
         else:
             raise ValueError("need names dx and d_weight")
     if bias:
-        out["d_bias"] = ops._empty((E, N), dtype=_F32, device=dev)
-    ws = ops._empty((nbytes,), dtype=_U8, device=dev)
+        out["d_bias"] = _new((E, N), _F32, dev)
+    ws = _new((nbytes,), _U8, dev)
     st = lib.mok_grouped_linear_bwd(dy.data_ptr(), dy_type, x.data_ptr(), weight.data_ptr(), counts.data_ptr(),
                                     z.data_ptr() if act else None, act, M, E, N, K, _opt(out.get("dx")), _opt(out.get("d_weight")),
                                     _opt(out.get("d_bias")), ws.data_ptr(), nbytes, ops._raw_stream(at))
@@ -215,8 +241,8 @@ def _int4_new(shape, group, zeros, dev):
         raise ValueError(f"expected [N, K] or [matrices, N, K], got {tuple(shape)}")
     matrices = shape[0] if len(shape) == 3 else 1
     nc, ns, nz = _int4_sizes(matrices, shape[-2], shape[-1], group)
-    w = Int4Weight(ops._empty((nc,), dtype=_U8, device=dev), ops._empty((ns,), dtype=_BF16, device=dev),
-                   ops._empty((nz,), dtype=_U8, device=dev) if zeros else None, tuple(shape), group)
+    w = Int4Weight(_new((nc,), _U8, dev), _new((ns,), _BF16, dev),
+                   _new((nz,), _U8, dev) if zeros else None, tuple(shape), group)
     return w, matrices
 
 
@@ -281,7 +307,7 @@ def int4_dequantize(weight: Int4Weight, stream=None) -> torch.Tensor:
         with torch.cuda.stream(stream):
             return int4_dequantize(weight)
     matrices, N, K, at = _int4_args(weight)
-    out = ops._empty(weight.shape, dtype=_BF16, device=weight.codes.device)
+    out = _new(weight.shape, _BF16, weight.codes.device)
     st = _lib.load().mok_int4_dequantize(weight.codes.data_ptr(), weight.scales.data_ptr(), _opt(weight.zeros), matrices, N, K,
                                          weight.group, out.data_ptr(), ops._raw_stream(at))
     if st:
@@ -330,7 +356,7 @@ def int4_linear(x, weight: Int4Weight, bias=None, activation: str = "none", expe
     if rows > _lib.MOK_INT4_MAX_ROWS:
         raise ValueError(f"int4_linear is for up to {_lib.MOK_INT4_MAX_ROWS} rows of y, got {rows}: take int4_dequantize with linear "
                          "or grouped_linear")
-    y = ops._empty((*lead, N), dtype=out_dtype, device=x.device)
+    y = _new((*lead, N), out_dtype, x.device)
     st = _lib.load().mok_int4_linear(x.data_ptr(), weight.codes.data_ptr(), weight.scales.data_ptr(), _opt(weight.zeros), matrices, N,
                                      K, weight.group, _opt(experts), rows, each, _opt(bias), bias_type, act, y.data_ptr(), out_type,
                                      ops._raw_stream(at))

@@ -143,6 +143,8 @@ def _calls():
 @pytest.mark.parametrize("name", sorted(_calls()))
 def test_operators_refuse_other_devices(stub, monkeypatch, name):  # noqa: F811
     monkeypatch.setattr(experts, "_int4_sizes", lambda *a: (64, 64, 64))
+    monkeypatch.setattr(experts, "_workspace", lambda *a: 4096)
+    monkeypatch.setattr(experts, "_new", lambda shape, dtype, dev: torch.zeros(shape, dtype=dtype))
     call, args = _calls()[name]
     make = lambda index, **other: [on(other.get(f"a{i}", index), *s, dtype=d)  # noqa: E731
                                    for i, (s, d) in enumerate(args)]
