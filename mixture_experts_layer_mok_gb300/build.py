@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmok.so")
 SOURCES = ["api.cu", "kernels.cu", "gemm_fwd.cu", "gemm_mx.cu", "gemm_pair.cu", "gemm_bwd_a.cu", "gemm_bwd_b.cu",
            "api_ops.cu", "norm.cu", "adamw.cu", "linear.cu",
-           "api_experts.cu", "route.cu", "grouped.cu", "int4.cu"]
+           "api_experts.cu", "route.cu", "grouped.cu", "int4.cu", "int4_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

@@ -360,6 +360,9 @@ mok_status_t mok_int4_linear(const uint16_t* x, const uint8_t* codes, const uint
   a.act = activation;
   a.out_f32 = y_dtype == MOK_DTYPE_F32;
   a.bias_f32 = bias_dtype == MOK_DTYPE_F32;
+  // more than 8 rows of x and a matrix of some size: the tensor core with codes in TMEM.  Measured, that and mma.sync: 12 rows times
+  // 2048 x 2048 5.0 and 4.2 us, 7168 x 2048 7.4 and 7.5, 16384 x 8192 27 and 35; 64 rows 8.9 and 6.5, 12.7 and 18.6, 39 and 108
+  if (!experts && rows > 8 && static_cast<int64_t>(N) * K > 1ll << 23) return run_int4_tc(a, static_cast<cudaStream_t>(stream));
   MOK_CUDA(launch_int4_linear(a, sms, static_cast<cudaStream_t>(stream)));
   return MOK_OK;
 }

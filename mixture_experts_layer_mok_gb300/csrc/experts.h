@@ -77,6 +77,8 @@ cudaError_t launch_int4_pack(const uint8_t* q, const uint16_t* qs, const uint8_t
 cudaError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, const Int4Shape& s,
                                    uint16_t* out, cudaStream_t st);
 cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t st);
+// The same for one matrix, by the tensor core of int4_tc.cu.
+mok_status_t run_int4_tc(const Int4LinearArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- products grouped by expert
 constexpr int kMaxGroups = MOK_GROUPED_MAX_E;

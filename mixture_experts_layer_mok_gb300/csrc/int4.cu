@@ -501,12 +501,12 @@ __global__ void __launch_bounds__(32 * kInt4Warps, COLS <= 8 ? 4 : 1) int4_split
 }
 
 // ---- warps that share x: many rows of w
-// grid {groups of 16 row tiles, rows of x in steps of 8 NG}, one matrix.  A warp
-// makes 32 rows of w over all of K; the block's warps go through K together, so
-// that a block of x is fetched once for 256 rows of w.
-template <int NG, int GPB, bool ZEROS>
+// grid {groups of 16 row tiles}, one matrix, up to 8 rows of x (more of them are for
+// int4_tc.cu).  A warp makes 32 rows of w over all of K; the block's warps go
+// through K together, so that a block of x is fetched once for 256 rows of w.
+template <int GPB, bool ZEROS>
 struct Int4WideCfg {
-  static constexpr int kCols = 8 * NG, kRowTiles = 2 * kInt4Warps;
+  static constexpr int kCols = 8, kRowTiles = 2 * kInt4Warps;
   static constexpr int kStages = 3;
   static constexpr int kTile = Int4Chunk<GPB, ZEROS, 1>::kBytes;
   static constexpr int kStageBytes = kRowTiles * kTile + kCols * kXColumn<1>;
@@ -515,9 +515,9 @@ struct Int4WideCfg {
   static_assert(kSmemBytes <= 112 * 1024, "two blocks to an SM");
 };
 
-template <int NG, int GPB, bool ZEROS>
+template <int GPB, bool ZEROS>
 __global__ void __launch_bounds__(32 * kInt4Warps, 2) int4_wide_kernel(const Int4LinearArgs a) {
-  using C = Int4WideCfg<NG, GPB, ZEROS>;
+  using C = Int4WideCfg<GPB, ZEROS>;
   constexpr int kCols = C::kCols, D = C::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -525,15 +525,13 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 2) int4_wide_kernel(const Int
   griddep_launch_dependents();
   const int nb = a.w.blocks(), row_tiles = static_cast<int>(a.w.row_tiles());
   const int rt = static_cast<int>(blockIdx.x) * C::kRowTiles + 2 * warp;   // this warp's first row tile
-  const int c0 = static_cast<int>(blockIdx.y) * kCols, cols = min(kCols, a.rows - c0);
+  const int cols = a.rows;
   Int4Source<GPB, ZEROS, 1> src[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) src[r].start(a, static_cast<long long>(min(rt + r, row_tiles - 1)) * nb, lane);
-  // this thread's pieces of x: columns tid / 16 and + 16 (those without a row are not stored)
+  // this thread's piece of x: column tid / 16, where there is one
   const int p = threadIdx.x & 15, col = threadIdx.x >> 4;
-  const uint16_t* xp[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) xp[i] = a.x + static_cast<long long>(c0 + min(col + 16 * i, cols - 1)) * a.w.K;
+  const uint16_t* const xp = col < cols ? a.x + static_cast<long long>(col) * a.w.K : nullptr;
   int ahead = 0;
   const auto fetch = [&]() {
     if (ahead < nb) {
@@ -541,45 +539,34 @@ __global__ void __launch_bounds__(32 * kInt4Warps, 2) int4_wide_kernel(const Int
 #pragma unroll
       for (int r = 0; r < 2; ++r) src[r].fetch(st + (2 * warp + r) * C::kTile, 1, 1, lane);
       const int k = ahead * kInt4Block + p * 8, from = k < a.w.K ? k : 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (col + 16 * i < cols) cp_async16(st + C::kRowTiles * C::kTile + (col + 16 * i) * kXColumn<1> + p * 16, xp[i] + from, k < a.w.K ? 16u : 0u);
+      if (xp) cp_async16(st + C::kRowTiles * C::kTile + col * kXColumn<1> + p * 16, xp + from, k < a.w.K ? 16u : 0u);
       ++ahead;
     }
     cp_async_commit();
   };
 #pragma unroll
   for (int i = 0; i < D - 1; ++i) fetch();
-  float acc[2][NG][4];
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int c = 0; c < NG; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][c][i] = 0.f;
+  float acc[2][1][4] = {};
 #pragma unroll 1
   for (int kb = 0; kb < nb; ++kb) {
     cp_async_wait<D - 2>();
     __syncthreads();   // every thread's copies are there, and the stage that is filled next has been read
     fetch();
     const uint8_t* st = smem + kb % D * C::kStageBytes;
-    block_products<kCols, NG, 2, GPB, ZEROS, 1>(acc, st + 2 * warp * C::kTile, C::kTile, st + C::kRowTiles * C::kTile, 0, lane);
+    block_products<kCols, 1, 2, GPB, ZEROS, 1>(acc, st + 2 * warp * C::kTile, C::kTile, st + C::kRowTiles * C::kTile, 0, lane);
   }
   cp_async_wait<0>();
   __syncthreads();
   float* out = reinterpret_cast<float*>(smem) + warp * kCols * 33;   // [kCols][33] of this warp's 32 rows of w
 #pragma unroll
   for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int c = 0; c < NG; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) out[(c * 8 + 2 * t + (i & 1)) * 33 + r * 16 + g + 8 * (i >> 1)] = acc[r][c][i];
+    for (int i = 0; i < 4; ++i) out[(2 * t + (i & 1)) * 33 + r * 16 + g + 8 * (i >> 1)] = acc[r][0][i];
   __syncwarp();
   const int n = rt * kInt4Rows + lane;
   if (n >= a.w.N) return;
   const float bias = int4_bias(a, n);
 #pragma unroll 4
-  for (int c = 0; c < cols; ++c) store_out(a, c0 + c, n, act_of(out[c * 33 + lane] + bias, a.act));
+  for (int c = 0; c < cols; ++c) store_out(a, c, n, act_of(out[c * 33 + lane] + bias, a.act));
 }
 
 // The kernels' shared memory is above the default limit, which is raised once per
@@ -613,21 +600,22 @@ cudaError_t split_launch(const Int4LinearArgs& a, int num_sms, cudaStream_t st) 
   const int warps = static_cast<long long>(x) * y * 4 < 10ll * num_sms ? 8 : 4;
   return launch_dependent(kern, dim3(x, y), dim3(32 * warps), warps * C::kWarpBytes, st, a);
 }
-template <int NG, int GPB, bool ZEROS>
+template <int GPB, bool ZEROS>
 cudaError_t wide_launch(const Int4LinearArgs& a, cudaStream_t st) {
-  using C = Int4WideCfg<NG, GPB, ZEROS>;
-  auto kern = int4_wide_kernel<NG, GPB, ZEROS>;
+  using C = Int4WideCfg<GPB, ZEROS>;
+  auto kern = int4_wide_kernel<GPB, ZEROS>;
   static SmemLimit limit;
   const cudaError_t err = limit.raise(kern, C::kSmemBytes);
   if (err != cudaSuccess) return err;
   const unsigned x = static_cast<unsigned>((a.w.row_tiles() + C::kRowTiles - 1) / C::kRowTiles);
-  return launch_dependent(kern, dim3(x, (a.rows + C::kCols - 1) / C::kCols), dim3(32 * kInt4Warps), C::kSmemBytes, st, a);
+  return launch_dependent(kern, dim3(x), dim3(32 * kInt4Warps), C::kSmemBytes, st, a);
 }
 
 // COLS columns of x at a time; wide: shared x.
 template <int COLS, int GPB, bool ZEROS>
 cudaError_t int4_kind(const Int4LinearArgs& a, bool wide, int num_sms, cudaStream_t st) {
-  if (wide) return wide_launch<(COLS < 8 ? 1 : COLS / 8), GPB, ZEROS>(a, st);
+  if constexpr (COLS <= 8)
+    if (wide) return wide_launch<GPB, ZEROS>(a, st);
   constexpr int R = COLS > 8 ? 2 : 1;   // two row tiles to a block halve the bytes of x
   return a.experts ? split_launch<COLS, R, GPB, ZEROS, true>(a, num_sms, st) : split_launch<COLS, R, GPB, ZEROS, false>(a, num_sms, st);
 }
@@ -666,7 +654,7 @@ cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_
   const double per = a.experts ? static_cast<double>(a.rows) / static_cast<double>(a.w.matrices) : static_cast<double>(a.rows);
   const int cols = per > 16 ? 32 : per > 8 ? 16 : per > 2 ? 8 : 2;
   // rows of w enough for 256 to a block
-  const bool wide = !a.experts && a.w.row_tiles() / (2 * kInt4Warps) * ((a.rows + cols - 1) / cols) >= num_sms;
+  const bool wide = !a.experts && a.rows <= 8 && a.w.row_tiles() / (2 * kInt4Warps) >= num_sms;
   if (cols == 32) return int4_group<32>(a, wide, num_sms, st);
   if (cols == 16) return int4_group<16>(a, wide, num_sms, st);
   if (cols == 8) return int4_group<8>(a, wide, num_sms, st);
