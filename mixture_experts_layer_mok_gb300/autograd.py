@@ -280,7 +280,8 @@ def route(logits, k: int, score: str = "softmax", normalize: bool = True, scale:
 
 
 class MoKRouter(torch.nn.Module):
-    """The router: logits in 32 bits by the projection operator, and the choice.
+    """The router: logits in 32 bits by the projection operator (E a multiple of
+    8), and the choice.
     Its ``Routing`` feeds ``MoKLayer``, or ``grouped_linear`` by its counts."""
 
     def __init__(self, H: int, E: int, k: int, score: str = "softmax", normalize: bool = True, scale: float = 1.0,

@@ -66,6 +66,7 @@ struct Int4LinearArgs {
   void* y;                   // [rows][N]
   int rows;                  // of y
   int x_div;                 // row r of y reads row r / x_div of x
+  int by_expert;             // (the launch's: a block to an expert, not to a row)
   int act;
   int out_f32, bias_f32;
   int* status;

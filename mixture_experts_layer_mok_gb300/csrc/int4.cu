@@ -339,11 +339,11 @@ __device__ __forceinline__ void store_out(const Int4LinearArgs& a, long long row
 
 // ---- warps that share K: few rows of w to a block
 // grid {groups of R row tiles, rows of x in steps of COLS; with experts: rows of
-// y}, 4 or 8 warps.  A block makes 16 R outputs of up to COLS rows; each warp
+// y, or the experts where they are fewer}, 4 or 8 warps.  A block makes 16 R outputs of up to COLS rows; each warp
 // takes a part of K through stages of its own, and their sums are added in order.
-// With experts the block of a row whose expert no earlier row has serves all
-// rows of that expert, and the others' blocks end at once: an expert's weights
-// are read once.
+// With experts, the block of an expert, or of a row whose expert no earlier row
+// has, serves all rows of that expert, and the others end at once: an expert's
+// weights are read once for COLS of its rows.
 template <int COLS, int R, int GPB, bool ZEROS>
 struct Int4SplitCfg {
   static constexpr int kCols = COLS, kRows = 16 * R, kGroups = COLS < 8 ? 1 : COLS / 8;
@@ -373,17 +373,26 @@ __global__ void __launch_bounds__(32 * kInt4Warps, COLS <= 8 ? 4 : 1) int4_split
   const bool few = EXPERTS && a.rows <= 32;
   if constexpr (EXPERTS) {
     const int r = blockIdx.y;
-    const long long id = few ? (lane < a.rows ? __ldg(a.experts + lane) : -2) : __ldg(a.experts + r);
-    matrix = few ? __shfl_sync(0xffffffffu, id, r) : id;
-    if (matrix < 0 || matrix >= a.w.matrices) {   // no expert: zeros; any id but -1 is an error besides
+    const long long id = few ? (lane < a.rows ? __ldg(a.experts + lane) : -2) : a.by_expert ? 0 : __ldg(a.experts + r);
+    matrix = a.by_expert ? r : few ? __shfl_sync(0xffffffffu, id, r) : id;
+    if (a.by_expert) {
+      if (r == 0) {   // rows of no expert: zeros; any id but -1 is an error besides
+        for (int i = warp; i < a.rows; i += blockDim.x >> 5) {
+          const long long e = __ldg(a.experts + i);
+          if (e >= 0 && e < a.w.matrices) continue;
+          if (e != -1 && lane == 0 && blockIdx.x == 0 && a.status) atomicCAS(a.status, 0, MOK_ERR_INDEX);
+          for (int n = n0 + lane; n < min(n0 + kRows, a.w.N); n += 32) store_out(a, i, n, 0.f);
+        }
+      }
+    } else if (matrix < 0 || matrix >= a.w.matrices) {
       if (matrix != -1 && threadIdx.x == 0 && blockIdx.x == 0 && a.status) atomicCAS(a.status, 0, MOK_ERR_INDEX);
       for (int n = n0 + threadIdx.x; n < min(n0 + kRows, a.w.N); n += blockDim.x) store_out(a, r, n, 0.f);
       return;
     }
     if (few) {   // each warp for itself
       same = __ballot_sync(0xffffffffu, id == matrix);
-      if (same & ((1u << r) - 1u)) return;
-    } else {
+      if (!a.by_expert && (same & ((1u << r) - 1u))) return;
+    } else if (!a.by_expert) {
       int earlier = 0;
       for (int i = threadIdx.x; i < r; i += blockDim.x) earlier |= __ldg(a.experts + i) == matrix;
       if (__syncthreads_or(earlier)) return;
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(32 * kInt4Warps, COLS <= 8 ? 4 : 1) int4_split
   // this warp's blocks of K
   const int each = nb / warps, more = nb - each * warps;
   const int kb0 = each * warp + min(warp, more), kb1 = kb0 + each + (warp < more ? 1 : 0);
-  int next = EXPERTS ? blockIdx.y : 0;
+  int next = EXPERTS && !a.by_expert ? blockIdx.y : 0;
   for (;;) {
     // the rows of y that this pass makes
     int cols;
@@ -594,7 +603,7 @@ cudaError_t split_launch(const Int4LinearArgs& a, int num_sms, cudaStream_t st) 
   const cudaError_t err = limit.raise(kern, kInt4Warps * C::kWarpBytes);
   if (err != cudaSuccess) return err;
   const unsigned x = static_cast<unsigned>((a.w.row_tiles() + R - 1) / R);
-  const unsigned y = EXPERTS ? a.rows : (a.rows + C::kCols - 1) / C::kCols;
+  const unsigned y = !EXPERTS ? (a.rows + C::kCols - 1) / C::kCols : a.by_expert ? static_cast<unsigned>(a.w.matrices) : a.rows;
   // 4 warps to a block, 8 where an SM would have fewer than ten warps.  Measured with 2, 4 and 8: one row times 7168 x 2048
   // 4.2, 3.5 and 4.1 us, 8 experts of 2048 x 7168 20.4, 17.7 and 19.5.
   const int warps = static_cast<long long>(x) * y * 4 < 10ll * num_sms ? 8 : 4;
@@ -649,12 +658,15 @@ cudaError_t launch_int4_dequantize(const uint8_t* codes, const uint16_t* scales,
   return launch_dependent(int4_dequantize_kernel, tile_grid(s.tiles()), dim3(256), 0, st, codes, scales, zeros, s, out);
 }
 
-cudaError_t launch_int4_linear(const Int4LinearArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_int4_linear(const Int4LinearArgs& args, int num_sms, cudaStream_t st) {
+  Int4LinearArgs a = args;
+  a.by_expert = a.experts && a.w.matrices < a.rows;
   // columns of the product: what there are, or with experts the rows that one has on average
   const double per = a.experts ? static_cast<double>(a.rows) / static_cast<double>(a.w.matrices) : static_cast<double>(a.rows);
-  const int cols = per > 16 ? 32 : per > 8 ? 16 : per > 2 ? 8 : 2;
-  // rows of w enough for 256 to a block
-  const bool wide = !a.experts && a.rows <= 8 && a.w.row_tiles() / (2 * kInt4Warps) >= num_sms;
+  const int cols = per > (a.experts ? 10 : 16) ? 32 : per > (a.experts ? 5 : 8) ? 16 : per > (a.experts ? 1.25 : 2) ? 8 : 2;
+  // rows of w for two blocks of 256 to an SM.  Measured, that and the other: one row times 40960 x 4096 33 and 22 us, times 152064 x
+  // 4096 64 and 66; eight rows 34 and 30, 66 and 101
+  const bool wide = !a.experts && a.rows <= 8 && a.w.row_tiles() / (2 * kInt4Warps) >= 2 * num_sms;
   if (cols == 32) return int4_group<32>(a, wide, num_sms, st);
   if (cols == 16) return int4_group<16>(a, wide, num_sms, st);
   if (cols == 8) return int4_group<8>(a, wide, num_sms, st);

@@ -3,8 +3,8 @@
 //
 // G lanes to a token, 32 / G tokens to a warp at a time; lane l of a token holds
 // the V consecutive logits from l V on, so that the lowest lane of several with the
-// same largest value holds the lowest index.  V is 8 up to 256 experts: fewer
-// lanes to a token of few experts, because a token's cost is in its reductions.
+// same largest value holds the lowest index.  Fewer lanes to a token of up to 64
+// experts, because a token's cost is in its reductions.
 //
 // The choice.  A whole warp to a token: the k-th largest of the lanes' largest
 // bounds the choice from below; the few logits that reach it (about k + 4 of 256
@@ -227,9 +227,9 @@ __device__ __forceinline__ void choose(uint32_t (&key)[V], int k, int lane, Scra
 // A round of a warp is 32 / P tokens: first G lanes to each in G / P passes, which
 // leave the picks and the sums in shared memory, then P lanes to each, which make
 // the weights of all of them at a time.
-template <class LT, int G, int V, bool MANY>
+template <class LT, int G, int V, int P, bool MANY>
 __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteArgs a) {
-  constexpr int P = G < 8 ? G : 8, S = kSlots<P, G, V, MANY>;
+  constexpr int S = kSlots<P, G, V, MANY>;
   using Scratch = RouteScratch<P, V, G>;
   extern __shared__ float shared[];   // with counts: [E] counts, then [kSumRows][E] sums of scores
   __shared__ __align__(16) Scratch scratches[kRouteWarps<V>];
@@ -540,31 +540,41 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_bwd_kernel(const Ro
   }
 }
 
-// Warps to a block, and blocks: fewer warps where that spreads few tokens over more
-// SMs; at most 32 warps to each of 152 SMs.
+// Lanes that make a token's weights, warps to a block, and blocks.  A token to a
+// round where that gives no SM more than 16 warps (1024 tokens among 256 experts
+// 6.0 us with four), fewer warps to a block where that spreads few rounds over
+// more SMs; at most 32 warps to each of 152 SMs.
 struct RouteGrid {
+  bool alone;   // a token to a round (of more than 64 experts)
   int warps, blocks;
 };
 RouteGrid route_grid(long long T, int E) {
-  const int each = E <= 32 ? 8 : 4;   // tokens of a warp's round
+  const bool alone = E > 64 && T <= 16 * 152;
+  const int each = alone ? 1 : E <= 32 ? 8 : 4;   // tokens of a round
   const long long all = (T + each - 1) / each;
   const int warps = all <= 4 * 152 ? 1 : all <= 16 * 152 ? 4 : E <= 256 ? kRouteWarps<8> : kRouteWarps<16>;
   const long long want = (all + warps - 1) / warps;
   const long long most = 32 / warps * 152;
-  return {warps, static_cast<int>(want < most ? want : most)};
+  return {alone, warps, static_cast<int>(want < most ? want : most)};
 }
 
+template <class LT, int G, int V, int P>
+cudaError_t route_picks(const RouteArgs& a, RouteGrid r, size_t smem, cudaStream_t st) {
+  const dim3 g(r.blocks), b(32 * r.warps);
+  return a.k <= P ? launch_dependent(route_kernel<LT, G, V, P, false>, g, b, smem, st, a)
+                  : launch_dependent(route_kernel<LT, G, V, P, true>, g, b, smem, st, a);
+}
 template <class LT, int G, int V>
 cudaError_t route_lanes(const RouteArgs& a, RouteGrid r, size_t smem, cudaStream_t st) {
-  const dim3 g(r.blocks), b(32 * r.warps);
-  return a.k <= (G < 8 ? G : 8) ? launch_dependent(route_kernel<LT, G, V, false>, g, b, smem, st, a)
-                                : launch_dependent(route_kernel<LT, G, V, true>, g, b, smem, st, a);
+  if constexpr (G == 32)
+    if (r.alone) return route_picks<LT, G, V, 32>(a, r, smem, st);
+  return route_picks<LT, G, V, (G < 8 ? G : 8)>(a, r, smem, st);
 }
 template <class LT>
 cudaError_t route_typed(const RouteArgs& a, RouteGrid r, size_t smem, cudaStream_t st) {
   if (a.E <= 32) return route_lanes<LT, 4, 8>(a, r, smem, st);
   if (a.E <= 64) return route_lanes<LT, 8, 8>(a, r, smem, st);
-  if (a.E <= 128) return route_lanes<LT, 16, 8>(a, r, smem, st);
+  if (a.E <= 128) return route_lanes<LT, 32, 4>(a, r, smem, st);   // (16 lanes and 8 logits each, largest by largest, took 14 us for 16384 tokens)
   if (a.E <= 256) return route_lanes<LT, 32, 8>(a, r, smem, st);
   if (a.E <= 512) return route_lanes<LT, 32, 16>(a, r, smem, st);
   return route_lanes<LT, 32, 32>(a, r, smem, st);

@@ -92,8 +92,9 @@ def _check(y, z64, size, act, K, group, out):
 ONE = [(1, 8, 32, 32), (1, 7168, 2048, 128), (1, 1000, 4096, 64), (2, 17, 96, 32), (3, 1, 128, 64), (7, 264, 160, 32), (8, 513, 1024, 128),
        (9, 40, 384, 128), (16, 2056, 512, 64), (17, 136, 7168, 128), (31, 33, 224, 32), (32, 4096, 256, 128), (33, 100, 640, 64),
        (64, 520, 1152, 128), (100, 24, 192, 64), (1000, 72, 320, 32)]
-# rows of w enough for the variant whose warps share x
-WIDE = [(1, 39169, 96, 32), (5, 39168, 640, 128), (12, 41000, 192, 64), (16, 39200, 1024, 32), (31, 40007, 704, 64), (33, 30000, 128, 128),
+# rows of w enough for the variant whose warps share x, and many rows of both
+WIDE = [(1, 39169, 96, 32), (5, 39168, 640, 128), (1, 77824, 96, 32), (6, 78001, 320, 64), (3, 77840, 256, 128), (8, 80000, 160, 32),
+        (130, 4200, 2048, 128), (9, 30001, 320, 64), (33, 8200, 1056, 32), (20, 1100, 8192, 128), (64, 520, 16384, 32), (12, 41000, 192, 64), (16, 39200, 1024, 32), (31, 40007, 704, 64), (33, 30000, 128, 128),
         (64, 39168, 256, 64)]
 
 
@@ -116,7 +117,8 @@ def test_one_matrix(rows, N, K, group, zeros, bias, act, out):
 
 
 EXPERTS = [(1, 1, 2, 8, 32, 32), (1, 8, 256, 72, 256, 32), (3, 2, 5, 40, 384, 128), (16, 6, 64, 136, 320, 64), (64, 8, 128, 24, 256, 128),
-           (40, 3, 4, 100, 512, 64), (200, 1, 2, 520, 128, 128), (1, 6, 8, 2056, 2048, 128)]
+           (40, 3, 4, 100, 512, 64), (200, 1, 2, 520, 128, 128), (1, 6, 8, 2056, 2048, 128), (4, 4, 8, 72, 256, 64), (12, 8, 9, 33, 320, 32),
+           (30, 8, 40, 136, 192, 64), (100, 8, 100, 17, 256, 128)]
 
 
 @pytest.mark.parametrize("rows,k,E,N,K,group", EXPERTS)
@@ -146,15 +148,16 @@ def test_experts(rows, k, E, N, K, group, zeros, bias, act, out):
     assert torch.equal(m.int4_linear(each, w, bias=b, activation=act, experts=ids, out_dtype=out), y)
 
 
-def test_ids_out_of_range_give_zeros_and_the_status():
+@pytest.mark.parametrize("rows", [1, 3, 30])
+def test_ids_out_of_range_give_zeros_and_the_status(rows):
     m = mok()
     from mixture_experts_layer_mok_gb300 import _lib
 
     g = _gen(3)
     codes, scales, zero, values = _weight(g, (4,), 24, 128, 64, False)
     w = m.int4_pack(codes, scales, zero)
-    x = _rand(g, 3, 128)
-    ids = torch.tensor([[0, 4], [-7, 1], [1 << 40, 2]], device="cuda")
+    x = _rand(g, rows, 128)
+    ids = torch.tensor([[0, 4], [-7, 1], [1 << 40, 2]] * 10, device="cuda")[:rows].contiguous()
     y = m.int4_linear(x, w, experts=ids)
     assert m.linear_status() == _lib.MOK_ERR_INDEX and m.linear_status() == 0
     ok = (ids >= 0) & (ids < 4)

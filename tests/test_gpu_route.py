@@ -161,6 +161,9 @@ def test_no_tokens_and_leading_axes():
     y = _logits(12, 16, BF16)
     a, b = m.route(y, 3), m.route(y.view(3, 4, 16), 3)
     assert b.experts.shape == (3, 4, 3) and b.lse.shape == (3, 4) and torch.equal(a.weights, b.weights.view(12, 3))
+    c = m.route(y[2].clone(), 3, balance=True)
+    assert c.experts.shape == (3,) and c.lse.shape == () and torch.equal(c.weights, a.weights[2]) and c.counts.sum().item() == 3
+    assert torch.equal(m.route_backward(c.weights, y[2].clone(), c.experts), m.route_backward(a.weights, y, a.experts)[2])
 
 
 @pytest.mark.parametrize("T,E,k", SHAPES)
@@ -240,6 +243,26 @@ def test_backward_ignores_ids_outside_and_sums_repeated_ones():
             if 0 <= e < 16:
                 ref[t, e] += s[t, e] * (1 - s[t, e])
     _close(d, ref, 64 * U * ref, "ids")
+
+
+def test_refusals():
+    m = mok()
+    x = _logits(8, 16, F32)
+    r = m.route(x, 2)
+    for call in (lambda: m.route(x, 0), lambda: m.route(x, 17), lambda: m.route(x, 2, score="top"), lambda: m.route(x.half(), 2),
+                 lambda: m.route(x[:, ::2], 2), lambda: m.route(x, 2, bias=torch.zeros(8, device="cuda")),
+                 lambda: m.route(x, 2, bias=torch.zeros(16, device="cuda", dtype=BF16)), lambda: m.route(x.new_zeros(2, 1025), 2),
+                 lambda: m.route(x.new_zeros(2, 100), 65), lambda: m.route_backward(r.weights[:, :1].contiguous(), x, r.experts),
+                 lambda: m.route_backward(r.weights.double(), x, r.experts), lambda: m.route_backward(r.weights, x, r.experts.int()),
+                 lambda: m.route_backward(r.weights, x, r.experts, d_lse=torch.zeros(7, device="cuda")),
+                 lambda: m.route_backward(r.weights, x, r.experts, d_mean_score=torch.zeros(8, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    for scale in (float("nan"), float("inf")):
+        with pytest.raises(m.MokError):
+            m.route(x, 2, scale=scale)
+    with pytest.raises(m.MokError):                     # a view that begins between 16 bytes
+        m.route(torch.zeros(8 * 16 + 1, device="cuda")[1:].view(8, 16), 2)
 
 
 def test_streams_and_graph():
