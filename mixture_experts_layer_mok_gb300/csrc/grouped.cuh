@@ -7,6 +7,10 @@
 //     dx       l = k, k = n:  A = W_e^T (W_e is [k][l]),     B = dz rows
 //   weight kernel  D[c][l] = sum_m dz[m][c] x[m][l], m the rows of one group.
 //
+// Measured, the rows kernel: 32768 rows of 64 groups of 1024 x 2048 with SiLU and z
+// 109 us (DRAM and tensor pipe 58% busy each), 131072 of 2048 x 4096 1200, 512 rows
+// of 256 groups of 2048 x 7168 800 (the weights' bytes).
+//
 // Both are persistent CTA pairs with two accumulator buffers.  In the rows
 // kernel the weights run over the tensor core's M (256 over two SMs) and a
 // group's rows over its N, which is any multiple of 32 up to 256: a group of 300

@@ -14,7 +14,8 @@
 // what is left of its own, and only the lane that held the last one looks for its
 // next.
 //
-// Bound by instructions: per token of 256 experts some 400 for a warp.
+// Bound by instructions: per token of 256 experts 534 for a warp (issue slots 67%
+// busy, DRAM 18%): 65536 tokens with loads and mean scores 41 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
