@@ -14,8 +14,11 @@
 // what is left of its own, and only the lane that held the last one looks for its
 // next.
 //
-// Bound by instructions: per token of 256 experts 534 for a warp (issue slots 67%
-// busy, DRAM 18%): 65536 tokens with loads and mean scores 41 us.
+// Bound by instructions: per token of 256 experts 476 for a warp (355 of them for
+// k = 1 without loads; issue slots 64% busy, DRAM 22%).  65536 tokens with loads and
+// mean scores take 36 us: 41 with tokens handed out round by round, whose last
+// round was a third full, with a logit to an instruction in the sums, and without
+// the next token's logits on their way during a choice.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -125,19 +128,52 @@ __device__ __forceinline__ float lanes_max(float v) {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
-// The token's largest logit (0 where it is -inf: exp(x - 0) is then 0 for all)
-// and e[i] = exp(x[i] - it), good to 2^-21 or so; returns the sum of e.
+// Two sums, or two products, in one instruction.
+__device__ __forceinline__ void add_pair(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul_pair(float& a0, float& a1, float b) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b));
+}
+
+// e[i] = exp(x[i] - top), good to 2^-21 or so; returns the sum of e over the token.
 template <int G, int V>
-__device__ __forceinline__ float exps(const float (&x)[V], float (&e)[V], float& top) {
-  float m = x[0];
+__device__ __forceinline__ float exps(const float (&x)[V], float (&e)[V], float top) {
+  float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-  for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
-  m = lanes_max<G>(m);
-  top = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
+  for (int i = 0; i < V; i += 2) {
+    float d0 = x[i], d1 = x[i + 1];
+    add_pair(d0, d1, -top, -top);
+    mul_pair(d0, d1, kLog2e);
+    e[i] = fast_exp2(d0), e[i + 1] = fast_exp2(d1);
+    add_pair(sum0, sum1, e[i], e[i + 1]);
+  }
+  return lanes_sum<G>(sum0 + sum1);
+}
+// s[i] = 1 / (1 + exp(-x[i])), good to 2^-21 or so.
+template <int V>
+__device__ __forceinline__ void logistics(const float (&x)[V], float (&s)[V]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) sum += e[i] = fast_exp2((x[i] - top) * kLog2e);
-  return lanes_sum<G>(sum);
+  for (int i = 0; i < V; i += 2) {
+    float d0 = x[i], d1 = x[i + 1];
+    mul_pair(d0, d1, -kLog2e);
+    d0 = fast_exp2(d0), d1 = fast_exp2(d1);
+    add_pair(d0, d1, 1.f, 1.f);
+    s[i] = fast_rcp(d0), s[i + 1] = fast_rcp(d1);
+  }
+}
+template <int V>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[V]) {
+  uint32_t m = key[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = max(m, key[i]);
+  return m;
 }
 
 // Picks that each of a token's P lanes holds (the j-th is slot j / P of lane j %
@@ -156,53 +192,53 @@ struct RouteScratch {
   static constexpr int kTokens = 32 / P;
   Pick picks[kTokens][G * V < MOK_ROUTE_MAX_K ? G * V : MOK_ROUTE_MAX_K];
   float top[kTokens], total[kTokens];
-  uint4 list[G == 32 ? 17 : 1];   // what reaches the bound: two of (key, index) each, one key of 0 behind; the rest of too many
+  uint4 keys[G == 32 ? 9 : 1];   // of what reaches the bound, if no more than 32 do, with zeros behind
+  int index[G == 32 ? 32 : 1];
   int found;
 };
 
-// The k largest keys of a token, largest first, into its picks.
+// The k largest keys of a token, largest first, into its picks; most: the lane's
+// largest, first: the token's.
 template <int G, int V, class Scratch>
-__device__ __forceinline__ void choose(uint32_t (&key)[V], int k, int lane, Scratch& scratch, Pick* picks) {
+__device__ __forceinline__ void choose(uint32_t (&key)[V], uint32_t most, uint32_t first, int k, int lane, Scratch& scratch, Pick* picks) {
   const int l = lane % G;
-  uint32_t most = key[0];
-#pragma unroll
-  for (int i = 1; i < V; ++i) most = max(most, key[i]);
   if (G == 32 && k <= 32) {
-    uint2* const list = reinterpret_cast<uint2*>(scratch.list);
-    uint32_t left = most, least = 0;
+    uint32_t* const keys = reinterpret_cast<uint32_t*>(scratch.keys);
+    if (lane == 0) scratch.found = 0;
+    uint32_t left = most == first ? 0 : most, least = first;
 #pragma unroll 2
-    for (int j = 0; j < k; ++j) {   // (equal ones go at one time: the bound is then lower than it need be)
+    for (int j = 1; j < k; ++j) {   // (equal ones go at one time: the bound is then lower than it need be)
       least = lanes_max<G>(left);
       if (left == least) left = 0;
     }
     uint32_t in = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) in |= key[i] >= least ? 1u << i : 0u;
-    if (lane == 0) scratch.found = 0;
     __syncwarp();
-    if (in) {   // in any order: the ranks below do not depend on it
-      int at = atomicAdd(&scratch.found, __popc(in));
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if ((in >> i) & 1u) list[min(at++, 33)] = make_uint2(key[i], lane * V + i);
-    }
+    int at = 0;
+    if (in) at = atomicAdd(&scratch.found, __popc(in));   // in any order: the ranks below do not depend on it
     __syncwarp();
     const int all = scratch.found;
     if (all <= 32) {
-      if (lane == 0) list[all].x = 0;
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if ((in >> i) & 1u) keys[at] = key[i], scratch.index[at] = lane * V + i, ++at;
+      }
+      if (lane < 4) keys[all + lane] = 0;
       __syncwarp();
-      const uint2 me = list[lane];
+      const uint32_t me = keys[lane];
       int rank = 0;
-#pragma unroll 2
-      for (int j = 0; j < all; j += 2) {
-        const uint4 v = scratch.list[j / 2];
-        rank += (v.x > me.x ? 1 : 0) + (v.z > me.x ? 1 : 0);
+      for (int j = 0; j < all; j += 4) {
+        const uint4 v = scratch.keys[j / 4];
+        rank += (v.x > me ? 1 : 0) + (v.y > me ? 1 : 0) + (v.z > me ? 1 : 0) + (v.w > me ? 1 : 0);
       }
       if (lane >= all) rank = 0;
+      const int index = lane < all ? scratch.index[lane] : 0;
       if (__reduce_add_sync(kAll, rank) != all * (all - 1) / 2 && lane < all) {   // equal ones: in the order of their indices
-        for (int j = 0; j < all; ++j) rank += list[j].x == me.x && list[j].y < me.y ? 1 : 0;
+        for (int j = 0; j < all; ++j) rank += keys[j] == me && scratch.index[j] < index ? 1 : 0;
       }
-      if (lane < all && rank < k) picks[rank] = Pick{static_cast<int>(me.y), me.x};
+      if (lane < all && rank < k) picks[rank] = Pick{index, me};
       __syncwarp();
       return;
     }
@@ -247,21 +283,36 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteA
   float mean[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) mean[i] = 0.f;
-  const long long step = static_cast<long long>(gridDim.x) * warps * (32 / P);
-  for (long long t0 = (static_cast<long long>(blockIdx.x) * warps + warp) * (32 / P); t0 < a.T; t0 += step) {
+  // this warp's tokens, one after the other: as many passes' as any other warp's, or one pass's more
+  const unsigned passes = static_cast<unsigned>((a.T + 32 / G - 1) / (32 / G)), all_warps = gridDim.x * warps,
+                 mine = blockIdx.x * warps + warp, each = passes / all_warps, more = passes - each * all_warps;
+  const long long begin = static_cast<long long>(each * mine + min(mine, more)) * (32 / G);
+  const long long end = min(a.T, begin + static_cast<long long>(each + (mine < more ? 1 : 0)) * (32 / G));
+  const LT* const logits = static_cast<const LT*>(a.logits);
+  float x[V];   // the next token's are on their way while the choice of the last one is made
+  if (begin < end) load_logits<LT, V>(logits + min(begin + lane / G, end - 1) * a.E, a.E, l, x);   // (behind the last token: that one again)
+  for (long long t0 = begin; t0 < end; t0 += 32 / P) {
 #pragma unroll 1
-    for (int pass = 0; pass < G / P && t0 + pass * (32 / G) < a.T; ++pass) {
+    for (int pass = 0; pass < G / P && t0 + pass * (32 / G) < end; ++pass) {
       const int at = pass * (32 / G) + lane / G;   // the token's place in the round
-      const bool live = t0 + at < a.T;
-      const LT* row = static_cast<const LT*>(a.logits) + (live ? t0 + at : t0) * a.E;   // (behind the last token: the first again)
-      float x[V], s[V], top;
-      load_logits<LT, V>(row, a.E, l, x);
+      const bool live = t0 + at < end;
+      float s[V];
+      // the choice: by the logits, in whose order the scores are, or by score + bias; what lies behind the last expert is -inf
+      // and behind everything
+      uint32_t key[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = order_key(x[i]);
+      uint32_t most = largest(key), first = lanes_max<G>(most);
+      float top = key_value(first);
+      if (top == -INFINITY) top = 0.f;   // exp(x - 0) is 0 for all
       const float total = exps<G, V>(x, s, top);
       if (l == 0) scratch.top[at] = top, scratch.total[at] = total;
       if (a.sigmoid) {
-        if (balance || a.bias) {
+        if (a.bias) {   // a choice is by the exact ones
 #pragma unroll
-          for (int i = 0; i < V; ++i) s[i] = a.bias ? sigmoid(x[i]) : logistic(x[i]);   // (a choice is by the exact ones)
+          for (int i = 0; i < V; ++i) s[i] = sigmoid(x[i]);
+        } else if (balance) {
+          logistics(x, s);
         }
       } else if (balance || a.bias) {
         const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
@@ -270,24 +321,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteA
       }
       if (balance && live) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) mean[i] += s[i];
+        for (int i = 0; i < V; i += 2) add_pair(mean[i], mean[i + 1], s[i], s[i + 1]);
       }
-      // the choice: by the logits, in whose order the scores are, or by score + bias; what lies behind the last expert is -inf
-      // and behind everything
-      uint32_t key[V];
+      if (a.bias) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = l * V + i;
-        float by = x[i];
-        if (a.bias && e < a.E && x[i] != -INFINITY) by = s[i] + __ldg(a.bias + e);
-        key[i] = order_key(by);
+        for (int i = 0; i < V; ++i) {
+          const int e = l * V + i;
+          if (e < a.E && x[i] != -INFINITY) key[i] = order_key(s[i] + __ldg(a.bias + e));
+        }
+        most = largest(key), first = lanes_max<G>(most);
       }
-      choose<G, V>(key, a.k, lane, scratch, scratch.picks[at]);
+      load_logits<LT, V>(logits + min(t0 + at + 32 / G, end - 1) * a.E, a.E, l, x);
+      choose<G, V>(key, most, first, a.k, lane, scratch, scratch.picks[at]);
     }
     __syncwarp();
     const int p = lane % P, at = lane / P;
     const long long t = t0 + at;
-    const bool live = t < a.T;
+    const bool live = t < end;
     const float top = live ? scratch.top[at] : 0.f, total = live ? scratch.total[at] : 1.f;
     if (p == 0 && live) a.lse[t] = top == INFINITY ? top : top + logf(total);
     const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
@@ -361,31 +411,35 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteA
   }
 }
 
-// The blocks' parts joined in order: 32 experts a block, 32 parts in step.
-__global__ void __launch_bounds__(1024) route_join_kernel(const float* __restrict__ part, int n, int E, float inv_t,
-                                                          int* __restrict__ counts, float* __restrict__ mean_score) {
-  __shared__ float s[32][33];
-  __shared__ int c[32][33];
+// The blocks' parts joined in a fixed order: 8 experts a block, 64 parts in step,
+// so that few loads of a thread follow one another.
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const float* __restrict__ part, int n, int E, float inv_t,
+                                                                  int* __restrict__ counts, float* __restrict__ mean_score) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float s[kWarps][8];
+  __shared__ int c[kWarps][8];
   griddep_wait();
   griddep_launch_dependents();
-  const int e = blockIdx.x * 32 + threadIdx.x;
+  const int lane = threadIdx.x & 31, e = blockIdx.x * 8 + (lane & 7);
   float v = 0.f;
   int m = 0;
   if (e < E) {
     const int* part_cnt = reinterpret_cast<const int*>(part + static_cast<long long>(n) * E);
-#pragma unroll 4
-    for (int b = threadIdx.y; b < n; b += 32) {
+#pragma unroll 5
+    for (int b = threadIdx.x >> 3; b < n; b += kJoinThreads / 8) {
       v += part[static_cast<long long>(b) * E + e];
       m += part_cnt[static_cast<long long>(b) * E + e];
     }
   }
-  s[threadIdx.y][threadIdx.x] = v;
-  c[threadIdx.y][threadIdx.x] = m;
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) v += __shfl_xor_sync(kAll, v, o), m += __shfl_xor_sync(kAll, m, o);
+  if (lane < 8) s[threadIdx.x >> 5][lane] = v, c[threadIdx.x >> 5][lane] = m;
   __syncthreads();
-  if (threadIdx.y == 0 && e < E) {
+  if (threadIdx.x < 8 && e < E) {
     v = 0.f, m = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v += s[i][threadIdx.x], m += c[i][threadIdx.x];
+    for (int i = 0; i < kWarps; ++i) v += s[i][threadIdx.x], m += c[i][threadIdx.x];
     counts[e] = m;
     mean_score[e] = v * inv_t;
   }
@@ -428,6 +482,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_bwd_kernel(const Ro
     float x[V], p[V], top = 0.f, inv = 0.f;
     if (dense_softmax || a.d_lse || (a.sigmoid && a.d_mean_score)) load_logits<LT, V>(row, a.E, l, x);
     if (dense_softmax || a.d_lse) {
+      float m = x[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
+      m = lanes_max<G>(m);
+      top = m == -INFINITY ? 0.f : m;
       const float total = exps<G, V>(x, p, top);
       inv = total > 0.f || total != total ? 1.f / total : 0.f;
 #pragma unroll
@@ -608,7 +667,7 @@ cudaError_t launch_route(const RouteArgs& a, int f32, cudaStream_t st) {
   const size_t smem = a.counts ? static_cast<size_t>(1 + kSumRows) * a.E * sizeof(float) : 0;   // at most 20 KB
   const cudaError_t err = r.blocks == 0 ? cudaSuccess : f32 ? route_typed<float>(a, r, smem, st) : route_typed<uint16_t>(a, r, smem, st);
   if (err != cudaSuccess || !a.counts) return err;
-  return launch_dependent(route_join_kernel, dim3((a.E + 31) / 32), dim3(32, 32), 0, st, static_cast<const float*>(a.part), r.blocks,
+  return launch_dependent(route_join_kernel, dim3((a.E + 7) / 8), dim3(kJoinThreads), 0, st, static_cast<const float*>(a.part), r.blocks,
                           a.E, a.T > 0 ? 1.f / static_cast<float>(a.T) : 0.f, a.counts, a.mean_score);
 }
 
