@@ -36,7 +36,8 @@ mok_status_t launch_rows(const GroupedRowsMaps& maps, const GroupedRowsParams& p
   static KernelInfo info;
   int n = 0;
   MOK_CUDA(resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2, &n));
-  const long long items = (static_cast<long long>(p.M) / 256 + (p.E < p.M ? p.E : p.M)) * p.l_tiles;   // at most
+  // at most, and with tiles in parts of 64 rows or more
+  const long long items = (static_cast<long long>(p.M) / 256 + static_cast<long long>(p.M) / 64 + (p.E < p.M ? p.E : p.M)) * p.l_tiles;
   const int pairs = items < n ? static_cast<int>(items) : n;
   MOK_CUDA(launch_clusters(kern, dim3(2 * pairs), C::kThreads, C::kSmemBytes, 2, st, maps, p));
   return MOK_OK;

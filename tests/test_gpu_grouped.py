@@ -97,6 +97,24 @@ def test_forward(case, act, bias, out, save_z):
     assert torch.equal(again, y)
 
 
+@pytest.mark.parametrize("counts", [[63], [64], [127], [128], [129], [191], [192], [255], [256], [0, 257], [320, 130], [64] * 39,
+                                    [256] * 76 + [200], [256] * 80 + [1, 129], [130] * 19])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [256, 264])
+def test_few_tiles(counts, out, N):
+    """A last round of few tiles, which are cut by rows: each count around the parts' 64."""
+    m = mok()
+    E, M, K = len(counts), sum(counts) + 3, 136
+    g = _gen(M + N)
+    x, w, b = _rand(g, M, K), _rand(g, E, N, K, std=K ** -0.5), _rand(g, E, N, dtype=F32)
+    x[M - 3:] = float("nan")
+    y, _ = m.grouped_linear(x, w, _counts(counts), bias=b, out_dtype=T[out])
+    assert m.linear_status() == 0
+    _, y64, size = _forward64(x, w, b, counts, "none")
+    _within(y, y64, 1.13 * _f(K) * size + 4e-6 * 2 * y64.abs() + (U * y64.abs() if out == "bf16" else 0.0), "y")
+    assert (y[M - 3:] == 0).all()
+
+
 @pytest.mark.parametrize("case", range(len(CASES)))
 @pytest.mark.parametrize("act,bias,dyt", [("none", False, "bf16"), ("none", True, "bf16"), ("gelu", True, "bf16"),
                                           ("silu", True, "f32"), ("none", True, "f32"), ("relu", False, "bf16")])
