@@ -341,7 +341,7 @@ __device__ __forceinline__ void store_out(const Int4LinearArgs& a, long long row
 
 // ---- warps that share K: few rows of w to a block
 // grid {groups of R row tiles, rows of x in steps of COLS; with experts: rows of
-// y, or the experts where they are fewer}, 4 or 8 warps.  A block makes 16 R outputs of up to COLS rows; each warp
+// y, or the experts where they are fewer}, 1 to 8 warps.  A block makes 16 R outputs of up to COLS rows; each warp
 // takes a part of K through stages of its own, and their sums are added in order.
 // With experts, the block of an expert, or of a row whose expert no earlier row
 // has, serves all rows of that expert, and the others end at once: an expert's
@@ -607,8 +607,14 @@ cudaError_t split_launch(const Int4LinearArgs& a, int num_sms, cudaStream_t st) 
   const unsigned x = static_cast<unsigned>((a.w.row_tiles() + R - 1) / R);
   const unsigned y = !EXPERTS ? (a.rows + C::kCols - 1) / C::kCols : a.by_expert ? static_cast<unsigned>(a.w.matrices) : a.rows;
   // 4 warps to a block, 8 where an SM would have fewer than ten warps.  Measured with 2, 4 and 8: one row times 7168 x 2048
-  // 4.2, 3.5 and 4.1 us, 8 experts of 2048 x 7168 20.4, 17.7 and 19.5.
-  const int warps = static_cast<long long>(x) * y * 4 < 10ll * num_sms ? 8 : 4;
+  // 4.2, 3.5 and 4.1 us, 8 experts of 2048 x 7168 20.4, 17.7 and 19.5.  Two or one where K is short and there are many blocks, of
+  // which an SM then holds more.  Measured with 1, 2 and 4: 42 rows among 55 experts of 9712 x 384 29, 37 and 53 us, 120 rows among
+  // 64 of 2048 x 512 18.5, 21.5 and 31, 256 rows among 64 of 4096 x 2048 104, 115 and 138, 64 rows among 8 of 8192 x 2048 38, 38
+  // and 43; but one row times 49152 x 2048 20.3, 15.6 and 15.2, and 8 experts of 4096 x 4096 24.6, 22.6 and 20.5.
+  const long long all = static_cast<long long>(x) * y;
+  const int blocks = a.w.blocks();
+  int warps = all * 4 < 10ll * num_sms ? 8 : 4;
+  if (blocks <= 16 && all >= 12ll * num_sms) warps = all >= 32ll * num_sms && (COLS > 2 || blocks <= 8) ? 1 : 2;
   return launch_dependent(kern, dim3(x, y), dim3(32 * warps), warps * C::kWarpBytes, st, a);
 }
 template <int GPB, bool ZEROS>
