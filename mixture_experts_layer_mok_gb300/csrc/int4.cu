@@ -379,11 +379,12 @@ __global__ void __launch_bounds__(32 * kInt4Warps, COLS <= 8 ? 4 : 1) int4_split
     matrix = a.by_expert ? r : few ? __shfl_sync(0xffffffffu, id, r) : id;
     if (a.by_expert) {
       if (r == 0) {   // rows of no expert: zeros; any id but -1 is an error besides
-        for (int i = warp; i < a.rows; i += blockDim.x >> 5) {
-          const long long e = __ldg(a.experts + i);
-          if (e >= 0 && e < a.w.matrices) continue;
-          if (e != -1 && lane == 0 && blockIdx.x == 0 && a.status) atomicCAS(a.status, 0, MOK_ERR_INDEX);
-          for (int n = n0 + lane; n < min(n0 + kRows, a.w.N); n += 32) store_out(a, i, n, 0.f);
+        for (int f = warp * 32; f < a.rows; f += blockDim.x) {   // 32 of them at a time
+          const long long e = f + lane < a.rows ? __ldg(a.experts + f + lane) : 0;
+          const bool none = e < 0 || e >= a.w.matrices;
+          if (none && e != -1 && blockIdx.x == 0 && a.status) atomicCAS(a.status, 0, MOK_ERR_INDEX);
+          for (unsigned m = __ballot_sync(0xffffffffu, none); m; m &= m - 1)
+            for (int n = n0 + lane; n < min(n0 + kRows, a.w.N); n += 32) store_out(a, f + __ffs(m) - 1, n, 0.f);
         }
       }
     } else if (matrix < 0 || matrix >= a.w.matrices) {
@@ -606,14 +607,15 @@ cudaError_t split_launch(const Int4LinearArgs& a, int num_sms, cudaStream_t st) 
   if (err != cudaSuccess) return err;
   const unsigned x = static_cast<unsigned>((a.w.row_tiles() + R - 1) / R);
   const unsigned y = !EXPERTS ? (a.rows + C::kCols - 1) / C::kCols : a.by_expert ? static_cast<unsigned>(a.w.matrices) : a.rows;
-  // 4 warps to a block, 8 where an SM would have fewer than ten warps.  Measured with 2, 4 and 8: one row times 7168 x 2048
-  // 4.2, 3.5 and 4.1 us, 8 experts of 2048 x 7168 20.4, 17.7 and 19.5.  Two or one where K is short and there are many blocks, of
+  // 4 warps to a block, 8 where an SM would have fewer than ten warps and each has a block of K.  Measured with 2, 4 and 8: one row
+  // times 7168 x 2048 4.2, 3.5 and 4.1 us, 8 experts of 2048 x 7168 20.4, 17.7 and 19.5, 12 rows times 2048 x 2048 8.4, 5.2 and
+  // 4.3, 30 rows times 7504 x 512 7.4, 5.6 and 7.8.  Two or one where K is short and there are many blocks, of
   // which an SM then holds more.  Measured with 1, 2 and 4: 42 rows among 55 experts of 9712 x 384 29, 37 and 53 us, 120 rows among
   // 64 of 2048 x 512 18.5, 21.5 and 31, 256 rows among 64 of 4096 x 2048 104, 115 and 138, 64 rows among 8 of 8192 x 2048 38, 38
   // and 43; but one row times 49152 x 2048 20.3, 15.6 and 15.2, and 8 experts of 4096 x 4096 24.6, 22.6 and 20.5.
   const long long all = static_cast<long long>(x) * y;
   const int blocks = a.w.blocks();
-  int warps = all * 4 < 10ll * num_sms ? 8 : 4;
+  int warps = all * 4 < 10ll * num_sms && blocks >= 8 ? 8 : 4;
   if (blocks <= 16 && all >= 12ll * num_sms) warps = all >= 32ll * num_sms && (COLS > 2 || blocks <= 8) ? 1 : 2;
   return launch_dependent(kern, dim3(x, y), dim3(32 * warps), warps * C::kWarpBytes, st, a);
 }
