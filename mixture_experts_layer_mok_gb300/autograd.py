@@ -267,7 +267,8 @@ class RouteFunction(torch.autograd.Function):
         logits, chosen = ctx.saved_tensors
         if d_weights is None and d_lse is None and d_mean_score is None:
             return (None,) * 7
-        d_weights = torch.zeros(chosen.shape, device=chosen.device) if d_weights is None else _incoming(d_weights)
+        d_weights = (torch.zeros(chosen.shape, dtype=torch.float32, device=chosen.device) if d_weights is None
+                     else _incoming(d_weights))
         d = experts.route_backward(d_weights, logits, chosen, *ctx.route, None if d_lse is None else _incoming(d_lse),
                                    None if d_mean_score is None else _incoming(d_mean_score))
         return d, None, None, None, None, None, None
