@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256) grouped_dz_kernel(const __grid_constant__
   make_plan(plan, start, blockIdx.x == 0 && blockIdx.y == 0, threadIdx.y * 32 + threadIdx.x, 256);
   const int E = plan.E, col = (blockIdx.x * 32 + threadIdx.x) * 8;
   int r0 = blockIdx.y * chunk;
-  const int r1 = min(r0 + chunk, start[E]);
+  const int r1 = r0 + min(chunk, start[E] - r0);   // (r0 + chunk may pass 2^31)
   if (r0 >= r1) return;
   for (int e = part ? find_group(start, E, r0, threadIdx.x) : 0; r0 < r1; ++e) {
     const int end = part ? min(start[e + 1], r1) : r1;   // without sums the groups do not matter
@@ -173,7 +173,7 @@ template <class DY>
 cudaError_t dz_launch(const Plan& plan, const GroupedDzCall& d, int N, cudaStream_t st) {
   const DY* dy = static_cast<const DY*>(d.dy);
   const int chunk = grouped_dz_chunk(plan.M, N);
-  const dim3 grid((N + 255) / 256, (plan.M + chunk - 1) / chunk), block(32, kDzRows);
+  const dim3 grid((N + 255) / 256, (plan.M - 1) / chunk + 1), block(32, kDzRows);
   const auto launch = [&](auto kern) { return launch_dependent(kern, grid, block, 0, st, plan, dy, d.z, N, chunk, d.dz, d.part); };
   switch (d.act) {
     case LIN_RELU: return launch(grouped_dz_kernel<DY, LIN_RELU>);
@@ -251,8 +251,8 @@ mok_status_t run_grouped_weights(const GroupedWeightCall& c, const void* plan, c
 int grouped_dz_chunk(int M, int N) {
   // about 8 blocks for each of 152 SMs, a chunk no shorter than 4 steps
   const int cols = (N + 255) / 256, want = (1216 + cols - 1) / cols;
-  const int rows = ((M + want - 1) / want + kDzRows - 1) / kDzRows * kDzRows;
-  return rows < 4 * kDzRows ? 4 * kDzRows : rows;
+  const long long rows = ((static_cast<long long>(M) + want - 1) / want + kDzRows - 1) / kDzRows * kDzRows;
+  return rows < 4 * kDzRows ? 4 * kDzRows : static_cast<int>(rows);
 }
 
 cudaError_t launch_grouped_bias(const GroupedBias& b, const void* plan, int E, int N, cudaStream_t st) {
