@@ -117,6 +117,12 @@ struct GroupedRowsCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
+// A length cut evenly into parts, in steps of 32: a part's length (count + parts
+// may pass 2^31).
+__host__ __device__ constexpr int even_part(int count, int parts) { return ((count - 1) / parts + 32) & ~31; }
+static_assert(even_part(1, 1) == 32 && even_part(257, 2) == 160 && even_part(224, 3) == 96, "rounded up");
+static_assert(even_part(0x7fffffff - 512, (0x7fffffff - 512 + 255) / 256) == 256, "the largest group");
+
 struct RowsItem {
   int e, l0, m0, rows, n;   // group, first l, first row, rows, and the tensor core's N
 };
@@ -140,13 +146,13 @@ __device__ __forceinline__ bool rows_item(const GroupedRowsParams& p, const Grou
   const int t0 = g.tile[it.e], tiles = g.tile[it.e + 1] - t0, first = g.start[it.e], count = g.start[it.e + 1] - first;
   int ct, lt;
   unit_and_col(idx - t0 * p.l_tiles, tiles, p.l_tiles, 4, ct, lt);
-  const int each = ((count + tiles - 1) / tiles + 31) & ~31;
+  const int each = even_part(count, tiles);
   it.l0 = lt * 256;
   it.m0 = first + ct * each;
   it.rows = min(each, count - ct * each);
   if (parts > 1) {
     parts = max(min(parts, it.rows / 64), 1);
-    const int rows = ((it.rows + parts - 1) / parts + 31) & ~31;
+    const int rows = even_part(it.rows, parts);
     it.m0 += part * rows;
     it.rows = min(rows, it.rows - part * rows);
     if (it.rows <= 0) return false;

@@ -330,3 +330,44 @@ def test_refusals():
             m.grouped_linear_backward(dy, x, w, c, **kw)
     with pytest.raises(m.MokError):           # 16-byte alignment: a view that begins between
         m.grouped_linear(torch.ones(4 * 64 + 4, dtype=BF16, device="cuda")[4:].view(4, 64), w, c)
+
+
+def test_as_many_rows_as_there_can_be():
+    """2^31 - 513 rows of 8: tiles, chunks and offsets at the end of 32 bits.  Rows
+    of small integers among zeros, so that every result is exact in bf16, and NaN
+    behind the last expert's rows."""
+    m = mok()
+    M, tail, first = (1 << 31) - 513, 5, 7
+    last = M - tail
+    spans = [(0, 300), (last // 2 - 300, last // 2 + 300), (last - 3000, last)]
+    g = torch.Generator("cuda").manual_seed(0)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").to(BF16)  # noqa: E731
+    counts = torch.tensor([first, last - first], dtype=torch.int32, device="cuda")
+    w = ints(2, 8, 8)
+    each = w[(torch.cat([torch.arange(a, b) for a, b in spans]) >= first).long().cuda()].double()   # each kept row's weight
+
+    def rows():
+        t = torch.zeros(M, 8, dtype=BF16, device="cuda")
+        for a, b in spans:
+            t[a:b] = ints(b - a, 8)
+        t[last:] = float("nan")
+        return t, torch.cat([t[a:b] for a, b in spans]).double()
+
+    def check(y, ref):
+        assert torch.equal(torch.cat([y[a:b] for a, b in spans]).double(), ref)
+        for a, b in spans:
+            y[a:b] = 0
+        assert not any((y[i:i + (1 << 27)] != 0).any().item() for i in range(0, M, 1 << 27))
+
+    x, kept = rows()
+    y, _ = m.grouped_linear(x, w, counts)
+    check(y, torch.einsum("rk,rnk->rn", kept, each))
+    del y
+    z, kept = rows()                 # its own gradient too: ReLU passes what is above 0
+    got = m.grouped_linear_backward(z, x, w, counts, z=z, activation="relu", bias=True, need=("dx",))
+    dz = kept.clamp(min=0)
+    check(got["dx"], torch.einsum("rn,rnk->rk", dz, each))
+    assert torch.equal(got["d_bias"].double(), torch.stack([dz[:first].sum(0), dz[first:].sum(0)]))
+    assert m.linear_status() == 0
+    del x, z, got
+    torch.cuda.empty_cache()
