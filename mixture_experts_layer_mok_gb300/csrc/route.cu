@@ -305,16 +305,26 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteA
       uint32_t most = largest(key), first = lanes_max<G>(most);
       float top = key_value(first);
       if (top == -INFINITY) top = 0.f;   // exp(x - 0) is 0 for all
-      const float total = exps<G, V>(x, s, top);
+      float total;
+      if (a.bias && !a.sigmoid) {   // a choice is by the exact scores
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = expf(x[i] - top), sum += s[i];
+        total = lanes_sum<G>(sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = total == 0.f ? 0.f : s[i] / total;
+      } else {
+        total = exps<G, V>(x, s, top);
+      }
       if (l == 0) scratch.top[at] = top, scratch.total[at] = total;
       if (a.sigmoid) {
-        if (a.bias) {   // a choice is by the exact ones
+        if (a.bias) {   // likewise
 #pragma unroll
           for (int i = 0; i < V; ++i) s[i] = sigmoid(x[i]);
         } else if (balance) {
           logistics(x, s);
         }
-      } else if (balance || a.bias) {
+      } else if (balance && !a.bias) {
         const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) s[i] *= inv;
