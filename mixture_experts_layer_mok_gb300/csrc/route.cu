@@ -263,9 +263,10 @@ __device__ __forceinline__ void choose(uint32_t (&key)[V], uint32_t most, uint32
 
 // A round of a warp is 32 / P tokens: first G lanes to each in G / P passes, which
 // leave the picks and the sums in shared memory, then P lanes to each, which make
-// the weights of all of them at a time.
-template <class LT, int G, int V, int P, bool MANY>
-__global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteArgs a) {
+// the weights of all of them at a time.  BIAS: the choice is by score + bias, in
+// kernels of their own, as exact scores take registers.
+template <class LT, int G, int V, int P, bool MANY, bool BIAS>
+__global__ void __launch_bounds__(32 * kRouteWarps<V>, V <= 8 ? 2 : 0) route_kernel(const RouteArgs a) {
   constexpr int S = kSlots<P, G, V, MANY>;
   using Scratch = RouteScratch<P, V, G>;
   extern __shared__ float shared[];   // with counts: [E] counts, then [kSumRows][E] sums of scores
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteA
       float top = key_value(first);
       if (top == -INFINITY) top = 0.f;   // exp(x - 0) is 0 for all
       float total;
-      if (a.bias && !a.sigmoid) {   // a choice is by the exact scores
+      if (BIAS && !a.sigmoid) {   // a choice is by the exact scores
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) s[i] = expf(x[i] - top), sum += s[i];
@@ -318,13 +319,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteA
       }
       if (l == 0) scratch.top[at] = top, scratch.total[at] = total;
       if (a.sigmoid) {
-        if (a.bias) {   // likewise
+        if (BIAS) {   // likewise
 #pragma unroll
           for (int i = 0; i < V; ++i) s[i] = sigmoid(x[i]);
         } else if (balance) {
           logistics(x, s);
         }
-      } else if (balance && !a.bias) {
+      } else if (balance && !BIAS) {
         const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) s[i] *= inv;
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteA
 #pragma unroll
         for (int i = 0; i < V; i += 2) add_pair(mean[i], mean[i + 1], s[i], s[i + 1]);
       }
-      if (a.bias) {
+      if (BIAS) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int e = l * V + i;
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>) route_kernel(const RouteA
       if (p + P * h < a.k && live) {
         const Pick pick = scratch.picks[at][p + P * h];
         id[h] = pick.id;
-        logit[h] = a.bias ? logit_at(static_cast<const LT*>(a.logits) + t * a.E, pick.id) : key_value(pick.key);
+        logit[h] = BIAS ? logit_at(static_cast<const LT*>(a.logits) + t * a.E, pick.id) : key_value(pick.key);
         first = fmaxf(first, logit[h]);
       }
     }
@@ -631,8 +632,9 @@ RouteGrid route_grid(long long T, int E) {
 template <class LT, int G, int V, int P>
 cudaError_t route_picks(const RouteArgs& a, RouteGrid r, size_t smem, cudaStream_t st) {
   const dim3 g(r.blocks), b(32 * r.warps);
-  return a.k <= P ? launch_dependent(route_kernel<LT, G, V, P, false>, g, b, smem, st, a)
-                  : launch_dependent(route_kernel<LT, G, V, P, true>, g, b, smem, st, a);
+  const auto launch = [&](auto kern) { return launch_dependent(kern, g, b, smem, st, a); };
+  if (a.bias) return a.k <= P ? launch(route_kernel<LT, G, V, P, false, true>) : launch(route_kernel<LT, G, V, P, true, true>);
+  return a.k <= P ? launch(route_kernel<LT, G, V, P, false, false>) : launch(route_kernel<LT, G, V, P, true, false>);
 }
 template <class LT, int G, int V>
 cudaError_t route_lanes(const RouteArgs& a, RouteGrid r, size_t smem, cudaStream_t st) {
