@@ -557,9 +557,10 @@ mok_status_t mok_linear_status(int* status);
 
 /* ---- router: logits -> experts and their weights --------------------------
  * logits [T][E], bf16 or fp32.  s = softmax(logits) or sigmoid(logits), in fp32.
- * The k experts of the largest s + bias (bias fp32 [E] or NULL; -inf logits
- * last whatever the bias; ties to the lowest index, NaN above all), in that
- * order, and for each the weight
+ * The k experts of the largest s + bias (bias fp32 [E], the sum in fp32; of equal
+ * sums the larger logit first, of equal logits the lowest index), or with NULL of
+ * the largest logits, whose order the scores have; -inf logits last whatever the
+ * bias, NaN above all.  In that order, and for each the weight
  *   normalize:  scale s_j / sum of the k chosen s      else:  scale s_j
  * (0 where that sum is 0).  The bias decides the choice alone.
  * experts int64 [T][k], weights fp32 [T][k]; lse fp32 [T] = log sum exp(logits),

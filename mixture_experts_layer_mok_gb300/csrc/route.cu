@@ -197,10 +197,19 @@ struct RouteScratch {
   int found;
 };
 
+// The order of logit i of a row; 0, below all others, behind the last.
+template <class LT>
+__device__ __forceinline__ uint32_t logit_key(const LT* row, int E, int i) {
+  return i < E ? order_key(logit_at(row, i)) : 0u;
+}
+
 // The k largest keys of a token, largest first, into its picks; most: the lane's
-// largest, first: the token's.
-template <int G, int V, class Scratch>
-__device__ __forceinline__ void choose(uint32_t (&key)[V], uint32_t most, uint32_t first, int k, int lane, Scratch& scratch, Pick* picks) {
+// largest, first: the token's.  BIAS: of equal keys the one of the largest logit
+// comes first (scores that 32 bits do not tell apart, beside equal biases: as
+// without a bias); then, and without BIAS at once, the one of the lowest index.
+template <int G, int V, bool BIAS, class LT, class Scratch>
+__device__ __forceinline__ void choose(uint32_t (&key)[V], uint32_t most, uint32_t first, int k, int lane, Scratch& scratch, Pick* picks,
+                                       const LT* row, int E) {
   const int l = lane % G;
   if (G == 32 && k <= 32) {
     uint32_t* const keys = reinterpret_cast<uint32_t*>(scratch.keys);
@@ -235,7 +244,16 @@ __device__ __forceinline__ void choose(uint32_t (&key)[V], uint32_t most, uint32
       }
       if (lane >= all) rank = 0;
       const int index = lane < all ? scratch.index[lane] : 0;
-      if (__reduce_add_sync(kAll, rank) != all * (all - 1) / 2 && lane < all) {   // equal ones: in the order of their indices
+      const bool equal = __reduce_add_sync(kAll, rank) != all * (all - 1) / 2;
+      if constexpr (BIAS) {
+        if (equal) {
+          const uint32_t mine = lane < all ? logit_key(row, E, index) : 0u;
+          for (int j = 0; j < all; ++j) {
+            const uint32_t its = __shfl_sync(kAll, mine, j);
+            if (lane < all && keys[j] == me) rank += its > mine || (its == mine && scratch.index[j] < index) ? 1 : 0;
+          }
+        }
+      } else if (equal && lane < all) {
         for (int j = 0; j < all; ++j) rank += keys[j] == me && scratch.index[j] < index ? 1 : 0;
       }
       if (lane < all && rank < k) picks[rank] = Pick{index, me};
@@ -243,9 +261,11 @@ __device__ __forceinline__ void choose(uint32_t (&key)[V], uint32_t most, uint32
       return;
     }
   }
+  bool ties = false;
   for (int j = 0; j < k; ++j) {
     const uint32_t best = lanes_max<G>(most);
     const unsigned hit = (__ballot_sync(kAll, most == best) >> (lane - l)) & (kAll >> (32 - G));
+    if (BIAS) ties |= (hit & (hit - 1)) != 0;
     if (l == __ffs(hit) - 1) {
       most = 0;
       bool found = false;
@@ -256,6 +276,38 @@ __device__ __forceinline__ void choose(uint32_t (&key)[V], uint32_t most, uint32
         found = found || it;
         most = max(most, key[i]);
       }
+      if (BIAS) ties |= most == best;
+    }
+  }
+  __syncwarp();
+  if (!BIAS || !__any_sync(kAll, ties)) return;
+  // equal keys: once more, by logit among them
+  for (int j = 0; j < k; ++j) {
+    const Pick pick = picks[j];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (l * V + i == pick.id) key[i] = pick.key;
+  }
+  __syncwarp();
+  for (int j = 0; j < k; ++j) {
+    most = largest(key);
+    const uint32_t best = lanes_max<G>(most);
+    uint32_t top = 0;
+    int slot = -1;
+    if (most == best) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t its = key[i] == best ? logit_key(row, E, l * V + i) : 0u;
+        if (its > top) top = its, slot = i;
+      }
+    }
+    const uint32_t over = lanes_max<G>(top);
+    const unsigned hit = (__ballot_sync(kAll, slot >= 0 && top == over) >> (lane - l)) & (kAll >> (32 - G));
+    if (l == __ffs(hit) - 1) {
+      picks[j] = Pick{l * V + slot, best};
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i == slot) key[i] = 0;
     }
   }
   __syncwarp();
@@ -343,7 +395,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<V>, V <= 8 ? 2 : 0) route_ker
         most = largest(key), first = lanes_max<G>(most);
       }
       load_logits<LT, V>(logits + min(t0 + at + 32 / G, end - 1) * a.E, a.E, l, x);
-      choose<G, V>(key, most, first, a.k, lane, scratch, scratch.picks[at]);
+      choose<G, V, BIAS>(key, most, first, a.k, lane, scratch, scratch.picks[at], logits + min(t0 + at, end - 1) * a.E, a.E);
     }
     __syncwarp();
     const int p = lane % P, at = lane / P;

@@ -75,9 +75,9 @@ def route(logits, k: int, score: str = "softmax", normalize: bool = True, scale:
           stream=None) -> Routing:
     """Each token's k experts and their weights.  logits bf16 or fp32 [..., E];
     scores s = softmax or sigmoid of them; the choice is by s + ``bias`` (fp32
-    [E]), ties to the lowest index; weights scale s_j / sum of the chosen s, or
-    scale s_j without ``normalize``.  ``balance``: also counts and mean_score,
-    for a balance loss.  E up to 1024, k up to 64."""
+    [E]), ties to the larger logit, and then to the lowest index; weights scale
+    s_j / sum of the chosen s, or scale s_j without ``normalize``.  ``balance``:
+    also counts and mean_score, for a balance loss.  E up to 1024, k up to 64."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return route(logits, k, score, normalize, scale, bias, balance)

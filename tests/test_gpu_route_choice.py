@@ -33,3 +33,57 @@ def test_softmax_scores_of_a_choice_are_the_exact_ones(E, k, T):
         assert (experts == experts[0]).all()
         got, top = by[experts[0]], by.topk(k).values
         assert ((top - got) <= 4 * U * c).all(), ((top - got) / c / U).max().item()
+
+
+# (E, k): every number of lanes and of logits to a lane, few picks and more than lanes or 32
+WIDTHS = [(3, 3), (8, 3), (32, 32), (33, 4), (40, 5), (64, 12), (65, 7), (96, 6), (128, 40), (200, 8), (256, 20), (256, 33), (384, 9),
+          (512, 64), (777, 12), (1024, 8), (1024, 64)]
+
+
+def _spread(T, E, seed):
+    """Whole numbers from -300 to 300, so that scores saturate or underflow, or
+    differ by far more than their errors; masked and equal ones among them."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randint(-300, 301, (T, E), device="cuda", generator=g).float()
+    x[torch.rand(T, E, device="cuda", generator=g) < 0.1] = -float("inf")
+    x[0] = 7.0
+    if T > 2:
+        x[1] = -float("inf")
+        x[2, E // 2] = float("nan")
+    return x
+
+
+def _logit_order(x, k):
+    """Largest logits, NaN before them, lowest index of equal ones."""
+    return torch.sort(torch.nan_to_num(x, nan=1e30, neginf=-1e30), dim=1, descending=True, stable=True).indices[:, :k]
+
+
+@pytest.mark.parametrize("E,k", WIDTHS)
+@pytest.mark.parametrize("T", [5, 3000])     # a token to a round of a warp, and several
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_bias_for_all_experts_changes_no_choice(E, k, T, score, dtype):
+    m = mok()
+    x = _spread(T, E, E + k).to(dtype)       # (up to 300: bf16 rounds beyond 256 to even numbers)
+    want = _logit_order(x.float(), k)
+    plain = m.route(x, k, score=score)
+    assert torch.equal(plain.experts, want)
+    for level in (0.0, 0.25, -3.0):
+        r = m.route(x, k, score=score, bias=torch.full((E,), level, device="cuda"), balance=True)
+        assert torch.equal(r.experts, want)
+        assert torch.equal(r.counts.long(), torch.bincount(want.flatten(), minlength=E))
+
+
+@pytest.mark.parametrize("E,k", WIDTHS)
+@pytest.mark.parametrize("T", [5, 3000])
+def test_equal_sums_go_by_logit_and_then_by_index(E, k, T):
+    """Sigmoids of 20 and more are 1 in 32 bits; biases of three values."""
+    m = mok()
+    g = torch.Generator("cuda").manual_seed(E * k)
+    x = torch.randint(20, 40, (T, E), device="cuda", generator=g).float()
+    bias = torch.randint(-1, 2, (E,), device="cuda", generator=g) / 4
+    order = torch.sort(x, dim=1, descending=True, stable=True).indices
+    order = order.gather(1, torch.sort(bias[order], dim=1, descending=True, stable=True).indices)[:, :k]
+    r = m.route(x, k, score="sigmoid", bias=bias)
+    assert torch.equal(r.experts, order)
+    assert (r.weights - 1 / k).abs().max().item() <= 8 * U / k
