@@ -616,7 +616,8 @@ mok_status_t mok_grouped_linear_bwd(const void* dy, int dy_dtype, const uint16_t
  *   zeros NULL:  scale = bf16(max |w| / 7), q = clamp(round(w / scale) + 8)
  *   else, over lo = min(w, 0) and hi = max(w, 0):  scale = bf16((hi - lo) / 15),
  *     zero = clamp(round(-lo / scale)), q = clamp(round(w / scale) + zero)
- * (clamped to 0..15; scale 0 where all of a group is 0).
+ * (clamped to 0..15; scale 0 where all of a group is 0, and NaN, so that all of its
+ * values are, where one is NaN or infinite).
  * mok_int4_pack takes codes [matrices][N][K / 2], two to a byte, the even
  * column's in the low half, scales [matrices][N][K / group] and zeros, a byte
  * each (the low four bits).  mok_int4_dequantize gives the values in bf16. */

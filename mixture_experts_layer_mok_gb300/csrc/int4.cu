@@ -63,7 +63,8 @@ __device__ __forceinline__ float bf16_round(float v) { return __bfloat162float(_
 
 // Symmetric: scale = bf16(amax / 7), q = round(w / scale) + 8; with zeros: the
 // range [lo, hi] that holds 0, scale = bf16((hi - lo) / 15), zero = round(-lo /
-// scale), q = round(w / scale) + zero; both clamped to 0..15.
+// scale), q = round(w / scale) + zero; both clamped to 0..15.  A group with a
+// value that is not finite gets a NaN scale.
 template <bool F32, bool ZEROS>
 __global__ void __launch_bounds__(256) int4_quantize_kernel(const void* __restrict__ w, const Int4Shape s, uint8_t* __restrict__ codes,
                                                             uint16_t* __restrict__ scales, uint8_t* __restrict__ zeros) {
@@ -73,14 +74,15 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const void* __restri
   if (t.tile >= s.tiles()) return;   // whole blocks
   float v[8] = {};
   if (t.in) load_vals<8>(w, F32, t.row * s.K + t.k, v);
-  float lo = 0.f, hi = 0.f;
+  float lo = 0.f, hi = 0.f, none = 0.f;   // none: 0, or NaN where a value is not finite, which the range would not show
 #pragma unroll
-  for (int i = 0; i < 8; ++i) lo = fminf(lo, v[i]), hi = fmaxf(hi, v[i]);
+  for (int i = 0; i < 8; ++i) lo = fminf(lo, v[i]), hi = fmaxf(hi, v[i]), none = fmaf(v[i], 0.f, none);
   for (int o = 1; o < s.group / 8; o <<= 1) {   // the group's threads: 4, 8 or 16 neighbours
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    none += __shfl_xor_sync(0xffffffffu, none, o);
   }
-  const float scale = bf16_round(ZEROS ? (hi - lo) / 15.f : fmaxf(-lo, hi) / 7.f);
+  const float scale = bf16_round(ZEROS ? (hi - lo) / 15.f : fmaxf(-lo, hi) / 7.f) + none;
   float zero = 8.f;
   if (ZEROS) zero = scale > 0.f ? fminf(fmaxf(rintf(-lo / scale), 0.f), 15.f) : 0.f;
   int q[8];

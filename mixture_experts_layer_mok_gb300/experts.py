@@ -262,7 +262,8 @@ def _int4_args(weight):
 def int4_quantize(w, group: int = 128, zeros: bool = False, stream=None) -> Int4Weight:
     """w bf16 or fp32 [N, K] or [matrices, N, K] in 4 bits, to the nearest:
     symmetric about 8, or with ``zeros`` over each group's own range.  group 32,
-    64 or 128, K a multiple of it."""
+    64 or 128, K a multiple of it.  A group with a NaN or an infinity becomes NaN
+    as a whole."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return int4_quantize(w, group, zeros)

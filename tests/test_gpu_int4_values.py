@@ -1,0 +1,51 @@
+"""4-bit weights of values at the ends of their types: what is not finite, ranges
+beyond the largest number, and zeros with more than four bits."""
+import pytest
+import torch
+
+from tests.gpu_util import mok
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _weights(lead, N, K, dtype, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return (torch.randn(*lead, N, K, generator=g, device="cuda") * 0.05).to(dtype)
+
+
+@pytest.mark.parametrize("lead,N,K,group", [((), 3, 32, 32), ((), 24, 384, 128), ((3,), 17, 320, 64), ((2,), 33, 224, 32)])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_group_with_a_value_that_is_not_finite_is_nan(lead, N, K, group, zeros, dtype):
+    m = mok()
+    w = _weights(lead, N, K, dtype, N + K)
+    clean = m.int4_dequantize(m.int4_quantize(w, group, zeros))
+    inf, nan = float("inf"), float("nan")
+    rows = w.view(-1, K)
+    at = [(0, 0, nan), (1, K - 1, inf), (2, group // 2, -inf)]
+    if N > 16:
+        at += [(16, K - group, -nan), (N - 1, 7, nan), (N - 1, 8, inf)]
+    hit = torch.zeros(rows.shape[0], K // group, dtype=torch.bool, device="cuda")
+    for r, k, v in at:
+        rows[r, k] = v
+        hit[r, k // group] = True
+    rows[-1, K - group:] = nan                       # nothing else in the group
+    hit[-1, -1] = True
+    got = m.int4_dequantize(m.int4_quantize(w, group, zeros))
+    hit = hit.repeat_interleave(group, -1).view(w.shape)
+    assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("rows,N,K", [(1, 100, 512), (30, 100, 512), (5, 39200, 96), (20, 8200, 1056)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_products_show_it_in_that_row_alone(rows, N, K, zeros):
+    m = mok()
+    w = _weights((), N, K, BF16, 1)
+    x = _weights((), rows, K, BF16, 2)
+    clean = m.int4_linear(x, m.int4_quantize(w, 32, zeros))
+    w[N // 2, K // 2] = float("nan")
+    y = m.int4_linear(x, m.int4_quantize(w, 32, zeros))
+    assert torch.isnan(y[:, N // 2]).all()
+    y[:, N // 2] = clean[:, N // 2]
+    assert torch.equal(y, clean)
