@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const void* __restri
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     none += __shfl_xor_sync(0xffffffffu, none, o);
   }
-  const float scale = bf16_round(ZEROS ? (hi - lo) / 15.f : fmaxf(-lo, hi) / 7.f) + none;
+  const float range = hi - lo;   // (may pass the largest number, which a fifteenth of it does not)
+  const float step = !ZEROS ? fmaxf(-lo, hi) / 7.f : isinf(range) ? hi / 15.f - lo / 15.f : range / 15.f;
+  const float scale = bf16_round(step) + none;
   float zero = 8.f;
   if (ZEROS) zero = scale > 0.f ? fminf(fmaxf(rintf(-lo / scale), 0.f), 15.f) : 0.f;
   int q[8];

@@ -49,3 +49,18 @@ def test_products_show_it_in_that_row_alone(rows, N, K, zeros):
     assert torch.isnan(y[:, N // 2]).all()
     y[:, N // 2] = clean[:, N // 2]
     assert torch.equal(y, clean)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_range_beyond_the_largest_number(group, dtype):
+    """lo and hi of 3e38 each: hi - lo is not a number of 32 bits, a fifteenth of it is."""
+    m = mok()
+    g = torch.Generator("cuda").manual_seed(0)
+    w = ((torch.rand(40, 256, generator=g, device="cuda") * 2 - 1) * 3e38).to(dtype)
+    w[:, ::32], w[:, 1::32] = 3e38, -3e38
+    v = w.double().view(40, -1, group)
+    scale = ((v.amax(-1) - v.amin(-1)) / 15).float().to(BF16).double()
+    got = m.int4_dequantize(m.int4_quantize(w, group, True)).double().view_as(v)
+    # half a step for the value and half a step for the zero, a scale off by 2^-8 of itself over 15 steps, and bf16 values
+    assert ((got - v).abs() <= scale[..., None] * (1 + 15 * 2.0 ** -8) + v.abs() * 2.0 ** -7).all()
