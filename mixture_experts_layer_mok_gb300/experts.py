@@ -22,12 +22,18 @@ _I32, _I64 = torch.int32, torch.int64
 
 # A contiguous tensor on the current device.  A call here makes up to six, and a
 # small kernel takes less time than torch.empty's argument parsing does; the
-# allocation underneath is the same.
+# allocation underneath is the same.  Where something watches over allocations (a
+# dispatch or function mode, the filling of fresh memory in deterministic runs),
+# they go through torch.empty, which shows them to it.
 _strided = getattr(getattr(torch._C._dynamo, "guards", None), "_empty_strided_cuda", None)
+_dispatch_modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+_function_modes = getattr(torch._C, "_len_torch_function_stack", None)
+if _dispatch_modes is None or _function_modes is None:
+    _strided = None
 
 
 def _new(shape, dtype, dev):
-    if _strided is None:
+    if _strided is None or _dispatch_modes() or _function_modes() or torch.are_deterministic_algorithms_enabled():
         return ops._empty(shape, dtype=dtype, device=dev)
     shape = tuple(shape)   # (not a torch.Size)
     n = len(shape)

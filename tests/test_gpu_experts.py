@@ -127,3 +127,24 @@ def test_refuses_second_derivatives():
     g, = torch.autograd.grad(y.float().square().sum(), w, create_graph=True)
     with pytest.raises(RuntimeError):
         g.float().sum().backward()
+
+
+def test_dispatch_modes_see_the_outputs():
+    m = mok()
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Count(TorchDispatchMode):
+        made = 0
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            if "empty" in str(func):
+                Count.made += out.numel() * out.element_size()
+            return out
+
+    x = torch.randn(64, 32, device="cuda")
+    plain = m.route(x, 4)
+    with Count():
+        r = m.route(x, 4)
+    assert Count.made == 64 * 4 * (8 + 4) + 64 * 4
+    assert torch.equal(r.experts, plain.experts) and torch.equal(r.weights, plain.weights) and torch.equal(r.lse, plain.lse)
