@@ -5,7 +5,8 @@ by expert with their gradients, and the projections with 4-bit weights
 
 They serve experts that the layer's fixed SwiGLU does not express, and the
 decoding of single tokens.  The calls follow those of ``ops``: ``stream``,
-contiguous tensors on the current GPU, 16-byte aligned.
+contiguous tensors on the current GPU, 16-byte aligned; autograd does not
+record them (``autograd.route`` and ``autograd.grouped_linear`` are its faces).
 """
 from __future__ import annotations
 
@@ -285,7 +286,8 @@ def int4_quantize(w, group: int = 128, zeros: bool = False, stream=None) -> Int4
 def int4_pack(codes, scales, zeros=None, stream=None) -> Int4Weight:
     """An ``Int4Weight`` of codes made elsewhere: uint8 [..., N, K / 2], two to a
     byte, the even column's in the low half; scales bf16 [..., N, K / group],
-    zeros uint8 of their shape (0..15) or None."""
+    zeros uint8 of their shape, 0..15 in the low four bits (the others do not
+    count: a zero of 16 would be 0), or None."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return int4_pack(codes, scales, zeros)
@@ -329,7 +331,9 @@ def int4_linear(x, weight: Int4Weight, bias=None, activation: str = "none", expe
     x [..., K] times each of its row's matrices (or x [..., k, K], a row for
     each), bias [matrices, N]; id -1 gives zeros.  bias bf16 or fp32; y in
     ``out_dtype`` (bf16 or fp32), rounded once from fp32; the weights' values are
-    not rounded."""
+    not rounded.  For decoding: autograd does not record it, and y has no graph
+    where x requires a gradient; a frozen 4-bit weight that is trained through is
+    ``int4_dequantize`` under ``autograd.linear`` or ``autograd.grouped_linear``."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return int4_linear(x, weight, bias, activation, experts, out_dtype)

@@ -64,3 +64,12 @@ def test_a_range_beyond_the_largest_number(group, dtype):
     got = m.int4_dequantize(m.int4_quantize(w, group, True)).double().view_as(v)
     # half a step for the value and half a step for the zero, a scale off by 2^-8 of itself over 15 steps, and bf16 values
     assert ((got - v).abs() <= scale[..., None] * (1 + 15 * 2.0 ** -8) + v.abs() * 2.0 ** -7).all()
+
+
+def test_zeros_count_by_their_low_four_bits():
+    m = mok()
+    g = torch.Generator("cuda").manual_seed(0)
+    codes = torch.randint(0, 256, (3, 20, 80), generator=g, device="cuda", dtype=torch.uint8)
+    scales = (torch.rand(3, 20, 5, generator=g, device="cuda") + 0.5).to(BF16)
+    zeros = torch.randint(0, 256, (3, 20, 5), generator=g, device="cuda", dtype=torch.uint8)
+    assert torch.equal(m.int4_dequantize(m.int4_pack(codes, scales, zeros)), m.int4_dequantize(m.int4_pack(codes, scales, zeros & 15)))
