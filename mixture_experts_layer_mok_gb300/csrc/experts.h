@@ -96,8 +96,10 @@ struct GroupedRowsParams {
   int bias_f32;
   void* out;             // [M][L]
   uint16_t* z;           // [M][L] bf16 or NULL
-  // the kernel before it on the stream is one that waited for all before itself, and whose results this one does not read:
-  // it starts as that one's CTAs leave, and waits for it at its end
+  // The kernel before it on the stream is grouped_weight_kernel, none of whose results this one reads: it starts as that
+  // one's CTAs leave, without a wait, and waits for it at its end.  Right behind that kernel alone, each of whose CTAs waits
+  // for all before it and only then lets the next kernel start: behind one that does so earlier, or that is not there, x
+  // (dz) would be read before the pass that writes it has ended.
   int beside_last;
   int* status;
 };

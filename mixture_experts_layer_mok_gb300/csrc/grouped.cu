@@ -36,7 +36,7 @@ mok_status_t launch_rows(const GroupedRowsMaps& maps, const GroupedRowsParams& p
   static KernelInfo info;
   int n = 0;
   MOK_CUDA(resident_clusters(kern, info, C::kThreads, C::kSmemBytes, 2, &n));
-  // at most, and with tiles in parts of 64 rows or more
+  // at most, and with tiles in as many parts as they have 64 rows
   const long long items = (static_cast<long long>(p.M) / 256 + static_cast<long long>(p.M) / 64 + (p.E < p.M ? p.E : p.M)) * p.l_tiles;
   const int pairs = items < n ? static_cast<int>(items) : n;
   MOK_CUDA(launch_clusters(kern, dim3(2 * pairs), C::kThreads, C::kSmemBytes, 2, st, maps, p));
@@ -110,6 +110,9 @@ struct DzPiece {
 // sums over the rows of group e in a chunk: from one pair (chunk, e) to the next
 // at least one of the two grows, so that no two share a place.  The first block
 // also writes the plan.
+// dz goes to the tensor core's products, whose operands are bf16: one rounding more
+// than the formula in 32 bits has (2.3e-3 of relative error in dx and d_weight for
+// 1.7e-3), as in the dense projection.  The sums are of the unrounded values.
 // Bound by memory: 201 MB of 32768 x 1024, two of three read, take 30 us.
 template <class DY, int ACT>
 __global__ void __launch_bounds__(256) grouped_dz_kernel(const __grid_constant__ Plan plan, const DY* __restrict__ dy,

@@ -7,9 +7,10 @@
 //     dx       l = k, k = n:  A = W_e^T (W_e is [k][l]),     B = dz rows
 //   weight kernel  D[c][l] = sum_m dz[m][c] x[m][l], m the rows of one group.
 //
-// Measured, the rows kernel: 32768 rows of 64 groups of 1024 x 2048 with SiLU and z
-// 106 us (DRAM and tensor pipe 58% busy each), 131072 of 2048 x 4096 1200, 512 rows
-// of 256 groups of 2048 x 7168 800 (the weights' bytes).
+// Measured, the rows kernel in short graph replays: 32768 rows of 64 groups of 1024
+// x 2048 with SiLU and z 106 us (DRAM and tensor pipe 58% busy each), 131072 of 2048
+// x 4096 1200 to 1240, 512 rows of 256 groups of 2048 x 7168 780 (the weights' bytes).
+// Calls in a long loop take 118 to 120, 1400 to 1413 (the power limit) and 785 to 833.
 //
 // Both are persistent CTA pairs with two accumulator buffers.  In the rows
 // kernel the weights run over the tensor core's M (256 over two SMs) and a
@@ -130,8 +131,9 @@ struct RowsItem {
 // group of 4 of its row tiles l goes on outside the rows, so that the CTAs at
 // work at one time share few rows of both operands.  The last round's items,
 // where half the pairs or more would have none, are cut by rows into up to 4
-// parts of 64 rows at least, for each of which the tensor core takes less time: 256
-// rows of one group of 1024 x 4096 18 us, and 25 whole; 32768 rows of 64 groups 2 us
+// parts, for each of which the tensor core takes less time: as many as a tile has
+// whole 64s of rows, of equal length in steps of 32, so that the last may be short
+// (200 rows: 96, 96 and 8).  256 rows of one group of 1024 x 4096 18 us, and 25 whole; 32768 rows of 64 groups 2 us
 // less of 108; 16 rows of 8 groups, which are not cut, 0.2 us more of 8.
 __device__ __forceinline__ bool rows_item(const GroupedRowsParams& p, const GroupTable& g, int idx, int lane, RowsItem& it) {
   int part = 0, parts = 1;
@@ -519,9 +521,10 @@ struct GroupedWeightParams {
   GroupedBias bias;
   int* status;
 };
-// 16 epilogue warps, each of which stores a block of 128-byte rows.  Bound by
-// memory where groups are short: 64 groups of 1024 x 2048 take 70 us with one
-// row each, as a memset of the 268 MB would (4.05 TB/s), and 110 with 512.
+// 16 epilogue warps, each of which stores a block of 128-byte rows.  64 groups
+// of 1024 x 2048 take 110 us with 512 rows each and 70 with one: a tile's own chain of
+// loads, products and reads (58 without the stores), not the 268 MB, which a fill
+// writes in 37 (7.3 TB/s).
 struct GroupedWeightCfg {
   static constexpr int kStages = 5, kEpiWarps = 16, kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kOutBytes = 4096;   // an epilogue warp's 32 x 64 block in bf16
@@ -616,7 +619,7 @@ __global__ void __launch_bounds__(GroupedWeightCfg::kThreads, 1) grouped_weight_
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  griddep_wait();
+  griddep_wait();   // before the next kernel may start: see GroupedRowsParams::beside_last
   griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   if (warp == 0) {

@@ -64,7 +64,9 @@ __device__ __forceinline__ float bf16_round(float v) { return __bfloat162float(_
 // Symmetric: scale = bf16(amax / 7), q = round(w / scale) + 8; with zeros: the
 // range [lo, hi] that holds 0, scale = bf16((hi - lo) / 15), zero = round(-lo /
 // scale), q = round(w / scale) + zero; both clamped to 0..15.  A group with a
-// value that is not finite gets a NaN scale.
+// value that is not finite gets a NaN scale.  64 matrices of 2048 x 2048 in bf16
+// take 427 to 488 us, 680 MB or so that a copy moves in 100: a tile to a block, with
+// its place to find, and eight divisions to a thread.
 template <bool F32, bool ZEROS>
 __global__ void __launch_bounds__(256) int4_quantize_kernel(const void* __restrict__ w, const Int4Shape s, uint8_t* __restrict__ codes,
                                                             uint16_t* __restrict__ scales, uint8_t* __restrict__ zeros) {
@@ -99,7 +101,8 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const void* __restri
   }
 }
 
-// From row-major codes, two to a byte, the even column's in the low half.
+// From row-major codes, two to a byte, the even column's in the low half: as many
+// matrices 275 to 292 us, 285 MB or so that a copy moves in 42.
 __global__ void __launch_bounds__(256) int4_pack_kernel(const uint8_t* __restrict__ qp, const uint16_t* __restrict__ qs,
                                                         const uint8_t* __restrict__ qz, const Int4Shape s, uint8_t* __restrict__ codes,
                                                         uint16_t* __restrict__ scales, uint8_t* __restrict__ zeros) {
@@ -121,9 +124,9 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const uint8_t* __restric
 }
 
 // Up to kReadTiles neighbours along K to a block, a tile's loads not waiting for
-// another's.  Bound by memory: 64 matrices of 2048 x 2048 166 us, in which 537 of
-// 680 MB are written (4.0 TB/s, as a memset); a tile to a block, with its place to
-// find, took about 260.
+// another's: 64 matrices of 2048 x 2048 151 us (groups of 128) to 181 (of 32, with
+// zeros), 680 MB or so that a copy moves in 100; a tile to a block, with its place
+// to find, took about 260.
 constexpr int kReadTiles = 8;
 __global__ void __launch_bounds__(256) int4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
                                                               const uint8_t* __restrict__ zeros, const Int4Shape s,
@@ -185,8 +188,9 @@ dim3 tile_grid(long long tiles) {
 // meets the 16 bytes of x's columns 32 j + 8 t .. + 7 as they lie in memory.
 // Codes, scales and x come in through shared memory by asynchronous copies some
 // stages ahead: registers would hold too few bytes in flight (8 experts of 2048 x
-// 7168 took 30 us so, and 19 with stages: 245 instructions a tile, issue slots 52%
-// busy, DRAM 40%).  One row times 7168 x 2048: 3.5 us.
+// 7168 took 30 us so, and 19 with stages in graph replays, 20.4 in calls on other
+// experts: 245 instructions a tile, issue slots 52% busy, DRAM 40%).  One row times
+// 7168 x 2048: 3.6 us.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -642,7 +646,7 @@ cudaError_t split_launch(const Int4LinearArgs& a, int num_sms, cudaStream_t st) 
   if (err != cudaSuccess) return err;
   const unsigned x = static_cast<unsigned>((a.w.row_tiles() + R - 1) / R);
   const unsigned y = !EXPERTS ? (a.rows + C::kCols - 1) / C::kCols : a.by_expert ? static_cast<unsigned>(a.w.matrices) : a.rows;
-  // 4 warps to a block, 8 where an SM would have fewer than ten warps and each has a block of K.  Measured with 2, 4 and 8: one row
+  // 4 warps to a block, 8 where an SM would have fewer than ten warps and each has a block of K.  Measured (graph replays, here and below) with 2, 4 and 8: one row
   // times 7168 x 2048 4.2, 3.5 and 4.1 us, 8 experts of 2048 x 7168 20.4, 17.7 and 19.5, 12 rows times 2048 x 2048 8.4, 5.2 and
   // 4.3, 30 rows times 7504 x 512 7.4, 5.6 and 7.8.  Two or one where K is short and there are many blocks, of
   // which an SM then holds more.  Measured with 1, 2 and 4: 42 rows among 55 experts of 9712 x 384 29, 37 and 53 us, 120 rows among

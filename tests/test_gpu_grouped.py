@@ -371,3 +371,10 @@ def test_as_many_rows_as_there_can_be():
     assert m.linear_status() == 0
     del x, z, got
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("counts", [[136], [136] * 3, [200], [208], [224], [232, 200, 8], [256] * 76 + [200], [0, 136, 0, 224]])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_parts_that_leave_few_rows(counts, out):
+    """Tiles of a last round whose parts, in steps of 32 rows, leave 8 or 16 for the last."""
+    test_few_tiles(counts, out, 264)
