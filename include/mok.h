@@ -556,6 +556,8 @@ mok_status_t mok_linear_bwd(const void* dy, int dy_dtype, const uint16_t* x, con
 mok_status_t mok_linear_status(int* status);
 
 /* ---- router: logits -> experts and their weights --------------------------
+ * (No output of the calls from here to mok_int4_linear may overlap an input.)
+ *
  * logits [T][E], bf16 or fp32.  s = softmax(logits) or sigmoid(logits), in fp32.
  * The k experts of the largest s + bias (bias fp32 [E], the sum in fp32; of equal
  * sums the larger logit first, of equal logits the lowest index), or with NULL of

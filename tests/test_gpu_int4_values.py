@@ -73,3 +73,25 @@ def test_zeros_count_by_their_low_four_bits():
     scales = (torch.rand(3, 20, 5, generator=g, device="cuda") + 0.5).to(BF16)
     zeros = torch.randint(0, 256, (3, 20, 5), generator=g, device="cuda", dtype=torch.uint8)
     assert torch.equal(m.int4_dequantize(m.int4_pack(codes, scales, zeros)), m.int4_dequantize(m.int4_pack(codes, scales, zeros & 15)))
+
+
+@pytest.mark.parametrize("E,N,K", [(0, 24, 96), (0, 8200, 1056), (3, 40, 160), (66000, 1, 32)])
+def test_as_many_rows_as_there_can_be(E, N, K):
+    """65535 rows: of one matrix by both kernels, of few experts and of more experts
+    than rows.  Rows, codes and scales are whole numbers and powers of two, so that
+    the sums are exact."""
+    m = mok()
+    g = torch.Generator("cuda").manual_seed(N)
+    k, rows = 3 if E else 1, 65535
+    codes = torch.randint(0, 256, (E, N, K // 2) if E else (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.exp2(torch.randint(-3, 2, codes.shape[:-1] + (K // 32,), generator=g, device="cuda").float()).to(BF16)
+    w = m.int4_pack(codes, scales)
+    x = torch.randint(-2, 3, (rows // k, K), generator=g, device="cuda").to(BF16)
+    values = m.int4_dequantize(w).float()      # (exact: four bits times a power of two)
+    if not E:
+        assert torch.equal(m.int4_linear(x, w, out_dtype=F32), x.float() @ values.t())
+        return
+    ids = torch.randint(-1, E, (rows // k, k), generator=g, device="cuda")
+    y = m.int4_linear(x, w, experts=ids, out_dtype=F32)
+    ref = torch.einsum("tknc,tc->tkn", values[ids.clamp(min=0)], x.float()) * (ids >= 0)[..., None]
+    assert torch.equal(y, ref) and m.linear_status() == 0
