@@ -87,3 +87,19 @@ def test_equal_sums_go_by_logit_and_then_by_index(E, k, T):
     r = m.route(x, k, score="sigmoid", bias=bias)
     assert torch.equal(r.experts, order)
     assert (r.weights - 1 / k).abs().max().item() <= 8 * U / k
+
+
+@pytest.mark.parametrize("E,k", [(8, 8), (40, 38), (96, 32), (96, 40), (200, 64), (1000, 33)])
+@pytest.mark.parametrize("T", [3, 2600])
+def test_biases_that_open_and_close_experts(E, k, T):
+    """+inf before all, -inf behind all but masked logits; each of them in the logits' order."""
+    m = mok()
+    g = torch.Generator("cuda").manual_seed(E)
+    x = torch.randint(20, 40, (T, E), device="cuda", generator=g).float()
+    x[:, ::5] = -float("inf")
+    bias = torch.zeros(E, device="cuda")
+    bias[3::4], bias[1::3] = float("inf"), -float("inf")
+    level = torch.where(torch.isinf(x), torch.full_like(x, -2.0), torch.sign(bias).expand_as(x))
+    order = torch.sort(torch.nan_to_num(x, neginf=-1.0), dim=1, descending=True, stable=True).indices
+    order = order.gather(1, torch.sort(level.gather(1, order), dim=1, descending=True, stable=True).indices)[:, :k]
+    assert torch.equal(m.route(x, k, score="sigmoid", bias=bias).experts, order)
